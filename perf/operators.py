@@ -330,11 +330,11 @@ def _norm_bwd(st):
 
 def _code(x, top, power):
     """8-bit codes of x (float64): |x| = scale * (|code| / top)^power with the block's largest value
-    as its scale (kept in float32), to the nearest code; a positive second moment keeps a code of at
-    least 1."""
+    as its scale (kept in float32), to the nearest code, the smaller one at half-way points (which equal
+    ratios of 16-bit gradients hit exactly); a positive second moment keeps a code of at least 1."""
     x = x.view(-1, BLOCK)
     scale = x.abs().amax(1, keepdim=True)
-    c = torch.floor(top * (x.abs() / scale.clamp_min(1e-300)) ** (1.0 / power) + 0.5).clamp_max(top)
+    c = torch.ceil(top * (x.abs() / scale.clamp_min(1e-300)) ** (1.0 / power) - (0.5 + 1e-10)).clamp_max(top)
     if power == 4:
         c = torch.where(x > 0, c.clamp_min(1), c)
         return c.to(torch.uint8).view(-1), scale.float().view(-1)
@@ -442,7 +442,7 @@ def exact(case, seed):
             x = x.view(-1, BLOCK)
             scale = x.abs().max(1, keepdim=True).values
             unit = torch.where(scale > 0, x.abs() / scale, torch.zeros_like(x))
-            edges = ((torch.arange(top, device=DEV, dtype=torch.float64) + 0.5) / top) ** power
+            edges = ((torch.arange(top, device=DEV, dtype=torch.float64) + 0.5) / top) ** power * (1 + 2.0 ** -40)
             level = torch.bucketize(unit, edges, right=True)
             level = torch.maximum(level, (x > 0).long()) if power == 4 else level
             return (scale * (level.double() / top) ** power * x.sign()).view(-1)
