@@ -17,6 +17,11 @@
  *   qha_dense_project         the dense projection (float32 products on matrix cores) with ReLU
  *   qha_dense_backward        its gradients dA and dW in one pass (float32 products on matrix cores)
  *
+ * and the operators that make a training step of those layers:
+ *
+ *   qha_adamw_step            one AdamW step over many tensors, moments in float32 or 8-bit codes
+ *   qha_adamw_values          8-bit moments read back as float32 values
+ *
  * plus small set-up helpers.  Conventions shared by every entry point:
  *   - Array arguments are caller-owned.  Pointers documented as "device" must be HIP device
  *     memory (or host memory the device can access); "host" pointers are read on the CPU.
@@ -363,6 +368,62 @@ int qha_dense_backward(int64_t m, int64_t n, int64_t k, const float* dh, int64_t
                        const float* a, int64_t lda, const float* w, int64_t ldw, float* da, int64_t ldda,
                        float* dw, int64_t lddw, void* workspace, size_t workspace_bytes, void* stream);
 size_t qha_dense_backward_workspace(int64_t m, int64_t n, int64_t k);
+
+/* ------------------------------------------------------------------------------------------
+ * Training operators
+ * ---------------------------------------------------------------------------------------- */
+
+/* element types */
+#define QHA_F32 0
+#define QHA_BF16 1
+#define QHA_F16 2
+
+/* One AdamW step over a list of tensors.  With g = grad_scale * grad, for every element:
+ *   m = beta1 m + (1 - beta1) g,    v = beta2 v + (1 - beta2) g^2,
+ *   param = param (1 - lr weight_decay) - lr (m / (1 - beta1^step)) / (sqrt(v / (1 - beta2^step)) + eps)
+ * param is float32; grad is grad_type; copy (nullable) receives the new parameter rounded to
+ * copy_type (nearest even), for models that compute in 16 bits on float32 weights.
+ * state_bits = 32: m and v are float32[n]; the update runs in float32.
+ * state_bits = 8: m is int8[n] and v uint8[n] in blocks of QHA_ADAMW_BLOCK consecutive elements (the
+ * last one short), one float32 scale per block in m_scale / v_scale [ceil(n / QHA_ADAMW_BLOCK)]:
+ *   m = m_scale sign(c) (c / 127)^2,    v = v_scale (c / 255)^4
+ * (the step between neighbouring codes grows with the value, so one block spans a range of 1.6e4 in
+ * m and of 4e9 in v).  A block's scale is its largest magnitude; codes are the nearest ones,
+ * decided as in float64 (a ratio to the largest within 2^-40 of a half-way point, where equal ratios of
+ * 16-bit gradients fall, goes to the smaller magnitude), and a v > 0 keeps a code of
+ * at least 1, so that no element's denominator collapses.  Both moments are updated in float64 and
+ * the parameter from the updated moments before they are coded.  A block with a moment that is not finite in
+ * float32 gets a NaN scale and codes 0: all its moments then read as NaN.
+ * tensors: host array, read during the call (the device pointers in it must stay valid until the
+ * work is done).  Tensors must not overlap.  Elements are accessed by 4 where a tensor's pointers
+ * are aligned to 4 elements (codes: to 4 bytes), one by one otherwise; param, the scales and 32-bit
+ * moments need 4-byte alignment, 16-bit gradients and copies 2.  step counts from 1 and is a host
+ * value: a captured call replays the same one.  Up to 48 tensors go in one launch.  Tensors with
+ * n = 0 are skipped (their pointers may be NULL).
+ * Errors: INVALID_ARG (null or misaligned pointers, n < 0, an n beyond 2^40, unknown types or state
+ * bits, lr, eps or weight_decay negative or not finite, a beta outside [0, 1), step < 1, a grad_scale that is not
+ * finite), HIP. */
+#define QHA_ADAMW_BLOCK 256
+typedef struct qha_adamw_tensor {
+  int64_t n;               /* elements */
+  float* param;            /* device float32[n], updated */
+  const void* grad;        /* device grad_type[n] */
+  void* copy;              /* device copy_type[n], written, or NULL */
+  void* m;                 /* device float32[n] or int8[n], updated */
+  void* v;                 /* device float32[n] or uint8[n], updated */
+  float* m_scale;          /* device, one per block (8-bit moments), updated */
+  float* v_scale;
+} qha_adamw_tensor;
+
+int qha_adamw_step(const qha_adamw_tensor* tensors, int64_t n_tensors, int32_t state_bits, int32_t grad_type,
+                   int32_t copy_type, double lr, double beta1, double beta2, double eps, double weight_decay,
+                   double grad_scale, int64_t step, void* stream);
+
+/* Reads n elements of 8-bit moments back as float32 values (the formulas of qha_adamw_step, rounded
+ * once): m, v codes and their scales as there, m_out and v_out device float32[n].  Either triple may
+ * be all NULL.  Errors: INVALID_ARG, HIP. */
+int qha_adamw_values(const int8_t* m, const float* m_scale, float* m_out, const uint8_t* v, const float* v_scale,
+                     float* v_out, int64_t n, void* stream);
 
 /* ------------------------------------------------------------------------------------------
  * Host-side width control (plain host memory, no device work)

@@ -43,6 +43,8 @@ QHA_OK, QHA_ERR_INVALID_ARG, QHA_ERR_UNSUPPORTED, QHA_ERR_HIP, QHA_ERR_WORKSPACE
 NORM_GCN, NORM_MEAN = 0, 1
 PRO_NONE, PRO_RELU_MASK = 0, 1
 EPI_NONE, EPI_RELU = 0, 1
+F32, BF16, F16 = 0, 1, 2
+ADAMW_BLOCK = 256
 DEFAULT_CHUNK = 512
 DEFAULT_GROUP_EDGES = 256
 GROUP_ROWS = 15
@@ -124,6 +126,10 @@ _dense_bwd = _sig("qha_dense_backward", _i32, _i64, _i64, _i64, _vp, _i64, _vp, 
                   _vp, _i64, _vp, _sz, _vp)
 _dense_bwd_ws = _sig("qha_dense_backward_workspace", _sz, _i64, _i64, _i64)
 
+_adamw_step = _sig("qha_adamw_step", _i32, _vp, _i64, _i32, _i32, _i32, C.c_double, C.c_double, C.c_double,
+                   C.c_double, C.c_double, C.c_double, _i64, _vp)
+_adamw_values = _sig("qha_adamw_values", _i32, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _vp)
+
 EXPORTED = ["qha_abi_version", "qha_status_string", "qha_last_error", "qha_pack_layout", "qha_pack_classes",
             "qha_edge_weights", "qha_validate_csr",
             "qha_csr_transpose", "qha_agg_plan_size", "qha_agg_plan_fill", "qha_agg_workspace_bytes",
@@ -131,7 +137,7 @@ EXPORTED = ["qha_abi_version", "qha_status_string", "qha_last_error", "qha_pack_
             "qha_aggregate_bwd",
             "qha_aggregate_bwd_quantize", "qha_dense_project", "qha_dense_project_workspace", "qha_dense_backward",
             "qha_dense_backward_workspace", "qha_mask_levels", "qha_node_bits", "qha_level_order",
-            "qha_coordinator_init", "qha_coordinator_step"]
+            "qha_coordinator_init", "qha_coordinator_step", "qha_adamw_step", "qha_adamw_values"]
 
 
 class QhaError(RuntimeError):
@@ -509,3 +515,115 @@ def dense_backward(dh, h, a, w, da, dw, workspace=None, stream=None):
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     _check(_dense_bwd(int(m), int(n), int(k), pg, ldg, ph, ldh, pa, lda, pw, ldw, pda, ldda, pdw, lddw, ws_ptr,
                       ws_bytes, _stream(stream)), "qha_dense_backward")
+
+
+# ------------------------------------------------------------------------------------------------
+# training operators
+# ------------------------------------------------------------------------------------------------
+
+_TYPES = {torch.float32: F32, torch.bfloat16: BF16, torch.float16: F16}
+
+
+def _type(dtype, name):
+    try:
+        return _TYPES[dtype]
+    except KeyError:
+        raise TypeError(f"{name} must be float32, bfloat16 or float16, got {dtype}") from None
+
+
+def _flat(t, name, n=None, dtype=None):
+    """Checks that t is a contiguous GPU tensor (of n elements, of dtype); returns its pointer."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch tensor")
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must live on the GPU")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if n is not None and t.numel() != n:
+        raise ValueError(f"{name} has {t.numel()} elements, expected {n}")
+    return t.data_ptr()
+
+
+class AdamW:
+    """AdamW over a list of float32 parameter tensors, updated in place by qha_adamw_step.
+
+    Moments are kept in flat tensors in which every parameter starts at a multiple of ADAMW_BLOCK
+    elements (`starts`): m and v float32 (bits=32), or int8 / uint8 codes with one float32 scale per
+    block in m_scale and v_scale (bits=8).  They and the step count t are all of the state: copy
+    them to save or resume.  `copies`, if given, are tensors of one 16-bit or float32 type that
+    receive the rounded parameters."""
+
+    def __init__(self, params, bits: int = 32, betas=(0.9, 0.999), eps: float = 1e-8, weight_decay: float = 0.01,
+                 copies=None):
+        if bits not in (8, 32):
+            raise ValueError(f"bits must be 8 or 32, got {bits}")
+        self.params = list(params)
+        self.copies = None if copies is None else list(copies)
+        self.bits, self.betas, self.eps, self.weight_decay = bits, tuple(betas), eps, weight_decay
+        self.t = 0
+        if self.copies is not None and len(self.copies) != len(self.params):
+            raise ValueError(f"{len(self.copies)} copies for {len(self.params)} parameters")
+        n = len(self.params)
+        self.sizes = [0] * n
+        self.starts = []
+        at = 0
+        for i, p in enumerate(self.params):
+            _flat(p, f"params[{i}]", dtype=torch.float32)
+            if p.device != self.params[0].device:
+                raise ValueError("parameters must live on one GPU")
+            self.sizes[i] = p.numel()
+            self.starts.append(at)
+            at += -(-p.numel() // ADAMW_BLOCK) * ADAMW_BLOCK
+        self._copy_type = F32
+        if self.copies:
+            self._copy_type = _type(self.copies[0].dtype, "copies")
+            for i, c in enumerate(self.copies):
+                _flat(c, f"copies[{i}]", self.sizes[i], self.copies[0].dtype)
+        dev = self.params[0].device if n else "cuda"
+        wide = bits == 32
+        self.m = torch.zeros(at, dtype=torch.float32 if wide else torch.int8, device=dev)
+        self.v = torch.zeros(at, dtype=torch.float32 if wide else torch.uint8, device=dev)
+        self.m_scale = None if wide else torch.zeros(at // ADAMW_BLOCK, dtype=torch.float32, device=dev)
+        self.v_scale = None if wide else torch.zeros(at // ADAMW_BLOCK, dtype=torch.float32, device=dev)
+        # one qha_adamw_tensor per row: n, param, grad, copy, m, v, m_scale, v_scale
+        self._table = np.zeros((max(n, 1), 8), dtype=np.int64)
+        for i, s in enumerate(self.starts):
+            e = 4 if wide else 1
+            self._table[i] = (self.sizes[i], self.params[i].data_ptr(), 0,
+                              self.copies[i].data_ptr() if self.copies else 0, self.m.data_ptr() + s * e,
+                              self.v.data_ptr() + s * e,
+                              0 if wide else self.m_scale.data_ptr() + s // ADAMW_BLOCK * 4,
+                              0 if wide else self.v_scale.data_ptr() + s // ADAMW_BLOCK * 4)
+        self._table_ptr = self._table.ctypes.data
+
+    def step(self, grads, lr: float, grad_scale: float = 1.0, stream=None):
+        """One step with grads (one tensor per parameter, of one type; scaled by grad_scale)."""
+        n = len(self.params)
+        if len(grads) != n:
+            raise ValueError(f"{len(grads)} gradients for {n} parameters")
+        if n == 0:
+            return
+        dtype = grads[0].dtype
+        for i, g in enumerate(grads):
+            if g.dtype != dtype or g.numel() != self.sizes[i] or not g.is_cuda or not g.is_contiguous():
+                _flat(g, f"grads[{i}]", self.sizes[i], dtype)
+        self._table[:n, 2] = [g.data_ptr() for g in grads]
+        status = _adamw_step(self._table_ptr, n, self.bits, _type(dtype, "grads"), self._copy_type, lr, *self.betas,
+                             self.eps, self.weight_decay, grad_scale, self.t + 1, _stream(stream))
+        _check(status, "qha_adamw_step")
+        self.t += 1
+
+    def values(self, m_out=None, v_out=None, stream=None):
+        """The moments as flat float32 tensors (into m_out and v_out, or new ones; 32-bit moments are
+        returned as they are)."""
+        if self.bits == 32:
+            return self.m, self.v
+        n = self.m.numel()
+        m_out = torch.empty(n, dtype=torch.float32, device=self.m.device) if m_out is None else m_out
+        v_out = torch.empty(n, dtype=torch.float32, device=self.m.device) if v_out is None else v_out
+        _check(_adamw_values(self.m.data_ptr(), self.m_scale.data_ptr(), _flat(m_out, "m_out", n, torch.float32),
+                             self.v.data_ptr(), self.v_scale.data_ptr(), _flat(v_out, "v_out", n, torch.float32), n,
+                             _stream(stream)), "qha_adamw_values")
+        return m_out, v_out

@@ -1,0 +1,264 @@
+// AdamW over many tensors in one launch, with moments in float32 or in 8-bit block codes.
+//
+// Mathematics: m = b1 m + (1 - b1) g, v = b2 v + (1 - b2) g^2, p = p (1 - lr wd) - lr m^ / (sqrt(v^) + eps)
+// with m^ = m / (1 - b1^t), v^ = v / (1 - b2^t).  8-bit moments are companded per block of 256 elements:
+// m = s sign(c) (c / 127)^2 and v = s (c / 255)^4, which spaces the codes by about 2 / c of the value, so
+// a small moment beside a large one keeps a code; s is the block's largest magnitude.
+//
+// Bound: memory.  Per element 28 bytes move with float32 moments and gradients, 18 with 8-bit
+// moments, 16-bit gradients and a 16-bit copy; the arithmetic hides behind it, which is why the 8-bit
+// form can afford float64 moments: a code is then the same whichever way its inputs were summed.
+//
+// Mapping: a block of 256 threads takes chunks of 1024 consecutive elements, four per thread (16-byte
+// accesses), so that one wavefront holds exactly one 256-element code block and finds its largest
+// magnitude with wavefront reductions.  The tensors' pointers travel in the kernel arguments (48
+// tensors in one launch, nothing copied to the device), and a block finds its tensor by bisection.
+#include "qha_internal.hpp"
+
+#include "../../include/qha.h"
+
+#pragma clang fp contract(off)
+
+namespace qha {
+namespace {
+
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
+typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
+typedef int8_t i8x4 __attribute__((ext_vector_type(4)));
+typedef uint8_t u8x4 __attribute__((ext_vector_type(4)));
+
+// Four consecutive elements from index i on of an array of n, as one access when `vec` (the array is
+// aligned and the four are inside), else element by element (0 past the end).
+template <typename V, typename E>
+__device__ __forceinline__ V load4(const void* p, int64_t i, int64_t n, bool vec) {
+  const E* q = static_cast<const E*>(p) + i;
+  if (vec) return *reinterpret_cast<const V*>(q);
+  V r = {};
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    if (i + j < n) r[j] = q[j];
+  return r;
+}
+
+template <typename V, typename E>
+__device__ __forceinline__ void store4(void* p, int64_t i, int64_t n, bool vec, V x) {
+  E* q = static_cast<E*>(p) + i;
+  if (vec) {
+    *reinterpret_cast<V*>(q) = x;
+    return;
+  }
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    if (i + j < n) q[j] = x[j];
+}
+
+__device__ __forceinline__ f32x4 load_grad(const void* g, int32_t type, int64_t i, int64_t n, bool vec) {
+  if (type == QHA_F32) return load4<f32x4, float>(g, i, n, vec);
+  if (type == QHA_BF16) return __builtin_convertvector((load4<bf16x4, __bf16>(g, i, n, vec)), f32x4);
+  return __builtin_convertvector((load4<f16x4, _Float16>(g, i, n, vec)), f32x4);
+}
+
+__device__ __forceinline__ void store_copy(void* c, int32_t type, int64_t i, int64_t n, bool vec, f32x4 p) {
+  if (type == QHA_BF16) store4<bf16x4, __bf16>(c, i, n, vec, __builtin_convertvector(p, bf16x4));
+  else if (type == QHA_F16) store4<f16x4, _Float16>(c, i, n, vec, __builtin_convertvector(p, f16x4));
+  else store4<f32x4, float>(c, i, n, vec, p);
+}
+
+__device__ __forceinline__ float wave_max(float x) {
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) x = fmaxf(x, __shfl_xor(x, o, 64));
+  return x;
+}
+
+__device__ __forceinline__ double lane_double(double x, int lane) {
+  const uint64_t b = __builtin_bit_cast(uint64_t, x);
+  const uint32_t lo = __builtin_amdgcn_readlane(static_cast<uint32_t>(b), lane);
+  const uint32_t hi = __builtin_amdgcn_readlane(static_cast<uint32_t>(b >> 32), lane);
+  return __builtin_bit_cast(double, static_cast<uint64_t>(hi) << 32 | lo);
+}
+
+// The wavefront's largest of the non-negative finite x: the largest float32 rounding narrows the
+// lanes that can hold it, almost always to one.
+__device__ __forceinline__ double wave_max_double(double x, float* rounded) {
+  const float f = static_cast<float>(x);
+  const float top = wave_max(f);
+  *rounded = top;
+  uint64_t who = __ballot(f == top);
+  double best = 0.0;
+  while (who) {
+    best = fmax(best, lane_double(x, __builtin_ctzll(who)));
+    who &= who - 1;
+  }
+  return best;
+}
+
+// Nearest code of ratio = |x| / largest in [0, 1]: TOP ratio^(1/POWER), rounded.  The root is taken
+// in float32 (off by less than 1e-4 codes); within 2e-4 of a half-way point the decision is made in
+// float64 on ratio itself, whose half-way points are ((c + 1/2) / TOP)^POWER.  16-bit gradients put
+// ratios exactly on some of those (1/4 is code 63 1/2 of 127), where the last bit of ratio would
+// decide: a ratio has to be over the point by 2^-40 of it to go up.
+template <int TOP, int POWER>
+__device__ __forceinline__ int nearest_code(double ratio) {
+  float r = __builtin_amdgcn_sqrtf(static_cast<float>(ratio));
+  if (POWER == 4) r = __builtin_amdgcn_sqrtf(r);
+  const float t = r * TOP;
+  const float base = floorf(t);
+  bool up = t - base >= 0.5f;
+  if (fabsf(t - base - 0.5f) < 2e-4f) {
+    double e = (static_cast<double>(base) + 0.5) * (1.0 / TOP);
+    e *= e;
+    if (POWER == 4) e *= e;
+    up = ratio > e * (1.0 + 0x1p-40);
+  }
+  return min(static_cast<int>(base) + (up ? 1 : 0), TOP);
+}
+
+__device__ __forceinline__ f32x4 new_params(const AdamArgs& a, f32x4 p, f32x4 m, f32x4 v) {
+  f32x4 r;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) r[j] = p[j] * a.decay - a.step_size * (m[j] / (sqrtf(v[j]) * a.root_c2 + a.eps));
+  return r;
+}
+
+template <int BITS>
+__global__ __launch_bounds__(256) void adamw_kernel(AdamArgs a) {
+  int lo = 0, hi = a.n_tensors - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (blockIdx.x >= a.first[mid]) lo = mid;
+    else hi = mid - 1;
+  }
+  const AdamTensor t = a.t[lo];
+  const uintptr_t wide = reinterpret_cast<uintptr_t>(t.p) | (BITS == 32 ? reinterpret_cast<uintptr_t>(t.m) | reinterpret_cast<uintptr_t>(t.v) : 0) |
+                         (a.grad_type == QHA_F32 ? reinterpret_cast<uintptr_t>(t.g) : 0) | (a.copy_type == QHA_F32 ? reinterpret_cast<uintptr_t>(t.copy) : 0);
+  const uintptr_t half = (a.grad_type == QHA_F32 ? 0 : reinterpret_cast<uintptr_t>(t.g)) | (a.copy_type == QHA_F32 ? 0 : reinterpret_cast<uintptr_t>(t.copy));
+  const uintptr_t quarter = BITS == 8 ? reinterpret_cast<uintptr_t>(t.m) | reinterpret_cast<uintptr_t>(t.v) : 0;
+  const bool aligned = (wide & 15) == 0 && (half & 7) == 0 && (quarter & 3) == 0;
+  const int64_t begin = static_cast<int64_t>(blockIdx.x - a.first[lo]) * a.passes * 1024;
+  for (int pass = 0; pass < a.passes; ++pass) {
+    const int64_t i = begin + pass * 1024 + threadIdx.x * 4;
+    // a wavefront's 256 elements are one code block, so this leaves whole wavefronts only
+    if (begin + pass * 1024 + (threadIdx.x & ~63u) * 4 >= t.n) return;
+    const bool vec = aligned && i + 4 <= t.n;
+    f32x4 p = load4<f32x4, float>(t.p, i, t.n, vec);
+    f32x4 g = load_grad(t.g, a.grad_type, i, t.n, vec);
+    g *= a.grad_scale;
+    f32x4 m, v;
+    if (BITS == 32) {
+      const float b1 = static_cast<float>(a.beta1), b2 = static_cast<float>(a.beta2);
+      const float o1 = static_cast<float>(1.0 - a.beta1), o2 = static_cast<float>(1.0 - a.beta2);
+      m = load4<f32x4, float>(t.m, i, t.n, vec);
+      v = load4<f32x4, float>(t.v, i, t.n, vec);
+      m = m * b1 + g * o1;
+      v = v * b2 + (g * g) * o2;
+      store4<f32x4, float>(t.m, i, t.n, vec, m);
+      store4<f32x4, float>(t.v, i, t.n, vec, v);
+    } else {
+      const int64_t blk = i / kAdamBlock;
+      const i8x4 cm = load4<i8x4, int8_t>(t.m, i, t.n, vec);
+      const u8x4 cv = load4<u8x4, uint8_t>(t.v, i, t.n, vec);
+      const double sm = static_cast<double>(t.ms[blk]) * (a.beta1 / (127.0 * 127.0));
+      const double sv = static_cast<double>(t.vs[blk]) * (a.beta2 / (255.0 * 255.0 * 255.0 * 255.0));
+      double xm[4], xv[4], am = 0.0, av = 0.0;
+      bool fm = true, fv = true;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int c = cm[j];
+        const uint32_t u = static_cast<uint32_t>(cv[j]) * cv[j];
+        const double gd = static_cast<double>(g[j]);
+        xm[j] = sm * static_cast<double>(c * (c < 0 ? -c : c)) + gd * (1.0 - a.beta1);
+        xv[j] = sv * static_cast<double>(u * u) + (gd * gd) * (1.0 - a.beta2);
+        m[j] = static_cast<float>(xm[j]);
+        v[j] = static_cast<float>(xv[j]);
+        fm = fm && __builtin_isfinite(m[j]);
+        fv = fv && __builtin_isfinite(v[j]);
+        am = fmax(am, fabs(xm[j]));
+        av = fmax(av, xv[j]);
+      }
+      const bool ok_m = __all(fm), ok_v = __all(fv);
+      float sm32 = __builtin_nanf(""), sv32 = __builtin_nanf("");
+      i8x4 nm = {};
+      u8x4 nv = {};
+      if (ok_m) {
+        const double top = wave_max_double(am, &sm32);
+        const double inv = sm32 > 0.0f ? 1.0 / top : 0.0;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int c = nearest_code<127, 2>(fabs(xm[j]) * inv);
+          nm[j] = static_cast<int8_t>(xm[j] < 0.0 ? -c : c);
+        }
+      }
+      if (ok_v) {
+        const double top = wave_max_double(av, &sv32);
+        const double inv = sv32 > 0.0f ? 1.0 / top : 0.0;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int c = nearest_code<255, 4>(xv[j] * inv);
+          nv[j] = static_cast<uint8_t>(xv[j] > 0.0 ? max(c, 1) : 0);
+        }
+      }
+      store4<i8x4, int8_t>(t.m, i, t.n, vec, nm);
+      store4<u8x4, uint8_t>(t.v, i, t.n, vec, nv);
+      if ((threadIdx.x & 63) == 0) {
+        t.ms[blk] = sm32;
+        t.vs[blk] = sv32;
+      }
+    }
+    p = new_params(a, p, m, v);
+    store4<f32x4, float>(t.p, i, t.n, vec, p);
+    if (t.copy) store_copy(t.copy, a.copy_type, i, t.n, vec, p);
+  }
+}
+
+__global__ __launch_bounds__(256) void adamw_values_kernel(const int8_t* m, const float* ms, float* m_out,
+                                                           const uint8_t* v, const float* vs, float* v_out,
+                                                           int64_t n) {
+  const int64_t i = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) * 4;
+  if (i >= n) return;
+  const uintptr_t al = reinterpret_cast<uintptr_t>(m) | reinterpret_cast<uintptr_t>(v);
+  const uintptr_t ao = reinterpret_cast<uintptr_t>(m_out) | reinterpret_cast<uintptr_t>(v_out);
+  const bool vec = i + 4 <= n && (al & 3) == 0 && (ao & 15) == 0;
+  const int64_t blk = i / kAdamBlock;
+  if (m) {
+    const i8x4 c = load4<i8x4, int8_t>(m, i, n, vec);
+    const double s = static_cast<double>(ms[blk]) * (1.0 / (127.0 * 127.0));
+    f32x4 r;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) r[j] = static_cast<float>(s * static_cast<double>(c[j] * (c[j] < 0 ? -c[j] : c[j])));
+    store4<f32x4, float>(m_out, i, n, vec, r);
+  }
+  if (v) {
+    const u8x4 c = load4<u8x4, uint8_t>(v, i, n, vec);
+    const double s = static_cast<double>(vs[blk]) * (1.0 / (255.0 * 255.0 * 255.0 * 255.0));
+    f32x4 r;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const uint32_t u = static_cast<uint32_t>(c[j]) * c[j];
+      r[j] = static_cast<float>(s * static_cast<double>(u * u));
+    }
+    store4<f32x4, float>(v_out, i, n, vec, r);
+  }
+}
+
+}  // namespace
+
+// 1024-element passes per block: one while the whole step has few enough of them that every block
+// runs at once, else four, which quarters the look-ups of a block's tensor.
+int32_t adamw_passes(int64_t elements) { return elements <= (8LL << 20) ? 1 : 4; }
+
+hipError_t launch_adamw(const AdamArgs& a, int32_t state_bits, hipStream_t s) {
+  const uint32_t blocks = a.first[a.n_tensors];
+  if (blocks == 0) return hipSuccess;
+  if (state_bits == 8) adamw_kernel<8><<<blocks, 256, 0, s>>>(a);
+  else adamw_kernel<32><<<blocks, 256, 0, s>>>(a);
+  return hipGetLastError();
+}
+
+hipError_t launch_adamw_values(const int8_t* m, const float* ms, float* m_out, const uint8_t* v, const float* vs,
+                               float* v_out, int64_t n, hipStream_t s) {
+  adamw_values_kernel<<<static_cast<uint32_t>((n + 1023) / 1024), 256, 0, s>>>(m, ms, m_out, v, vs, v_out, n);
+  return hipGetLastError();
+}
+
+}  // namespace qha

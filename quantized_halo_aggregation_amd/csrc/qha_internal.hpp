@@ -183,6 +183,34 @@ hipError_t launch_quantize(const QuantArgs& a, int32_t d, hipStream_t s);
 hipError_t launch_gather(const GatherArgs& a, int32_t d, bool with_halo, hipStream_t s, bool quantize_out = false);
 hipError_t launch_gemm(const GemmArgs& a, hipStream_t s);
 
+// AdamW over a batch of tensors, passed to the kernel by value.  Tensor i's chunks are
+// first[i] .. first[i + 1] - 1 of the grid.
+constexpr int kAdamBatch = 48;
+constexpr int kAdamBlock = 256;      // elements that share one scale of an 8-bit moment
+struct AdamTensor {
+  int64_t n;
+  float* p;
+  const void* g;
+  void* copy;
+  void* m;
+  void* v;
+  float* ms;
+  float* vs;
+};
+struct AdamArgs {
+  AdamTensor t[kAdamBatch];
+  uint32_t first[kAdamBatch + 1];
+  int32_t n_tensors;
+  int32_t passes;                    // 1024-element passes per chunk
+  int32_t grad_type, copy_type;
+  float decay, step_size, root_c2, eps, grad_scale;   // root_c2 = 1 / sqrt(1 - beta2^step)
+  double beta1, beta2;
+};
+int32_t adamw_passes(int64_t elements);
+hipError_t launch_adamw(const AdamArgs& a, int32_t state_bits, hipStream_t s);
+hipError_t launch_adamw_values(const int8_t* m, const float* ms, float* m_out, const uint8_t* v, const float* vs,
+                               float* v_out, int64_t n, hipStream_t s);
+
 // Device address of the allocation-free aggregation's scratch (QHA_NOALLOC_SCRATCH_BYTES bytes) on
 // the current device, looked up once per device; nullptr, with *err set, if the lookup fails.
 void* noalloc_scratch(hipError_t* err);

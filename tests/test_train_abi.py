@@ -1,0 +1,72 @@
+"""Refusals of the training operators' entry points and of their binding, without a GPU.
+
+Argument-error cases pass fake (never dereferenced) device addresses: the checks must fire first.
+"""
+import numpy as np
+import pytest
+import torch
+
+from quantized_halo_aggregation_amd import binding as B
+
+FAKE = 0x10000
+
+
+def _adam(tensors=((10, FAKE, FAKE, 0, FAKE, FAKE, FAKE, FAKE),), n=None, bits=32, gt=B.F32, ct=B.F32, lr=1e-3, b1=0.9,
+          b2=0.999, eps=1e-8, wd=0.01, scale=1.0, step=1):
+    table = np.array(tensors, dtype=np.int64).reshape(-1, 8)
+    return B._adamw_step(table.ctypes.data if table.size else None, len(table) if n is None else n, bits, gt, ct, lr, b1,
+                         b2, eps, wd, scale, step, None)
+
+
+@pytest.mark.parametrize("bad", [
+    dict(n=-1), dict(bits=16), dict(gt=3), dict(ct=-1), dict(lr=-1.0), dict(lr=float("nan")), dict(eps=-1e-9),
+    dict(wd=float("inf")), dict(scale=float("nan")), dict(b1=1.0), dict(b2=-0.1), dict(b2=float("nan")), dict(step=0),
+    dict(tensors=(), n=1),
+    dict(tensors=((-1, FAKE, FAKE, 0, FAKE, FAKE, 0, 0),)),
+    dict(tensors=((1 << 41, FAKE, FAKE, 0, FAKE, FAKE, 0, 0),)),
+    dict(tensors=((10, 0, FAKE, 0, FAKE, FAKE, 0, 0),)),
+    dict(tensors=((10, FAKE, 0, 0, FAKE, FAKE, 0, 0),)),
+    dict(tensors=((10, FAKE, FAKE, 0, 0, FAKE, 0, 0),)),
+    dict(tensors=((10, FAKE, FAKE, 0, FAKE, 0, 0, 0),)),
+    dict(tensors=((10, FAKE, FAKE, 0, FAKE, FAKE, 0, FAKE),), bits=8),
+    dict(tensors=((10, FAKE, FAKE, 0, FAKE, FAKE, FAKE, 0),), bits=8),
+    dict(tensors=((10, FAKE + 2, FAKE, 0, FAKE, FAKE, 0, 0),)),
+    dict(tensors=((10, FAKE, FAKE + 2, 0, FAKE, FAKE, 0, 0),)),
+    dict(tensors=((10, FAKE, FAKE + 1, 0, FAKE, FAKE, 0, 0),), gt=B.BF16),
+    dict(tensors=((10, FAKE, FAKE, FAKE + 1, FAKE, FAKE, 0, 0),), ct=B.F16),
+    dict(tensors=((10, FAKE, FAKE, 0, FAKE + 2, FAKE, 0, 0),)),
+    dict(tensors=((10, FAKE, FAKE, 0, FAKE, FAKE, FAKE + 2, FAKE),), bits=8),
+    # a bad tensor after a good one
+    dict(tensors=((10, FAKE, FAKE, 0, FAKE, FAKE, 0, 0), (10, FAKE, FAKE, 0, FAKE, 0, 0, 0))),
+])
+def test_adamw_step_refuses(bad):
+    assert _adam(**bad) == B.QHA_ERR_INVALID_ARG
+    assert B._last_error()
+
+
+def test_adamw_step_without_elements_is_ok():
+    assert _adam(tensors=()) == B.QHA_OK
+    assert _adam(tensors=((0, 0, 0, 0, 0, 0, 0, 0),) * 60) == B.QHA_OK
+
+
+def test_adamw_values_refuses():
+    v = B._adamw_values
+    assert v(FAKE, FAKE, FAKE, None, None, None, -1, None) == B.QHA_ERR_INVALID_ARG
+    assert v(FAKE, None, FAKE, None, None, None, 5, None) == B.QHA_ERR_INVALID_ARG
+    assert v(None, None, None, FAKE, FAKE, None, 5, None) == B.QHA_ERR_INVALID_ARG
+    assert v(FAKE, FAKE, FAKE + 2, None, None, None, 5, None) == B.QHA_ERR_INVALID_ARG
+    assert v(FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, 0, None) == B.QHA_OK
+    assert v(None, None, None, None, None, None, 5, None) == B.QHA_OK
+
+
+def test_adamw_binding_refuses():
+    with pytest.raises(ValueError, match="8 or 32"):
+        B.AdamW([], bits=16)
+    with pytest.raises(TypeError, match="float32"):
+        B.AdamW([torch.zeros(4, dtype=torch.bfloat16)])
+    with pytest.raises(ValueError, match="GPU"):
+        B.AdamW([torch.zeros(4)])
+    with pytest.raises(TypeError, match="tensor"):
+        B.AdamW([np.zeros(4, np.float32)])
+    with pytest.raises(ValueError, match="copies"):
+        B.AdamW([], copies=[torch.zeros(4)])
