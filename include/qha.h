@@ -19,6 +19,8 @@
  *
  * and the operators that make a training step of those layers:
  *
+ *   qha_group_norm_fwd        group normalisation with an activation, channels last
+ *   qha_group_norm_bwd        its gradients
  *   qha_adamw_step            one AdamW step over many tensors, moments in float32 or 8-bit codes
  *   qha_adamw_values          8-bit moments read back as float32 values
  *
@@ -378,6 +380,45 @@ size_t qha_dense_backward_workspace(int64_t m, int64_t n, int64_t k);
 #define QHA_BF16 1
 #define QHA_F16 2
 
+/* activations */
+#define QHA_ACT_NONE 0
+#define QHA_ACT_RELU 1          /* z > 0 ? z : 0 */
+#define QHA_ACT_SILU 2          /* z / (1 + exp(-z)) */
+#define QHA_ACT_GELU 3          /* z (1 + erf(z / sqrt 2)) / 2 */
+
+/* Group normalisation with an activation, channels last.  x holds n_samples * positions rows of c
+ * channels (row r belongs to sample r / positions); the channels form n_groups groups of
+ * c / n_groups neighbours.  Per sample and group, over its positions and channels:
+ *   mean, var = the mean and the (biased) variance,   rstd = 1 / sqrt(var + eps)
+ *   y = act(weight (x - mean) rstd + bias)
+ * positions = 1 normalises every row (node) on its own; positions = all rows, a whole partition;
+ * n_groups = 1 with positions = 1 is a layer norm.  x and y have elements of `type`, leading
+ * dimensions ldx, ldy; y may be x.  weight, bias: device float32[c], nullable (1 and 0).  mean and rstd: device
+ * float32[n_samples * n_groups], written for the backward, both nullable.  Sums are formed in
+ * float64, or in float32 over one row held in registers (mean first, then squares about it), and
+ * their partials are added in a fixed order: results are deterministic.
+ * c is a multiple of 16 bytes of elements (4 or 8) and at most 8192; leading dimensions are at least
+ * c and multiples of the same; x, y (and dy, dx) are 16-byte aligned.  workspace: device, 16-byte
+ * aligned, qha_group_norm_workspace bytes.  n_samples = 0 is a no-op.
+ * Errors: INVALID_ARG, UNSUPPORTED (c above 8192), WORKSPACE, HIP. */
+int qha_group_norm_fwd(int64_t n_samples, int64_t positions, int32_t c, int32_t n_groups, int32_t type, const void* x,
+                       int64_t ldx, const float* weight, const float* bias, double eps, int32_t act, void* y,
+                       int64_t ldy, float* mean, float* rstd, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Gradients of qha_group_norm_fwd from its input and its saved statistics.  With xhat = (x - mean) rstd,
+ * dz = dy act'(weight xhat + bias) (the activation's argument is formed again; for ReLU in float64,
+ * since its sign decides) and q = weight dz:
+ *   dx = rstd (q - mean of q - xhat * mean of (q xhat))     means over the sample's group
+ *   dweight = sum of dz xhat,   dbias = sum of dz             over all rows
+ * dx may be dy or x.  dweight and dbias: device float32[c], overwritten (zeros when there are no
+ * rows), both nullable together.  Other arguments, limits, determinism and errors as there. */
+int qha_group_norm_bwd(int64_t n_samples, int64_t positions, int32_t c, int32_t n_groups, int32_t type, const void* dy,
+                       int64_t lddy, const void* x, int64_t ldx, const float* mean, const float* rstd,
+                       const float* weight, const float* bias, int32_t act, void* dx, int64_t lddx, float* dweight,
+                       float* dbias, void* workspace, size_t workspace_bytes, void* stream);
+/* Bytes of workspace for either direction (0 where none is needed). */
+size_t qha_group_norm_workspace(int64_t n_samples, int64_t positions, int32_t c, int32_t n_groups, int32_t backward);
+
 /* One AdamW step over a list of tensors.  With g = grad_scale * grad, for every element:
  *   m = beta1 m + (1 - beta1) g,    v = beta2 v + (1 - beta2) g^2,
  *   param = param (1 - lr weight_decay) - lr (m / (1 - beta1^step)) / (sqrt(v / (1 - beta2^step)) + eps)
@@ -400,7 +441,7 @@ size_t qha_dense_backward_workspace(int64_t m, int64_t n, int64_t k);
  * moments need 4-byte alignment, 16-bit gradients and copies 2.  step counts from 1 and is a host
  * value: a captured call replays the same one.  Up to 48 tensors go in one launch.  Tensors with
  * n = 0 are skipped (their pointers may be NULL).
- * Errors: INVALID_ARG (null or misaligned pointers, n < 0, an n beyond 2^40, unknown types or state
+ * Errors: INVALID_ARG (null or misaligned pointers, n < 0, an n beyond 2^35, unknown types or state
  * bits, lr, eps or weight_decay negative or not finite, a beta outside [0, 1), step < 1, a grad_scale that is not
  * finite), HIP. */
 #define QHA_ADAMW_BLOCK 256
@@ -421,7 +462,7 @@ int qha_adamw_step(const qha_adamw_tensor* tensors, int64_t n_tensors, int32_t s
 
 /* Reads n elements of 8-bit moments back as float32 values (the formulas of qha_adamw_step, rounded
  * once): m, v codes and their scales as there, m_out and v_out device float32[n].  Either triple may
- * be all NULL.  Errors: INVALID_ARG, HIP. */
+ * be all NULL.  n is at most 2^33.  Errors: INVALID_ARG, HIP. */
 int qha_adamw_values(const int8_t* m, const float* m_scale, float* m_out, const uint8_t* v, const float* v_scale,
                      float* v_out, int64_t n, void* stream);
 

@@ -44,6 +44,7 @@ NORM_GCN, NORM_MEAN = 0, 1
 PRO_NONE, PRO_RELU_MASK = 0, 1
 EPI_NONE, EPI_RELU = 0, 1
 F32, BF16, F16 = 0, 1, 2
+ACT_NONE, ACT_RELU, ACT_SILU, ACT_GELU = 0, 1, 2, 3
 ADAMW_BLOCK = 256
 DEFAULT_CHUNK = 512
 DEFAULT_GROUP_EDGES = 256
@@ -129,6 +130,11 @@ _dense_bwd_ws = _sig("qha_dense_backward_workspace", _sz, _i64, _i64, _i64)
 _adamw_step = _sig("qha_adamw_step", _i32, _vp, _i64, _i32, _i32, _i32, C.c_double, C.c_double, C.c_double,
                    C.c_double, C.c_double, C.c_double, _i64, _vp)
 _adamw_values = _sig("qha_adamw_values", _i32, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _vp)
+_group_norm_fwd = _sig("qha_group_norm_fwd", _i32, _i64, _i64, _i32, _i32, _i32, _vp, _i64, _vp, _vp, C.c_double,
+                       _i32, _vp, _i64, _vp, _vp, _vp, _sz, _vp)
+_group_norm_bwd = _sig("qha_group_norm_bwd", _i32, _i64, _i64, _i32, _i32, _i32, _vp, _i64, _vp, _i64, _vp, _vp, _vp,
+                       _vp, _i32, _vp, _i64, _vp, _vp, _vp, _sz, _vp)
+_group_norm_ws = _sig("qha_group_norm_workspace", _sz, _i64, _i64, _i32, _i32, _i32)
 
 EXPORTED = ["qha_abi_version", "qha_status_string", "qha_last_error", "qha_pack_layout", "qha_pack_classes",
             "qha_edge_weights", "qha_validate_csr",
@@ -137,7 +143,8 @@ EXPORTED = ["qha_abi_version", "qha_status_string", "qha_last_error", "qha_pack_
             "qha_aggregate_bwd",
             "qha_aggregate_bwd_quantize", "qha_dense_project", "qha_dense_project_workspace", "qha_dense_backward",
             "qha_dense_backward_workspace", "qha_mask_levels", "qha_node_bits", "qha_level_order",
-            "qha_coordinator_init", "qha_coordinator_step", "qha_adamw_step", "qha_adamw_values"]
+            "qha_coordinator_init", "qha_coordinator_step", "qha_adamw_step", "qha_adamw_values",
+            "qha_group_norm_fwd", "qha_group_norm_bwd", "qha_group_norm_workspace"]
 
 
 class QhaError(RuntimeError):
@@ -544,6 +551,74 @@ def _flat(t, name, n=None, dtype=None):
     if n is not None and t.numel() != n:
         raise ValueError(f"{name} has {t.numel()} elements, expected {n}")
     return t.data_ptr()
+
+
+def _matrix(t, name, dtype, rows, cols):
+    """(pointer, leading dimension) of a rows x cols matrix of dtype whose rows may be strided."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must live on the GPU")
+    if t.dim() != 2 or t.shape[0] != rows or t.shape[1] != cols:
+        raise ValueError(f"{name} must be {rows} x {cols}, got {tuple(t.shape)}")
+    ld, one = t.stride()
+    if one != 1 and cols > 1:
+        raise ValueError(f"{name} must be a 2-D tensor with contiguous rows")
+    return t.data_ptr(), ld if rows > 1 else max(ld, cols)
+
+
+def _vector(t, name, n):
+    return None if t is None else _flat(t, name, n, torch.float32)
+
+
+def _space(workspace):
+    if workspace is None:
+        return None, 0
+    if not workspace.is_cuda or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous GPU tensor")
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
+def group_norm_workspace(rows: int, positions: int, c: int, n_groups: int, backward=False) -> int:
+    return int(_group_norm_ws(rows // positions, positions, c, n_groups, int(backward)))
+
+
+def _samples(rows, positions):
+    if positions < 1 or rows % positions:
+        raise ValueError(f"{rows} rows are not whole samples of {positions} positions")
+    return rows // positions
+
+
+def group_norm_fwd(x, y, n_groups: int, weight=None, bias=None, mean=None, rstd=None, eps: float = 1e-5,
+                   act: int = ACT_NONE, positions: int = 1, workspace=None, stream=None):
+    """y = act(weight (x - mean) rstd + bias) over x [n_samples * positions, c], statistics per sample
+    and group of channels (written to mean, rstd [n_samples, n_groups] if given)."""
+    rows, c = x.shape
+    n = _samples(rows, positions)
+    px, ldx = _matrix(x, "x", x.dtype, rows, c)
+    py, ldy = _matrix(y, "y", x.dtype, rows, c)
+    ws, ws_bytes = _space(workspace)
+    _check(_group_norm_fwd(n, positions, c, n_groups, _type(x.dtype, "x"), px, ldx, _vector(weight, "weight", c),
+                           _vector(bias, "bias", c), eps, act, py, ldy, _vector(mean, "mean", n * n_groups),
+                           _vector(rstd, "rstd", n * n_groups), ws, ws_bytes, _stream(stream)), "qha_group_norm_fwd")
+
+
+def group_norm_bwd(dy, x, mean, rstd, dx, n_groups: int, weight=None, bias=None, dweight=None, dbias=None,
+                   act: int = ACT_NONE, positions: int = 1, workspace=None, stream=None):
+    """Gradients of group_norm_fwd: dx, and dweight and dbias (float32 [c]) if given."""
+    rows, c = x.shape
+    n = _samples(rows, positions)
+    pg, ldg = _matrix(dy, "dy", x.dtype, rows, c)
+    px, ldx = _matrix(x, "x", x.dtype, rows, c)
+    pd, ldd = _matrix(dx, "dx", x.dtype, rows, c)
+    ws, ws_bytes = _space(workspace)
+    _check(_group_norm_bwd(n, positions, c, n_groups, _type(x.dtype, "x"), pg, ldg, px, ldx,
+                           _flat(mean, "mean", n * n_groups, torch.float32),
+                           _flat(rstd, "rstd", n * n_groups, torch.float32), _vector(weight, "weight", c),
+                           _vector(bias, "bias", c), act, pd, ldd, _vector(dweight, "dweight", c),
+                           _vector(dbias, "dbias", c), ws, ws_bytes, _stream(stream)), "qha_group_norm_bwd")
 
 
 class AdamW:

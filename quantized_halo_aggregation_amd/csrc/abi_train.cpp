@@ -20,12 +20,132 @@ int hip_status(hipError_t e, const char* what) {
 
 bool aligned(const void* p, uintptr_t bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0; }
 
+constexpr int64_t kMaxRows = 2147483647LL;
+
 bool known_type(int32_t t) { return t == QHA_F32 || t == QHA_BF16 || t == QHA_F16; }
 uintptr_t type_bytes(int32_t t) { return t == QHA_F32 ? 4 : 2; }
 
 }  // namespace
 
+namespace {
+
+// Checks the arguments both directions of the group norm share and fills the kernel arguments.
+int take_norm(qha::NormArgs& a, int64_t n_samples, int64_t positions, int32_t c, int32_t n_groups, int32_t type,
+              int32_t act, const float* weight, const float* bias) {
+  std::memset(&a, 0, sizeof(a));
+  if (n_samples < 0 || positions < 1 || n_samples > kMaxRows / positions) return fail(QHA_ERR_INVALID_ARG, "bad sizes");
+  if (!known_type(type)) return fail(QHA_ERR_INVALID_ARG, "unknown element type %d", type);
+  if (act < QHA_ACT_NONE || act > QHA_ACT_GELU) return fail(QHA_ERR_INVALID_ARG, "unknown activation %d", act);
+  const int32_t vec = static_cast<int32_t>(16 / type_bytes(type));
+  if (c < 1 || c % vec != 0) return fail(QHA_ERR_INVALID_ARG, "c=%d must be a multiple of %d", c, vec);
+  if (c > 8192) return fail(QHA_ERR_UNSUPPORTED, "c=%d is above 8192", c);
+  if (n_groups < 1 || c % n_groups != 0) return fail(QHA_ERR_INVALID_ARG, "%d groups do not divide c=%d", n_groups, c);
+  if (!aligned(weight, 16) || !aligned(bias, 16)) return fail(QHA_ERR_INVALID_ARG, "weight / bias are not 16-byte aligned");
+  a.samples = n_samples;
+  a.positions = positions;
+  a.c = c;
+  a.groups = n_groups;
+  a.type = type;
+  a.act = act;
+  a.w = weight;
+  a.b = bias;
+  return QHA_OK;
+}
+
+int check_rows(const char* name, const void* p, int64_t ld, int64_t c, int32_t type) {
+  const int64_t vec = static_cast<int64_t>(16 / type_bytes(type));
+  if (!p) return fail(QHA_ERR_INVALID_ARG, "%s is NULL", name);
+  if (ld < c || ld % vec != 0) return fail(QHA_ERR_INVALID_ARG, "%s: leading dimension %lld must be >= %lld and a multiple of %lld", name, (long long)ld, (long long)c, (long long)vec);
+  if (!aligned(p, 16)) return fail(QHA_ERR_INVALID_ARG, "%s is not 16-byte aligned", name);
+  return QHA_OK;
+}
+
+int take_norm_workspace(qha::NormArgs& a, bool backward, void* ws, size_t bytes) {
+  qha::norm_plan(a, backward);
+  const size_t need = qha::norm_workspace(a, backward);
+  if (need == 0) return QHA_OK;
+  if (!ws || bytes < need) return fail(QHA_ERR_WORKSPACE, "workspace of %zu bytes needed, %zu given", need, ws ? bytes : (size_t)0);
+  if (!aligned(ws, 16)) return fail(QHA_ERR_INVALID_ARG, "workspace is not 16-byte aligned");
+  a.chan_part = static_cast<float*>(ws);
+  const size_t chan = static_cast<size_t>(a.sum_blocks) * 2 * static_cast<size_t>(a.c) * sizeof(float);
+  a.group_part = reinterpret_cast<double*>(static_cast<char*>(ws) + (chan + 15) / 16 * 16);
+  return QHA_OK;
+}
+
+}  // namespace
+
 extern "C" {
+
+size_t qha_group_norm_workspace(int64_t n_samples, int64_t positions, int32_t c, int32_t n_groups, int32_t backward) {
+  if (n_samples <= 0 || positions <= 0 || n_samples > kMaxRows / positions || c <= 0 || c > 8192 || n_groups <= 0 || c % n_groups != 0) return 0;
+  size_t need = 0;
+  for (int32_t type : {QHA_F32, QHA_BF16}) {       // the element type is not asked for: room for each
+    qha::NormArgs a;
+    std::memset(&a, 0, sizeof(a));
+    a.samples = n_samples;
+    a.positions = positions;
+    a.c = c;
+    a.groups = n_groups;
+    a.type = type;
+    qha::norm_plan(a, backward != 0);
+    const size_t b = qha::norm_workspace(a, backward != 0);
+    need = b > need ? b : need;
+  }
+  return need;
+}
+
+int qha_group_norm_fwd(int64_t n_samples, int64_t positions, int32_t c, int32_t n_groups, int32_t type, const void* x,
+                       int64_t ldx, const float* weight, const float* bias, double eps, int32_t act, void* y,
+                       int64_t ldy, float* mean, float* rstd, void* workspace, size_t workspace_bytes, void* stream) {
+  qha::NormArgs a;
+  int st = take_norm(a, n_samples, positions, c, n_groups, type, act, weight, bias);
+  if (st) return st;
+  if (!(eps >= 0.0) || !std::isfinite(eps)) return fail(QHA_ERR_INVALID_ARG, "eps must be finite and not negative");
+  if ((mean == nullptr) != (rstd == nullptr)) return fail(QHA_ERR_INVALID_ARG, "mean and rstd come together");
+  if (!aligned(mean, 4) || !aligned(rstd, 4)) return fail(QHA_ERR_INVALID_ARG, "mean / rstd misaligned");
+  if (n_samples == 0) return ok();
+  if ((st = check_rows("x", x, ldx, c, type)) || (st = check_rows("y", y, ldy, c, type))) return st;
+  if ((st = take_norm_workspace(a, false, workspace, workspace_bytes))) return st;
+  a.x = x;
+  a.ldx = ldx;
+  a.y = y;
+  a.ldy = ldy;
+  a.eps = eps;
+  a.mean = mean;
+  a.rstd = rstd;
+  return hip_status(qha::launch_norm_fwd(a, static_cast<hipStream_t>(stream)), "group_norm_fwd");
+}
+
+int qha_group_norm_bwd(int64_t n_samples, int64_t positions, int32_t c, int32_t n_groups, int32_t type, const void* dy,
+                       int64_t lddy, const void* x, int64_t ldx, const float* mean, const float* rstd,
+                       const float* weight, const float* bias, int32_t act, void* dx, int64_t lddx, float* dweight,
+                       float* dbias, void* workspace, size_t workspace_bytes, void* stream) {
+  qha::NormArgs a;
+  int st = take_norm(a, n_samples, positions, c, n_groups, type, act, weight, bias);
+  if (st) return st;
+  if ((dweight == nullptr) != (dbias == nullptr)) return fail(QHA_ERR_INVALID_ARG, "dweight and dbias come together");
+  if (!aligned(dweight, 4) || !aligned(dbias, 4)) return fail(QHA_ERR_INVALID_ARG, "dweight / dbias misaligned");
+  if (n_samples > 0) {
+    if (!mean || !rstd || !aligned(mean, 4) || !aligned(rstd, 4)) return fail(QHA_ERR_INVALID_ARG, "mean / rstd out of contract");
+    if ((st = check_rows("dy", dy, lddy, c, type)) || (st = check_rows("x", x, ldx, c, type)) ||
+        (st = check_rows("dx", dx, lddx, c, type)))
+      return st;
+    if ((st = take_norm_workspace(a, true, workspace, workspace_bytes))) return st;
+  } else if (!dweight) {
+    return ok();
+  }
+  a.dy = dy;
+  a.lddy = lddy;
+  a.x = x;
+  a.ldx = ldx;
+  a.y = dx;
+  a.ldy = lddx;
+  a.mean = const_cast<float*>(mean);
+  a.rstd = const_cast<float*>(rstd);
+  a.dw = dweight;
+  a.db = dbias;
+  return hip_status(qha::launch_norm_bwd(a, static_cast<hipStream_t>(stream)), "group_norm_bwd");
+}
 
 int qha_adamw_step(const qha_adamw_tensor* tensors, int64_t n_tensors, int32_t state_bits, int32_t grad_type,
                    int32_t copy_type, double lr, double beta1, double beta2, double eps, double weight_decay,
@@ -42,7 +162,7 @@ int qha_adamw_step(const qha_adamw_tensor* tensors, int64_t n_tensors, int32_t s
   int64_t total = 0;
   for (int64_t i = 0; i < n_tensors; ++i) {
     const qha_adamw_tensor& t = tensors[i];
-    if (t.n < 0 || t.n > (1LL << 40)) return fail(QHA_ERR_INVALID_ARG, "tensor %lld: bad size", (long long)i);
+    if (t.n < 0 || t.n > (1LL << 35)) return fail(QHA_ERR_INVALID_ARG, "tensor %lld: bad size", (long long)i);
     if (t.n == 0) continue;
     if (!t.param || !t.grad || !t.m || !t.v || (state_bits == 8 && (!t.m_scale || !t.v_scale)))
       return fail(QHA_ERR_INVALID_ARG, "tensor %lld: NULL pointer", (long long)i);
@@ -51,7 +171,6 @@ int qha_adamw_step(const qha_adamw_tensor* tensors, int64_t n_tensors, int32_t s
         (state_bits == 8 && (!aligned(t.m_scale, 4) || !aligned(t.v_scale, 4))))
       return fail(QHA_ERR_INVALID_ARG, "tensor %lld: misaligned pointer", (long long)i);
     total += t.n;
-    if (total > (1LL << 42)) return fail(QHA_ERR_INVALID_ARG, "too many elements");
   }
   qha::AdamArgs a;
   std::memset(&a, 0, sizeof(a));
@@ -76,7 +195,7 @@ int qha_adamw_step(const qha_adamw_tensor* tensors, int64_t n_tensors, int32_t s
       const qha_adamw_tensor& t = tensors[i];
       if (t.n == 0) continue;
       const int64_t more = (t.n + chunk - 1) / chunk;
-      if (k > 0 && blocks + more > 0x7FFFFFFFLL) break;
+      if (k > 0 && blocks + more > qha::kMaxBlocks) break;
       a.t[k] = {t.n, t.param, t.grad, t.copy, t.m, t.v, t.m_scale, t.v_scale};
       a.first[k++] = static_cast<uint32_t>(blocks);
       blocks += more;
@@ -92,7 +211,7 @@ int qha_adamw_step(const qha_adamw_tensor* tensors, int64_t n_tensors, int32_t s
 
 int qha_adamw_values(const int8_t* m, const float* m_scale, float* m_out, const uint8_t* v, const float* v_scale,
                      float* v_out, int64_t n, void* stream) {
-  if (n < 0 || n > (1LL << 40)) return fail(QHA_ERR_INVALID_ARG, "bad size");
+  if (n < 0 || n > (1LL << 33)) return fail(QHA_ERR_INVALID_ARG, "bad size");
   if (n == 0) return ok();
   const bool has_m = m || m_scale || m_out, has_v = v || v_scale || v_out;
   if ((has_m && !(m && m_scale && m_out)) || (has_v && !(v && v_scale && v_out))) return fail(QHA_ERR_INVALID_ARG, "NULL pointer");

@@ -1,0 +1,54 @@
+// Activations of the training operators and 16-byte accesses to float32 / bf16 / f16 rows.
+#pragma once
+
+#include <hip/hip_runtime.h>
+
+#include <cstdint>
+
+#include "../../include/qha.h"
+
+namespace qha {
+
+// act(z); `act` is uniform over a launch, so the branch costs one scalar test.
+__device__ __forceinline__ float activate(float z, int32_t act) {
+  if (act == QHA_ACT_RELU) return z > 0.0f ? z : 0.0f;
+  if (act == QHA_ACT_SILU) return z / (1.0f + expf(-z));
+  if (act == QHA_ACT_GELU) return 0.5f * z * (1.0f + erff(z * 0.70710678118654752f));
+  return z;
+}
+
+// act(z) and act'(z).
+__device__ __forceinline__ float activate_both(float z, int32_t act, float* slope) {
+  if (act == QHA_ACT_RELU) {
+    *slope = z > 0.0f ? 1.0f : 0.0f;
+    return z > 0.0f ? z : 0.0f;
+  }
+  if (act == QHA_ACT_SILU) {
+    const float s = 1.0f / (1.0f + expf(-z));
+    *slope = s * (1.0f + z * (1.0f - s));
+    return z * s;
+  }
+  if (act == QHA_ACT_GELU) {
+    const float cdf = 0.5f * (1.0f + erff(z * 0.70710678118654752f));
+    *slope = cdf + z * (0.39894228040143268f * expf(-0.5f * z * z));
+    return z * cdf;
+  }
+  *slope = 1.0f;
+  return z;
+}
+
+// 16 bytes of T: N elements, converted to and from float32 (one rounding, to nearest even).
+template <typename T>
+struct Pack {
+  static constexpr int N = 16 / sizeof(T);
+  typedef T vec __attribute__((ext_vector_type(N)));
+  typedef float wide __attribute__((ext_vector_type(N)));
+  static __device__ __forceinline__ wide load(const T* p) {
+    return __builtin_convertvector(*reinterpret_cast<const vec*>(p), wide);
+  }
+  static __device__ __forceinline__ void store(T* p, wide x) {
+    *reinterpret_cast<vec*>(p) = __builtin_convertvector(x, vec);
+  }
+};
+
+}  // namespace qha

@@ -183,6 +183,37 @@ hipError_t launch_quantize(const QuantArgs& a, int32_t d, hipStream_t s);
 hipError_t launch_gather(const GatherArgs& a, int32_t d, bool with_halo, hipStream_t s, bool quantize_out = false);
 hipError_t launch_gemm(const GemmArgs& a, hipStream_t s);
 
+// Blocks of 256 threads in one launch: a grid holds fewer than 2^32 threads.
+constexpr int64_t kMaxBlocks = (1LL << 24) - 1;
+
+// Group normalisation (channels last).  A sample's rows are cut into `chunks` pieces of chunk_rows
+// rows (the last one short); (sample, chunk) pairs are the work items, chunk fastest.
+struct NormArgs {
+  int64_t samples, positions;
+  int32_t c, groups, type, act;
+  const void* x;
+  int64_t ldx;
+  const void* dy;                    // backward
+  int64_t lddy;
+  void* y;                           // forward: y; backward: dx
+  int64_t ldy;
+  const float* w;
+  const float* b;
+  double eps;
+  float* mean;                       // written by the forward, read by the backward
+  float* rstd;
+  float* dw;
+  float* db;
+  int64_t chunks, chunk_rows;
+  int64_t sum_blocks;                // backward: blocks that leave a channel partial
+  double* group_part;                // [items][groups][2]
+  float* chan_part;                  // [sum_blocks][2][c]
+};
+void norm_plan(NormArgs& a, bool backward);
+size_t norm_workspace(const NormArgs& a, bool backward);
+hipError_t launch_norm_fwd(const NormArgs& a, hipStream_t s);
+hipError_t launch_norm_bwd(const NormArgs& a, hipStream_t s);
+
 // AdamW over a batch of tensors, passed to the kernel by value.  Tensor i's chunks are
 // first[i] .. first[i + 1] - 1 of the grid.
 constexpr int kAdamBatch = 48;

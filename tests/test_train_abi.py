@@ -70,3 +70,54 @@ def test_adamw_binding_refuses():
         B.AdamW([np.zeros(4, np.float32)])
     with pytest.raises(ValueError, match="copies"):
         B.AdamW([], copies=[torch.zeros(4)])
+
+
+def _norm_fwd(n=10, p=3, c=64, g=4, t=B.F32, x=FAKE, ldx=64, w=FAKE, b=FAKE, eps=1e-5, act=0, y=FAKE, ldy=64, mean=FAKE,
+              rstd=FAKE, ws=FAKE, wsb=1 << 30):
+    return B._group_norm_fwd(n, p, c, g, t, x, ldx, w, b, eps, act, y, ldy, mean, rstd, ws, wsb, None)
+
+
+def _norm_bwd(n=10, p=3, c=64, g=4, t=B.F32, dy=FAKE, lddy=64, x=FAKE, ldx=64, mean=FAKE, rstd=FAKE, w=FAKE, b=FAKE,
+              act=0, dx=FAKE, lddx=64, dw=FAKE, db=FAKE, ws=FAKE, wsb=1 << 30):
+    return B._group_norm_bwd(n, p, c, g, t, dy, lddy, x, ldx, mean, rstd, w, b, act, dx, lddx, dw, db, ws, wsb, None)
+
+
+SHARED = [dict(n=-1), dict(p=0), dict(n=1 << 20, p=1 << 20), dict(c=0), dict(c=66), dict(c=60, t=B.BF16), dict(g=0), dict(g=5),
+          dict(t=3), dict(act=4), dict(act=-1), dict(w=FAKE + 4), dict(b=FAKE + 8), dict(x=None), dict(x=FAKE + 4),
+          dict(ldx=60), dict(ldx=66), dict(ldx=68, t=B.F16), dict(ws=FAKE + 8)]
+
+
+@pytest.mark.parametrize("bad", SHARED + [dict(y=None), dict(ldy=32), dict(y=FAKE + 2), dict(eps=-1.0),
+                                          dict(eps=float("inf")), dict(mean=None), dict(rstd=None), dict(mean=FAKE + 2)])
+def test_group_norm_fwd_refuses(bad):
+    assert _norm_fwd(**bad) == B.QHA_ERR_INVALID_ARG
+    assert B._last_error()
+
+
+@pytest.mark.parametrize("bad", SHARED + [dict(dy=None), dict(lddy=0), dict(dx=None), dict(lddx=62), dict(mean=None),
+                                          dict(rstd=None), dict(dw=None), dict(db=None), dict(dw=FAKE + 2)])
+def test_group_norm_bwd_refuses(bad):
+    assert _norm_bwd(**bad) == B.QHA_ERR_INVALID_ARG
+    assert B._last_error()
+
+
+def test_group_norm_limits_and_workspace():
+    wide = dict(c=8448, ldx=8448, g=1)
+    assert _norm_fwd(ldy=8448, **wide) == B.QHA_ERR_UNSUPPORTED
+    assert _norm_bwd(lddy=8448, lddx=8448, **wide) == B.QHA_ERR_UNSUPPORTED
+    need = B.group_norm_workspace(30, 3, 64, 4, backward=True)
+    assert need > 0
+    assert _norm_bwd(ws=None) == B.QHA_ERR_WORKSPACE
+    assert _norm_bwd(wsb=15) == B.QHA_ERR_WORKSPACE
+    assert _norm_fwd(ws=None, wsb=0) == B.QHA_ERR_WORKSPACE
+    assert _norm_fwd(n=0, x=None, y=None) == B.QHA_OK
+    assert _norm_bwd(n=0, dw=None, db=None, x=None) == B.QHA_OK
+    assert B.group_norm_workspace(0, 1, 64, 4) == 0
+
+
+def test_group_norm_binding_refuses():
+    x = torch.zeros(6, 16)
+    with pytest.raises(ValueError, match="GPU"):
+        B.group_norm_fwd(x, x, 2)
+    with pytest.raises(ValueError, match="whole samples"):
+        B.group_norm_fwd(x, x, 2, positions=4)
