@@ -19,6 +19,8 @@
  *
  * and the operators that make a training step of those layers:
  *
+ *   qha_gated_project         two projections, an activation of one and their product in one kernel
+ *   qha_gated_backward        its gradients
  *   qha_group_norm_fwd        group normalisation with an activation, channels last
  *   qha_group_norm_bwd        its gradients
  *   qha_adamw_step            one AdamW step over many tensors, moments in float32 or 8-bit codes
@@ -385,6 +387,37 @@ size_t qha_dense_backward_workspace(int64_t m, int64_t n, int64_t k);
 #define QHA_ACT_RELU 1          /* z > 0 ? z : 0 */
 #define QHA_ACT_SILU 2          /* z / (1 + exp(-z)) */
 #define QHA_ACT_GELU 3          /* z (1 + erf(z / sqrt 2)) / 2 */
+
+/* Gated projection of m rows (nodes, tokens): with W_gate, W_up [n x k],
+ *   gate = A W_gate^T,   up = A W_up^T,   H = act(gate) * up
+ * A [m x k], the weights, H and, if given, gate and up [m x n] (kept for the backward; nullable
+ * together) have elements of `type`, row-major with leading dimensions that are at least the row
+ * width and multiples of 16 bytes of elements (4 or 8); n and k are multiples of the same and at most
+ * 65536; all are 16-byte aligned.  Products run on the matrix cores: 16-bit values as they are,
+ * float32 values split exactly into three bf16 parts whose six largest part products are kept (the
+ * dropped ones total below 2^-23 of the product); sums are float32, and H is formed from the float32
+ * gate and up and rounded once.  H, gate and up must not overlap A or the weights.  workspace:
+ * device, 16-byte aligned, qha_gated_workspace bytes (0 for 16-bit types).  m = 0 or n = 0 is a no-op.
+ * Errors: INVALID_ARG, UNSUPPORTED (more than 2^22 tiles of 128 rows and 64 columns: cut the rows),
+ * WORKSPACE, HIP. */
+int qha_gated_project(int64_t m, int64_t n, int64_t k, int32_t type, const void* a, int64_t lda, const void* w_gate,
+                      int64_t ldwg, const void* w_up, int64_t ldwu, int32_t act, void* h, int64_t ldh, void* gate,
+                      int64_t ldg, void* up, int64_t ldu, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Its gradients, from dH and the forward's A, gate and up:
+ *   dgate = dH up act'(gate),  dup = dH act(gate),   dA = dgate W_gate + dup W_up   (elements of type)
+ *   dW_gate = dgate^T A,  dW_up = dup^T A            (float32 [n x k], overwritten; zeros when m = 0)
+ * dgate and dup are the matrix cores' operands: float32 in three parts; in 16-bit types rounded once for
+ * dA, which is rounded itself, and in two parts for the float32 weight gradients.  dA is nullable (a first layer needs none) and must not overlap the other arrays.  Long
+ * reductions are split into float32 partials (workspace) added in float64 in a fixed order; results
+ * are deterministic.  Other arguments and errors as in qha_gated_project. */
+int qha_gated_backward(int64_t m, int64_t n, int64_t k, int32_t type, const void* dh, int64_t lddh, const void* gate,
+                       int64_t ldg, const void* up, int64_t ldu, const void* a, int64_t lda, const void* w_gate,
+                       int64_t ldwg, const void* w_up, int64_t ldwu, int32_t act, void* da, int64_t ldda, float* dw_gate,
+                       int64_t lddwg, float* dw_up, int64_t lddwu, void* workspace, size_t workspace_bytes,
+                       void* stream);
+/* Bytes of workspace for either direction. */
+size_t qha_gated_workspace(int32_t type, int64_t m, int64_t n, int64_t k, int32_t backward);
 
 /* Group normalisation with an activation, channels last.  x holds n_samples * positions rows of c
  * channels (row r belongs to sample r / positions); the channels form n_groups groups of

@@ -135,6 +135,11 @@ _group_norm_fwd = _sig("qha_group_norm_fwd", _i32, _i64, _i64, _i32, _i32, _i32,
 _group_norm_bwd = _sig("qha_group_norm_bwd", _i32, _i64, _i64, _i32, _i32, _i32, _vp, _i64, _vp, _i64, _vp, _vp, _vp,
                        _vp, _i32, _vp, _i64, _vp, _vp, _vp, _sz, _vp)
 _group_norm_ws = _sig("qha_group_norm_workspace", _sz, _i64, _i64, _i32, _i32, _i32)
+_gated_project = _sig("qha_gated_project", _i32, _i64, _i64, _i64, _i32, _vp, _i64, _vp, _i64, _vp, _i64, _i32, _vp,
+                      _i64, _vp, _i64, _vp, _i64, _vp, _sz, _vp)
+_gated_backward = _sig("qha_gated_backward", _i32, _i64, _i64, _i64, _i32, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _i64,
+                       _vp, _i64, _vp, _i64, _i32, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _sz, _vp)
+_gated_ws = _sig("qha_gated_workspace", _sz, _i32, _i64, _i64, _i64, _i32)
 
 EXPORTED = ["qha_abi_version", "qha_status_string", "qha_last_error", "qha_pack_layout", "qha_pack_classes",
             "qha_edge_weights", "qha_validate_csr",
@@ -144,7 +149,7 @@ EXPORTED = ["qha_abi_version", "qha_status_string", "qha_last_error", "qha_pack_
             "qha_aggregate_bwd_quantize", "qha_dense_project", "qha_dense_project_workspace", "qha_dense_backward",
             "qha_dense_backward_workspace", "qha_mask_levels", "qha_node_bits", "qha_level_order",
             "qha_coordinator_init", "qha_coordinator_step", "qha_adamw_step", "qha_adamw_values",
-            "qha_group_norm_fwd", "qha_group_norm_bwd", "qha_group_norm_workspace"]
+            "qha_gated_project", "qha_gated_backward", "qha_gated_workspace", "qha_group_norm_fwd", "qha_group_norm_bwd", "qha_group_norm_workspace"]
 
 
 class QhaError(RuntimeError):
@@ -579,6 +584,50 @@ def _space(workspace):
     if not workspace.is_cuda or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous GPU tensor")
     return workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
+def gated_project_workspace(dtype, m: int, n: int, k: int) -> int:
+    return int(_gated_ws(_type(dtype, "dtype"), m, n, k, 0))
+
+
+def gated_backward_workspace(dtype, m: int, n: int, k: int) -> int:
+    return int(_gated_ws(_type(dtype, "dtype"), m, n, k, 1))
+
+
+def gated_project(a, w_gate, w_up, h, gate=None, up=None, act: int = ACT_SILU, workspace=None, stream=None):
+    """h = act(a w_gate^T) * (a w_up^T); gate and up, if given, receive the two products."""
+    t = a.dtype
+    m, k = a.shape
+    n = w_gate.shape[0]
+    pa, lda = _matrix(a, "a", t, m, k)
+    pg, ldwg = _matrix(w_gate, "w_gate", t, n, k)
+    pu, ldwu = _matrix(w_up, "w_up", t, n, k)
+    ph, ldh = _matrix(h, "h", t, m, n)
+    qg, ldg = (None, 0) if gate is None else _matrix(gate, "gate", t, m, n)
+    qu, ldu = (None, 0) if up is None else _matrix(up, "up", t, m, n)
+    ws, ws_bytes = _space(workspace)
+    _check(_gated_project(m, n, k, _type(t, "a"), pa, lda, pg, ldwg, pu, ldwu, act, ph, ldh, qg, ldg, qu, ldu, ws,
+                          ws_bytes, _stream(stream)), "qha_gated_project")
+
+
+def gated_backward(dh, gate, up, a, w_gate, w_up, da, dw_gate, dw_up, act: int = ACT_SILU, workspace=None, stream=None):
+    """Gradients of gated_project from dh and the kept gate and up: da (or None), and the float32
+    weight gradients dw_gate and dw_up."""
+    t = a.dtype
+    m, k = a.shape
+    n = w_gate.shape[0]
+    pdh, lddh = _matrix(dh, "dh", t, m, n)
+    pg, ldg = _matrix(gate, "gate", t, m, n)
+    pu, ldu = _matrix(up, "up", t, m, n)
+    pa, lda = _matrix(a, "a", t, m, k)
+    pwg, ldwg = _matrix(w_gate, "w_gate", t, n, k)
+    pwu, ldwu = _matrix(w_up, "w_up", t, n, k)
+    pda, ldda = (None, 0) if da is None else _matrix(da, "da", t, m, k)
+    pdg, lddg = _matrix(dw_gate, "dw_gate", torch.float32, n, k)
+    pdu, lddu = _matrix(dw_up, "dw_up", torch.float32, n, k)
+    ws, ws_bytes = _space(workspace)
+    _check(_gated_backward(m, n, k, _type(t, "a"), pdh, lddh, pg, ldg, pu, ldu, pa, lda, pwg, ldwg, pwu, ldwu, act, pda,
+                           ldda, pdg, lddg, pdu, lddu, ws, ws_bytes, _stream(stream)), "qha_gated_backward")
 
 
 def group_norm_workspace(rows: int, positions: int, c: int, n_groups: int, backward=False) -> int:

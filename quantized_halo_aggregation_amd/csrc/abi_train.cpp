@@ -21,6 +21,7 @@ int hip_status(hipError_t e, const char* what) {
 bool aligned(const void* p, uintptr_t bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0; }
 
 constexpr int64_t kMaxRows = 2147483647LL;
+constexpr int64_t kMaxWidth = 1 << 16;       // widths of a gated projection
 
 bool known_type(int32_t t) { return t == QHA_F32 || t == QHA_BF16 || t == QHA_F16; }
 uintptr_t type_bytes(int32_t t) { return t == QHA_F32 ? 4 : 2; }
@@ -74,7 +75,112 @@ int take_norm_workspace(qha::NormArgs& a, bool backward, void* ws, size_t bytes)
 
 }  // namespace
 
+namespace {
+
+int take_gated(qha::GatedArgs& g, int64_t m, int64_t n, int64_t k, int32_t type, int32_t act) {
+  std::memset(&g, 0, sizeof(g));
+  if (m < 0 || n < 0 || k < 0 || m > kMaxRows || n > kMaxWidth || k > kMaxWidth) return fail(QHA_ERR_INVALID_ARG, "bad sizes");
+  if (!known_type(type)) return fail(QHA_ERR_INVALID_ARG, "unknown element type %d", type);
+  if (act < QHA_ACT_NONE || act > QHA_ACT_GELU) return fail(QHA_ERR_INVALID_ARG, "unknown activation %d", act);
+  const int64_t vec = static_cast<int64_t>(16 / type_bytes(type));
+  if (n % vec || k % vec) return fail(QHA_ERR_INVALID_ARG, "n (%lld) and k (%lld) must be multiples of %lld", (long long)n, (long long)k, (long long)vec);
+  // product tiles of 128 x 128 in one launch
+  if ((m / 128 + 1) * (n / 64 + k / 128 + 2) > (1LL << 22)) return fail(QHA_ERR_UNSUPPORTED, "more than 2^22 tiles: cut the rows");
+  g.m = m;
+  g.n = n;
+  g.k = k;
+  g.type = type;
+  g.act = act;
+  return QHA_OK;
+}
+
+int take_gated_workspace(qha::GatedArgs& g, bool backward, void* ws, size_t bytes) {
+  const size_t need = qha::gated_workspace(g.type, g.m, g.n, g.k, backward);
+  if (need == 0) return QHA_OK;
+  if (!ws || bytes < need) return fail(QHA_ERR_WORKSPACE, "workspace of %zu bytes needed, %zu given", need, ws ? bytes : (size_t)0);
+  if (!aligned(ws, 16)) return fail(QHA_ERR_INVALID_ARG, "workspace is not 16-byte aligned");
+  g.ws = ws;
+  return QHA_OK;
+}
+
+}  // namespace
+
 extern "C" {
+
+size_t qha_gated_workspace(int32_t type, int64_t m, int64_t n, int64_t k, int32_t backward) {
+  qha::GatedArgs g;
+  if (take_gated(g, m, n, k, type, QHA_ACT_NONE) || n == 0 || k == 0) return 0;
+  return qha::gated_workspace(type, m, n, k, backward != 0);
+}
+
+int qha_gated_project(int64_t m, int64_t n, int64_t k, int32_t type, const void* a, int64_t lda, const void* w_gate,
+                      int64_t ldwg, const void* w_up, int64_t ldwu, int32_t act, void* h, int64_t ldh, void* gate,
+                      int64_t ldg, void* up, int64_t ldu, void* workspace, size_t workspace_bytes, void* stream) {
+  qha::GatedArgs g;
+  int st = take_gated(g, m, n, k, type, act);
+  if (st) return st;
+  if ((gate == nullptr) != (up == nullptr)) return fail(QHA_ERR_INVALID_ARG, "gate and up come together");
+  if (m == 0 || n == 0) return ok();
+  if (k == 0) return fail(QHA_ERR_INVALID_ARG, "k = 0");
+  if ((st = check_rows("a", a, lda, k, type)) || (st = check_rows("w_gate", w_gate, ldwg, k, type)) ||
+      (st = check_rows("w_up", w_up, ldwu, k, type)) || (st = check_rows("h", h, ldh, n, type)))
+    return st;
+  if (gate && ((st = check_rows("gate", gate, ldg, n, type)) || (st = check_rows("up", up, ldu, n, type)))) return st;
+  if ((st = take_gated_workspace(g, false, workspace, workspace_bytes))) return st;
+  g.a = a;
+  g.lda = lda;
+  g.wg = w_gate;
+  g.ldwg = ldwg;
+  g.wu = w_up;
+  g.ldwu = ldwu;
+  g.h = h;
+  g.ldh = ldh;
+  g.gate_out = gate;
+  g.up_out = up;
+  g.ldg = ldg;
+  g.ldu = ldu;
+  return hip_status(qha::launch_gated_fwd(g, static_cast<hipStream_t>(stream)), "gated_project");
+}
+
+int qha_gated_backward(int64_t m, int64_t n, int64_t k, int32_t type, const void* dh, int64_t lddh, const void* gate,
+                       int64_t ldg, const void* up, int64_t ldu, const void* a, int64_t lda, const void* w_gate,
+                       int64_t ldwg, const void* w_up, int64_t ldwu, int32_t act, void* da, int64_t ldda, float* dw_gate,
+                       int64_t lddwg, float* dw_up, int64_t lddwu, void* workspace, size_t workspace_bytes,
+                       void* stream) {
+  qha::GatedArgs g;
+  int st = take_gated(g, m, n, k, type, act);
+  if (st) return st;
+  if (n == 0 || k == 0) return fail(QHA_ERR_INVALID_ARG, "n and k must be positive");
+  if ((st = check_rows("w_gate", w_gate, ldwg, k, type)) || (st = check_rows("w_up", w_up, ldwu, k, type)) ||
+      (st = check_rows("dw_gate", dw_gate, lddwg, k, QHA_F32)) || (st = check_rows("dw_up", dw_up, lddwu, k, QHA_F32)))
+    return st;
+  if (m > 0) {
+    if ((st = check_rows("dh", dh, lddh, n, type)) || (st = check_rows("gate", gate, ldg, n, type)) ||
+        (st = check_rows("up", up, ldu, n, type)) || (st = check_rows("a", a, lda, k, type)))
+      return st;
+    if (da && (st = check_rows("da", da, ldda, k, type))) return st;
+  }
+  if ((st = take_gated_workspace(g, true, workspace, workspace_bytes))) return st;
+  g.dh = dh;
+  g.lddh = lddh;
+  g.gate = gate;
+  g.ldg = ldg;
+  g.up = up;
+  g.ldu = ldu;
+  g.a = a;
+  g.lda = lda;
+  g.wg = w_gate;
+  g.ldwg = ldwg;
+  g.wu = w_up;
+  g.ldwu = ldwu;
+  g.da = da;
+  g.ldda = ldda;
+  g.dwg = dw_gate;
+  g.lddwg = lddwg;
+  g.dwu = dw_up;
+  g.lddwu = lddwu;
+  return hip_status(qha::launch_gated_bwd(g, static_cast<hipStream_t>(stream)), "gated_backward");
+}
 
 size_t qha_group_norm_workspace(int64_t n_samples, int64_t positions, int32_t c, int32_t n_groups, int32_t backward) {
   if (n_samples <= 0 || positions <= 0 || n_samples > kMaxRows / positions || c <= 0 || c > 8192 || n_groups <= 0 || c % n_groups != 0) return 0;

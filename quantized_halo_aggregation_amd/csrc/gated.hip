@@ -1,0 +1,618 @@
+// Gated projection H = act(A Wg^T) * (A Wu^T) and its gradients on the matrix cores.
+//
+// Mathematics: G = A Wg^T, U = A Wu^T, H = act(G) U.  Backward: dG = dH U act'(G), dU = dH act(G),
+// dA = [dG dU] [Wg; Wu], [dWg; dWu] = [dG dU]^T A.  16-bit types multiply as they are; float32
+// values are split exactly into three bf16 parts (hi, mid, lo) and a product is rebuilt from the six part
+// products of weight >= 2^-16 of it (the dropped ones total below 2^-23 of the product).  All sums
+// are float32 in the matrix cores' accumulators; a reduction that is split leaves float32 partials that
+// are added in float64.
+//
+// One product kernel serves the three: a block owns a tile of C, steps through the reduction BK at a time
+// with two LDS buffers per operand, and its wavefronts own pieces of the tile as 32x32 accumulators.
+// Operands come in two orders.  Stored along the reduction (A and W in the forward, [dG dU] in dA)
+// their tiles lie row by row in LDS and a lane reads its eight values at once; stored across it (W in
+// dA, both operands of dW) the tile keeps the reduction index as its rows and the transposing LDS
+// read hands a lane its values.  Tiles go from memory to LDS directly, 16 bytes a lane, into places
+// permuted so that neither read meets bank conflicts; the last, partial step goes through registers,
+// which write zeros where the reduction ends.  The forward's B tile interleaves 32 rows of Wg with
+// 32 of Wu, so a wavefront holds G and U of the same columns and the activation and product happen in registers.
+// The matrix instruction's operands are swapped (C^T is formed), which leaves a lane four neighbouring
+// columns of a row to store at once.
+#include "act_common.hpp"
+#include "qha_internal.hpp"
+
+namespace qha {
+namespace {
+
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef short s16x8 __attribute__((ext_vector_type(8)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
+typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
+
+constexpr int64_t kXcds = 8;        // accelerator complex dies, each with its own L2
+
+template <typename T>
+__device__ __forceinline__ f32x16 mma(s16x8 a, s16x8 b, f32x16 c);
+template <>
+__device__ __forceinline__ f32x16 mma<__bf16>(s16x8 a, s16x8 b, f32x16 c) {
+  return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+}
+template <>
+__device__ __forceinline__ f32x16 mma<_Float16>(s16x8 a, s16x8 b, f32x16 c) {
+  return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
+}
+
+// An operand of a product: 16-bit values in rows of ld, in `planes` copies `plane` elements apart (the
+// parts of float32 values).  Rows below `half` come from p0 and the others from p1, unless half is
+// at least the row count.
+struct Operand {
+  const uint16_t* p0;
+  const uint16_t* p1;
+  int64_t ld, plane;
+  int64_t rows;        // stored rows
+  int64_t half;
+  int64_t cols;        // stored columns (a multiple of 8)
+};
+
+enum { ORDER_ROWS = 0, ORDER_PAIRS = 1, ORDER_CROSS = 2 };
+// ORDER_ROWS:  stored along the reduction; tile row r is stored row r0 + r
+// ORDER_PAIRS: the same, tile rows alternate between p0 and p1 by 32 (p0 and p1 hold `rows` rows each)
+// ORDER_CROSS: stored across the reduction; tile rows are steps of the reduction, stored columns c0 + c
+
+// Places of 16-byte chunks in a tile's LDS image.  Along the reduction: rows of BK values.  Across it:
+// BK rows of WIDTH values.  The permutation is its own inverse.
+template <int BK>
+__device__ __forceinline__ int permute_along(int row, int chunk) {
+  return BK == 64 ? chunk ^ (row & 7) : chunk ^ ((row >> 1) & 3);
+}
+__device__ __forceinline__ int permute_cross(int k, int chunk) { return chunk ^ (((k & 3) << 1) | ((k & 4) << 1)); }
+
+template <int ORDER>
+__device__ __forceinline__ const uint16_t* chunk_at(const Operand& o, int64_t first, int row, int col, int64_t k0) {
+  if (ORDER == ORDER_CROSS) {
+    // row: step of the reduction; col: column of the tile
+    const int64_t k = k0 + row;
+    int64_t c = first + col;
+    c = c < o.cols ? c : o.cols - 8;           // columns past the end repeat the last ones and are not stored
+    return (k < o.half ? o.p0 + k * o.ld : o.p1 + (k - o.half) * o.ld) + c;
+  }
+  int64_t r;
+  const uint16_t* p = o.p0;
+  if (ORDER == ORDER_PAIRS) {
+    const int b = row >> 5;
+    r = first + (b >> 1) * 32 + (row & 31);
+    if (b & 1) p = o.p1;
+  } else {
+    r = first + row;
+  }
+  r = r < o.rows ? r : o.rows - 1;             // rows past the end repeat the last one and are not stored
+  return p + r * o.ld + k0 + col;
+}
+
+// Waits for this wavefront's loads into LDS; a barrier after it makes them visible to the block.
+__device__ __forceinline__ void loads_done() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+
+// One plane of a tile: ROWS x COLS values (tile rows and columns as stored) to LDS.  `whole`: the BK steps lie
+// inside the reduction; otherwise chunks at or past its end kend become zero.
+template <int ORDER, int ROWS, int COLS, int NT>
+__device__ __forceinline__ void stage(const Operand& o, int64_t plane, int64_t first, int64_t k0, int64_t kend,
+                                      bool whole, uint16_t* lds) {
+  constexpr int PER = COLS / 8;
+  constexpr int N = ROWS * PER / NT;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const int q = i * NT + threadIdx.x;
+    const int row = q / PER;
+    const int c = ORDER == ORDER_CROSS ? permute_cross(row, q % PER) : permute_along<COLS>(row, q % PER);
+    if (whole) {
+      const uint16_t* src = chunk_at<ORDER>(o, first, row, c * 8, k0) + plane;
+      __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)src,
+                                       (__attribute__((address_space(3))) void*)(lds + (i * NT + wave * 64) * 8), 16, 0, 0);
+    } else {
+      const bool in = ORDER == ORDER_CROSS ? k0 + row < kend : k0 + c * 8 < kend;
+      u32x4 v = {0, 0, 0, 0};
+      if (in) v = *reinterpret_cast<const u32x4*>(chunk_at<ORDER>(o, first, row, c * 8, k0) + plane);
+      *reinterpret_cast<u32x4*>(lds + q * 8) = v;
+    }
+  }
+}
+
+// The matrix operand of 32 tile rows (or columns) from `at` on, 16 steps of the reduction from ks on:
+// lane l holds row l % 32, steps 8 (l / 32) .. + 7.
+template <int ORDER, int COLS>
+__device__ __forceinline__ s16x8 fragment(const uint16_t* lds, int at, int ks, int lane) {
+  if (ORDER == ORDER_CROSS) {
+    // the transposing read takes 4 steps x 16 columns per 16 lanes: lane j of them addresses step
+    // j / 4, columns 4 (j % 4), and receives four steps of column j
+    const int j = lane & 15;
+    const int col = at + ((lane >> 4) & 1) * 16 + 4 * (j & 3);
+    const int k = ks + (lane >> 5) * 8 + (j >> 2);
+    const int off = (col & 7);
+    const uint16_t* lo = lds + k * COLS + permute_cross(k, col >> 3) * 8 + off;
+    const uint16_t* hi = lds + (k + 4) * COLS + permute_cross(k + 4, col >> 3) * 8 + off;
+    const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)lo);
+    const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)hi);
+    return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
+  }
+  const int row = at + (lane & 31);
+  const int c = permute_along<COLS>(row, (ks >> 3) + (lane >> 5));
+  return *reinterpret_cast<const s16x8*>(lds + row * COLS + c * 8);
+}
+
+struct ProductArgs {
+  Operand a, b;
+  int64_t m, n;             // C is m x n (forward: n columns of H)
+  int64_t k;                // reduction
+  int64_t k_each;           // steps of the reduction per split (a multiple of BK)
+  int32_t m_tiles, n_tiles, splits;
+  // forward
+  void* h;
+  void* gate;
+  void* up;
+  int64_t ldh, ldg, ldu;
+  int32_t act;
+  // dA: c; dW: c, with rows from `half` on in c1, or the split's partial
+  void* c;
+  float* c1;
+  int64_t ldc, ldc1;
+  int64_t half;
+  int64_t pad_from;         // dW: rows from here to `half` of either half are padding
+  float* partial;           // [splits][m][n] when splits > 1
+};
+
+enum { OUT_GATED = 0, OUT_DA = 1, OUT_DW = 2 };
+
+template <typename O>
+__device__ __forceinline__ void store4(O* p, f32x4 v);
+template <>
+__device__ __forceinline__ void store4<float>(float* p, f32x4 v) { *reinterpret_cast<f32x4*>(p) = v; }
+template <>
+__device__ __forceinline__ void store4<__bf16>(__bf16* p, f32x4 v) {
+  *reinterpret_cast<bf16x4*>(p) = __builtin_convertvector(v, bf16x4);
+}
+template <>
+__device__ __forceinline__ void store4<_Float16>(_Float16* p, f32x4 v) {
+  *reinterpret_cast<f16x4*>(p) = __builtin_convertvector(v, f16x4);
+}
+
+// Tiles dealt to the XCDs in bands: consecutive blocks go to the eight XCDs in turn, so block b takes
+// position b / 8 of band b % 8; within a band, tiles run down groups of eight row tiles before the next
+// column tile, so that both operands' tiles are found in that XCD's L2.
+__device__ __forceinline__ bool tile_of(const ProductArgs& p, int64_t b, int64_t* mt, int64_t* nt, int64_t* sp) {
+  const int64_t tiles = static_cast<int64_t>(p.m_tiles) * p.n_tiles * p.splits;
+  const int64_t band = (tiles + kXcds - 1) / kXcds;
+  const int64_t t = (b % kXcds) * band + b / kXcds;
+  if (b / kXcds >= band || t >= tiles) return false;
+  const int64_t plane = static_cast<int64_t>(p.m_tiles) * p.n_tiles;
+  *sp = t / plane;
+  const int64_t r = t % plane;
+  const int64_t group = 8 * p.n_tiles;
+  const int64_t g = r / group, in = r % group;
+  const int64_t rows = p.m_tiles - 8 * g < 8 ? p.m_tiles - 8 * g : 8;
+  *mt = 8 * g + in % rows;
+  *nt = in / rows;
+  return true;
+}
+
+// T: 16-bit type of the planes; O: type of the stored result; PA, PB: parts of A's and B's values (1 and 1,
+// 2 and 1, or 3 and 3).
+// BM x BN tile of C (forward: BN counts the rows of Wg and Wu together), wavefronts of WM x WN.
+template <typename T, typename O, int PA, int PB, int OA, int OB, int OUT, int BM, int BN, int BK, int WM, int WN>
+__global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) void product_kernel(ProductArgs p) {
+  constexpr int NT = (BM / WM) * (BN / WN) * 64;
+  constexpr int A_ROWS = OA == ORDER_CROSS ? BK : BM, A_COLS = OA == ORDER_CROSS ? BM : BK;
+  constexpr int B_ROWS = OB == ORDER_CROSS ? BK : BN, B_COLS = OB == ORDER_CROSS ? BN : BK;
+  constexpr int A_SIZE = BM * BK, B_SIZE = BN * BK, BUF = PA * A_SIZE + PB * B_SIZE;
+  constexpr int MI = WM / 32, NI = WN / 32;
+  __shared__ __attribute__((aligned(16))) uint16_t lds[2 * BUF];
+
+  int64_t mt, nt, sp;
+  if (!tile_of(p, blockIdx.x, &mt, &nt, &sp)) return;
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wm = wave / (BN / WN), wn = wave % (BN / WN);
+  const int64_t m0 = mt * BM;
+  const int64_t n0 = nt * (OUT == OUT_GATED ? BN / 2 : BN);
+  const int64_t kbeg = sp * p.k_each;
+  const int64_t kend = kbeg + p.k_each < p.k ? kbeg + p.k_each : p.k;
+
+  auto load = [&](int64_t k0, int buf) {
+    uint16_t* base = lds + buf * BUF;
+    const bool whole = k0 + BK <= kend;
+#pragma unroll
+    for (int pl = 0; pl < PA; ++pl)
+      stage<OA, A_ROWS, A_COLS, NT>(p.a, pl * p.a.plane, m0, k0, kend, whole, base + pl * A_SIZE);
+#pragma unroll
+    for (int pl = 0; pl < PB; ++pl)
+      stage<OB, B_ROWS, B_COLS, NT>(p.b, pl * p.b.plane, n0, k0, kend, whole, base + PA * A_SIZE + pl * B_SIZE);
+  };
+
+  f32x16 acc[MI][NI];
+#pragma unroll
+  for (int i = 0; i < MI; ++i)
+#pragma unroll
+    for (int j = 0; j < NI; ++j)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.0f;
+
+  if (kbeg < kend) load(kbeg, 0);
+  loads_done();
+  __syncthreads();
+  int buf = 0;
+  for (int64_t k0 = kbeg; k0 < kend; k0 += BK, buf ^= 1) {
+    if (k0 + BK < kend) load(k0 + BK, buf ^ 1);
+    const uint16_t* at = lds + buf * BUF;
+    const uint16_t* bt = at + PA * A_SIZE;
+#pragma unroll
+    for (int ks = 0; ks < BK; ks += 16) {
+      s16x8 fa[MI][PA], fb[NI][PB];
+#pragma unroll
+      for (int pl = 0; pl < PA; ++pl)
+#pragma unroll
+        for (int i = 0; i < MI; ++i) fa[i][pl] = fragment<OA, A_COLS>(at + pl * A_SIZE, wm * WM + i * 32, ks, lane);
+#pragma unroll
+      for (int pl = 0; pl < PB; ++pl)
+#pragma unroll
+        for (int j = 0; j < NI; ++j) fb[j][pl] = fragment<OB, B_COLS>(bt + pl * B_SIZE, wn * WN + j * 32, ks, lane);
+#pragma unroll
+      for (int i = 0; i < MI; ++i)
+#pragma unroll
+        for (int j = 0; j < NI; ++j) {
+          f32x16 c = acc[i][j];
+          // smallest part products first
+          if constexpr (PB == 3) {
+            c = mma<T>(fb[j][1], fa[i][1], c);
+            c = mma<T>(fb[j][0], fa[i][2], c);
+            c = mma<T>(fb[j][2], fa[i][0], c);
+            c = mma<T>(fb[j][0], fa[i][1], c);
+            c = mma<T>(fb[j][1], fa[i][0], c);
+          } else if constexpr (PA == 2) {
+            c = mma<T>(fb[j][0], fa[i][1], c);
+          }
+          acc[i][j] = mma<T>(fb[j][0], fa[i][0], c);
+        }
+    }
+    loads_done();
+    __syncthreads();
+  }
+
+  // element r of lane l is row l % 32, column 8 (r / 4) + 4 (l / 32) + r % 4 of its 32x32 block
+  const int half4 = (lane >> 5) * 4;
+#pragma unroll
+  for (int i = 0; i < MI; ++i) {
+    const int64_t row = m0 + wm * WM + i * 32 + (lane & 31);
+    if (row >= p.m) continue;
+    if (OUT == OUT_DW && (row < p.half ? row : row - p.half) >= p.pad_from) continue;
+    if constexpr (OUT == OUT_GATED) {
+#pragma unroll
+      for (int j = 0; j < NI; j += 2) {
+        const int64_t c0 = n0 + (wn * WN + j * 32) / 2 + half4;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int64_t col = c0 + 8 * q;
+          if (col >= p.n) continue;
+          f32x4 g, u, h;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            g[e] = acc[i][j][4 * q + e];
+            u[e] = acc[i][j + 1][4 * q + e];
+            h[e] = activate(g[e], p.act) * u[e];
+          }
+          store4<O>(static_cast<O*>(p.h) + row * p.ldh + col, h);
+          if (p.gate) store4<O>(static_cast<O*>(p.gate) + row * p.ldg + col, g);
+          if (p.up) store4<O>(static_cast<O*>(p.up) + row * p.ldu + col, u);
+        }
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < NI; ++j)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int64_t col = n0 + wn * WN + j * 32 + half4 + 8 * q;
+          if (col >= p.n) continue;
+          f32x4 v;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) v[e] = acc[i][j][4 * q + e];
+          if (p.splits > 1) store4<float>(p.partial + (sp * p.m + row) * p.n + col, v);
+          else if (OUT == OUT_DW && row >= p.half) store4<float>(p.c1 + (row - p.half) * p.ldc1 + col, v);
+          else store4<O>(static_cast<O*>(p.c) + row * p.ldc + col, v);
+        }
+    }
+  }
+}
+
+// dWg and dWu (or their rows below and from `half` on) from the splits' partials, added in order in float64.
+__global__ __launch_bounds__(256) void sum_splits_kernel(ProductArgs p, int64_t n4) {
+  const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  if (i >= p.m * n4) return;
+  const int64_t row = i / n4, col = i % n4 * 4;
+  if ((row < p.half ? row : row - p.half) >= p.pad_from) return;
+  double s[4] = {0.0, 0.0, 0.0, 0.0};
+#pragma unroll 4
+  for (int k = 0; k < p.splits; ++k) {
+    const f32x4 v = *reinterpret_cast<const f32x4*>(p.partial + (k * p.m + row) * p.n + col);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) s[e] += static_cast<double>(v[e]);
+  }
+  f32x4 r;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) r[e] = static_cast<float>(s[e]);
+  float* to = row < p.half ? static_cast<float*>(p.c) + row * p.ldc : p.c1 + (row - p.half) * p.ldc1;
+  store4<float>(to + col, r);
+}
+
+// x = hi + mid + lo exactly: each part is rounded to nearest even, the remainders are exact in float32.
+__device__ __forceinline__ void split3(f32x4 x, bf16x4& h, bf16x4& m, bf16x4& l) {
+  h = __builtin_convertvector(x, bf16x4);
+  const f32x4 r = x - __builtin_convertvector(h, f32x4);
+  m = __builtin_convertvector(r, bf16x4);
+  l = __builtin_convertvector(r - __builtin_convertvector(m, f32x4), bf16x4);
+}
+
+// Planes [3][rows_out][cols_out] of the parts of a float32 matrix, zero where it ends.
+__global__ __launch_bounds__(256) void split_kernel(const float* x, int64_t ld, int64_t rows, int64_t cols, __bf16* out,
+                                                    int64_t rows_out, int64_t cols_out, int64_t plane) {
+  const int64_t per = cols_out / 4;
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < rows_out * per;
+       i += static_cast<int64_t>(gridDim.x) * 256) {
+    const int64_t r = i / per, c = i % per * 4;
+    f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
+    if (r < rows && c < cols) v = *reinterpret_cast<const f32x4*>(x + r * ld + c);
+    bf16x4 h, m, l;
+    split3(v, h, m, l);
+    __bf16* o = out + r * cols_out + c;
+    *reinterpret_cast<bf16x4*>(o) = h;
+    *reinterpret_cast<bf16x4*>(o + plane) = m;
+    *reinterpret_cast<bf16x4*>(o + 2 * plane) = l;
+  }
+}
+
+// [dG dU] (each n_out columns wide, zero past n) as the products' operand: the float32 values in three bf16
+// parts, or for 16-bit T in two parts of T.  dA is stored in T and takes the first part alone (one rounding of each
+// term, as its own result has); dW is float32 and takes both, which leaves 2^-18 (bf16) of a term.
+template <typename T>
+__global__ __launch_bounds__(256) void gate_grad_kernel(GatedArgs p, uint16_t* out, int64_t n_out, int64_t plane) {
+  const int64_t per = n_out / 4;
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < p.m * per;
+       i += static_cast<int64_t>(gridDim.x) * 256) {
+    const int64_t r = i / per, c = i % per * 4;
+    f32x4 dg = {0.0f, 0.0f, 0.0f, 0.0f}, du = dg;
+    if (c < p.n) {
+      typedef T vec __attribute__((ext_vector_type(4)));
+      const f32x4 dh = __builtin_convertvector(*reinterpret_cast<const vec*>(static_cast<const T*>(p.dh) + r * p.lddh + c), f32x4);
+      const f32x4 g = __builtin_convertvector(*reinterpret_cast<const vec*>(static_cast<const T*>(p.gate) + r * p.ldg + c), f32x4);
+      const f32x4 u = __builtin_convertvector(*reinterpret_cast<const vec*>(static_cast<const T*>(p.up) + r * p.ldu + c), f32x4);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        float slope;
+        const float f = activate_both(g[e], p.act, &slope);
+        dg[e] = dh[e] * u[e] * slope;
+        du[e] = dh[e] * f;
+      }
+    }
+    uint16_t* o = out + r * 2 * n_out + c;
+    if constexpr (sizeof(T) == 4) {
+      bf16x4 h, m, l;
+      split3(dg, h, m, l);
+      *reinterpret_cast<bf16x4*>(o) = h;
+      *reinterpret_cast<bf16x4*>(o + plane) = m;
+      *reinterpret_cast<bf16x4*>(o + 2 * plane) = l;
+      split3(du, h, m, l);
+      *reinterpret_cast<bf16x4*>(o + n_out) = h;
+      *reinterpret_cast<bf16x4*>(o + n_out + plane) = m;
+      *reinterpret_cast<bf16x4*>(o + n_out + 2 * plane) = l;
+    } else {
+      typedef T vec __attribute__((ext_vector_type(4)));
+      const vec g1 = __builtin_convertvector(dg, vec), u1 = __builtin_convertvector(du, vec);
+      *reinterpret_cast<vec*>(o) = g1;
+      *reinterpret_cast<vec*>(o + n_out) = u1;
+      store4<T>(reinterpret_cast<T*>(o + plane), dg - __builtin_convertvector(g1, f32x4));
+      store4<T>(reinterpret_cast<T*>(o + n_out + plane), du - __builtin_convertvector(u1, f32x4));
+    }
+  }
+}
+
+uint32_t stride_blocks(int64_t items) {
+  const int64_t b = (items + 255) / 256;
+  return static_cast<uint32_t>(b < 16384 ? (b > 0 ? b : 1) : 16384);
+}
+
+int64_t up8(int64_t x) { return (x + 7) / 8 * 8; }
+
+template <typename T, typename O, int PA, int PB, int OA, int OB, int OUT, int BM, int BN, int BK, int WM, int WN>
+hipError_t run_product(ProductArgs p, hipStream_t s) {
+  p.m_tiles = static_cast<int32_t>((p.m + BM - 1) / BM);
+  const int64_t wide = OUT == OUT_GATED ? BN / 2 : BN;
+  p.n_tiles = static_cast<int32_t>((p.n + wide - 1) / wide);
+  const int64_t tiles = static_cast<int64_t>(p.m_tiles) * p.n_tiles * p.splits;
+  const int64_t blocks = (tiles + kXcds - 1) / kXcds * kXcds;
+  product_kernel<T, O, PA, PB, OA, OB, OUT, BM, BN, BK, WM, WN>
+      <<<static_cast<uint32_t>(blocks), (BM / WM) * (BN / WN) * 64, 0, s>>>(p);
+  return hipGetLastError();
+}
+
+template <typename T, typename O, int PA, int PB, int OA, int OB, int OUT>
+hipError_t product(const ProductArgs& p, hipStream_t s) {
+  constexpr int BK = PA + PB > 3 ? 32 : 64;
+  return run_product<T, O, PA, PB, OA, OB, OUT, 128, 128, BK, 64, 64>(p, s);
+}
+
+Operand plain(const void* p, int64_t ld, int64_t rows, int64_t cols, int64_t plane = 0) {
+  return {static_cast<const uint16_t*>(p), nullptr, ld, plane, rows, INT64_MAX, cols};
+}
+
+constexpr int64_t kSplitStep = 64;       // a split's steps are a multiple of it
+constexpr int64_t kDwTiles = 512;        // blocks that fill the compute units twice
+
+// Splits of dW's reduction over the rows: enough tiles for every compute unit, each of at least 256 rows.
+int32_t dw_splits(int64_t m, int64_t n, int64_t k) {
+  const int64_t tiles = ((2 * n + 127) / 128) * ((k + 127) / 128);
+  int64_t s = (kDwTiles + tiles - 1) / tiles;
+  const int64_t most = (m + 255) / 256;
+  s = s < most ? s : most;
+  return static_cast<int32_t>(s < 1 ? 1 : s);
+}
+
+struct Space {
+  int64_t a, w, grad, partial;     // bytes
+};
+
+int64_t up16(int64_t x) { return (x + 15) / 16 * 16; }
+
+Space gated_space(int32_t type, int64_t m, int64_t n, int64_t k, bool backward) {
+  Space s = {0, 0, 0, 0};
+  const int64_t planes = type == QHA_F32 ? 3 : 1;
+  if (type == QHA_F32) {
+    s.a = up16(planes * m * up8(k) * 2);
+    s.w = up16(planes * 2 * up8(n) * up8(k) * 2);
+  }
+  if (backward) {
+    s.grad = up16((type == QHA_F32 ? 3 : 2) * m * 2 * up8(n) * 2);
+    const int64_t splits = dw_splits(m, n, k);
+    s.partial = splits > 1 ? up16(splits * 2 * up8(n) * k * 4) : 0;
+  }
+  return s;
+}
+
+template <typename T>
+hipError_t fwd16(const GatedArgs& g, hipStream_t s) {
+  ProductArgs p = {};
+  p.a = plain(g.a, g.lda, g.m, g.k);
+  p.b = plain(g.wg, g.ldwg, g.n, g.k);
+  p.b.p1 = static_cast<const uint16_t*>(g.wu);
+  p.m = g.m;
+  p.n = g.n;
+  p.k = p.k_each = g.k;
+  p.splits = 1;
+  p.h = g.h;
+  p.gate = g.gate_out;
+  p.up = g.up_out;
+  p.ldh = g.ldh;
+  p.ldg = g.ldg;
+  p.ldu = g.ldu;
+  p.act = g.act;
+  return product<T, T, 1, 1, ORDER_ROWS, ORDER_PAIRS, OUT_GATED>(p, s);
+}
+
+void split(const float* x, int64_t ld, int64_t rows, int64_t cols, uint16_t* out, int64_t rows_out, int64_t plane,
+           hipStream_t s) {
+  split_kernel<<<stride_blocks(rows_out * up8(cols) / 4), 256, 0, s>>>(x, ld, rows, cols, reinterpret_cast<__bf16*>(out),
+                                                                       rows_out, up8(cols), plane);
+}
+
+hipError_t fwd32(const GatedArgs& g, hipStream_t s) {
+  const Space sp = gated_space(QHA_F32, g.m, g.n, g.k, false);
+  uint16_t* a3 = static_cast<uint16_t*>(g.ws);
+  uint16_t* w3 = reinterpret_cast<uint16_t*>(static_cast<char*>(g.ws) + sp.a);
+  const int64_t k8 = up8(g.k), n8 = up8(g.n);
+  split(static_cast<const float*>(g.a), g.lda, g.m, g.k, a3, g.m, g.m * k8, s);
+  split(static_cast<const float*>(g.wg), g.ldwg, g.n, g.k, w3, n8, 2 * n8 * k8, s);
+  split(static_cast<const float*>(g.wu), g.ldwu, g.n, g.k, w3 + n8 * k8, n8, 2 * n8 * k8, s);
+  ProductArgs p = {};
+  p.a = plain(a3, k8, g.m, k8, g.m * k8);
+  p.b = plain(w3, k8, n8, k8, 2 * n8 * k8);
+  p.b.p1 = w3 + n8 * k8;
+  p.m = g.m;
+  p.n = g.n;
+  p.k = p.k_each = k8;
+  p.splits = 1;
+  p.h = g.h;
+  p.gate = g.gate_out;
+  p.up = g.up_out;
+  p.ldh = g.ldh;
+  p.ldg = g.ldg;
+  p.ldu = g.ldu;
+  p.act = g.act;
+  return product<__bf16, float, 3, 3, ORDER_ROWS, ORDER_PAIRS, OUT_GATED>(p, s);
+}
+
+template <typename T, typename O, int PL>
+hipError_t bwd(const GatedArgs& g, hipStream_t s) {
+  const Space sp = gated_space(g.type, g.m, g.n, g.k, true);
+  char* ws = static_cast<char*>(g.ws);
+  uint16_t* a3 = reinterpret_cast<uint16_t*>(ws);
+  uint16_t* w3 = reinterpret_cast<uint16_t*>(ws + sp.a);
+  uint16_t* grad = reinterpret_cast<uint16_t*>(ws + sp.a + sp.w);
+  float* partial = reinterpret_cast<float*>(ws + sp.a + sp.w + sp.grad);
+  const int64_t k8 = up8(g.k), n8 = up8(g.n);
+  if (g.m > 0) gate_grad_kernel<O><<<stride_blocks(g.m * n8 / 4), 256, 0, s>>>(g, grad, n8, g.m * 2 * n8);
+  Operand a, w;
+  if (PL == 3) {
+    if (g.m > 0) split(static_cast<const float*>(g.a), g.lda, g.m, g.k, a3, g.m, g.m * k8, s);
+    split(static_cast<const float*>(g.wg), g.ldwg, g.n, g.k, w3, n8, 2 * n8 * k8, s);
+    split(static_cast<const float*>(g.wu), g.ldwu, g.n, g.k, w3 + n8 * k8, n8, 2 * n8 * k8, s);
+    a = plain(a3, k8, g.m, k8, g.m * k8);
+    w = plain(w3, k8, 2 * n8, k8, 2 * n8 * k8);
+    w.p1 = w3 + n8 * k8;
+  } else {
+    a = plain(g.a, g.lda, g.m, g.k);
+    w = plain(g.wg, g.ldwg, 2 * g.n, g.k);
+    w.p1 = static_cast<const uint16_t*>(g.wu);
+  }
+  w.half = n8;
+  const Operand d = plain(grad, 2 * n8, g.m, 2 * n8, g.m * 2 * n8);
+  hipError_t e = hipSuccess;
+  if (g.m > 0 && g.da) {
+    ProductArgs p = {};
+    p.a = d;
+    p.b = w;
+    p.m = g.m;
+    p.n = g.k;
+    p.k = p.k_each = 2 * n8;
+    p.splits = 1;
+    p.half = INT64_MAX;
+    p.c = g.da;
+    p.ldc = g.ldda;
+    e = product<T, O, PL, PL, ORDER_ROWS, ORDER_CROSS, OUT_DA>(p, s);
+    if (e != hipSuccess) return e;
+  }
+  ProductArgs p = {};
+  p.a = d;
+  p.b = a;
+  p.m = 2 * n8;
+  p.n = g.k;
+  p.k = g.m;
+  p.splits = dw_splits(g.m, g.n, g.k);
+  p.k_each = ((g.m + p.splits - 1) / p.splits + kSplitStep - 1) / kSplitStep * kSplitStep;
+  p.half = n8;
+  p.c = g.dwg;
+  p.ldc = g.lddwg;
+  p.c1 = g.dwu;
+  p.ldc1 = g.lddwu;
+  p.partial = partial;
+  // rows n .. n8 - 1 of either half are padding of a width that is no multiple of 8
+  p.pad_from = g.n;
+  e = product<T, float, PL == 3 ? 3 : 2, PL, ORDER_CROSS, ORDER_CROSS, OUT_DW>(p, s);
+  if (e != hipSuccess) return e;
+  if (p.splits > 1) {
+    const int64_t n4 = g.k / 4;
+    sum_splits_kernel<<<static_cast<uint32_t>((p.m * n4 + 255) / 256), 256, 0, s>>>(p, n4);
+    e = hipGetLastError();
+  }
+  return e;
+}
+
+}  // namespace
+
+size_t gated_workspace(int32_t type, int64_t m, int64_t n, int64_t k, bool backward) {
+  const Space s = gated_space(type, m, n, k, backward);
+  return static_cast<size_t>(s.a + s.w + s.grad + s.partial);
+}
+
+hipError_t launch_gated_fwd(const GatedArgs& g, hipStream_t s) {
+  if (g.type == QHA_F32) return fwd32(g, s);
+  return g.type == QHA_BF16 ? fwd16<__bf16>(g, s) : fwd16<_Float16>(g, s);
+}
+
+hipError_t launch_gated_bwd(const GatedArgs& g, hipStream_t s) {
+  if (g.type == QHA_F32) return bwd<__bf16, float, 3>(g, s);
+  return g.type == QHA_BF16 ? bwd<__bf16, __bf16, 1>(g, s) : bwd<_Float16, _Float16, 1>(g, s);
+}
+
+}  // namespace qha

@@ -183,6 +183,39 @@ hipError_t launch_quantize(const QuantArgs& a, int32_t d, hipStream_t s);
 hipError_t launch_gather(const GatherArgs& a, int32_t d, bool with_halo, hipStream_t s, bool quantize_out = false);
 hipError_t launch_gemm(const GemmArgs& a, hipStream_t s);
 
+// Gated projection; the forward writes h and, if given, gate_out and up_out (strides ldg, ldu); the
+// backward reads dh, gate and up.
+struct GatedArgs {
+  int64_t m, n, k;
+  int32_t type, act;
+  const void* a;
+  int64_t lda;
+  const void* wg;
+  int64_t ldwg;
+  const void* wu;
+  int64_t ldwu;
+  void* h;
+  int64_t ldh;
+  void* gate_out;
+  void* up_out;
+  const void* dh;
+  int64_t lddh;
+  const void* gate;
+  int64_t ldg;
+  const void* up;
+  int64_t ldu;
+  void* da;
+  int64_t ldda;
+  float* dwg;
+  int64_t lddwg;
+  float* dwu;
+  int64_t lddwu;
+  void* ws;
+};
+size_t gated_workspace(int32_t type, int64_t m, int64_t n, int64_t k, bool backward);
+hipError_t launch_gated_fwd(const GatedArgs& g, hipStream_t s);
+hipError_t launch_gated_bwd(const GatedArgs& g, hipStream_t s);
+
 // Blocks of 256 threads in one launch: a grid holds fewer than 2^32 threads.
 constexpr int64_t kMaxBlocks = (1LL << 24) - 1;
 

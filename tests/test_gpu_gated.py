@@ -1,0 +1,227 @@
+"""qha_gated_project and qha_gated_backward against the float64 oracle.
+
+Tolerances count roundings, u = 2^-24 the unit roundoff of float32.  A dot product of length L sums
+exact products (16-bit types) or part products that total the product to 2^-23 (float32) in float32
+accumulators, whose additions may truncate: at most 2 (L + 8) u of the sum of its terms' sizes S.
+H = act(G) U is off by 1.13 |U| eG + |act(G)| eU (slopes are below 1.13) and 16 u of (|G| + 1) |U|; stored
+values are rounded once more, by at most half a step (eps / 2).  dG = dH U act'(G) and dU = dH act(G) come
+from the stored G and U: 16 u of |dH U| (1 + |G|) and of |dH| (1 + |G|); as 16-bit operands they are
+rounded by half a step.  Those errors go through dA and dW with the sizes of the other factor.
+"""
+import numpy as np
+import pytest
+
+import gpu_helpers as H
+from oracle import train as T
+
+pytestmark = pytest.mark.gpu
+U = 2.0 ** -24
+HALF = {"float32": 2.0 ** -24, "bfloat16": 2.0 ** -8, "float16": 2.0 ** -11}
+TINY = {"float32": 1e-44, "bfloat16": 1e-40, "float16": 2.0 ** -25}      # half a step of subnormals
+KINDS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3}
+SHAPES = [(1, 8, 8), (1, 512, 256), (2, 64, 1024), (7, 40, 24), (16, 128, 136), (17, 8, 512), (33, 200, 64), (64, 72, 200),
+          (100, 256, 128), (129, 136, 128), (300, 64, 264), (513, 328, 72), (1001, 128, 128), (2500, 16, 16),
+          (1030, 512, 320)]
+
+
+def _np(t):
+    return t.float().cpu().numpy().astype(np.float64)
+
+
+def _data(m, n, k, dtype, seed):
+    import torch
+    rng = np.random.default_rng(seed)
+    mk = lambda *s, f=1.0: torch.from_numpy((rng.standard_normal(s) * f).astype(np.float32)).to(getattr(torch, dtype))
+    return mk(m, k), mk(n, k, f=1 / np.sqrt(k)), mk(n, k, f=1 / np.sqrt(k)), mk(m, n)
+
+
+def _space(need):
+    import torch
+    return torch.empty(max(need, 16), dtype=torch.uint8, device="cuda")
+
+
+def _forward(a, wg, wu, kind, kept=True):
+    import torch
+    from quantized_halo_aggregation_amd import binding as B
+    m, n, k = a.shape[0], wg.shape[0], a.shape[1]
+    out = [torch.full((m, n), float("nan"), dtype=a.dtype, device="cuda") for _ in range(3)]
+    B.gated_project(a, wg, wu, out[0], gate=out[1] if kept else None, up=out[2] if kept else None, act=KINDS[kind],
+                    workspace=_space(B.gated_project_workspace(a.dtype, m, n, k)))
+    return out
+
+
+def _check_forward(m, n, k, dtype, kind):
+    a, wg, wu, _ = _data(m, n, k, dtype, m + n + k)
+    h, gate, up = _forward(a.cuda(), wg.cuda(), wu.cuda(), kind)
+    rh, rg, ru = T.gated(_np(a), _np(wg), _np(wu), kind)
+    eg, eu = (2 * (k + 8) * U * (np.abs(_np(a)) @ np.abs(_np(w)).T) for w in (wg, wu))
+    fin = lambda e, ref: e + HALF[dtype] * (np.abs(ref) + e) + TINY[dtype]
+    eh = 1.13 * (np.abs(ru) + eu) * eg + np.abs(T.act(rg, kind)) * eu + 16 * U * (np.abs(rg) + 1) * np.abs(ru)
+    for name, got, ref, e in (("gate", gate, rg, eg), ("up", up, ru, eu), ("h", h, rh, eh)):
+        err, bound = np.abs(_np(got) - ref), fin(e, ref)
+        assert (err <= bound).all(), (name, float((err / bound).max()))
+    alone, _, _ = _forward(a.cuda(), wg.cuda(), wu.cuda(), kind, kept=False)
+    assert (alone == h).all()
+
+
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16", "float16"])
+@pytest.mark.parametrize("shape", SHAPES, ids=lambda s: "x".join(map(str, s)))
+def test_forward(shape, dtype):
+    H.require_gpu()
+    kind = list(KINDS)[sum(shape) // 8 % 4]
+    H.note(f"gated fwd {shape} {dtype} {kind}")
+    _check_forward(*shape, dtype, kind)
+
+
+@pytest.mark.parametrize("shape", [(5, 12, 20), (200, 68, 36), (131, 4, 4)], ids=lambda s: "x".join(map(str, s)))
+def test_float32_widths_that_are_multiples_of_four(shape):
+    H.require_gpu()
+    H.note(f"gated fwd and bwd {shape} float32")
+    _check_forward(*shape, "float32", "silu")
+    _check_backward(*shape, "float32", "silu")
+
+
+def _check_backward(m, n, k, dtype, kind):
+    import torch
+    from quantized_halo_aggregation_amd import binding as B
+    a, wg, wu, dh = _data(m, n, k, dtype, m + 3 * n + k)
+    gate = (_np(a) @ _np(wg).T)
+    up = (_np(a) @ _np(wu).T)
+    t = getattr(torch, dtype)
+    gate, up = (torch.from_numpy(x.astype(np.float32)).to(t) for x in (gate, up))
+    da = torch.full((m, k), float("nan"), dtype=t, device="cuda")
+    dwg, dwu = (torch.full((n, k), float("nan"), device="cuda") for _ in range(2))
+    args = [x.cuda() for x in (dh, gate, up, a, wg, wu)]
+    ws = _space(B.gated_backward_workspace(t, m, n, k))
+    B.gated_backward(*args, da, dwg, dwu, act=KINDS[kind], workspace=ws)
+    fdh, fg, fu, fa, fwg, fwu = (_np(x) for x in (dh, gate, up, a, wg, wu))
+    rda, rdwg, rdwu = T.gated_backward(fdh, fg, fu, fa, fwg, fwu, kind)
+    dg, du = np.abs(fdh * fu * T.act_slope(fg, kind)), np.abs(fdh * T.act(fg, kind))
+    half = 0.0 if dtype == "float32" else HALF[dtype]
+    tiny = 0.0 if dtype == "float32" else TINY[dtype]
+    edg = 16 * U * np.abs(fdh * fu) * (1 + np.abs(fg)) + half * dg + tiny
+    edu = 16 * U * np.abs(fdh) * (1 + np.abs(fg)) + half * du + tiny
+    dg, du = dg + edg, du + edu
+    awg, awu, aa = np.abs(fwg), np.abs(fwu), np.abs(fa)
+    eda = edg @ awg + edu @ awu + 2 * (2 * n + 8) * U * (dg @ awg + du @ awu)
+    eda = eda + HALF[dtype] * (np.abs(rda) + eda) + TINY[dtype]
+    for name, got, ref, e in (("da", da, rda, eda), ("dwg", dwg, rdwg, edg.T @ aa + 2 * (m + 8) * U * (dg.T @ aa)),
+                              ("dwu", dwu, rdwu, edu.T @ aa + 2 * (m + 8) * U * (du.T @ aa))):
+        err = np.abs(_np(got) - ref)
+        assert (err <= e + 1e-44).all(), (name, float((err / (e + 1e-44)).max()))
+    again = [torch.empty_like(x) for x in (dwg, dwu)]
+    B.gated_backward(*args, None, *again, act=KINDS[kind], workspace=ws)       # a first layer needs no dA
+    assert torch.equal(again[0], dwg) and torch.equal(again[1], dwu), "results must be deterministic"
+
+
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16", "float16"])
+@pytest.mark.parametrize("shape", SHAPES, ids=lambda s: "x".join(map(str, s)))
+def test_backward(shape, dtype):
+    H.require_gpu()
+    kind = list(KINDS)[(sum(shape) // 8 + 1) % 4]
+    H.note(f"gated bwd {shape} {dtype} {kind}")
+    _check_backward(*shape, dtype, kind)
+
+
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
+def test_many_rows(dtype):
+    H.require_gpu()
+    H.note(f"gated 20011 rows {dtype}")
+    _check_forward(20011, 128, 128, dtype, "silu")
+    _check_backward(20011, 128, 64, dtype, "relu")
+
+
+@pytest.mark.parametrize("dtype", ["float32", "float16"])
+def test_strided_operands(dtype):
+    """Every array a column slice of a wider buffer: the same bits, and nothing written beside them."""
+    H.require_gpu()
+    import torch
+    from quantized_halo_aggregation_amd import binding as B
+    t = getattr(torch, dtype)
+    for m, n, k in ((3, 64, 72), (300, 136, 72)):
+        H.note(f"gated strided {m} {dtype}")
+        a, wg, wu, dh = (x.cuda() for x in _data(m, n, k, dtype, 4))
+        h, gate, up = _forward(a, wg, wu, "gelu")
+        da = torch.empty_like(a)
+        dws = [torch.empty(n, k, device="cuda") for _ in range(2)]
+        ws = _space(B.gated_backward_workspace(t, m, n, k))
+        B.gated_backward(dh, gate, up, a, wg, wu, da, *dws, act=3, workspace=ws)
+        wide = []
+
+        def slot(x, fill=True):
+            buf = torch.full((x.shape[0], x.shape[1] + 32), 5.0, dtype=x.dtype, device="cuda")
+            view = buf[:, 16:16 + x.shape[1]]
+            if fill:
+                view.copy_(x)
+            wide.append((buf, x.shape[1]))
+            return view
+        sa, sg, su, sdh = (slot(x) for x in (a, wg, wu, dh))
+        oh, og, ou = (slot(h, False) for _ in range(3))
+        B.gated_project(sa, sg, su, oh, gate=og, up=ou, act=3, workspace=_space(B.gated_project_workspace(t, m, n, k)))
+        assert torch.equal(oh, h) and torch.equal(og, gate) and torch.equal(ou, up)
+        oda, odg, odu = slot(da, False), slot(dws[0], False), slot(dws[1], False)
+        B.gated_backward(sdh, og, ou, sa, sg, su, oda, odg, odu, act=3, workspace=ws)
+        assert torch.equal(oda, da) and torch.equal(odg, dws[0]) and torch.equal(odu, dws[1])
+        for buf, w in wide:
+            assert (buf[:, :16] == 5).all() and (buf[:, 16 + w:] == 5).all()
+
+
+def test_values_that_are_not_finite_stay_in_their_rows():
+    H.require_gpu()
+    import torch
+    for m in (5, 200):
+        for dtype in ("float32", "bfloat16"):
+            H.note(f"gated not finite {m} {dtype}")
+            a, wg, wu, _ = _data(m, 64, 40, dtype, 8)
+            a[m - 1, 3], a[1, 0] = float("nan"), float("inf")
+            h, _, _ = _forward(a.cuda(), wg.cuda(), wu.cuda(), "silu")
+            bad = ~np.isfinite(_np(h)).all(1)
+            assert bad[m - 1] and set(np.flatnonzero(bad)) <= {1, m - 1}
+
+
+def test_no_rows():
+    H.require_gpu()
+    import torch
+    from quantized_halo_aggregation_amd import binding as B
+    H.note("gated without rows")
+    for t in (torch.float32, torch.bfloat16):
+        a, h = torch.empty(0, 16, dtype=t, device="cuda"), torch.empty(0, 24, dtype=t, device="cuda")
+        w = torch.ones(24, 16, dtype=t, device="cuda")
+        dws = [torch.ones(24, 16, device="cuda") for _ in range(2)]
+        B.gated_project(a, w, w, h)
+        B.gated_backward(h, h, h, a, w, w, a, *dws, workspace=_space(B.gated_backward_workspace(t, 0, 24, 16)))
+        assert all((d == 0).all() for d in dws)
+
+
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
+def test_graph_replays_equal_the_eager_call(dtype):
+    H.require_gpu()
+    import torch
+    from quantized_halo_aggregation_amd import binding as B
+    t = getattr(torch, dtype)
+    for m, n, k in ((4, 64, 128), (700, 136, 64)):
+        H.note(f"gated graph {m} {dtype}")
+        a, wg, wu, dh = (x.cuda() for x in _data(m, n, k, dtype, 2))
+        out = [torch.zeros(m, n, dtype=t, device="cuda") for _ in range(3)] + [torch.zeros_like(a)] + \
+              [torch.zeros(n, k, device="cuda") for _ in range(2)]
+        ws = _space(max(B.gated_backward_workspace(t, m, n, k), B.gated_project_workspace(t, m, n, k)))
+
+        def step():
+            B.gated_project(a, wg, wu, out[0], gate=out[1], up=out[2], workspace=ws)
+            B.gated_backward(dh, out[1], out[2], a, wg, wu, *out[3:], workspace=ws)
+        step()
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            step()
+        for i in range(4):
+            a.mul_(1.25)
+            wg.add_(0.0625 * i)
+            step()
+            want = [x.clone() for x in out]
+            for x in out:
+                x.zero_()
+            graph.replay()
+            torch.cuda.synchronize()
+            for x, y in zip(want, out):
+                assert torch.equal(x, y), i

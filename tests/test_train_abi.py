@@ -121,3 +121,52 @@ def test_group_norm_binding_refuses():
         B.group_norm_fwd(x, x, 2)
     with pytest.raises(ValueError, match="whole samples"):
         B.group_norm_fwd(x, x, 2, positions=4)
+
+
+def _gated_fwd(m=10, n=64, k=32, t=B.F32, a=FAKE, lda=32, wg=FAKE, ldwg=32, wu=FAKE, ldwu=32, act=2, h=FAKE, ldh=64,
+               gate=FAKE, ldg=64, up=FAKE, ldu=64, ws=FAKE, wsb=1 << 30):
+    return B._gated_project(m, n, k, t, a, lda, wg, ldwg, wu, ldwu, act, h, ldh, gate, ldg, up, ldu, ws, wsb, None)
+
+
+def _gated_bwd(m=10, n=64, k=32, t=B.F32, dh=FAKE, lddh=64, gate=FAKE, ldg=64, up=FAKE, ldu=64, a=FAKE, lda=32, wg=FAKE,
+               ldwg=32, wu=FAKE, ldwu=32, act=2, da=FAKE, ldda=32, dwg=FAKE, lddwg=32, dwu=FAKE, lddwu=32, ws=FAKE,
+               wsb=1 << 30):
+    return B._gated_backward(m, n, k, t, dh, lddh, gate, ldg, up, ldu, a, lda, wg, ldwg, wu, ldwu, act, da, ldda, dwg,
+                             lddwg, dwu, lddwu, ws, wsb, None)
+
+
+GATED = [dict(m=-1), dict(n=-8), dict(k=-8), dict(n=62), dict(k=30), dict(k=36, t=B.BF16, lda=40, ldwg=40, ldwu=40),
+         dict(n=1 << 17), dict(t=5), dict(act=7), dict(a=None), dict(a=FAKE + 4), dict(lda=28), dict(lda=34), dict(wg=None),
+         dict(ldwg=16), dict(wu=FAKE + 8), dict(ldwu=33), dict(ldg=60), dict(up=FAKE + 2), dict(ldu=0), dict(gate=None),
+         dict(up=None), dict(ws=FAKE + 8)]
+
+
+@pytest.mark.parametrize("bad", GATED + [dict(h=None), dict(ldh=63), dict(h=FAKE + 8), dict(k=0)])
+def test_gated_project_refuses(bad):
+    assert _gated_fwd(**bad) == B.QHA_ERR_INVALID_ARG
+    assert B._last_error()
+
+
+@pytest.mark.parametrize("bad", GATED + [dict(dh=None), dict(lddh=32), dict(da=FAKE + 4), dict(ldda=31), dict(dwg=None),
+                                         dict(lddwg=30), dict(dwu=None), dict(dwu=FAKE + 4), dict(lddwu=28), dict(n=0),
+                                         dict(k=0)])
+def test_gated_backward_refuses(bad):
+    assert _gated_bwd(**bad) == B.QHA_ERR_INVALID_ARG
+    assert B._last_error()
+
+
+def test_gated_limits_and_workspace():
+    assert B.gated_project_workspace(torch.bfloat16, 1000, 64, 32) == 0
+    assert B.gated_project_workspace(torch.float32, 1000, 64, 32) > 0
+    assert _gated_fwd(ws=None, wsb=0) == B.QHA_ERR_WORKSPACE
+    assert _gated_bwd(wsb=100) == B.QHA_ERR_WORKSPACE
+    assert _gated_fwd(m=0, a=None, h=None, ws=None, wsb=0) == B.QHA_OK
+    assert _gated_fwd(m=1 << 30, n=1 << 12, ldh=1 << 12, ldg=1 << 12, ldu=1 << 12) == B.QHA_ERR_UNSUPPORTED
+    with pytest.raises(TypeError, match="float32, bfloat16 or float16"):
+        B.gated_project_workspace(torch.float64, 1, 8, 8)
+
+
+def test_gated_binding_refuses():
+    a, w, h = torch.zeros(4, 16), torch.zeros(8, 16), torch.zeros(4, 8)
+    with pytest.raises(ValueError, match="GPU"):
+        B.gated_project(a, w, w, h)
