@@ -16,7 +16,8 @@ CSRC = os.path.join(PKG, "csrc")
 OUT = os.path.join(PKG, "libqha.so")
 BUILD_DIR = os.path.join(PKG, "_build")
 SOURCES = ["abi.cpp", "control.cpp", "quantize.hip", "gather.hip", "gemm.hip", "panel.hip",
-           "abi_train.cpp", "adamw.hip", "norm.hip", "gated.hip"]
+           "abi_train.cpp", "adamw.hip", "norm.hip", "norm_rows.hip",
+           "gated.hip"]
 HEADERS = ["qha_internal.hpp"]
 
 ARCH = "gfx950"

@@ -37,6 +37,20 @@ __device__ __forceinline__ float activate_both(float z, int32_t act, float* slop
   return z;
 }
 
+// dz = dy act'(z), z = w xhat + b; for ReLU the sign of z is that of the float64 value.
+__device__ __forceinline__ float grad_z(float dy, float x, float mean, float rstd, float xhat, float w, float b,
+                                        int32_t act) {
+  if (act == QHA_ACT_NONE) return dy;
+  if (act == QHA_ACT_RELU) {
+    const double z = (static_cast<double>(x) - static_cast<double>(mean)) * static_cast<double>(rstd) *
+                         static_cast<double>(w) + static_cast<double>(b);
+    return z > 0.0 ? dy : 0.0f;
+  }
+  float slope;
+  activate_both(xhat * w + b, act, &slope);
+  return dy * slope;
+}
+
 // 16 bytes of T: N elements, converted to and from float32 (one rounding, to nearest even).
 template <typename T>
 struct Pack {

@@ -6,7 +6,8 @@
 //
 // Bound: memory (x read and y written once at the least; dy, x and dx in the backward).
 //
-// Samples of many positions take two launches.  A block of 256 threads owns a chunk of a sample's rows
+// Samples of one position whose vectors lie in one group take one pass with the row in registers
+// (norm_rows.hip); the others two launches.  A block of 256 threads owns a chunk of a sample's rows
 // and all channels: a thread keeps one 16-byte vector of channels (several where the row has more
 // than 256 vectors) and walks down the rows, so loads are whole rows and nothing is exchanged until
 // the chunk ends; then the vectors' sums meet in LDS and one pair per group goes to the workspace.
@@ -234,20 +235,6 @@ __global__ __launch_bounds__(NT) void norm_apply_kernel(NormArgs a) {
   }
 }
 
-// dz = dy act'(z), z = w xhat + b; for ReLU the sign of z is that of the float64 value.
-__device__ __forceinline__ float grad_z(float dy, float x, float mean, float rstd, float xhat, float w, float b,
-                                        int32_t act) {
-  if (act == QHA_ACT_NONE) return dy;
-  if (act == QHA_ACT_RELU) {
-    const double z = (static_cast<double>(x) - static_cast<double>(mean)) * static_cast<double>(rstd) *
-                         static_cast<double>(w) + static_cast<double>(b);
-    return z > 0.0 ? dy : 0.0f;
-  }
-  float slope;
-  activate_both(xhat * w + b, act, &slope);
-  return dy * slope;
-}
-
 // One block's items: per item the group sums of q and q xhat, over all of them the channel sums of dz and dz xhat.
 template <typename T, int R, bool VG>
 __global__ __launch_bounds__(NT) void norm_grad_sums_kernel(NormArgs a) {
@@ -449,6 +436,12 @@ constexpr int64_t kNormItems = 2048;     // eight blocks for each compute unit
 
 // Chunks: enough items for kNormItems blocks, but no chunk of fewer than four rows per thread.
 void norm_plan(NormArgs& a, bool backward) {
+  if (norm_rows_fit(a)) {
+    a.chunks = 0;
+    a.chunk_rows = 1;
+    a.sum_blocks = backward ? norm_rows_blocks(a) : 0;
+    return;
+  }
   const int nvec = vectors(a);
   const int64_t rows_par = nvec < NT ? NT / nvec : 1;
   int64_t chunks = (kNormItems + a.samples - 1) / a.samples;
@@ -466,7 +459,12 @@ size_t norm_workspace(const NormArgs& a, bool backward) {
   return (chan + 15) / 16 * 16 + part;
 }
 
-hipError_t launch_norm_fwd(const NormArgs& a, hipStream_t s) { return launch(a, false, s); }
-hipError_t launch_norm_bwd(const NormArgs& a, hipStream_t s) { return launch(a, true, s); }
+hipError_t launch_norm_fwd(const NormArgs& a, hipStream_t s) {
+  return norm_rows_fit(a) ? launch_norm_rows(a, false, s) : launch(a, false, s);
+}
+
+hipError_t launch_norm_bwd(const NormArgs& a, hipStream_t s) {
+  return a.samples > 0 && norm_rows_fit(a) ? launch_norm_rows(a, true, s) : launch(a, true, s);
+}
 
 }  // namespace qha

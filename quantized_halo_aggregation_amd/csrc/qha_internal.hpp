@@ -244,6 +244,9 @@ struct NormArgs {
 };
 void norm_plan(NormArgs& a, bool backward);
 size_t norm_workspace(const NormArgs& a, bool backward);
+bool norm_rows_fit(const NormArgs& a);
+int64_t norm_rows_blocks(const NormArgs& a);
+hipError_t launch_norm_rows(const NormArgs& a, bool backward, hipStream_t s);
 hipError_t launch_norm_fwd(const NormArgs& a, hipStream_t s);
 hipError_t launch_norm_bwd(const NormArgs& a, hipStream_t s);
 
