@@ -9,10 +9,16 @@
 
 namespace qha {
 
+// exp(-z) and 1 / x on the transcendental units.  The exponent z log2(e) is rounded once, so exp(-z) is off by
+// 1.5 |z| u of itself (u = 2^-24); where it matters it is multiplied by a sigmoid's slope, which
+// falls faster than |z| grows, and sigmoids stay within 2 u.  Past exp's range the sigmoid is 0.
+__device__ __forceinline__ float exp_neg(float z) { return __builtin_amdgcn_exp2f(fminf(z * -1.44269504088896341f, 127.0f)); }
+__device__ __forceinline__ float sigmoid(float z) { return z == z ? __builtin_amdgcn_rcpf(1.0f + exp_neg(z)) : z; }
+
 // act(z); `act` is uniform over a launch, so the branch costs one scalar test.
 __device__ __forceinline__ float activate(float z, int32_t act) {
   if (act == QHA_ACT_RELU) return z > 0.0f ? z : 0.0f;
-  if (act == QHA_ACT_SILU) return z / (1.0f + expf(-z));
+  if (act == QHA_ACT_SILU) return z * sigmoid(z);
   if (act == QHA_ACT_GELU) return 0.5f * z * (1.0f + erff(z * 0.70710678118654752f));
   return z;
 }
@@ -24,13 +30,13 @@ __device__ __forceinline__ float activate_both(float z, int32_t act, float* slop
     return z > 0.0f ? z : 0.0f;
   }
   if (act == QHA_ACT_SILU) {
-    const float s = 1.0f / (1.0f + expf(-z));
+    const float s = sigmoid(z);
     *slope = s * (1.0f + z * (1.0f - s));
     return z * s;
   }
   if (act == QHA_ACT_GELU) {
     const float cdf = 0.5f * (1.0f + erff(z * 0.70710678118654752f));
-    *slope = cdf + z * (0.39894228040143268f * expf(-0.5f * z * z));
+    *slope = cdf + z * (0.39894228040143268f * exp_neg(0.5f * z * z));
     return z * cdf;
   }
   *slope = 1.0f;

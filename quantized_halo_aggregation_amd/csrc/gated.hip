@@ -48,14 +48,13 @@ __device__ __forceinline__ f32x16 mma<_Float16>(s16x8 a, s16x8 b, f32x16 c) {
 }
 
 // An operand of a product: 16-bit values in rows of ld, in `planes` copies `plane` elements apart (the
-// parts of float32 values).  Rows below `half` come from p0 and the others from p1, unless half is
-// at least the row count.
+// parts of float32 values).
 struct Operand {
   const uint16_t* p0;
-  const uint16_t* p1;
-  int64_t ld, plane;
+  const uint16_t* p1;  // the second matrix of pairs, or of the reduction's second segment
+  int64_t ld, ld1;     // of p0 and p1
+  int64_t plane;
   int64_t rows;        // stored rows
-  int64_t half;
   int64_t cols;        // stored columns (a multiple of 8)
 };
 
@@ -72,56 +71,82 @@ __device__ __forceinline__ int permute_along(int row, int chunk) {
 }
 __device__ __forceinline__ int permute_cross(int k, int chunk) { return chunk ^ (((k & 3) << 1) | ((k & 4) << 1)); }
 
-template <int ORDER>
-__device__ __forceinline__ const uint16_t* chunk_at(const Operand& o, int64_t first, int row, int col, int64_t k0) {
-  if (ORDER == ORDER_CROSS) {
-    // row: step of the reduction; col: column of the tile
-    const int64_t k = k0 + row;
-    int64_t c = first + col;
-    c = c < o.cols ? c : o.cols - 8;           // columns past the end repeat the last ones and are not stored
-    return (k < o.half ? o.p0 + k * o.ld : o.p1 + (k - o.half) * o.ld) + c;
-  }
-  int64_t r;
-  const uint16_t* p = o.p0;
-  if (ORDER == ORDER_PAIRS) {
-    const int b = row >> 5;
-    r = first + (b >> 1) * 32 + (row & 31);
-    if (b & 1) p = o.p1;
-  } else {
-    r = first + row;
-  }
-  r = r < o.rows ? r : o.rows - 1;             // rows past the end repeat the last one and are not stored
-  return p + r * o.ld + k0 + col;
-}
-
 // Waits for this wavefront's loads into LDS; a barrier after it makes them visible to the block.
 __device__ __forceinline__ void loads_done() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
 
-// One plane of a tile: ROWS x COLS values (tile rows and columns as stored) to LDS.  `whole`: the BK steps lie
-// inside the reduction; otherwise chunks at or past its end kend become zero.
+// 16 bytes a lane from memory to LDS, lane i of the wavefront to `to` + 16 i.  Written as assembly because
+// the compiler would wait for all such loads before any LDS read that it cannot tell apart from their
+// destination (the transposing reads), and so undo the double buffering; nothing comes back in a
+// register, and loads_done() waits.
+__device__ __forceinline__ void load_to_lds(const uint16_t* from, uint32_t to) {
+  asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(from), "s"(to) : "memory");
+}
+
+__device__ __forceinline__ uint32_t lds_address(const uint16_t* p) {
+  return static_cast<uint32_t>(reinterpret_cast<uintptr_t>((const __attribute__((address_space(3))) uint16_t*)p));
+}
+
+// A thread's share of a tile of ROWS x COLS values (as stored): its N 16-byte chunks, one per NT.
 template <int ORDER, int ROWS, int COLS, int NT>
-__device__ __forceinline__ void stage(const Operand& o, int64_t plane, int64_t first, int64_t k0, int64_t kend,
-                                      bool whole, uint16_t* lds) {
-  constexpr int PER = COLS / 8;
-  constexpr int N = ROWS * PER / NT;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+struct Stager {
+  static constexpr int PER = COLS / 8;
+  static constexpr int N = ROWS * PER / NT;
+  static_assert(ROWS * PER % NT == 0, "whole chunks per thread");
+  const uint16_t* at[N];
+
+  static __device__ __forceinline__ int row(int i) { return (i * NT + static_cast<int>(threadIdx.x)) / PER; }
+  static __device__ __forceinline__ int chunk(int i) {
+    const int q = (i * NT + static_cast<int>(threadIdx.x)) % PER;
+    return ORDER == ORDER_CROSS ? permute_cross(row(i), q) : permute_along<COLS>(row(i), q);
+  }
+  // base: the operand at the reduction's step k0; first: the tile's first stored row (along) or column
+  // (across).  Rows and columns past the end repeat the last ones; their results are not stored.
+  __device__ __forceinline__ void start(const Operand& o, const uint16_t* base, int64_t ld, int64_t first, int64_t k0) {
 #pragma unroll
-  for (int i = 0; i < N; ++i) {
-    const int q = i * NT + threadIdx.x;
-    const int row = q / PER;
-    const int c = ORDER == ORDER_CROSS ? permute_cross(row, q % PER) : permute_along<COLS>(row, q % PER);
-    if (whole) {
-      const uint16_t* src = chunk_at<ORDER>(o, first, row, c * 8, k0) + plane;
-      __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)src,
-                                       (__attribute__((address_space(3))) void*)(lds + (i * NT + wave * 64) * 8), 16, 0, 0);
-    } else {
-      const bool in = ORDER == ORDER_CROSS ? k0 + row < kend : k0 + c * 8 < kend;
-      u32x4 v = {0, 0, 0, 0};
-      if (in) v = *reinterpret_cast<const u32x4*>(chunk_at<ORDER>(o, first, row, c * 8, k0) + plane);
-      *reinterpret_cast<u32x4*>(lds + q * 8) = v;
+    for (int i = 0; i < N; ++i) {
+      if (ORDER == ORDER_CROSS) {
+        int64_t c = first + chunk(i) * 8;
+        c = c < o.cols ? c : o.cols - 8;
+        at[i] = base + (k0 + row(i)) * ld + c;
+      } else {
+        int64_t r;
+        const uint16_t* p = base;
+        if (ORDER == ORDER_PAIRS) {
+          const int b = row(i) >> 5;
+          r = first + (b >> 1) * 32 + (row(i) & 31);
+          if (b & 1) {
+            p = o.p1;
+            ld = o.ld1;
+          } else {
+            ld = o.ld;
+          }
+        } else {
+          r = first + row(i);
+        }
+        r = r < o.rows ? r : o.rows - 1;
+        at[i] = p + r * ld + k0 + chunk(i) * 8;
+      }
     }
   }
-}
+  __device__ __forceinline__ void load(int64_t plane, const uint16_t* lds) const {
+    const uint32_t to = lds_address(lds) + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) * 1024;
+#pragma unroll
+    for (int i = 0; i < N; ++i) load_to_lds(at[i] + plane, to + i * NT * 16);
+  }
+  __device__ __forceinline__ void next(int64_t ld) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) at[i] += ORDER == ORDER_CROSS ? ROWS * ld : COLS;
+  }
+  // The last, partial step: `left` steps of the reduction remain, the others become zero.
+  __device__ __forceinline__ void load_partial(int64_t plane, int64_t left, uint16_t* lds) const {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      u32x4 v = {0, 0, 0, 0};
+      if ((ORDER == ORDER_CROSS ? row(i) : chunk(i) * 8) < left) v = *reinterpret_cast<const u32x4*>(at[i] + plane);
+      *reinterpret_cast<u32x4*>(lds + (i * NT + threadIdx.x) * 8) = v;
+    }
+  }
+};
 
 // The matrix operand of 32 tile rows (or columns) from `at` on, 16 steps of the reduction from ks on:
 // lane l holds row l % 32, steps 8 (l / 32) .. + 7.
@@ -148,7 +173,8 @@ __device__ __forceinline__ s16x8 fragment(const uint16_t* lds, int at, int ks, i
 struct ProductArgs {
   Operand a, b;
   int64_t m, n;             // C is m x n (forward: n columns of H)
-  int64_t k;                // reduction
+  int64_t k;                // reduction: `segments` of k steps; the second takes A's columns from k on and B's p1
+  int32_t segments;
   int64_t k_each;           // steps of the reduction per split (a multiple of BK)
   int32_t m_tiles, n_tiles, splits;
   // forward
@@ -180,6 +206,37 @@ template <>
 __device__ __forceinline__ void store4<_Float16>(_Float16* p, f32x4 v) {
   *reinterpret_cast<f16x4*>(p) = __builtin_convertvector(v, f16x4);
 }
+
+// 32 rows x CW columns of results on their way out through a wavefront's own piece of LDS.  Rows are 16 bytes
+// longer than their values, which spreads a column of lanes over the banks.
+template <typename O, int CW>
+struct RowWriter {
+  static constexpr int STRIDE = CW * sizeof(O) + 16;
+  static constexpr int PER = CW * sizeof(O) / 16;       // 16-byte pieces of a row
+  char* mine;
+  int lane;
+  __device__ __forceinline__ RowWriter(uint16_t* lds, int wave, int ln)
+      : mine(reinterpret_cast<char*>(lds) + wave * 32 * STRIDE), lane(ln) {}
+  // four values of row lane % 32, from column c + 4 (lane / 32) on
+  __device__ __forceinline__ void put(int c, f32x4 v) {
+    store4<O>(reinterpret_cast<O*>(mine + (lane & 31) * STRIDE + (c + (lane >> 5) * 4) * sizeof(O)), v);
+  }
+  // rows r0 .. of the output that lie in [0, rows), columns c0 .. below cols
+  __device__ __forceinline__ void flush(O* to, int64_t ld, int64_t r0, int64_t rows, int64_t c0, int64_t cols) {
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    constexpr int E = 16 / sizeof(O);
+#pragma unroll
+    for (int s = 0; s < 32 * PER / 64; ++s) {
+      const int r = (s * 64 + lane) / PER, q = (s * 64 + lane) % PER;
+      const u32x4 v = *reinterpret_cast<const u32x4*>(mine + r * STRIDE + q * 16);
+      const int64_t row = r0 + r, col = c0 + q * E;
+      if (row >= 0 && row < rows && col < cols) *reinterpret_cast<u32x4*>(to + row * ld + col) = v;
+    }
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+  }
+};
 
 // Tiles dealt to the XCDs in bands: consecutive blocks go to the eight XCDs in turn, so block b takes
 // position b / 8 of band b % 8; within a band, tiles run down groups of eight row tiles before the next
@@ -222,17 +279,6 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) void product_kernel(Pro
   const int64_t kbeg = sp * p.k_each;
   const int64_t kend = kbeg + p.k_each < p.k ? kbeg + p.k_each : p.k;
 
-  auto load = [&](int64_t k0, int buf) {
-    uint16_t* base = lds + buf * BUF;
-    const bool whole = k0 + BK <= kend;
-#pragma unroll
-    for (int pl = 0; pl < PA; ++pl)
-      stage<OA, A_ROWS, A_COLS, NT>(p.a, pl * p.a.plane, m0, k0, kend, whole, base + pl * A_SIZE);
-#pragma unroll
-    for (int pl = 0; pl < PB; ++pl)
-      stage<OB, B_ROWS, B_COLS, NT>(p.b, pl * p.b.plane, n0, k0, kend, whole, base + PA * A_SIZE + pl * B_SIZE);
-  };
-
   f32x16 acc[MI][NI];
 #pragma unroll
   for (int i = 0; i < MI; ++i)
@@ -241,25 +287,24 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) void product_kernel(Pro
 #pragma unroll
       for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.0f;
 
-  if (kbeg < kend) load(kbeg, 0);
-  loads_done();
-  __syncthreads();
-  int buf = 0;
-  for (int64_t k0 = kbeg; k0 < kend; k0 += BK, buf ^= 1) {
-    if (k0 + BK < kend) load(k0 + BK, buf ^ 1);
-    const uint16_t* at = lds + buf * BUF;
+  auto multiply = [&](const uint16_t* at) {
     const uint16_t* bt = at + PA * A_SIZE;
-#pragma unroll
-    for (int ks = 0; ks < BK; ks += 16) {
-      s16x8 fa[MI][PA], fb[NI][PB];
+    s16x8 fa[2][MI][PA], fb[2][NI][PB];
+    auto fetch = [&](int ks, int to) {
 #pragma unroll
       for (int pl = 0; pl < PA; ++pl)
 #pragma unroll
-        for (int i = 0; i < MI; ++i) fa[i][pl] = fragment<OA, A_COLS>(at + pl * A_SIZE, wm * WM + i * 32, ks, lane);
+        for (int i = 0; i < MI; ++i) fa[to][i][pl] = fragment<OA, A_COLS>(at + pl * A_SIZE, wm * WM + i * 32, ks, lane);
 #pragma unroll
       for (int pl = 0; pl < PB; ++pl)
 #pragma unroll
-        for (int j = 0; j < NI; ++j) fb[j][pl] = fragment<OB, B_COLS>(bt + pl * B_SIZE, wn * WN + j * 32, ks, lane);
+        for (int j = 0; j < NI; ++j) fb[to][j][pl] = fragment<OB, B_COLS>(bt + pl * B_SIZE, wn * WN + j * 32, ks, lane);
+    };
+    fetch(0, 0);
+#pragma unroll
+    for (int ks = 0; ks < BK; ks += 16) {
+      const int now = ks / 16 & 1;
+      if (ks + 16 < BK) fetch(ks + 16, now ^ 1);
 #pragma unroll
       for (int i = 0; i < MI; ++i)
 #pragma unroll
@@ -267,62 +312,112 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) void product_kernel(Pro
           f32x16 c = acc[i][j];
           // smallest part products first
           if constexpr (PB == 3) {
-            c = mma<T>(fb[j][1], fa[i][1], c);
-            c = mma<T>(fb[j][0], fa[i][2], c);
-            c = mma<T>(fb[j][2], fa[i][0], c);
-            c = mma<T>(fb[j][0], fa[i][1], c);
-            c = mma<T>(fb[j][1], fa[i][0], c);
+            c = mma<T>(fb[now][j][1], fa[now][i][1], c);
+            c = mma<T>(fb[now][j][0], fa[now][i][2], c);
+            c = mma<T>(fb[now][j][2], fa[now][i][0], c);
+            c = mma<T>(fb[now][j][0], fa[now][i][1], c);
+            c = mma<T>(fb[now][j][1], fa[now][i][0], c);
           } else if constexpr (PA == 2) {
-            c = mma<T>(fb[j][0], fa[i][1], c);
+            c = mma<T>(fb[now][j][0], fa[now][i][1], c);
           }
-          acc[i][j] = mma<T>(fb[j][0], fa[i][0], c);
+          acc[i][j] = mma<T>(fb[now][j][0], fa[now][i][0], c);
         }
     }
+  };
+
+  Stager<OA, A_ROWS, A_COLS, NT> sa;
+  Stager<OB, B_ROWS, B_COLS, NT> sb;
+  for (int seg = 0; seg < p.segments; ++seg) {
+    const int64_t ldb = seg ? p.b.ld1 : p.b.ld;
+    sa.start(p.a, p.a.p0 + (seg ? p.k : 0), p.a.ld, m0, kbeg);
+    sb.start(p.b, seg ? p.b.p1 : p.b.p0, ldb, n0, kbeg);
+    auto load = [&](uint16_t* to) {
+#pragma unroll
+      for (int pl = 0; pl < PA; ++pl) sa.load(pl * p.a.plane, to + pl * A_SIZE);
+#pragma unroll
+      for (int pl = 0; pl < PB; ++pl) sb.load(pl * p.b.plane, to + PA * A_SIZE + pl * B_SIZE);
+      sa.next(p.a.ld);
+      sb.next(ldb);
+    };
+    const int64_t steps = kbeg < kend ? (kend - kbeg) / BK : 0, left = kbeg < kend ? (kend - kbeg) % BK : 0;
+    if (steps > 0) load(lds);
     loads_done();
     __syncthreads();
+    for (int64_t t = 0; t < steps; ++t) {
+      // the other buffer was read before the last barrier
+      if (t + 1 < steps) load(lds + ((t + 1) & 1) * BUF);
+      multiply(lds + (t & 1) * BUF);
+      loads_done();
+      __syncthreads();
+    }
+    if (left > 0) {
+#pragma unroll
+      for (int pl = 0; pl < PA; ++pl) sa.load_partial(pl * p.a.plane, left, lds + pl * A_SIZE);
+#pragma unroll
+      for (int pl = 0; pl < PB; ++pl) sb.load_partial(pl * p.b.plane, left, lds + PA * A_SIZE + pl * B_SIZE);
+      __syncthreads();
+      multiply(lds);
+      __syncthreads();
+    }
   }
 
-  // element r of lane l is row l % 32, column 8 (r / 4) + 4 (l / 32) + r % 4 of its 32x32 block
-  const int half4 = (lane >> 5) * 4;
+  // Element r of lane l is row l % 32, column 8 (r / 4) + 4 (l / 32) + r % 4 of its 32x32 block.  A
+  // wavefront's 32 rows pass through a piece of LDS of its own (the loop's last barrier has freed it), so that a
+  // row leaves in 16-byte stores of neighbouring lanes.
+  constexpr int CW = OUT == OUT_GATED ? WN / 2 : WN;
+  const int64_t row0 = m0 + wm * WM;
+  const int64_t col0 = n0 + wn * CW;
 #pragma unroll
   for (int i = 0; i < MI; ++i) {
-    const int64_t row = m0 + wm * WM + i * 32 + (lane & 31);
-    if (row >= p.m) continue;
-    if (OUT == OUT_DW && (row < p.half ? row : row - p.half) >= p.pad_from) continue;
+    const int64_t r0 = row0 + i * 32;
+    if (r0 >= p.m) break;
     if constexpr (OUT == OUT_GATED) {
+      RowWriter<O, CW> out(lds, wave, lane);
+      auto put = [&](void* to, int64_t ld, auto value) {
 #pragma unroll
-      for (int j = 0; j < NI; j += 2) {
-        const int64_t c0 = n0 + (wn * WN + j * 32) / 2 + half4;
+        for (int j = 0; j < NI; j += 2)
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const int64_t col = c0 + 8 * q;
-          if (col >= p.n) continue;
-          f32x4 g, u, h;
+          for (int q = 0; q < 4; ++q) {
+            f32x4 v;
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            g[e] = acc[i][j][4 * q + e];
-            u[e] = acc[i][j + 1][4 * q + e];
-            h[e] = activate(g[e], p.act) * u[e];
+            for (int e = 0; e < 4; ++e) v[e] = value(acc[i][j][4 * q + e], acc[i][j + 1][4 * q + e]);
+            out.put(j * 16 + 8 * q, v);
           }
-          store4<O>(static_cast<O*>(p.h) + row * p.ldh + col, h);
-          if (p.gate) store4<O>(static_cast<O*>(p.gate) + row * p.ldg + col, g);
-          if (p.up) store4<O>(static_cast<O*>(p.up) + row * p.ldu + col, u);
-        }
-      }
-    } else {
+        out.flush(static_cast<O*>(to), ld, r0, p.m, col0, p.n);
+      };
+      put(p.h, p.ldh, [&](float g, float u) { return activate(g, p.act) * u; });
+      if (p.gate) put(p.gate, p.ldg, [](float g, float) { return g; });
+      if (p.up) put(p.up, p.ldu, [](float, float u) { return u; });
+    } else if (OUT == OUT_DW || p.splits > 1) {
+      RowWriter<float, CW> out(lds, wave, lane);
 #pragma unroll
       for (int j = 0; j < NI; ++j)
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-          const int64_t col = n0 + wn * WN + j * 32 + half4 + 8 * q;
-          if (col >= p.n) continue;
           f32x4 v;
 #pragma unroll
           for (int e = 0; e < 4; ++e) v[e] = acc[i][j][4 * q + e];
-          if (p.splits > 1) store4<float>(p.partial + (sp * p.m + row) * p.n + col, v);
-          else if (OUT == OUT_DW && row >= p.half) store4<float>(p.c1 + (row - p.half) * p.ldc1 + col, v);
-          else store4<O>(static_cast<O*>(p.c) + row * p.ldc + col, v);
+          out.put(j * 32 + 8 * q, v);
         }
+      if (p.splits > 1) {
+        out.flush(p.partial + sp * p.m * p.n, p.n, r0, p.m, col0, p.n);
+      } else {
+        // rows of the first half, then of the second; what lies between is padding
+        out.flush(static_cast<float*>(p.c), p.ldc, r0, p.pad_from, col0, p.n);
+        out.flush(p.c1, p.ldc1, r0 - p.half, p.pad_from, col0, p.n);
+      }
+    } else {
+      RowWriter<O, CW> out(lds, wave, lane);
+#pragma unroll
+      for (int j = 0; j < NI; ++j)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          f32x4 v;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) v[e] = acc[i][j][4 * q + e];
+          out.put(j * 32 + 8 * q, v);
+        }
+      out.flush(static_cast<O*>(p.c), p.ldc, r0, p.m, col0, p.n);
     }
   }
 }
@@ -437,23 +532,41 @@ hipError_t run_product(ProductArgs p, hipStream_t s) {
   return hipGetLastError();
 }
 
+constexpr int64_t kUnits = 256;          // compute units; a block with a large tile fills one
+
+int64_t tiles_of(int64_t m, int64_t n, int64_t bm, int64_t bn) { return ((m + bm - 1) / bm) * ((n + bn - 1) / bn); }
+
+// Tile shapes.  Larger tiles read LDS less per product and need enough of them to occupy the compute
+// units: forward of 16384 x 2048 -> 8192 bf16, 1044 us in 256 x 256 tiles (4096 of them) against
+// 1335 us in 128 x 128; dA of 8191 x 8192 -> 1024, 212 us in 256 x 256 (128 tiles, half the chip) against
+// 152 us in 128 x 128; its dW 253 us in 256 x 128 against 331 us.  Three-part products: forward of 300k x 128
+// -> 128, 205 us in 128 x 256 (one column of tiles: A is read once) against 260 us in 128 x 128.
 template <typename T, typename O, int PA, int PB, int OA, int OB, int OUT>
 hipError_t product(const ProductArgs& p, hipStream_t s) {
-  constexpr int BK = PA + PB > 3 ? 32 : 64;
-  return run_product<T, O, PA, PB, OA, OB, OUT, 128, 128, BK, 64, 64>(p, s);
+  const int64_t n = OUT == OUT_GATED ? 2 * p.n : p.n;       // rows of the B operand
+  if constexpr (PA == 1) {
+    if (tiles_of(p.m, n, 256, 256) * p.splits >= 2 * kUnits) return run_product<T, O, PA, PB, OA, OB, OUT, 256, 256, 64, 128, 64>(p, s);
+    return run_product<T, O, PA, PB, OA, OB, OUT, 128, 128, 64, 64, 64>(p, s);
+  } else if constexpr (PA == 2) {
+    if (p.m > 128 && tiles_of(p.m, n, 256, 128) * p.splits >= kUnits) return run_product<T, O, PA, PB, OA, OB, OUT, 256, 128, 64, 64, 64>(p, s);
+    return run_product<T, O, PA, PB, OA, OB, OUT, 128, 128, 64, 64, 64>(p, s);
+  } else {
+    if (n > 128 && tiles_of(p.m, n, 128, 256) * p.splits >= kUnits) return run_product<T, O, PA, PB, OA, OB, OUT, 128, 256, 32, 64, 64>(p, s);
+    if (p.m > 128 && tiles_of(p.m, n, 256, 128) * p.splits >= kUnits) return run_product<T, O, PA, PB, OA, OB, OUT, 256, 128, 32, 64, 64>(p, s);
+    return run_product<T, O, PA, PB, OA, OB, OUT, 128, 128, 32, 64, 64>(p, s);
+  }
 }
 
 Operand plain(const void* p, int64_t ld, int64_t rows, int64_t cols, int64_t plane = 0) {
-  return {static_cast<const uint16_t*>(p), nullptr, ld, plane, rows, INT64_MAX, cols};
+  return {static_cast<const uint16_t*>(p), nullptr, ld, ld, plane, rows, cols};
 }
 
 constexpr int64_t kSplitStep = 64;       // a split's steps are a multiple of it
-constexpr int64_t kDwTiles = 512;        // blocks that fill the compute units twice
 
-// Splits of dW's reduction over the rows: enough tiles for every compute unit, each of at least 256 rows.
+// Splits of dW's reduction over the rows: enough 256 x 128 tiles for every compute unit, each of at least 256 rows.
 int32_t dw_splits(int64_t m, int64_t n, int64_t k) {
-  const int64_t tiles = ((2 * n + 127) / 128) * ((k + 127) / 128);
-  int64_t s = (kDwTiles + tiles - 1) / tiles;
+  const int64_t tiles = tiles_of(2 * up8(n), k, 256, 128);
+  int64_t s = (kUnits + tiles - 1) / tiles;
   const int64_t most = (m + 255) / 256;
   s = s < most ? s : most;
   return static_cast<int32_t>(s < 1 ? 1 : s);
@@ -486,10 +599,11 @@ hipError_t fwd16(const GatedArgs& g, hipStream_t s) {
   p.a = plain(g.a, g.lda, g.m, g.k);
   p.b = plain(g.wg, g.ldwg, g.n, g.k);
   p.b.p1 = static_cast<const uint16_t*>(g.wu);
+  p.b.ld1 = g.ldwu;
   p.m = g.m;
   p.n = g.n;
   p.k = p.k_each = g.k;
-  p.splits = 1;
+  p.splits = p.segments = 1;
   p.h = g.h;
   p.gate = g.gate_out;
   p.up = g.up_out;
@@ -521,7 +635,7 @@ hipError_t fwd32(const GatedArgs& g, hipStream_t s) {
   p.m = g.m;
   p.n = g.n;
   p.k = p.k_each = k8;
-  p.splits = 1;
+  p.splits = p.segments = 1;
   p.h = g.h;
   p.gate = g.gate_out;
   p.up = g.up_out;
@@ -548,14 +662,14 @@ hipError_t bwd(const GatedArgs& g, hipStream_t s) {
     split(static_cast<const float*>(g.wg), g.ldwg, g.n, g.k, w3, n8, 2 * n8 * k8, s);
     split(static_cast<const float*>(g.wu), g.ldwu, g.n, g.k, w3 + n8 * k8, n8, 2 * n8 * k8, s);
     a = plain(a3, k8, g.m, k8, g.m * k8);
-    w = plain(w3, k8, 2 * n8, k8, 2 * n8 * k8);
+    w = plain(w3, k8, n8, k8, 2 * n8 * k8);
     w.p1 = w3 + n8 * k8;
   } else {
     a = plain(g.a, g.lda, g.m, g.k);
-    w = plain(g.wg, g.ldwg, 2 * g.n, g.k);
+    w = plain(g.wg, g.ldwg, g.n, g.k);
     w.p1 = static_cast<const uint16_t*>(g.wu);
+    w.ld1 = g.ldwu;
   }
-  w.half = n8;
   const Operand d = plain(grad, 2 * n8, g.m, 2 * n8, g.m * 2 * n8);
   hipError_t e = hipSuccess;
   if (g.m > 0 && g.da) {
@@ -564,7 +678,8 @@ hipError_t bwd(const GatedArgs& g, hipStream_t s) {
     p.b = w;
     p.m = g.m;
     p.n = g.k;
-    p.k = p.k_each = 2 * n8;
+    p.k = p.k_each = n8;
+    p.segments = 2;
     p.splits = 1;
     p.half = INT64_MAX;
     p.c = g.da;
@@ -578,6 +693,7 @@ hipError_t bwd(const GatedArgs& g, hipStream_t s) {
   p.m = 2 * n8;
   p.n = g.k;
   p.k = g.m;
+  p.segments = 1;
   p.splits = dw_splits(g.m, g.n, g.k);
   p.k_each = ((g.m + p.splits - 1) / p.splits + kSplitStep - 1) / kSplitStep * kSplitStep;
   p.half = n8;

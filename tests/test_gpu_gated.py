@@ -166,6 +166,31 @@ def test_strided_operands(dtype):
             assert (buf[:, :16] == 5).all() and (buf[:, 16 + w:] == 5).all()
 
 
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
+def test_every_array_with_a_stride_of_its_own(dtype):
+    H.require_gpu()
+    import torch
+    from quantized_halo_aggregation_amd import binding as B
+    t = getattr(torch, dtype)
+    for m, n, k in ((2, 72, 64), (200, 136, 200)):
+        H.note(f"gated own strides {m} {dtype}")
+        a, wg, wu, dh = (x.cuda() for x in _data(m, n, k, dtype, 6))
+        h, gate, up = _forward(a, wg, wu, "silu")
+        da, dws = torch.empty_like(a), [torch.empty(n, k, device="cuda") for _ in range(2)]
+        ws = _space(B.gated_backward_workspace(t, m, n, k))
+        B.gated_backward(dh, gate, up, a, wg, wu, da, *dws, workspace=ws)
+        pad = iter(range(8, 200, 8))
+
+        def own(x):
+            view = torch.full((x.shape[0], x.shape[1] + next(pad)), 3.0, dtype=x.dtype, device="cuda")[:, :x.shape[1]]
+            return view.copy_(x)
+        sa, sg, su, sdh, oh, og, ou, oda, odg, odu = (own(x) for x in (a, wg, wu, dh, h * 0, gate * 0, up * 0, da * 0, dws[0] * 0, dws[1] * 0))
+        B.gated_project(sa, sg, su, oh, gate=og, up=ou, workspace=_space(B.gated_project_workspace(t, m, n, k)))
+        assert torch.equal(oh, h) and torch.equal(og, gate) and torch.equal(ou, up)
+        B.gated_backward(sdh, og, ou, sa, sg, su, oda, odg, odu, workspace=ws)
+        assert torch.equal(oda, da) and torch.equal(odg, dws[0]) and torch.equal(odu, dws[1])
+
+
 def test_values_that_are_not_finite_stay_in_their_rows():
     H.require_gpu()
     import torch
