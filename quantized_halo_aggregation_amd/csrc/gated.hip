@@ -21,6 +21,8 @@
 #include "act_common.hpp"
 #include "qha_internal.hpp"
 
+#include <type_traits>
+
 namespace qha {
 namespace {
 
@@ -45,6 +47,17 @@ __device__ __forceinline__ f32x16 mma<__bf16>(s16x8 a, s16x8 b, f32x16 c) {
 template <>
 __device__ __forceinline__ f32x16 mma<_Float16>(s16x8 a, s16x8 b, f32x16 c) {
   return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
+}
+
+template <typename T>
+__device__ __forceinline__ f32x4 mma16(s16x8 a, s16x8 b, f32x4 c);
+template <>
+__device__ __forceinline__ f32x4 mma16<__bf16>(s16x8 a, s16x8 b, f32x4 c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+}
+template <>
+__device__ __forceinline__ f32x4 mma16<_Float16>(s16x8 a, s16x8 b, f32x4 c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
 }
 
 // An operand of a product: 16-bit values in rows of ld, in `planes` copies `plane` elements apart (the
@@ -188,7 +201,7 @@ struct ProductArgs {
   float* c1;
   int64_t ldc, ldc1;
   int64_t half;
-  int64_t pad_from;         // dW: rows from here to `half` of either half are padding
+  int64_t pad_from;         // dW: rows from here to `half` of either half are padding (dA: half and pad_from are m)
   float* partial;           // [splits][m][n] when splits > 1
 };
 
@@ -422,12 +435,14 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) void product_kernel(Pro
   }
 }
 
-// dWg and dWu (or their rows below and from `half` on) from the splits' partials, added in order in float64.
+// dA, or dWg and dWu (the rows below and from `half` on), from the splits' partials, added in order in float64.
+template <typename O>
 __global__ __launch_bounds__(256) void sum_splits_kernel(ProductArgs p, int64_t n4) {
   const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
   if (i >= p.m * n4) return;
   const int64_t row = i / n4, col = i % n4 * 4;
-  if ((row < p.half ? row : row - p.half) >= p.pad_from) return;
+  const int64_t in = row < p.half ? row : row - p.half;
+  if (in >= p.pad_from) return;
   double s[4] = {0.0, 0.0, 0.0, 0.0};
 #pragma unroll 4
   for (int k = 0; k < p.splits; ++k) {
@@ -438,8 +453,8 @@ __global__ __launch_bounds__(256) void sum_splits_kernel(ProductArgs p, int64_t 
   f32x4 r;
 #pragma unroll
   for (int e = 0; e < 4; ++e) r[e] = static_cast<float>(s[e]);
-  float* to = row < p.half ? static_cast<float*>(p.c) + row * p.ldc : p.c1 + (row - p.half) * p.ldc1;
-  store4<float>(to + col, r);
+  if (row < p.half) store4<O>(static_cast<O*>(p.c) + row * p.ldc + col, r);
+  else store4<float>(p.c1 + in * p.ldc1 + col, r);
 }
 
 // x = hi + mid + lo exactly: each part is rounded to nearest even, the remainders are exact in float32.
@@ -513,6 +528,123 @@ __global__ __launch_bounds__(256) void gate_grad_kernel(GatedArgs p, uint16_t* o
   }
 }
 
+// Few rows (decoded tokens, queried nodes): the weights are read once at memory's rate and the tiles above
+// would leave most of the chip idle.  A block owns 16 columns of H and all rows (16 MB of them); its eight
+// wavefronts take every eighth 32-step piece of the reduction, read their 16 rows of Wg and Wu straight from
+// memory as matrix operands (16 bytes a lane, four pieces in flight), and meet in LDS.
+template <typename T, int MB>
+__global__ __launch_bounds__(512) void few_rows_kernel(GatedArgs p) {
+  constexpr bool F32 = sizeof(T) == 4;
+  typedef typename std::conditional<F32, __bf16, T>::type P;       // the matrix cores' type
+  constexpr int PL = F32 ? 3 : 1;
+  __shared__ f32x4 sums[8][2][MB][64];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t c0 = static_cast<int64_t>(blockIdx.x) * 16;
+  int64_t wrow = c0 + (lane & 15);
+  wrow = wrow < p.n ? wrow : p.n - 1;                 // repeats the last row; its columns are not stored
+  const int64_t kq = (lane >> 4) * 8;
+  const T* gp = static_cast<const T*>(p.wg) + wrow * p.ldwg;
+  const T* up = static_cast<const T*>(p.wu) + wrow * p.ldwu;
+  const T* ap[MB];
+#pragma unroll
+  for (int b = 0; b < MB; ++b) {
+    int64_t r = b * 16 + (lane & 15);
+    r = r < p.m ? r : p.m - 1;
+    ap[b] = static_cast<const T*>(p.a) + r * p.lda;
+  }
+  f32x4 acc[2][MB];
+#pragma unroll
+  for (int b = 0; b < MB; ++b) acc[0][b] = acc[1][b] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+
+  struct Piece {
+    u32x4 w[F32 ? 2 : 1];
+  };
+  auto read = [&](const T* x, int64_t k) {
+    Piece r;
+#pragma unroll
+    for (int h = 0; h < (F32 ? 2 : 1); ++h) {
+      r.w[h] = u32x4{0, 0, 0, 0};
+      if (k + 4 * h < p.k) r.w[h] = *reinterpret_cast<const u32x4*>(x + k + 4 * h);
+    }
+    return r;
+  };
+  struct Parts {
+    s16x8 p[PL];
+  };
+  auto parts = [&](const Piece& x) {
+    Parts r;
+    if constexpr (F32) {
+      bf16x4 h[2], m[2], l[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) split3(__builtin_bit_cast(f32x4, x.w[i]), h[i], m[i], l[i]);
+      r.p[0] = __builtin_bit_cast(s16x8, __builtin_shufflevector(h[0], h[1], 0, 1, 2, 3, 4, 5, 6, 7));
+      r.p[1] = __builtin_bit_cast(s16x8, __builtin_shufflevector(m[0], m[1], 0, 1, 2, 3, 4, 5, 6, 7));
+      r.p[2] = __builtin_bit_cast(s16x8, __builtin_shufflevector(l[0], l[1], 0, 1, 2, 3, 4, 5, 6, 7));
+    } else {
+      r.p[0] = __builtin_bit_cast(s16x8, x.w[0]);
+    }
+    return r;
+  };
+  auto madd = [&](const Parts& w, const Parts& a, f32x4 c) {
+    if constexpr (F32) {
+      c = mma16<P>(w.p[1], a.p[1], c);
+      c = mma16<P>(w.p[0], a.p[2], c);
+      c = mma16<P>(w.p[2], a.p[0], c);
+      c = mma16<P>(w.p[0], a.p[1], c);
+      c = mma16<P>(w.p[1], a.p[0], c);
+    }
+    return mma16<P>(w.p[0], a.p[0], c);
+  };
+  constexpr int AHEAD = MB <= 2 ? 4 : F32 && MB == 8 ? 1 : 2;
+  for (int64_t k0 = wave * 32; k0 < p.k; k0 += 256 * AHEAD) {
+    Piece g[AHEAD], u[AHEAD], a[AHEAD][MB];
+#pragma unroll
+    for (int t = 0; t < AHEAD; ++t) {
+      const int64_t k = k0 + 256 * t + kq;            // past the reduction's end everything reads as zero
+      g[t] = read(gp, k);
+      u[t] = read(up, k);
+#pragma unroll
+      for (int b = 0; b < MB; ++b) a[t][b] = read(ap[b], k);
+    }
+#pragma unroll
+    for (int t = 0; t < AHEAD; ++t) {
+      const Parts wg = parts(g[t]), wu = parts(u[t]);
+#pragma unroll
+      for (int b = 0; b < MB; ++b) {
+        const Parts x = parts(a[t][b]);
+        acc[0][b] = madd(wg, x, acc[0][b]);
+        acc[1][b] = madd(wu, x, acc[1][b]);
+      }
+    }
+  }
+#pragma unroll
+  for (int b = 0; b < MB; ++b) {
+    sums[wave][0][b][lane] = acc[0][b];
+    sums[wave][1][b][lane] = acc[1][b];
+  }
+  __syncthreads();
+  // element e of lane l is row l % 16, column 4 (l / 16) + e
+  for (int i = threadIdx.x; i < MB * 64; i += 512) {
+    const int b = i >> 6, l = i & 63;
+    f32x4 g = sums[0][0][b][l], u = sums[0][1][b][l], h;
+#pragma unroll
+    for (int w = 1; w < 8; ++w) {
+      g += sums[w][0][b][l];
+      u += sums[w][1][b][l];
+    }
+    const int64_t row = b * 16 + (l & 15), col = c0 + (l >> 4) * 4;
+    if (row >= p.m || col >= p.n) continue;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) h[e] = activate(g[e], p.act) * u[e];
+    store4<T>(static_cast<T*>(p.h) + row * p.ldh + col, h);
+    if (p.gate_out) {
+      store4<T>(static_cast<T*>(p.gate_out) + row * p.ldg + col, g);
+      store4<T>(static_cast<T*>(p.up_out) + row * p.ldu + col, u);
+    }
+  }
+}
+
 uint32_t stride_blocks(int64_t items) {
   const int64_t b = (items + 255) / 256;
   return static_cast<uint32_t>(b < 16384 ? (b > 0 ? b : 1) : 16384);
@@ -572,6 +704,18 @@ int32_t dw_splits(int64_t m, int64_t n, int64_t k) {
   return static_cast<int32_t>(s < 1 ? 1 : s);
 }
 
+// Splits of dA's reduction over the gate's (and the up's) columns where its tiles are few.
+int32_t da_splits(int64_t m, int64_t n, int64_t k) {
+  const int64_t tiles = tiles_of(m, k, 128, 128);
+  int64_t s = kUnits / (tiles > 0 ? tiles : 1);
+  const int64_t most = (n + 255) / 256;
+  s = s < most ? s : most;
+  return static_cast<int32_t>(s < 1 ? 1 : s);
+}
+
+// Rows that few_rows_kernel takes: up to 16 always, up to 128 while the tiles would not fill the chip.
+bool few_rows(int64_t m, int64_t n) { return m <= 16 || (m <= 128 && tiles_of(m, 2 * n, 128, 128) < kUnits); }
+
 struct Space {
   int64_t a, w, grad, partial;     // bytes
 };
@@ -581,7 +725,7 @@ int64_t up16(int64_t x) { return (x + 15) / 16 * 16; }
 Space gated_space(int32_t type, int64_t m, int64_t n, int64_t k, bool backward) {
   Space s = {0, 0, 0, 0};
   const int64_t planes = type == QHA_F32 ? 3 : 1;
-  if (type == QHA_F32) {
+  if (type == QHA_F32 && (backward || !few_rows(m, n))) {
     s.a = up16(planes * m * up8(k) * 2);
     s.w = up16(planes * 2 * up8(n) * up8(k) * 2);
   }
@@ -589,8 +733,31 @@ Space gated_space(int32_t type, int64_t m, int64_t n, int64_t k, bool backward) 
     s.grad = up16((type == QHA_F32 ? 3 : 2) * m * 2 * up8(n) * 2);
     const int64_t splits = dw_splits(m, n, k);
     s.partial = splits > 1 ? up16(splits * 2 * up8(n) * k * 4) : 0;
+    // dA's partials are read before dW writes its own to the same place
+    const int64_t da = da_splits(m, n, k);
+    const int64_t need = da > 1 ? up16(da * m * k * 4) : 0;
+    s.partial = s.partial > need ? s.partial : need;
   }
   return s;
+}
+
+int64_t split_each(int64_t k, int32_t splits) { return ((k + splits - 1) / splits + kSplitStep - 1) / kSplitStep * kSplitStep; }
+
+template <typename O>
+hipError_t sum_splits(const ProductArgs& p, hipStream_t s) {
+  const int64_t n4 = p.n / 4;
+  sum_splits_kernel<O><<<static_cast<uint32_t>((p.m * n4 + 255) / 256), 256, 0, s>>>(p, n4);
+  return hipGetLastError();
+}
+
+template <typename T>
+hipError_t fwd_few(const GatedArgs& g, hipStream_t s) {
+  const uint32_t blocks = static_cast<uint32_t>((g.n + 15) / 16);
+  if (g.m <= 16) few_rows_kernel<T, 1><<<blocks, 512, 0, s>>>(g);
+  else if (g.m <= 32) few_rows_kernel<T, 2><<<blocks, 512, 0, s>>>(g);
+  else if (g.m <= 64) few_rows_kernel<T, 4><<<blocks, 512, 0, s>>>(g);
+  else few_rows_kernel<T, 8><<<blocks, 512, 0, s>>>(g);
+  return hipGetLastError();
 }
 
 template <typename T>
@@ -678,13 +845,16 @@ hipError_t bwd(const GatedArgs& g, hipStream_t s) {
     p.b = w;
     p.m = g.m;
     p.n = g.k;
-    p.k = p.k_each = n8;
+    p.k = n8;
     p.segments = 2;
-    p.splits = 1;
-    p.half = INT64_MAX;
+    p.splits = da_splits(g.m, g.n, g.k);
+    p.k_each = split_each(n8, p.splits);
+    p.half = p.pad_from = g.m;
     p.c = g.da;
     p.ldc = g.ldda;
+    p.partial = partial;
     e = product<T, O, PL, PL, ORDER_ROWS, ORDER_CROSS, OUT_DA>(p, s);
+    if (e == hipSuccess && p.splits > 1) e = sum_splits<O>(p, s);
     if (e != hipSuccess) return e;
   }
   ProductArgs p = {};
@@ -695,7 +865,7 @@ hipError_t bwd(const GatedArgs& g, hipStream_t s) {
   p.k = g.m;
   p.segments = 1;
   p.splits = dw_splits(g.m, g.n, g.k);
-  p.k_each = ((g.m + p.splits - 1) / p.splits + kSplitStep - 1) / kSplitStep * kSplitStep;
+  p.k_each = split_each(g.m, p.splits);
   p.half = n8;
   p.c = g.dwg;
   p.ldc = g.lddwg;
@@ -705,12 +875,7 @@ hipError_t bwd(const GatedArgs& g, hipStream_t s) {
   // rows n .. n8 - 1 of either half are padding of a width that is no multiple of 8
   p.pad_from = g.n;
   e = product<T, float, PL == 3 ? 3 : 2, PL, ORDER_CROSS, ORDER_CROSS, OUT_DW>(p, s);
-  if (e != hipSuccess) return e;
-  if (p.splits > 1) {
-    const int64_t n4 = g.k / 4;
-    sum_splits_kernel<<<static_cast<uint32_t>((p.m * n4 + 255) / 256), 256, 0, s>>>(p, n4);
-    e = hipGetLastError();
-  }
+  if (e == hipSuccess && p.splits > 1) e = sum_splits<float>(p, s);
   return e;
 }
 
@@ -722,6 +887,7 @@ size_t gated_workspace(int32_t type, int64_t m, int64_t n, int64_t k, bool backw
 }
 
 hipError_t launch_gated_fwd(const GatedArgs& g, hipStream_t s) {
+  if (few_rows(g.m, g.n)) return g.type == QHA_F32 ? fwd_few<float>(g, s) : g.type == QHA_BF16 ? fwd_few<__bf16>(g, s) : fwd_few<_Float16>(g, s);
   if (g.type == QHA_F32) return fwd32(g, s);
   return g.type == QHA_BF16 ? fwd16<__bf16>(g, s) : fwd16<_Float16>(g, s);
 }

@@ -131,6 +131,31 @@ def test_many_rows(dtype):
     _check_backward(20011, 128, 64, dtype, "relu")
 
 
+@pytest.mark.parametrize("shape,dtype", [((8200, 2056, 72), "bfloat16"), ((8200, 2056, 72), "float16"),
+                                         ((33000, 136, 40), "float32"), ((66000, 8, 24), "float32"),
+                                         ((17000, 264, 136), "bfloat16"), ((17000, 136, 260), "float32")],
+                         ids=lambda v: "x".join(map(str, v)) if isinstance(v, tuple) else v)
+def test_large_tiles(shape, dtype):
+    """Enough tiles for the wider tile shapes, each with ragged last rows, columns and steps."""
+    H.require_gpu()
+    H.note(f"gated large tiles {shape} {dtype}")
+    if shape[1] % 8 == 0 or dtype == "float32":
+        _check_forward(*shape, dtype, "silu")
+        _check_backward(*shape, dtype, "silu")
+
+
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
+@pytest.mark.parametrize("shape", [(1, 72, 4104), (15, 1000, 520), (32, 24, 264), (48, 520, 1032), (65, 136, 512), (128, 2048, 64)],
+                         ids=lambda s: "x".join(map(str, s)))
+def test_few_rows(shape, dtype):
+    """The kernel for few rows over its row counts, with reductions longer and shorter than a block's turn, and
+    split gradients."""
+    H.require_gpu()
+    H.note(f"gated few rows {shape} {dtype}")
+    _check_forward(*shape, dtype, "silu")
+    _check_backward(*shape, dtype, "gelu")
+
+
 @pytest.mark.parametrize("dtype", ["float32", "float16"])
 def test_strided_operands(dtype):
     """Every array a column slice of a wider buffer: the same bits, and nothing written beside them."""

@@ -138,7 +138,7 @@ def _gated_bwd(m=10, n=64, k=32, t=B.F32, dh=FAKE, lddh=64, gate=FAKE, ldg=64, u
 GATED = [dict(m=-1), dict(n=-8), dict(k=-8), dict(n=62), dict(k=30), dict(k=36, t=B.BF16, lda=40, ldwg=40, ldwu=40),
          dict(n=1 << 17), dict(t=5), dict(act=7), dict(a=None), dict(a=FAKE + 4), dict(lda=28), dict(lda=34), dict(wg=None),
          dict(ldwg=16), dict(wu=FAKE + 8), dict(ldwu=33), dict(ldg=60), dict(up=FAKE + 2), dict(ldu=0), dict(gate=None),
-         dict(up=None), dict(ws=FAKE + 8)]
+         dict(up=None), dict(m=1000, ws=FAKE + 8)]
 
 
 @pytest.mark.parametrize("bad", GATED + [dict(h=None), dict(ldh=63), dict(h=FAKE + 8), dict(k=0)])
@@ -158,7 +158,8 @@ def test_gated_backward_refuses(bad):
 def test_gated_limits_and_workspace():
     assert B.gated_project_workspace(torch.bfloat16, 1000, 64, 32) == 0
     assert B.gated_project_workspace(torch.float32, 1000, 64, 32) > 0
-    assert _gated_fwd(ws=None, wsb=0) == B.QHA_ERR_WORKSPACE
+    assert B.gated_project_workspace(torch.float32, 10, 64, 32) == 0        # few rows need none
+    assert _gated_fwd(m=1000, ws=None, wsb=0) == B.QHA_ERR_WORKSPACE
     assert _gated_bwd(wsb=100) == B.QHA_ERR_WORKSPACE
     assert _gated_fwd(m=0, a=None, h=None, ws=None, wsb=0) == B.QHA_OK
     assert _gated_fwd(m=1 << 30, n=1 << 12, ldh=1 << 12, ldg=1 << 12, ldu=1 << 12) == B.QHA_ERR_UNSUPPORTED
