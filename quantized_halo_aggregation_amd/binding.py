@@ -559,6 +559,10 @@ def _flat(t, name, n=None, dtype=None):
 
 def _matrix(t, name, dtype, rows, cols):
     """(pointer, leading dimension) of a rows x cols matrix of dtype whose rows may be strided."""
+    if type(t) is torch.Tensor and t.dtype is dtype and t.is_cuda and t.shape == (rows, cols):
+        ld, one = t.stride()
+        if one == 1 and rows > 1:
+            return t.data_ptr(), ld
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch tensor")
     if t.dtype != dtype:
@@ -729,10 +733,8 @@ class AdamW:
         if n == 0:
             return
         dtype = grads[0].dtype
-        for i, g in enumerate(grads):
-            if g.dtype != dtype or g.numel() != self.sizes[i] or not g.is_cuda or not g.is_contiguous():
-                _flat(g, f"grads[{i}]", self.sizes[i], dtype)
-        self._table[:n, 2] = [g.data_ptr() for g in grads]
+        self._table[:n, 2] = [g.data_ptr() if g.dtype is dtype and g.numel() == size and g.is_cuda and g.is_contiguous()
+                              else _flat(g, "a gradient", size, dtype) for g, size in zip(grads, self.sizes)]
         status = _adamw_step(self._table_ptr, n, self.bits, _type(dtype, "grads"), self._copy_type, lr, *self.betas,
                              self.eps, self.weight_decay, grad_scale, self.t + 1, _stream(stream))
         _check(status, "qha_adamw_step")

@@ -12,7 +12,8 @@
 // Mapping: a block of 256 threads takes chunks of 1024 consecutive elements, four per thread (16-byte
 // accesses), so that one wavefront holds exactly one 256-element code block and finds its largest
 // magnitude with wavefront reductions.  The tensors' pointers travel in the kernel arguments (48
-// tensors in one launch, nothing copied to the device), and a block finds its tensor by bisection.
+// tensors in one launch, nothing copied to the device), and a block finds its tensor by comparing their
+// first blocks in one step.
 #include "qha_internal.hpp"
 
 #include "../../include/qha.h"
@@ -65,10 +66,21 @@ __device__ __forceinline__ void store_copy(void* c, int32_t type, int64_t i, int
   else store4<f32x4, float>(c, i, n, vec, p);
 }
 
-__device__ __forceinline__ float wave_max(float x) {
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) x = fmaxf(x, __shfl_xor(x, o, 64));
-  return x;
+template <int CTRL, int ROWS>
+__device__ __forceinline__ uint32_t max_across(uint32_t x) {
+  const uint32_t y = static_cast<uint32_t>(__builtin_amdgcn_update_dpp(static_cast<int>(x), static_cast<int>(x), CTRL, ROWS, 0xf, false));
+  return x > y ? x : y;
+}
+
+// The wavefront's largest x, by exchanges within rows of 16 lanes and broadcasts between them.
+__device__ __forceinline__ uint32_t wave_max(uint32_t x) {
+  x = max_across<0xB1, 0xf>(x);         // lane ^ 1
+  x = max_across<0x4E, 0xf>(x);         // lane ^ 2
+  x = max_across<0x141, 0xf>(x);        // mirrored in 8
+  x = max_across<0x140, 0xf>(x);        // mirrored in 16
+  x = max_across<0x142, 0xa>(x);        // rows 1 and 3 take the row before
+  x = max_across<0x143, 0xc>(x);        // the upper half takes lane 31
+  return __builtin_amdgcn_readlane(x, 63);
 }
 
 __device__ __forceinline__ double lane_double(double x, int lane) {
@@ -78,57 +90,77 @@ __device__ __forceinline__ double lane_double(double x, int lane) {
   return __builtin_bit_cast(double, static_cast<uint64_t>(hi) << 32 | lo);
 }
 
-// The wavefront's largest of the non-negative finite x: the largest float32 rounding narrows the
-// lanes that can hold it, almost always to one.
-__device__ __forceinline__ double wave_max_double(double x, float* rounded) {
-  const float f = static_cast<float>(x);
-  const float top = wave_max(f);
-  *rounded = top;
-  uint64_t who = __ballot(f == top);
-  double best = 0.0;
-  while (who) {
-    best = fmax(best, lane_double(x, __builtin_ctzll(who)));
-    who &= who - 1;
+// The largest of the wavefront's four-element shares of |x|, whose float32 roundings are m: as float32
+// (*rounded), and as the float64 value.  Float32 magnitudes order as their bits do, with infinities
+// and NaN on top (*rounded then is not finite and the result unused); the lanes whose largest rounds to
+// the wavefront's, almost always one, hold the float64 value.
+__device__ __forceinline__ double wave_largest(const double (&x)[4], f32x4 m, float* rounded) {
+  uint32_t own = 0;
+  double wide = 0.0;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const uint32_t b = __float_as_uint(m[j]) & 0x7FFFFFFFu;
+    own = own > b ? own : b;
+    wide = fmax(wide, fabs(x[j]));
   }
-  return best;
+  const uint32_t top = wave_max(own);
+  *rounded = __uint_as_float(top);
+  const uint64_t who = __ballot(own == top);
+  if ((who & (who - 1)) == 0 || top == 0) return lane_double(wide, __builtin_ctzll(who));
+  wide = own == top ? wide : 0.0;
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) wide = fmax(wide, __shfl_xor(wide, o, 64));
+  return wide;
 }
 
-// Nearest code of ratio = |x| / largest in [0, 1]: TOP ratio^(1/POWER), rounded.  The root is taken
-// in float32 (off by less than 1e-4 codes); within 2e-4 of a half-way point the decision is made in
-// float64 on ratio itself, whose half-way points are ((c + 1/2) / TOP)^POWER.  16-bit gradients put
-// ratios exactly on some of those (1/4 is code 63 1/2 of 127), where the last bit of ratio would
+// Nearest codes of |x| inv (inv = 1 / largest): TOP (|x| inv)^(1/POWER), rounded.  The root is taken in
+// float32 (off by less than 7e-5 codes); where any of the four is within 1e-4 of a half-way point all are
+// decided in float64 on the ratios, whose half-way points are ((c + 1/2) / TOP)^POWER.  16-bit gradients put
+// ratios exactly on some of those (1/4 is code 63 1/2 of 127), where the last bit of the ratio would
 // decide: a ratio has to be over the point by 2^-40 of it to go up.
 template <int TOP, int POWER>
-__device__ __forceinline__ int nearest_code(double ratio) {
-  float r = __builtin_amdgcn_sqrtf(static_cast<float>(ratio));
-  if (POWER == 4) r = __builtin_amdgcn_sqrtf(r);
-  const float t = r * TOP;
-  const float base = floorf(t);
-  bool up = t - base >= 0.5f;
-  if (fabsf(t - base - 0.5f) < 2e-4f) {
-    double e = (static_cast<double>(base) + 0.5) * (1.0 / TOP);
-    e *= e;
-    if (POWER == 4) e *= e;
-    up = ratio > e * (1.0 + 0x1p-40);
+__device__ __forceinline__ void nearest_codes(const double (&x)[4], double inv, int (&code)[4]) {
+  float t[4];
+  bool near = false;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    float r = __builtin_amdgcn_sqrtf(static_cast<float>(fabs(x[j]) * inv));
+    if (POWER == 4) r = __builtin_amdgcn_sqrtf(r);
+    t[j] = r * TOP;
+    const float up = rintf(t[j]);
+    code[j] = static_cast<int>(up);
+    near = near || fabsf(t[j] - up) > 0.4999f;
   }
-  return min(static_cast<int>(base) + (up ? 1 : 0), TOP);
+  if (near) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const double base = floor(static_cast<double>(t[j]));
+      double e = (base + 0.5) * (1.0 / TOP);
+      e *= e;
+      if (POWER == 4) e *= e;
+      // away from a half-way point this is the rounding above
+      const bool up = fabs(x[j]) * inv > e * (1.0 + 0x1p-40);
+      code[j] = min(static_cast<int>(base) + (up ? 1 : 0), TOP);
+    }
+  }
 }
 
 __device__ __forceinline__ f32x4 new_params(const AdamArgs& a, f32x4 p, f32x4 m, f32x4 v) {
   f32x4 r;
+  // the reciprocal is the transcendental unit's, off by at most one step
 #pragma unroll
-  for (int j = 0; j < 4; ++j) r[j] = p[j] * a.decay - a.step_size * (m[j] / (sqrtf(v[j]) * a.root_c2 + a.eps));
+  for (int j = 0; j < 4; ++j)
+    r[j] = p[j] * a.decay - a.step_size * (m[j] * __builtin_amdgcn_rcpf(sqrtf(v[j]) * a.root_c2 + a.eps));
   return r;
 }
 
 template <int BITS>
 __global__ __launch_bounds__(256) void adamw_kernel(AdamArgs a) {
-  int lo = 0, hi = a.n_tensors - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (blockIdx.x >= a.first[mid]) lo = mid;
-    else hi = mid - 1;
-  }
+  // the tensor whose chunks include this block: the last one that starts at or before it (at most 48
+  // tensors, compared by one lane each: the kernel's arguments are read over a slow path, so in one go)
+  const int ln = threadIdx.x & 63;
+  const uint32_t start = ln < a.n_tensors ? a.first[ln] : 0xFFFFFFFFu;
+  const int lo = __builtin_amdgcn_readfirstlane(__popcll(__ballot(start <= blockIdx.x)) - 1);
   const AdamTensor t = a.t[lo];
   const uintptr_t wide = reinterpret_cast<uintptr_t>(t.p) | (BITS == 32 ? reinterpret_cast<uintptr_t>(t.m) | reinterpret_cast<uintptr_t>(t.v) : 0) |
                          (a.grad_type == QHA_F32 ? reinterpret_cast<uintptr_t>(t.g) : 0) | (a.copy_type == QHA_F32 ? reinterpret_cast<uintptr_t>(t.copy) : 0);
@@ -160,43 +192,36 @@ __global__ __launch_bounds__(256) void adamw_kernel(AdamArgs a) {
       const u8x4 cv = load4<u8x4, uint8_t>(t.v, i, t.n, vec);
       const double sm = static_cast<double>(t.ms[blk]) * (a.beta1 / (127.0 * 127.0));
       const double sv = static_cast<double>(t.vs[blk]) * (a.beta2 / (255.0 * 255.0 * 255.0 * 255.0));
-      double xm[4], xv[4], am = 0.0, av = 0.0;
-      bool fm = true, fv = true;
+      double xm[4], xv[4];
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const int c = cm[j];
         const uint32_t u = static_cast<uint32_t>(cv[j]) * cv[j];
         const double gd = static_cast<double>(g[j]);
-        xm[j] = sm * static_cast<double>(c * (c < 0 ? -c : c)) + gd * (1.0 - a.beta1);
-        xv[j] = sv * static_cast<double>(u * u) + (gd * gd) * (1.0 - a.beta2);
+        xm[j] = __builtin_fma(gd, 1.0 - a.beta1, sm * static_cast<double>(c * (c < 0 ? -c : c)));
+        xv[j] = __builtin_fma(gd * gd, 1.0 - a.beta2, sv * static_cast<double>(u * u));
         m[j] = static_cast<float>(xm[j]);
         v[j] = static_cast<float>(xv[j]);
-        fm = fm && __builtin_isfinite(m[j]);
-        fv = fv && __builtin_isfinite(v[j]);
-        am = fmax(am, fabs(xm[j]));
-        av = fmax(av, xv[j]);
       }
-      const bool ok_m = __all(fm), ok_v = __all(fv);
-      float sm32 = __builtin_nanf(""), sv32 = __builtin_nanf("");
+      float sm32, sv32;
       i8x4 nm = {};
       u8x4 nv = {};
-      if (ok_m) {
-        const double top = wave_max_double(am, &sm32);
-        const double inv = sm32 > 0.0f ? 1.0 / top : 0.0;
+      int code[4];
+      const double top_m = wave_largest(xm, m, &sm32);
+      if (__builtin_isfinite(sm32)) {
+        nearest_codes<127, 2>(xm, sm32 > 0.0f ? 1.0 / top_m : 0.0, code);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int c = nearest_code<127, 2>(fabs(xm[j]) * inv);
-          nm[j] = static_cast<int8_t>(xm[j] < 0.0 ? -c : c);
-        }
+        for (int j = 0; j < 4; ++j) nm[j] = static_cast<int8_t>(xm[j] < 0.0 ? -code[j] : code[j]);
+      } else {
+        sm32 = __builtin_nanf("");
       }
-      if (ok_v) {
-        const double top = wave_max_double(av, &sv32);
-        const double inv = sv32 > 0.0f ? 1.0 / top : 0.0;
+      const double top_v = wave_largest(xv, v, &sv32);
+      if (__builtin_isfinite(sv32)) {
+        nearest_codes<255, 4>(xv, sv32 > 0.0f ? 1.0 / top_v : 0.0, code);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int c = nearest_code<255, 4>(xv[j] * inv);
-          nv[j] = static_cast<uint8_t>(xv[j] > 0.0 ? max(c, 1) : 0);
-        }
+        for (int j = 0; j < 4; ++j) nv[j] = static_cast<uint8_t>(xv[j] > 0.0 ? max(code[j], 1) : 0);
+      } else {
+        sv32 = __builtin_nanf("");
       }
       store4<i8x4, int8_t>(t.m, i, t.n, vec, nm);
       store4<u8x4, uint8_t>(t.v, i, t.n, vec, nv);

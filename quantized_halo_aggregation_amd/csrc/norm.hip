@@ -167,26 +167,36 @@ __global__ __launch_bounds__(NT) void norm_sums_kernel(NormArgs a) {
   }
 }
 
-// Adds the sample's chunk pairs per group, in a fixed order, and hands each to `put`.
+// Adds the sample's chunk pairs per group, in a fixed order, and hands each to `put`.  Neighbouring threads
+// read neighbouring groups of one chunk; the threads of a group then meet in LDS.
 template <typename F>
-__device__ __forceinline__ void combine_chunks(const NormArgs& a, int64_t sample, const F& put) {
-  const int chunks = static_cast<int>(a.chunks);
-  const int ts = team_size(chunks);
-  const int team = threadIdx.x / ts, ln = threadIdx.x % ts, teams = NT / ts;
-  for (int g0 = 0; g0 < a.groups; g0 += teams) {
-    const int g = g0 + team;
-    double s = 0.0, q = 0.0;
-    if (g < a.groups)
-      for (int k = ln; k < chunks; k += ts) {
-        const double* p = a.group_part + ((sample * chunks + k) * a.groups + g) * 2;
-        s += p[0];
-        q += p[1];
+__device__ __forceinline__ void combine_chunks(const NormArgs& a, int64_t sample, double2* buf, const F& put) {
+  const int groups = a.groups;
+  const double2* part = reinterpret_cast<const double2*>(a.group_part) + sample * a.chunks * groups;
+  const int lanes = groups < NT ? NT / groups : 1;
+  for (int g0 = 0; g0 < groups; g0 += NT) {
+    const int lane = groups < NT ? static_cast<int>(threadIdx.x) / groups : 0;
+    const int g = groups < NT ? static_cast<int>(threadIdx.x) % groups : g0 + static_cast<int>(threadIdx.x);
+    double2 s = {0.0, 0.0};
+    if (lane < lanes && g < groups) {
+#pragma unroll 4
+      for (int64_t k = lane; k < a.chunks; k += lanes) {
+        const double2 p = part[k * groups + g];
+        s.x += p.x;
+        s.y += p.y;
       }
-    for (int o = ts >> 1; o > 0; o >>= 1) {
-      s += shfl_xor_d(s, o);
-      q += shfl_xor_d(q, o);
     }
-    if (g < a.groups && ln == 0) put(g, s, q);
+    if (lanes > 1) {
+      __syncthreads();
+      buf[threadIdx.x] = s;
+      __syncthreads();
+      if (lane == 0)
+        for (int k = 1; k < lanes; ++k) {
+          s.x += buf[k * groups + g].x;
+          s.y += buf[k * groups + g].y;
+        }
+    }
+    if (lane == 0 && g < groups) put(g, s.x, s.y);
   }
 }
 
@@ -194,6 +204,7 @@ template <typename T, int R, bool VG>
 __global__ __launch_bounds__(NT) void norm_apply_kernel(NormArgs a) {
   constexpr int V = Pack<T>::N;
   extern __shared__ float2 stat[];           // mean, rstd per group
+  __shared__ double2 buf[NT];
   const Place<R> at(a.c / V);
   const int per = a.c / a.groups;
   const double inv = 1.0 / (static_cast<double>(a.positions) * per);
@@ -201,7 +212,7 @@ __global__ __launch_bounds__(NT) void norm_apply_kernel(NormArgs a) {
     const Item it(a, item);
     const bool first = item % a.chunks == 0;
     __syncthreads();                           // the last item's statistics have been used
-    combine_chunks(a, it.sample, [&](int g, double s, double q) {
+    combine_chunks(a, it.sample, buf, [&](int g, double s, double q) {
       const double mean = s * inv, var = q * inv - mean * mean;
       const double rstd = 1.0 / sqrt((var < 0.0 ? 0.0 : var) + a.eps);
       stat[g] = make_float2(static_cast<float>(mean), static_cast<float>(rstd));
@@ -239,7 +250,7 @@ __global__ __launch_bounds__(NT) void norm_apply_kernel(NormArgs a) {
 template <typename T, int R, bool VG>
 __global__ __launch_bounds__(NT) void norm_grad_sums_kernel(NormArgs a) {
   constexpr int V = Pack<T>::N;
-  __shared__ double2 buf[NT * R];
+  __shared__ double2 buf[R == 1 ? NT * V / 2 : NT * R];
   const Place<R> at(a.c / V);
   const int per = a.c / a.groups;
   const int64_t items = a.samples * a.chunks;
@@ -296,22 +307,43 @@ __global__ __launch_bounds__(NT) void norm_grad_sums_kernel(NormArgs a) {
   }
   if (!a.dw) return;
   float* out = a.chan_part + static_cast<int64_t>(blockIdx.x) * 2 * a.c;
-#pragma unroll
-  for (int v = 0; v < V; ++v) {
-    __syncthreads();
+  if constexpr (R > 1) {                     // a thread has its channels to itself
 #pragma unroll
     for (int r = 0; r < R; ++r)
-      if (at.has(r)) buf[at.slot(r)] = make_double2(static_cast<double>(dw[r][v]), static_cast<double>(db[r][v]));
+      if (at.has(r))
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+          out[at.vec(r) * V + v] = dw[r][v];
+          out[a.c + at.vec(r) * V + v] = db[r][v];
+        }
+  } else {
+    // [rows_par][c] pairs, then neighbouring lanes share a channel
+    float2* pair = reinterpret_cast<float2*>(buf);
     __syncthreads();
-    for (int j = threadIdx.x; j < at.nvec; j += NT) {
+    if (at.active)
+#pragma unroll
+      for (int v = 0; v < V; ++v) pair[at.rl * a.c + at.tx * V + v] = make_float2(dw[0][v], db[0][v]);
+    __syncthreads();
+    int lanes = 1;
+    while (lanes < 64 && 2 * lanes * a.c <= NT) lanes *= 2;
+    const int ln = threadIdx.x % lanes;
+    for (int c0 = 0; c0 < a.c; c0 += NT / lanes) {
+      const int ch = c0 + threadIdx.x / lanes;
       double s = 0.0, q = 0.0;
-      for (int k = 0; k < at.rows_par; ++k) {
-        const double2 p = buf[k * at.nvec + j];
-        s += p.x;
-        q += p.y;
+      if (ch < a.c)
+#pragma unroll 4
+        for (int k = ln; k < at.rows_par; k += lanes) {
+          s += static_cast<double>(pair[k * a.c + ch].x);
+          q += static_cast<double>(pair[k * a.c + ch].y);
+        }
+      for (int o = lanes >> 1; o > 0; o >>= 1) {
+        s += shfl_xor_d(s, o);
+        q += shfl_xor_d(q, o);
       }
-      out[j * V + v] = static_cast<float>(s);
-      out[a.c + j * V + v] = static_cast<float>(q);
+      if (ln == 0 && ch < a.c) {
+        out[ch] = static_cast<float>(s);
+        out[a.c + ch] = static_cast<float>(q);
+      }
     }
   }
 }
@@ -338,9 +370,9 @@ template <typename T, int R, bool VG>
 __global__ __launch_bounds__(NT) void norm_grad_apply_kernel(NormArgs a, int32_t sum_cols) {
   constexpr int V = Pack<T>::N;
   extern __shared__ float2 stat[];           // mean of q, mean of q xhat per group
-  __shared__ double buf[NT];
+  __shared__ double2 pairs[NT];
   if (static_cast<int32_t>(blockIdx.x) < sum_cols) {
-    sum_channels(a, static_cast<int>(blockIdx.x), buf);
+    sum_channels(a, static_cast<int>(blockIdx.x), reinterpret_cast<double*>(pairs));
     return;
   }
   const Place<R> at(a.c / V);
@@ -350,7 +382,7 @@ __global__ __launch_bounds__(NT) void norm_grad_apply_kernel(NormArgs a, int32_t
   for (int64_t item = static_cast<int64_t>(blockIdx.x) - sum_cols; item < a.samples * a.chunks; item += step) {
     const Item it(a, item);
     __syncthreads();                           // the last item's means have been used
-    combine_chunks(a, it.sample, [&](int g, double s, double q) {
+    combine_chunks(a, it.sample, pairs, [&](int g, double s, double q) {
       stat[g] = make_float2(static_cast<float>(s * inv), static_cast<float>(q * inv));
     });
     __syncthreads();
@@ -430,7 +462,9 @@ hipError_t launch(const NormArgs& a, bool backward, hipStream_t s) {
   return hipGetLastError();
 }
 
-constexpr int64_t kNormItems = 2048;     // eight blocks for each compute unit
+// Four blocks for each compute unit: with eight, the second launch of 16 x 4096 x 512 bf16 spends more on
+// adding twice the chunks' pairs than it gains (57 against 39 us), with two it waits on memory (41 us).
+constexpr int64_t kNormItems = 1024;
 
 }  // namespace
 
