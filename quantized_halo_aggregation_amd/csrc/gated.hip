@@ -60,15 +60,15 @@ __device__ __forceinline__ f32x4 mma16<_Float16>(s16x8 a, s16x8 b, f32x4 c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
 }
 
-// An operand of a product: 16-bit values in rows of ld, in `planes` copies `plane` elements apart (the
-// parts of float32 values).
+// An operand of a product: rows of ld values, 16-bit ones in one or more planes `plane` values apart (the parts of
+// float32 values), or float32 ones that are split on their way out of LDS.
 struct Operand {
   const uint16_t* p0;
   const uint16_t* p1;  // the second matrix of pairs, or of the reduction's second segment
   int64_t ld, ld1;     // of p0 and p1
   int64_t plane;
   int64_t rows;        // stored rows
-  int64_t cols;        // stored columns (a multiple of 8)
+  int64_t cols;        // stored columns (a multiple of 16 bytes)
 };
 
 enum { ORDER_ROWS = 0, ORDER_PAIRS = 1, ORDER_CROSS = 2 };
@@ -76,13 +76,17 @@ enum { ORDER_ROWS = 0, ORDER_PAIRS = 1, ORDER_CROSS = 2 };
 // ORDER_PAIRS: the same, tile rows alternate between p0 and p1 by 32 (p0 and p1 hold `rows` rows each)
 // ORDER_CROSS: stored across the reduction; tile rows are steps of the reduction, stored columns c0 + c
 
-// Places of 16-byte chunks in a tile's LDS image.  Along the reduction: rows of BK values.  Across it:
-// BK rows of WIDTH values.  The permutation is its own inverse.
-template <int BK>
+// Places of 16-byte chunks in a tile's LDS image, PER chunks a row.  Along the reduction, the rows that a read
+// takes together fall on different banks.  Across it, a transposing read (16-bit) takes four rows at a
+// time, and the reads of float32 columns take two rows eight apart.  The permutations are their own inverses.
+template <int PER>
 __device__ __forceinline__ int permute_along(int row, int chunk) {
-  return BK == 64 ? chunk ^ (row & 7) : chunk ^ ((row >> 1) & 3);
+  return PER == 8 ? chunk ^ (row & 7) : chunk ^ ((row >> 1) & 3);
 }
-__device__ __forceinline__ int permute_cross(int k, int chunk) { return chunk ^ (((k & 3) << 1) | ((k & 4) << 1)); }
+template <bool RAW>
+__device__ __forceinline__ int permute_cross(int k, int chunk) {
+  return RAW ? chunk ^ (k & 8) : chunk ^ (((k & 3) << 1) | ((k & 4) << 1));
+}
 
 // Waits for this wavefront's loads into LDS; a barrier after it makes them visible to the block.
 __device__ __forceinline__ void loads_done() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
@@ -99,10 +103,12 @@ __device__ __forceinline__ uint32_t lds_address(const uint16_t* p) {
   return static_cast<uint32_t>(reinterpret_cast<uintptr_t>((const __attribute__((address_space(3))) uint16_t*)p));
 }
 
-// A thread's share of a tile of ROWS x COLS values (as stored): its N 16-byte chunks, one per NT.
-template <int ORDER, int ROWS, int COLS, int NT>
+// A thread's share of a tile of ROWS x COLS values (as stored): its N 16-byte chunks, one per NT.  RAW: float32.
+template <int ORDER, int ROWS, int COLS, int NT, bool RAW>
 struct Stager {
-  static constexpr int PER = COLS / 8;
+  static constexpr int W = RAW ? 4 : 8;            // values in a chunk
+  static constexpr int HALVES = RAW ? 2 : 1;       // 16-bit halves of a value
+  static constexpr int PER = COLS / W;
   static constexpr int N = ROWS * PER / NT;
   static_assert(ROWS * PER % NT == 0, "whole chunks per thread");
   const uint16_t* at[N];
@@ -110,17 +116,18 @@ struct Stager {
   static __device__ __forceinline__ int row(int i) { return (i * NT + static_cast<int>(threadIdx.x)) / PER; }
   static __device__ __forceinline__ int chunk(int i) {
     const int q = (i * NT + static_cast<int>(threadIdx.x)) % PER;
-    return ORDER == ORDER_CROSS ? permute_cross(row(i), q) : permute_along<COLS>(row(i), q);
+    return ORDER == ORDER_CROSS ? permute_cross<RAW>(row(i), q) : permute_along<PER>(row(i), q);
   }
-  // base: the operand at the reduction's step k0; first: the tile's first stored row (along) or column
-  // (across).  Rows and columns past the end repeat the last ones; their results are not stored.
+  // base: the operand's (or segment's) matrix; k0: first step of the reduction; first: the tile's first stored
+  // row (along) or column (across).  Rows and columns past the end repeat the last ones; their results
+  // are not stored.
   __device__ __forceinline__ void start(const Operand& o, const uint16_t* base, int64_t ld, int64_t first, int64_t k0) {
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       if (ORDER == ORDER_CROSS) {
-        int64_t c = first + chunk(i) * 8;
-        c = c < o.cols ? c : o.cols - 8;
-        at[i] = base + (k0 + row(i)) * ld + c;
+        int64_t c = first + chunk(i) * W;
+        c = c < o.cols ? c : o.cols - W;
+        at[i] = base + ((k0 + row(i)) * ld + c) * HALVES;
       } else {
         int64_t r;
         const uint16_t* p = base;
@@ -137,7 +144,7 @@ struct Stager {
           r = first + row(i);
         }
         r = r < o.rows ? r : o.rows - 1;
-        at[i] = p + r * ld + k0 + chunk(i) * 8;
+        at[i] = p + (r * ld + k0 + chunk(i) * W) * HALVES;
       }
     }
   }
@@ -148,14 +155,14 @@ struct Stager {
   }
   __device__ __forceinline__ void next(int64_t ld) {
 #pragma unroll
-    for (int i = 0; i < N; ++i) at[i] += ORDER == ORDER_CROSS ? ROWS * ld : COLS;
+    for (int i = 0; i < N; ++i) at[i] += (ORDER == ORDER_CROSS ? ROWS * ld : COLS) * HALVES;
   }
   // The last, partial step: `left` steps of the reduction remain, the others become zero.
   __device__ __forceinline__ void load_partial(int64_t plane, int64_t left, uint16_t* lds) const {
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       u32x4 v = {0, 0, 0, 0};
-      if ((ORDER == ORDER_CROSS ? row(i) : chunk(i) * 8) < left) v = *reinterpret_cast<const u32x4*>(at[i] + plane);
+      if ((ORDER == ORDER_CROSS ? row(i) : chunk(i) * W) < left) v = *reinterpret_cast<const u32x4*>(at[i] + plane);
       *reinterpret_cast<u32x4*>(lds + (i * NT + threadIdx.x) * 8) = v;
     }
   }
@@ -172,15 +179,55 @@ __device__ __forceinline__ s16x8 fragment(const uint16_t* lds, int at, int ks, i
     const int col = at + ((lane >> 4) & 1) * 16 + 4 * (j & 3);
     const int k = ks + (lane >> 5) * 8 + (j >> 2);
     const int off = (col & 7);
-    const uint16_t* lo = lds + k * COLS + permute_cross(k, col >> 3) * 8 + off;
-    const uint16_t* hi = lds + (k + 4) * COLS + permute_cross(k + 4, col >> 3) * 8 + off;
+    const uint16_t* lo = lds + k * COLS + permute_cross<false>(k, col >> 3) * 8 + off;
+    const uint16_t* hi = lds + (k + 4) * COLS + permute_cross<false>(k + 4, col >> 3) * 8 + off;
     const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)lo);
     const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)hi);
     return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
   }
   const int row = at + (lane & 31);
-  const int c = permute_along<COLS>(row, (ks >> 3) + (lane >> 5));
+  const int c = permute_along<COLS / 8>(row, (ks >> 3) + (lane >> 5));
   return *reinterpret_cast<const s16x8*>(lds + row * COLS + c * 8);
+}
+
+// x = hi + mid + lo exactly: each part is rounded to nearest even, the remainders are exact in float32.
+__device__ __forceinline__ void split3(f32x4 x, bf16x4& h, bf16x4& m, bf16x4& l) {
+  h = __builtin_convertvector(x, bf16x4);
+  const f32x4 r = x - __builtin_convertvector(h, f32x4);
+  m = __builtin_convertvector(r, bf16x4);
+  l = __builtin_convertvector(r - __builtin_convertvector(m, f32x4), bf16x4);
+}
+
+__device__ __forceinline__ void split8(f32x4 a, f32x4 b, s16x8 (&part)[3]) {
+  bf16x4 h[2], m[2], l[2];
+  split3(a, h[0], m[0], l[0]);
+  split3(b, h[1], m[1], l[1]);
+  part[0] = __builtin_bit_cast(s16x8, __builtin_shufflevector(h[0], h[1], 0, 1, 2, 3, 4, 5, 6, 7));
+  part[1] = __builtin_bit_cast(s16x8, __builtin_shufflevector(m[0], m[1], 0, 1, 2, 3, 4, 5, 6, 7));
+  part[2] = __builtin_bit_cast(s16x8, __builtin_shufflevector(l[0], l[1], 0, 1, 2, 3, 4, 5, 6, 7));
+}
+
+// The same of a float32 tile: the three parts of its values.
+template <int ORDER, int COLS>
+__device__ __forceinline__ void fragment_raw(const uint16_t* lds, int at, int ks, int lane, s16x8 (&part)[3]) {
+  const float* x = reinterpret_cast<const float*>(lds);
+  f32x4 a, b;
+  if (ORDER == ORDER_CROSS) {
+    const int col = at + (lane & 31);
+    const int k = ks + (lane >> 5) * 8;              // bit 3 of k .. k + 7 is that of k
+    const float* p = x + k * COLS + permute_cross<true>(k, col >> 2) * 4 + (col & 3);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      a[e] = p[e * COLS];
+      b[e] = p[(e + 4) * COLS];
+    }
+  } else {
+    const int row = at + (lane & 31);
+    const int c = (ks >> 2) + (lane >> 5) * 2;
+    a = *reinterpret_cast<const f32x4*>(x + row * COLS + permute_along<COLS / 4>(row, c) * 4);
+    b = *reinterpret_cast<const f32x4*>(x + row * COLS + permute_along<COLS / 4>(row, c + 1) * 4);
+  }
+  split8(a, b, part);
 }
 
 struct ProductArgs {
@@ -196,12 +243,11 @@ struct ProductArgs {
   void* up;
   int64_t ldh, ldg, ldu;
   int32_t act;
-  // dA: c; dW: c, with rows from `half` on in c1, or the split's partial
+  // dA: c (half = m); dW: c, with rows from `half` on in c1; or the split's partial
   void* c;
   float* c1;
   int64_t ldc, ldc1;
   int64_t half;
-  int64_t pad_from;         // dW: rows from here to `half` of either half are padding (dA: half and pad_from are m)
   float* partial;           // [splits][m][n] when splits > 1
 };
 
@@ -271,14 +317,15 @@ __device__ __forceinline__ bool tile_of(const ProductArgs& p, int64_t b, int64_t
 }
 
 // T: 16-bit type of the planes; O: type of the stored result; PA, PB: parts of A's and B's values (1 and 1,
-// 2 and 1, or 3 and 3).
+// 2 and 1, or 3 and 3); RA, RB: they are split from float32 values in LDS (else stored as planes).
 // BM x BN tile of C (forward: BN counts the rows of Wg and Wu together), wavefronts of WM x WN.
-template <typename T, typename O, int PA, int PB, int OA, int OB, int OUT, int BM, int BN, int BK, int WM, int WN>
+template <typename T, typename O, int PA, int PB, bool RA, bool RB, int OA, int OB, int OUT, int BM, int BN, int BK, int WM, int WN>
 __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) void product_kernel(ProductArgs p) {
   constexpr int NT = (BM / WM) * (BN / WN) * 64;
   constexpr int A_ROWS = OA == ORDER_CROSS ? BK : BM, A_COLS = OA == ORDER_CROSS ? BM : BK;
   constexpr int B_ROWS = OB == ORDER_CROSS ? BK : BN, B_COLS = OB == ORDER_CROSS ? BN : BK;
-  constexpr int A_SIZE = BM * BK, B_SIZE = BN * BK, BUF = PA * A_SIZE + PB * B_SIZE;
+  constexpr int LA = RA ? 1 : PA, LB = RB ? 1 : PB;                   // planes in LDS
+  constexpr int A_SIZE = BM * BK * (RA ? 2 : 1), B_SIZE = BN * BK * (RB ? 2 : 1), BUF = LA * A_SIZE + LB * B_SIZE;
   constexpr int MI = WM / 32, NI = WN / 32;
   __shared__ __attribute__((aligned(16))) uint16_t lds[2 * BUF];
 
@@ -301,17 +348,27 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) void product_kernel(Pro
       for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.0f;
 
   auto multiply = [&](const uint16_t* at) {
-    const uint16_t* bt = at + PA * A_SIZE;
+    const uint16_t* bt = at + LA * A_SIZE;
     s16x8 fa[2][MI][PA], fb[2][NI][PB];
     auto fetch = [&](int ks, int to) {
 #pragma unroll
-      for (int pl = 0; pl < PA; ++pl)
+      for (int i = 0; i < MI; ++i) {
+        if constexpr (RA) {
+          fragment_raw<OA, A_COLS>(at, wm * WM + i * 32, ks, lane, fa[to][i]);
+        } else {
 #pragma unroll
-        for (int i = 0; i < MI; ++i) fa[to][i][pl] = fragment<OA, A_COLS>(at + pl * A_SIZE, wm * WM + i * 32, ks, lane);
+          for (int pl = 0; pl < PA; ++pl) fa[to][i][pl] = fragment<OA, A_COLS>(at + pl * A_SIZE, wm * WM + i * 32, ks, lane);
+        }
+      }
 #pragma unroll
-      for (int pl = 0; pl < PB; ++pl)
+      for (int j = 0; j < NI; ++j) {
+        if constexpr (RB) {
+          fragment_raw<OB, B_COLS>(bt, wn * WN + j * 32, ks, lane, fb[to][j]);
+        } else {
 #pragma unroll
-        for (int j = 0; j < NI; ++j) fb[to][j][pl] = fragment<OB, B_COLS>(bt + pl * B_SIZE, wn * WN + j * 32, ks, lane);
+          for (int pl = 0; pl < PB; ++pl) fb[to][j][pl] = fragment<OB, B_COLS>(bt + pl * B_SIZE, wn * WN + j * 32, ks, lane);
+        }
+      }
     };
     fetch(0, 0);
 #pragma unroll
@@ -338,17 +395,17 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) void product_kernel(Pro
     }
   };
 
-  Stager<OA, A_ROWS, A_COLS, NT> sa;
-  Stager<OB, B_ROWS, B_COLS, NT> sb;
+  Stager<OA, A_ROWS, A_COLS, NT, RA> sa;
+  Stager<OB, B_ROWS, B_COLS, NT, RB> sb;
   for (int seg = 0; seg < p.segments; ++seg) {
     const int64_t ldb = seg ? p.b.ld1 : p.b.ld;
-    sa.start(p.a, p.a.p0 + (seg ? p.k : 0), p.a.ld, m0, kbeg);
+    sa.start(p.a, p.a.p0 + (seg ? p.k * (RA ? 2 : 1) : 0), p.a.ld, m0, kbeg);
     sb.start(p.b, seg ? p.b.p1 : p.b.p0, ldb, n0, kbeg);
     auto load = [&](uint16_t* to) {
 #pragma unroll
-      for (int pl = 0; pl < PA; ++pl) sa.load(pl * p.a.plane, to + pl * A_SIZE);
+      for (int pl = 0; pl < LA; ++pl) sa.load(pl * p.a.plane, to + pl * A_SIZE);
 #pragma unroll
-      for (int pl = 0; pl < PB; ++pl) sb.load(pl * p.b.plane, to + PA * A_SIZE + pl * B_SIZE);
+      for (int pl = 0; pl < LB; ++pl) sb.load(pl * p.b.plane, to + LA * A_SIZE + pl * B_SIZE);
       sa.next(p.a.ld);
       sb.next(ldb);
     };
@@ -365,9 +422,9 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) void product_kernel(Pro
     }
     if (left > 0) {
 #pragma unroll
-      for (int pl = 0; pl < PA; ++pl) sa.load_partial(pl * p.a.plane, left, lds + pl * A_SIZE);
+      for (int pl = 0; pl < LA; ++pl) sa.load_partial(pl * p.a.plane, left, lds + pl * A_SIZE);
 #pragma unroll
-      for (int pl = 0; pl < PB; ++pl) sb.load_partial(pl * p.b.plane, left, lds + PA * A_SIZE + pl * B_SIZE);
+      for (int pl = 0; pl < LB; ++pl) sb.load_partial(pl * p.b.plane, left, lds + LA * A_SIZE + pl * B_SIZE);
       __syncthreads();
       multiply(lds);
       __syncthreads();
@@ -415,9 +472,9 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) void product_kernel(Pro
       if (p.splits > 1) {
         out.flush(p.partial + sp * p.m * p.n, p.n, r0, p.m, col0, p.n);
       } else {
-        // rows of the first half, then of the second; what lies between is padding
-        out.flush(static_cast<float*>(p.c), p.ldc, r0, p.pad_from, col0, p.n);
-        out.flush(p.c1, p.ldc1, r0 - p.half, p.pad_from, col0, p.n);
+        // rows of dW_gate, then of dW_up
+        out.flush(static_cast<float*>(p.c), p.ldc, r0, p.half, col0, p.n);
+        out.flush(p.c1, p.ldc1, r0 - p.half, p.m - p.half, col0, p.n);
       }
     } else {
       RowWriter<O, CW> out(lds, wave, lane);
@@ -441,8 +498,6 @@ __global__ __launch_bounds__(256) void sum_splits_kernel(ProductArgs p, int64_t 
   const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
   if (i >= p.m * n4) return;
   const int64_t row = i / n4, col = i % n4 * 4;
-  const int64_t in = row < p.half ? row : row - p.half;
-  if (in >= p.pad_from) return;
   double s[4] = {0.0, 0.0, 0.0, 0.0};
 #pragma unroll 4
   for (int k = 0; k < p.splits; ++k) {
@@ -454,15 +509,7 @@ __global__ __launch_bounds__(256) void sum_splits_kernel(ProductArgs p, int64_t 
 #pragma unroll
   for (int e = 0; e < 4; ++e) r[e] = static_cast<float>(s[e]);
   if (row < p.half) store4<O>(static_cast<O*>(p.c) + row * p.ldc + col, r);
-  else store4<float>(p.c1 + in * p.ldc1 + col, r);
-}
-
-// x = hi + mid + lo exactly: each part is rounded to nearest even, the remainders are exact in float32.
-__device__ __forceinline__ void split3(f32x4 x, bf16x4& h, bf16x4& m, bf16x4& l) {
-  h = __builtin_convertvector(x, bf16x4);
-  const f32x4 r = x - __builtin_convertvector(h, f32x4);
-  m = __builtin_convertvector(r, bf16x4);
-  l = __builtin_convertvector(r - __builtin_convertvector(m, f32x4), bf16x4);
+  else store4<float>(p.c1 + (row - p.half) * p.ldc1 + col, r);
 }
 
 // Planes [3][rows_out][cols_out] of the parts of a float32 matrix, zero where it ends.
@@ -483,47 +530,34 @@ __global__ __launch_bounds__(256) void split_kernel(const float* x, int64_t ld, 
   }
 }
 
-// [dG dU] (each n_out columns wide, zero past n) as the products' operand: the float32 values in three bf16
-// parts, or for 16-bit T in two parts of T.  dA is stored in T and takes the first part alone (one rounding of each
-// term, as its own result has); dW is float32 and takes both, which leaves 2^-18 (bf16) of a term.
+// [dG dU], 2n columns wide, as the products' operand: float32 values, or for 16-bit T two parts of T in two
+// planes.  dA is stored in T and takes the first part alone (one rounding of each term, as its own result
+// has); dW is float32 and takes both, which leaves 2^-18 (bf16) of a term.
 template <typename T>
-__global__ __launch_bounds__(256) void gate_grad_kernel(GatedArgs p, uint16_t* out, int64_t n_out, int64_t plane) {
-  const int64_t per = n_out / 4;
+__global__ __launch_bounds__(256) void gate_grad_kernel(GatedArgs p, T* out) {
+  typedef T vec __attribute__((ext_vector_type(4)));
+  const int64_t per = p.n / 4, plane = p.m * 2 * p.n;
   for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < p.m * per;
        i += static_cast<int64_t>(gridDim.x) * 256) {
     const int64_t r = i / per, c = i % per * 4;
-    f32x4 dg = {0.0f, 0.0f, 0.0f, 0.0f}, du = dg;
-    if (c < p.n) {
-      typedef T vec __attribute__((ext_vector_type(4)));
-      const f32x4 dh = __builtin_convertvector(*reinterpret_cast<const vec*>(static_cast<const T*>(p.dh) + r * p.lddh + c), f32x4);
-      const f32x4 g = __builtin_convertvector(*reinterpret_cast<const vec*>(static_cast<const T*>(p.gate) + r * p.ldg + c), f32x4);
-      const f32x4 u = __builtin_convertvector(*reinterpret_cast<const vec*>(static_cast<const T*>(p.up) + r * p.ldu + c), f32x4);
+    const f32x4 dh = __builtin_convertvector(*reinterpret_cast<const vec*>(static_cast<const T*>(p.dh) + r * p.lddh + c), f32x4);
+    const f32x4 g = __builtin_convertvector(*reinterpret_cast<const vec*>(static_cast<const T*>(p.gate) + r * p.ldg + c), f32x4);
+    const f32x4 u = __builtin_convertvector(*reinterpret_cast<const vec*>(static_cast<const T*>(p.up) + r * p.ldu + c), f32x4);
+    f32x4 dg, du;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        float slope;
-        const float f = activate_both(g[e], p.act, &slope);
-        dg[e] = dh[e] * u[e] * slope;
-        du[e] = dh[e] * f;
-      }
+    for (int e = 0; e < 4; ++e) {
+      float slope;
+      const float f = activate_both(g[e], p.act, &slope);
+      dg[e] = dh[e] * u[e] * slope;
+      du[e] = dh[e] * f;
     }
-    uint16_t* o = out + r * 2 * n_out + c;
-    if constexpr (sizeof(T) == 4) {
-      bf16x4 h, m, l;
-      split3(dg, h, m, l);
-      *reinterpret_cast<bf16x4*>(o) = h;
-      *reinterpret_cast<bf16x4*>(o + plane) = m;
-      *reinterpret_cast<bf16x4*>(o + 2 * plane) = l;
-      split3(du, h, m, l);
-      *reinterpret_cast<bf16x4*>(o + n_out) = h;
-      *reinterpret_cast<bf16x4*>(o + n_out + plane) = m;
-      *reinterpret_cast<bf16x4*>(o + n_out + 2 * plane) = l;
-    } else {
-      typedef T vec __attribute__((ext_vector_type(4)));
-      const vec g1 = __builtin_convertvector(dg, vec), u1 = __builtin_convertvector(du, vec);
-      *reinterpret_cast<vec*>(o) = g1;
-      *reinterpret_cast<vec*>(o + n_out) = u1;
-      store4<T>(reinterpret_cast<T*>(o + plane), dg - __builtin_convertvector(g1, f32x4));
-      store4<T>(reinterpret_cast<T*>(o + n_out + plane), du - __builtin_convertvector(u1, f32x4));
+    T* o = out + r * 2 * p.n + c;
+    const vec g1 = __builtin_convertvector(dg, vec), u1 = __builtin_convertvector(du, vec);
+    *reinterpret_cast<vec*>(o) = g1;
+    *reinterpret_cast<vec*>(o + p.n) = u1;
+    if constexpr (sizeof(T) == 2) {
+      store4<T>(o + plane, dg - __builtin_convertvector(g1, f32x4));
+      store4<T>(o + p.n + plane, du - __builtin_convertvector(u1, f32x4));
     }
   }
 }
@@ -575,12 +609,7 @@ __global__ __launch_bounds__(512) void few_rows_kernel(GatedArgs p) {
   auto parts = [&](const Piece& x) {
     Parts r;
     if constexpr (F32) {
-      bf16x4 h[2], m[2], l[2];
-#pragma unroll
-      for (int i = 0; i < 2; ++i) split3(__builtin_bit_cast(f32x4, x.w[i]), h[i], m[i], l[i]);
-      r.p[0] = __builtin_bit_cast(s16x8, __builtin_shufflevector(h[0], h[1], 0, 1, 2, 3, 4, 5, 6, 7));
-      r.p[1] = __builtin_bit_cast(s16x8, __builtin_shufflevector(m[0], m[1], 0, 1, 2, 3, 4, 5, 6, 7));
-      r.p[2] = __builtin_bit_cast(s16x8, __builtin_shufflevector(l[0], l[1], 0, 1, 2, 3, 4, 5, 6, 7));
+      split8(__builtin_bit_cast(f32x4, x.w[0]), __builtin_bit_cast(f32x4, x.w[1]), r.p);
     } else {
       r.p[0] = __builtin_bit_cast(s16x8, x.w[0]);
     }
@@ -652,14 +681,14 @@ uint32_t stride_blocks(int64_t items) {
 
 int64_t up8(int64_t x) { return (x + 7) / 8 * 8; }
 
-template <typename T, typename O, int PA, int PB, int OA, int OB, int OUT, int BM, int BN, int BK, int WM, int WN>
+template <typename T, typename O, int PA, int PB, bool RA, bool RB, int OA, int OB, int OUT, int BM, int BN, int BK, int WM, int WN>
 hipError_t run_product(ProductArgs p, hipStream_t s) {
   p.m_tiles = static_cast<int32_t>((p.m + BM - 1) / BM);
   const int64_t wide = OUT == OUT_GATED ? BN / 2 : BN;
   p.n_tiles = static_cast<int32_t>((p.n + wide - 1) / wide);
   const int64_t tiles = static_cast<int64_t>(p.m_tiles) * p.n_tiles * p.splits;
   const int64_t blocks = (tiles + kXcds - 1) / kXcds * kXcds;
-  product_kernel<T, O, PA, PB, OA, OB, OUT, BM, BN, BK, WM, WN>
+  product_kernel<T, O, PA, PB, RA, RB, OA, OB, OUT, BM, BN, BK, WM, WN>
       <<<static_cast<uint32_t>(blocks), (BM / WM) * (BN / WN) * 64, 0, s>>>(p);
   return hipGetLastError();
 }
@@ -673,19 +702,19 @@ int64_t tiles_of(int64_t m, int64_t n, int64_t bm, int64_t bn) { return ((m + bm
 // 1335 us in 128 x 128; dA of 8191 x 8192 -> 1024, 212 us in 256 x 256 (128 tiles, half the chip) against
 // 152 us in 128 x 128; its dW 253 us in 256 x 128 against 331 us.  Three-part products: forward of 300k x 128
 // -> 128, 205 us in 128 x 256 (one column of tiles: A is read once) against 260 us in 128 x 128.
-template <typename T, typename O, int PA, int PB, int OA, int OB, int OUT>
+template <typename T, typename O, int PA, int PB, bool RA, bool RB, int OA, int OB, int OUT>
 hipError_t product(const ProductArgs& p, hipStream_t s) {
   const int64_t n = OUT == OUT_GATED ? 2 * p.n : p.n;       // rows of the B operand
   if constexpr (PA == 1) {
-    if (tiles_of(p.m, n, 256, 256) * p.splits >= 2 * kUnits) return run_product<T, O, PA, PB, OA, OB, OUT, 256, 256, 64, 128, 64>(p, s);
-    return run_product<T, O, PA, PB, OA, OB, OUT, 128, 128, 64, 64, 64>(p, s);
+    if (tiles_of(p.m, n, 256, 256) * p.splits >= 2 * kUnits) return run_product<T, O, PA, PB, RA, RB, OA, OB, OUT, 256, 256, 64, 128, 64>(p, s);
+    return run_product<T, O, PA, PB, RA, RB, OA, OB, OUT, 128, 128, 64, 64, 64>(p, s);
   } else if constexpr (PA == 2) {
-    if (p.m > 128 && tiles_of(p.m, n, 256, 128) * p.splits >= kUnits) return run_product<T, O, PA, PB, OA, OB, OUT, 256, 128, 64, 64, 64>(p, s);
-    return run_product<T, O, PA, PB, OA, OB, OUT, 128, 128, 64, 64, 64>(p, s);
+    if (p.m > 128 && tiles_of(p.m, n, 256, 128) * p.splits >= kUnits) return run_product<T, O, PA, PB, RA, RB, OA, OB, OUT, 256, 128, 64, 64, 64>(p, s);
+    return run_product<T, O, PA, PB, RA, RB, OA, OB, OUT, 128, 128, 64, 64, 64>(p, s);
   } else {
-    if (n > 128 && tiles_of(p.m, n, 128, 256) * p.splits >= kUnits) return run_product<T, O, PA, PB, OA, OB, OUT, 128, 256, 32, 64, 64>(p, s);
-    if (p.m > 128 && tiles_of(p.m, n, 256, 128) * p.splits >= kUnits) return run_product<T, O, PA, PB, OA, OB, OUT, 256, 128, 32, 64, 64>(p, s);
-    return run_product<T, O, PA, PB, OA, OB, OUT, 128, 128, 32, 64, 64>(p, s);
+    if (n > 128 && tiles_of(p.m, n, 128, 256) * p.splits >= kUnits) return run_product<T, O, PA, PB, RA, RB, OA, OB, OUT, 128, 256, 32, 64, 64>(p, s);
+    if (p.m > 128 && tiles_of(p.m, n, 256, 128) * p.splits >= kUnits) return run_product<T, O, PA, PB, RA, RB, OA, OB, OUT, 256, 128, 32, 64, 64>(p, s);
+    return run_product<T, O, PA, PB, RA, RB, OA, OB, OUT, 128, 128, 32, 64, 64>(p, s);
   }
 }
 
@@ -697,7 +726,7 @@ constexpr int64_t kSplitStep = 64;       // a split's steps are a multiple of it
 
 // Splits of dW's reduction over the rows: enough 256 x 128 tiles for every compute unit, each of at least 256 rows.
 int32_t dw_splits(int64_t m, int64_t n, int64_t k) {
-  const int64_t tiles = tiles_of(2 * up8(n), k, 256, 128);
+  const int64_t tiles = tiles_of(2 * n, k, 256, 128);
   int64_t s = (kUnits + tiles - 1) / tiles;
   const int64_t most = (m + 255) / 256;
   s = s < most ? s : most;
@@ -717,22 +746,18 @@ int32_t da_splits(int64_t m, int64_t n, int64_t k) {
 bool few_rows(int64_t m, int64_t n) { return m <= 16 || (m <= 128 && tiles_of(m, 2 * n, 128, 128) < kUnits); }
 
 struct Space {
-  int64_t a, w, grad, partial;     // bytes
+  int64_t w, grad, partial;        // bytes
 };
 
 int64_t up16(int64_t x) { return (x + 15) / 16 * 16; }
 
 Space gated_space(int32_t type, int64_t m, int64_t n, int64_t k, bool backward) {
-  Space s = {0, 0, 0, 0};
-  const int64_t planes = type == QHA_F32 ? 3 : 1;
-  if (type == QHA_F32 && (backward || !few_rows(m, n))) {
-    s.a = up16(planes * m * up8(k) * 2);
-    s.w = up16(planes * 2 * up8(n) * up8(k) * 2);
-  }
+  Space s = {0, 0, 0};
+  if (type == QHA_F32 && (backward || !few_rows(m, n))) s.w = up16(3 * 2 * up8(n) * up8(k) * 2);
   if (backward) {
-    s.grad = up16((type == QHA_F32 ? 3 : 2) * m * 2 * up8(n) * 2);
+    s.grad = up16(m * 2 * n * 4);                  // float32, or two parts of 16 bits
     const int64_t splits = dw_splits(m, n, k);
-    s.partial = splits > 1 ? up16(splits * 2 * up8(n) * k * 4) : 0;
+    s.partial = splits > 1 ? up16(splits * 2 * n * k * 4) : 0;
     // dA's partials are read before dW writes its own to the same place
     const int64_t da = da_splits(m, n, k);
     const int64_t need = da > 1 ? up16(da * m * k * 4) : 0;
@@ -760,13 +785,25 @@ hipError_t fwd_few(const GatedArgs& g, hipStream_t s) {
   return hipGetLastError();
 }
 
-template <typename T>
-hipError_t fwd16(const GatedArgs& g, hipStream_t s) {
+// The float32 weights in three bf16 planes [n8 rows of W_gate, n8 rows of W_up][k8], zero past n and k.
+Operand weight_planes(const GatedArgs& g, void* ws, hipStream_t s) {
+  const int64_t n8 = up8(g.n), k8 = up8(g.k), plane = 2 * n8 * k8;
+  __bf16* w = static_cast<__bf16*>(ws);
+  const uint32_t blocks = stride_blocks(n8 * k8 / 4);
+  split_kernel<<<blocks, 256, 0, s>>>(static_cast<const float*>(g.wg), g.ldwg, g.n, g.k, w, n8, k8, plane);
+  split_kernel<<<blocks, 256, 0, s>>>(static_cast<const float*>(g.wu), g.ldwu, g.n, g.k, w + n8 * k8, n8, k8, plane);
+  return {reinterpret_cast<const uint16_t*>(w), reinterpret_cast<const uint16_t*>(w + n8 * k8), k8, k8, plane, n8, k8};
+}
+
+Operand weights16(const GatedArgs& g) {
+  return {static_cast<const uint16_t*>(g.wg), static_cast<const uint16_t*>(g.wu), g.ldwg, g.ldwu, 0, g.n, g.k};
+}
+
+template <typename T, typename O, int PL>
+hipError_t fwd(const GatedArgs& g, hipStream_t s) {
   ProductArgs p = {};
   p.a = plain(g.a, g.lda, g.m, g.k);
-  p.b = plain(g.wg, g.ldwg, g.n, g.k);
-  p.b.p1 = static_cast<const uint16_t*>(g.wu);
-  p.b.ld1 = g.ldwu;
+  p.b = PL == 3 ? weight_planes(g, g.ws, s) : weights16(g);
   p.m = g.m;
   p.n = g.n;
   p.k = p.k_each = g.k;
@@ -778,103 +815,52 @@ hipError_t fwd16(const GatedArgs& g, hipStream_t s) {
   p.ldg = g.ldg;
   p.ldu = g.ldu;
   p.act = g.act;
-  return product<T, T, 1, 1, ORDER_ROWS, ORDER_PAIRS, OUT_GATED>(p, s);
-}
-
-void split(const float* x, int64_t ld, int64_t rows, int64_t cols, uint16_t* out, int64_t rows_out, int64_t plane,
-           hipStream_t s) {
-  split_kernel<<<stride_blocks(rows_out * up8(cols) / 4), 256, 0, s>>>(x, ld, rows, cols, reinterpret_cast<__bf16*>(out),
-                                                                       rows_out, up8(cols), plane);
-}
-
-hipError_t fwd32(const GatedArgs& g, hipStream_t s) {
-  const Space sp = gated_space(QHA_F32, g.m, g.n, g.k, false);
-  uint16_t* a3 = static_cast<uint16_t*>(g.ws);
-  uint16_t* w3 = reinterpret_cast<uint16_t*>(static_cast<char*>(g.ws) + sp.a);
-  const int64_t k8 = up8(g.k), n8 = up8(g.n);
-  split(static_cast<const float*>(g.a), g.lda, g.m, g.k, a3, g.m, g.m * k8, s);
-  split(static_cast<const float*>(g.wg), g.ldwg, g.n, g.k, w3, n8, 2 * n8 * k8, s);
-  split(static_cast<const float*>(g.wu), g.ldwu, g.n, g.k, w3 + n8 * k8, n8, 2 * n8 * k8, s);
-  ProductArgs p = {};
-  p.a = plain(a3, k8, g.m, k8, g.m * k8);
-  p.b = plain(w3, k8, n8, k8, 2 * n8 * k8);
-  p.b.p1 = w3 + n8 * k8;
-  p.m = g.m;
-  p.n = g.n;
-  p.k = p.k_each = k8;
-  p.splits = p.segments = 1;
-  p.h = g.h;
-  p.gate = g.gate_out;
-  p.up = g.up_out;
-  p.ldh = g.ldh;
-  p.ldg = g.ldg;
-  p.ldu = g.ldu;
-  p.act = g.act;
-  return product<__bf16, float, 3, 3, ORDER_ROWS, ORDER_PAIRS, OUT_GATED>(p, s);
+  return product<T, O, PL, PL, PL == 3, false, ORDER_ROWS, ORDER_PAIRS, OUT_GATED>(p, s);
 }
 
 template <typename T, typename O, int PL>
 hipError_t bwd(const GatedArgs& g, hipStream_t s) {
   const Space sp = gated_space(g.type, g.m, g.n, g.k, true);
   char* ws = static_cast<char*>(g.ws);
-  uint16_t* a3 = reinterpret_cast<uint16_t*>(ws);
-  uint16_t* w3 = reinterpret_cast<uint16_t*>(ws + sp.a);
-  uint16_t* grad = reinterpret_cast<uint16_t*>(ws + sp.a + sp.w);
-  float* partial = reinterpret_cast<float*>(ws + sp.a + sp.w + sp.grad);
-  const int64_t k8 = up8(g.k), n8 = up8(g.n);
-  if (g.m > 0) gate_grad_kernel<O><<<stride_blocks(g.m * n8 / 4), 256, 0, s>>>(g, grad, n8, g.m * 2 * n8);
-  Operand a, w;
-  if (PL == 3) {
-    if (g.m > 0) split(static_cast<const float*>(g.a), g.lda, g.m, g.k, a3, g.m, g.m * k8, s);
-    split(static_cast<const float*>(g.wg), g.ldwg, g.n, g.k, w3, n8, 2 * n8 * k8, s);
-    split(static_cast<const float*>(g.wu), g.ldwu, g.n, g.k, w3 + n8 * k8, n8, 2 * n8 * k8, s);
-    a = plain(a3, k8, g.m, k8, g.m * k8);
-    w = plain(w3, k8, n8, k8, 2 * n8 * k8);
-    w.p1 = w3 + n8 * k8;
-  } else {
-    a = plain(g.a, g.lda, g.m, g.k);
-    w = plain(g.wg, g.ldwg, g.n, g.k);
-    w.p1 = static_cast<const uint16_t*>(g.wu);
-    w.ld1 = g.ldwu;
-  }
-  const Operand d = plain(grad, 2 * n8, g.m, 2 * n8, g.m * 2 * n8);
+  O* grad = reinterpret_cast<O*>(ws + sp.w);
+  float* partial = reinterpret_cast<float*>(ws + sp.w + sp.grad);
   hipError_t e = hipSuccess;
+  if (g.m > 0) gate_grad_kernel<O><<<stride_blocks(g.m * g.n / 4), 256, 0, s>>>(g, grad);
+  const Operand d = plain(grad, 2 * g.n, g.m, 2 * g.n, g.m * 2 * g.n);
   if (g.m > 0 && g.da) {
     ProductArgs p = {};
     p.a = d;
-    p.b = w;
+    p.b = PL == 3 ? weight_planes(g, ws, s) : weights16(g);
     p.m = g.m;
     p.n = g.k;
-    p.k = n8;
+    p.k = g.n;
     p.segments = 2;
     p.splits = da_splits(g.m, g.n, g.k);
-    p.k_each = split_each(n8, p.splits);
-    p.half = p.pad_from = g.m;
+    p.k_each = split_each(g.n, p.splits);
+    p.half = g.m;
     p.c = g.da;
     p.ldc = g.ldda;
     p.partial = partial;
-    e = product<T, O, PL, PL, ORDER_ROWS, ORDER_CROSS, OUT_DA>(p, s);
+    e = product<T, O, PL, PL, PL == 3, false, ORDER_ROWS, ORDER_CROSS, OUT_DA>(p, s);
     if (e == hipSuccess && p.splits > 1) e = sum_splits<O>(p, s);
     if (e != hipSuccess) return e;
   }
   ProductArgs p = {};
   p.a = d;
-  p.b = a;
-  p.m = 2 * n8;
+  p.b = plain(g.a, g.lda, g.m, g.k);
+  p.m = 2 * g.n;
   p.n = g.k;
   p.k = g.m;
   p.segments = 1;
   p.splits = dw_splits(g.m, g.n, g.k);
   p.k_each = split_each(g.m, p.splits);
-  p.half = n8;
+  p.half = g.n;
   p.c = g.dwg;
   p.ldc = g.lddwg;
   p.c1 = g.dwu;
   p.ldc1 = g.lddwu;
   p.partial = partial;
-  // rows n .. n8 - 1 of either half are padding of a width that is no multiple of 8
-  p.pad_from = g.n;
-  e = product<T, float, PL == 3 ? 3 : 2, PL, ORDER_CROSS, ORDER_CROSS, OUT_DW>(p, s);
+  e = product<T, float, PL == 3 ? 3 : 2, PL, PL == 3, PL == 3, ORDER_CROSS, ORDER_CROSS, OUT_DW>(p, s);
   if (e == hipSuccess && p.splits > 1) e = sum_splits<float>(p, s);
   return e;
 }
@@ -883,13 +869,13 @@ hipError_t bwd(const GatedArgs& g, hipStream_t s) {
 
 size_t gated_workspace(int32_t type, int64_t m, int64_t n, int64_t k, bool backward) {
   const Space s = gated_space(type, m, n, k, backward);
-  return static_cast<size_t>(s.a + s.w + s.grad + s.partial);
+  return static_cast<size_t>(s.w + s.grad + s.partial);
 }
 
 hipError_t launch_gated_fwd(const GatedArgs& g, hipStream_t s) {
   if (few_rows(g.m, g.n)) return g.type == QHA_F32 ? fwd_few<float>(g, s) : g.type == QHA_BF16 ? fwd_few<__bf16>(g, s) : fwd_few<_Float16>(g, s);
-  if (g.type == QHA_F32) return fwd32(g, s);
-  return g.type == QHA_BF16 ? fwd16<__bf16>(g, s) : fwd16<_Float16>(g, s);
+  if (g.type == QHA_F32) return fwd<__bf16, float, 3>(g, s);
+  return g.type == QHA_BF16 ? fwd<__bf16, __bf16, 1>(g, s) : fwd<_Float16, _Float16, 1>(g, s);
 }
 
 hipError_t launch_gated_bwd(const GatedArgs& g, hipStream_t s) {
