@@ -428,7 +428,7 @@ size_t qha_gated_workspace(int32_t type, int64_t m, int64_t n, int64_t k, int32_
  * n_groups = 1 with positions = 1 is a layer norm.  x and y have elements of `type`, leading
  * dimensions ldx, ldy; y may be x.  weight, bias: device float32[c], nullable (1 and 0).  mean and rstd: device
  * float32[n_samples * n_groups], written for the backward, both nullable.  Sums are formed in
- * float64, or in float32 over one row held in registers (mean first, then squares about it), and
+ * float64, or in float32 over one sample of at most 8192 values (mean first, then squares about it), and
  * their partials are added in a fixed order: results are deterministic.
  * c is a multiple of 16 bytes of elements (4 or 8) and at most 8192; leading dimensions are at least
  * c and multiples of the same; x, y (and dy, dx) are 16-byte aligned.  workspace: device, 16-byte

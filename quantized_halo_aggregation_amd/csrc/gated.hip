@@ -76,16 +76,19 @@ enum { ORDER_ROWS = 0, ORDER_PAIRS = 1, ORDER_CROSS = 2 };
 // ORDER_PAIRS: the same, tile rows alternate between p0 and p1 by 32 (p0 and p1 hold `rows` rows each)
 // ORDER_CROSS: stored across the reduction; tile rows are steps of the reduction, stored columns c0 + c
 
-// Places of 16-byte chunks in a tile's LDS image, PER chunks a row.  Along the reduction, the rows that a read
-// takes together fall on different banks.  Across it, a transposing read (16-bit) takes four rows at a
-// time, and the reads of float32 columns take two rows eight apart.  The permutations are their own inverses.
+// Places of 16-byte chunks in a tile's LDS image, PER chunks a row.  LDS serves 256 bytes at a time, so the reads
+// that go together must fall on different sixteenths of 256 bytes.  Along the reduction, 16 lanes read one
+// chunk of as many rows (rows of 128 or 64 bytes, two or four to 256).  Across it, a transposing read (16-bit)
+// takes 64 bytes of four rows at a time, and a read of float32 columns 128 bytes of two rows eight apart.
+// The permutations are their own inverses.
 template <int PER>
 __device__ __forceinline__ int permute_along(int row, int chunk) {
-  return PER == 8 ? chunk ^ (row & 7) : chunk ^ ((row >> 1) & 3);
+  static_assert(PER == 8 || PER == 4, "rows of 128 or 64 bytes");
+  return PER == 8 ? chunk ^ ((row >> 1) & 7) : chunk ^ ((row >> 2) & 3);
 }
 template <bool RAW>
 __device__ __forceinline__ int permute_cross(int k, int chunk) {
-  return RAW ? chunk ^ (k & 8) : chunk ^ (((k & 3) << 1) | ((k & 4) << 1));
+  return RAW ? chunk ^ (k & 8) : chunk ^ ((k & 3) << 2);
 }
 
 // Waits for this wavefront's loads into LDS; a barrier after it makes them visible to the block.
@@ -116,7 +119,8 @@ struct Stager {
   static __device__ __forceinline__ int row(int i) { return (i * NT + static_cast<int>(threadIdx.x)) / PER; }
   static __device__ __forceinline__ int chunk(int i) {
     const int q = (i * NT + static_cast<int>(threadIdx.x)) % PER;
-    return ORDER == ORDER_CROSS ? permute_cross<RAW>(row(i), q) : permute_along<PER>(row(i), q);
+    if constexpr (ORDER == ORDER_CROSS) return permute_cross<RAW>(row(i), q);
+    else return permute_along<PER>(row(i), q);
   }
   // base: the operand's (or segment's) matrix; k0: first step of the reduction; first: the tile's first stored
   // row (along) or column (across).  Rows and columns past the end repeat the last ones; their results
@@ -172,7 +176,7 @@ struct Stager {
 // lane l holds row l % 32, steps 8 (l / 32) .. + 7.
 template <int ORDER, int COLS>
 __device__ __forceinline__ s16x8 fragment(const uint16_t* lds, int at, int ks, int lane) {
-  if (ORDER == ORDER_CROSS) {
+  if constexpr (ORDER == ORDER_CROSS) {
     // the transposing read takes 4 steps x 16 columns per 16 lanes: lane j of them addresses step
     // j / 4, columns 4 (j % 4), and receives four steps of column j
     const int j = lane & 15;
@@ -184,10 +188,11 @@ __device__ __forceinline__ s16x8 fragment(const uint16_t* lds, int at, int ks, i
     const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)lo);
     const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)hi);
     return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
+  } else {
+    const int row = at + (lane & 31);
+    const int c = permute_along<COLS / 8>(row, (ks >> 3) + (lane >> 5));
+    return *reinterpret_cast<const s16x8*>(lds + row * COLS + c * 8);
   }
-  const int row = at + (lane & 31);
-  const int c = permute_along<COLS / 8>(row, (ks >> 3) + (lane >> 5));
-  return *reinterpret_cast<const s16x8*>(lds + row * COLS + c * 8);
 }
 
 // x = hi + mid + lo exactly: each part is rounded to nearest even, the remainders are exact in float32.
@@ -212,7 +217,7 @@ template <int ORDER, int COLS>
 __device__ __forceinline__ void fragment_raw(const uint16_t* lds, int at, int ks, int lane, s16x8 (&part)[3]) {
   const float* x = reinterpret_cast<const float*>(lds);
   f32x4 a, b;
-  if (ORDER == ORDER_CROSS) {
+  if constexpr (ORDER == ORDER_CROSS) {
     const int col = at + (lane & 31);
     const int k = ks + (lane >> 5) * 8;              // bit 3 of k .. k + 7 is that of k
     const float* p = x + k * COLS + permute_cross<true>(k, col >> 2) * 4 + (col & 3);
@@ -410,16 +415,17 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) void product_kernel(Pro
       sb.next(ldb);
     };
     const int64_t steps = kbeg < kend ? (kend - kbeg) / BK : 0, left = kbeg < kend ? (kend - kbeg) % BK : 0;
+    // Two buffers.  Three or four with as many steps in flight cost a second block on the compute unit or a
+    // larger tile, and lose: 300k x 128 float32 forward 248 and 262 us against 196, 16384 x 2048 -> 8192 bf16
+    // 1128 us with steps of 32 against 1054.
     if (steps > 0) load(lds);
-    loads_done();
-    __syncthreads();
     for (int64_t t = 0; t < steps; ++t) {
-      // the other buffer was read before the last barrier
+      loads_done();
+      __syncthreads();             // step t is there, and everyone has read step t - 1
       if (t + 1 < steps) load(lds + ((t + 1) & 1) * BUF);
       multiply(lds + (t & 1) * BUF);
-      loads_done();
-      __syncthreads();
     }
+    __syncthreads();
     if (left > 0) {
 #pragma unroll
       for (int pl = 0; pl < LA; ++pl) sa.load_partial(pl * p.a.plane, left, lds + pl * A_SIZE);

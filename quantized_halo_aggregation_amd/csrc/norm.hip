@@ -6,7 +6,7 @@
 //
 // Bound: memory (x read and y written once at the least; dy, x and dx in the backward).
 //
-// Samples of one position whose vectors lie in one group take one pass with the row in registers
+// Samples of at most 8192 values whose vectors lie in one group take one pass with the sample in registers
 // (norm_rows.hip); the others two launches.  A block of 256 threads owns a chunk of a sample's rows
 // and all channels: a thread keeps one 16-byte vector of channels (several where the row has more
 // than 256 vectors) and walks down the rows, so loads are whole rows and nothing is exchanged until

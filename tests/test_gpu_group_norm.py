@@ -168,6 +168,22 @@ def test_backward_of_many_rows(shape, kind):
     _check_bwd(shape, "float32", kind, affine=kind != "silu")
 
 
+SMALL = [(700, 4, 32, 1), (501, 9, 8, 1), (333, 2, 128, 4), (77, 7, 40, 5), (65, 3, 1032, 3), (50, 6, 256, 32), (9, 25, 320, 8),
+         (5, 2, 4096, 4), (40, 31, 16, 2), (3, 1000, 8, 1), (6, 3, 2048, 1), (19, 16, 64, 4),
+         (260, 2, 4096, 4), (257, 97, 64, 8), (300, 3, 2048, 1)]
+
+
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
+@pytest.mark.parametrize("shape", SMALL, ids=lambda s: "x".join(map(str, s)))
+def test_small_samples(shape, dtype):
+    """Samples that a team of threads holds whole: every team size and way of summing groups, and one just over."""
+    H.require_gpu()
+    kind = list(KINDS)[(shape[1] + shape[3]) % 4]
+    H.note(f"group norm small {shape} {dtype} {kind}")
+    _check_fwd(shape, dtype, kind)
+    _check_bwd(shape, dtype, kind)
+
+
 def test_strided_rows_and_in_place():
     """Column slices of wider buffers (the layout of concatenated halves), y in x's place, dx in dy's."""
     H.require_gpu()
