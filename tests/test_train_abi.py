@@ -72,12 +72,12 @@ def test_adamw_binding_refuses():
         B.AdamW([], copies=[torch.zeros(4)])
 
 
-def _norm_fwd(n=10, p=3, c=64, g=4, t=B.F32, x=FAKE, ldx=64, w=FAKE, b=FAKE, eps=1e-5, act=0, y=FAKE, ldy=64, mean=FAKE,
+def _norm_fwd(n=10, p=300, c=64, g=4, t=B.F32, x=FAKE, ldx=64, w=FAKE, b=FAKE, eps=1e-5, act=0, y=FAKE, ldy=64, mean=FAKE,
               rstd=FAKE, ws=FAKE, wsb=1 << 30):
     return B._group_norm_fwd(n, p, c, g, t, x, ldx, w, b, eps, act, y, ldy, mean, rstd, ws, wsb, None)
 
 
-def _norm_bwd(n=10, p=3, c=64, g=4, t=B.F32, dy=FAKE, lddy=64, x=FAKE, ldx=64, mean=FAKE, rstd=FAKE, w=FAKE, b=FAKE,
+def _norm_bwd(n=10, p=300, c=64, g=4, t=B.F32, dy=FAKE, lddy=64, x=FAKE, ldx=64, mean=FAKE, rstd=FAKE, w=FAKE, b=FAKE,
               act=0, dx=FAKE, lddx=64, dw=FAKE, db=FAKE, ws=FAKE, wsb=1 << 30):
     return B._group_norm_bwd(n, p, c, g, t, dy, lddy, x, ldx, mean, rstd, w, b, act, dx, lddx, dw, db, ws, wsb, None)
 
@@ -105,8 +105,9 @@ def test_group_norm_limits_and_workspace():
     wide = dict(c=8448, ldx=8448, g=1)
     assert _norm_fwd(ldy=8448, **wide) == B.QHA_ERR_UNSUPPORTED
     assert _norm_bwd(lddy=8448, lddx=8448, **wide) == B.QHA_ERR_UNSUPPORTED
-    need = B.group_norm_workspace(30, 3, 64, 4, backward=True)
-    assert need > 0
+    assert B.group_norm_workspace(3000, 300, 64, 4, backward=True) > 0
+    assert B.group_norm_workspace(30, 3, 64, 4) == 0        # samples held in registers need none forward
+    assert B.group_norm_workspace(30, 3, 64, 4, backward=True) > 0
     assert _norm_bwd(ws=None) == B.QHA_ERR_WORKSPACE
     assert _norm_bwd(wsb=15) == B.QHA_ERR_WORKSPACE
     assert _norm_fwd(ws=None, wsb=0) == B.QHA_ERR_WORKSPACE
