@@ -86,9 +86,11 @@ __device__ __forceinline__ int permute_along(int row, int chunk) {
   static_assert(PER == 8 || PER == 4, "rows of 128 or 64 bytes");
   return PER == 8 ? chunk ^ ((row >> 1) & 7) : chunk ^ ((row >> 2) & 3);
 }
-template <bool RAW>
+template <bool RAW, int PER>
 __device__ __forceinline__ int permute_cross(int k, int chunk) {
-  return RAW ? chunk ^ (k & 8) : chunk ^ ((k & 3) << 2);
+  static_assert(PER >= (RAW ? 16 : 8), "rows of at least 256 bytes of float32, 128 of 16-bit values");
+  if (RAW) return chunk ^ (k & 8);
+  return PER == 8 ? chunk ^ ((k & 2) << 1) : chunk ^ ((k & 3) << 2);
 }
 
 // Waits for this wavefront's loads into LDS; a barrier after it makes them visible to the block.
@@ -119,7 +121,7 @@ struct Stager {
   static __device__ __forceinline__ int row(int i) { return (i * NT + static_cast<int>(threadIdx.x)) / PER; }
   static __device__ __forceinline__ int chunk(int i) {
     const int q = (i * NT + static_cast<int>(threadIdx.x)) % PER;
-    if constexpr (ORDER == ORDER_CROSS) return permute_cross<RAW>(row(i), q);
+    if constexpr (ORDER == ORDER_CROSS) return permute_cross<RAW, PER>(row(i), q);
     else return permute_along<PER>(row(i), q);
   }
   // base: the operand's (or segment's) matrix; k0: first step of the reduction; first: the tile's first stored
@@ -183,8 +185,8 @@ __device__ __forceinline__ s16x8 fragment(const uint16_t* lds, int at, int ks, i
     const int col = at + ((lane >> 4) & 1) * 16 + 4 * (j & 3);
     const int k = ks + (lane >> 5) * 8 + (j >> 2);
     const int off = (col & 7);
-    const uint16_t* lo = lds + k * COLS + permute_cross<false>(k, col >> 3) * 8 + off;
-    const uint16_t* hi = lds + (k + 4) * COLS + permute_cross<false>(k + 4, col >> 3) * 8 + off;
+    const uint16_t* lo = lds + k * COLS + permute_cross<false, COLS / 8>(k, col >> 3) * 8 + off;
+    const uint16_t* hi = lds + (k + 4) * COLS + permute_cross<false, COLS / 8>(k + 4, col >> 3) * 8 + off;
     const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)lo);
     const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)hi);
     return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
@@ -220,7 +222,7 @@ __device__ __forceinline__ void fragment_raw(const uint16_t* lds, int at, int ks
   if constexpr (ORDER == ORDER_CROSS) {
     const int col = at + (lane & 31);
     const int k = ks + (lane >> 5) * 8;              // bit 3 of k .. k + 7 is that of k
-    const float* p = x + k * COLS + permute_cross<true>(k, col >> 2) * 4 + (col & 3);
+    const float* p = x + k * COLS + permute_cross<true, COLS / 4>(k, col >> 2) * 4 + (col & 3);
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       a[e] = p[e * COLS];
@@ -707,19 +709,26 @@ int64_t tiles_of(int64_t m, int64_t n, int64_t bm, int64_t bn) { return ((m + bm
 // units: forward of 16384 x 2048 -> 8192 bf16, 1044 us in 256 x 256 tiles (4096 of them) against
 // 1335 us in 128 x 128; dA of 8191 x 8192 -> 1024, 212 us in 256 x 256 (128 tiles, half the chip) against
 // 152 us in 128 x 128; its dW 253 us in 256 x 128 against 331 us.  Three-part products: forward of 300k x 128
-// -> 128, 205 us in 128 x 256 (one column of tiles: A is read once) against 260 us in 128 x 128.
+// -> 128, 205 us in 128 x 256 (one column of tiles: A is read once) against 260 us in 128 x 128.  Where even tiles of
+// 128 x 128 leave half the compute units idle, 64 x 64: forward of 512 x 1024 -> 2048 (128 tiles) bf16 11.9 against
+// 14.8 us, float32 54.8 against 59.6 us; of 1500 x 1136 -> 1224 (240 tiles) 21.1 against 18.9 us.
 template <typename T, typename O, int PA, int PB, bool RA, bool RB, int OA, int OB, int OUT>
 hipError_t product(const ProductArgs& p, hipStream_t s) {
   const int64_t n = OUT == OUT_GATED ? 2 * p.n : p.n;       // rows of the B operand
+  const bool few = tiles_of(p.m, n, 128, 128) * p.splits <= kUnits / 2;
   if constexpr (PA == 1) {
     if (tiles_of(p.m, n, 256, 256) * p.splits >= 2 * kUnits) return run_product<T, O, PA, PB, RA, RB, OA, OB, OUT, 256, 256, 64, 128, 64>(p, s);
+    if (few) return run_product<T, O, PA, PB, RA, RB, OA, OB, OUT, 64, 64, 64, 32, 64>(p, s);
     return run_product<T, O, PA, PB, RA, RB, OA, OB, OUT, 128, 128, 64, 64, 64>(p, s);
   } else if constexpr (PA == 2) {
-    if (p.m > 128 && tiles_of(p.m, n, 256, 128) * p.splits >= kUnits) return run_product<T, O, PA, PB, RA, RB, OA, OB, OUT, 256, 128, 64, 64, 64>(p, s);
+    if (p.m > 128 && tiles_of(p.m, n, 256, 128) * p.splits > kUnits / 2) return run_product<T, O, PA, PB, RA, RB, OA, OB, OUT, 256, 128, 64, 64, 64>(p, s);
     return run_product<T, O, PA, PB, RA, RB, OA, OB, OUT, 128, 128, 64, 64, 64>(p, s);
   } else {
-    if (n > 128 && tiles_of(p.m, n, 128, 256) * p.splits >= kUnits) return run_product<T, O, PA, PB, RA, RB, OA, OB, OUT, 128, 256, 32, 64, 64>(p, s);
-    if (p.m > 128 && tiles_of(p.m, n, 256, 128) * p.splits >= kUnits) return run_product<T, O, PA, PB, RA, RB, OA, OB, OUT, 256, 128, 32, 64, 64>(p, s);
+    if (n > 128 && tiles_of(p.m, n, 128, 256) * p.splits > kUnits / 2) return run_product<T, O, PA, PB, RA, RB, OA, OB, OUT, 128, 256, 32, 64, 64>(p, s);
+    if (p.m > 128 && tiles_of(p.m, n, 256, 128) * p.splits > kUnits / 2) return run_product<T, O, PA, PB, RA, RB, OA, OB, OUT, 256, 128, 32, 64, 64>(p, s);
+    if constexpr (OUT != OUT_DW) {
+      if (few) return run_product<T, O, PA, PB, RA, RB, OA, OB, OUT, 64, 64, 32, 32, 64>(p, s);
+    }
     return run_product<T, O, PA, PB, RA, RB, OA, OB, OUT, 128, 128, 32, 64, 64>(p, s);
   }
 }
@@ -730,10 +739,11 @@ Operand plain(const void* p, int64_t ld, int64_t rows, int64_t cols, int64_t pla
 
 constexpr int64_t kSplitStep = 64;       // a split's steps are a multiple of it
 
-// Splits of dW's reduction over the rows: enough 256 x 128 tiles for every compute unit, each of at least 256 rows.
+// Splits of dW's reduction over the rows: as many as keep the 256 x 128 tiles on the compute units at once (a few more
+// would take a second round), each of at least 256 rows.
 int32_t dw_splits(int64_t m, int64_t n, int64_t k) {
   const int64_t tiles = tiles_of(2 * n, k, 256, 128);
-  int64_t s = (kUnits + tiles - 1) / tiles;
+  int64_t s = kUnits / tiles;
   const int64_t most = (m + 255) / 256;
   s = s < most ? s : most;
   return static_cast<int32_t>(s < 1 ? 1 : s);
