@@ -190,16 +190,20 @@ __global__ __launch_bounds__(256) void adamw_kernel(AdamArgs a) {
       const int64_t blk = i / kAdamBlock;
       const i8x4 cm = load4<i8x4, int8_t>(t.m, i, t.n, vec);
       const u8x4 cv = load4<u8x4, uint8_t>(t.v, i, t.n, vec);
-      const double sm = static_cast<double>(t.ms[blk]) * (a.beta1 / (127.0 * 127.0));
-      const double sv = static_cast<double>(t.vs[blk]) * (a.beta2 / (255.0 * 255.0 * 255.0 * 255.0));
+      const double sm = static_cast<double>(t.ms[blk]);
+      const double sv = static_cast<double>(t.vs[blk]);
       double xm[4], xv[4];
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const int c = cm[j];
         const uint32_t u = static_cast<uint32_t>(cv[j]) * cv[j];
         const double gd = static_cast<double>(g[j]);
-        xm[j] = __builtin_fma(gd, 1.0 - a.beta1, sm * static_cast<double>(c * (c < 0 ? -c : c)));
-        xv[j] = __builtin_fma(gd * gd, 1.0 - a.beta2, sv * static_cast<double>(u * u));
+        // every product and sum rounded as the formula is written, so that a float64 program gets these very
+        // moments: 0.9 a + 0.1 b lies half-way between two float32 scales often enough for the last bit to matter
+        const double old_m = sm * static_cast<double>(c * (c < 0 ? -c : c)) * (1.0 / (127.0 * 127.0));
+        const double old_v = sv * static_cast<double>(u * u) * (1.0 / (255.0 * 255.0 * 255.0 * 255.0));
+        xm[j] = a.beta1 * old_m + (1.0 - a.beta1) * gd;
+        xv[j] = a.beta2 * old_v + (1.0 - a.beta2) * (gd * gd);
         m[j] = static_cast<float>(xm[j]);
         v[j] = static_cast<float>(xv[j]);
       }

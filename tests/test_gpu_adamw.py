@@ -149,6 +149,47 @@ def test_codes_at_half_way_points_and_wide_ranges():
     assert np.array_equal(np.isnan(H.host(opt.values()[1]))[:g.size], np.isnan(T.decode(cv, sv, 255, 4)))
 
 
+def test_scales_and_codes_are_those_of_the_formula_as_written():
+    """float64 moments from 16-bit gradients land half-way between two float32 scales in about one block of a hundred;
+    the formula's products and sums, each rounded, decide there too: three steps stay bit for bit equal."""
+    H.require_gpu()
+    import torch
+    from quantized_halo_aggregation_amd import binding as B
+    n, rng = 400_000, np.random.default_rng(12)
+    H.note("adamw 8 scales")
+    opt = B.AdamW([torch.zeros(n, device="cuda")], bits=8)
+    m, v, ms, vs = (np.zeros(n), np.zeros(n), np.zeros(-(-n // 256), np.float32), np.zeros(-(-n // 256), np.float32))
+    wide = lambda s: np.repeat(s.astype(np.float64), 256)[:n]
+    for _ in range(3):
+        g = torch.from_numpy(rng.standard_normal(n).astype(np.float32)).to(torch.bfloat16)
+        opt.step([g.cuda()], 1e-3)
+        gd = g.float().numpy().astype(np.float64)
+        x = 0.9 * ((wide(ms) * (m * np.abs(m))) * (1.0 / (127.0 * 127.0))) + (1.0 - 0.9) * gd
+        y = 0.999 * ((wide(vs) * ((v * v) * (v * v))) * (1.0 / 255.0 ** 4)) + (1.0 - 0.999) * (gd * gd)
+        (m, ms), (v, vs) = T.encode(x, 127, 2), T.encode(y, 255, 4)
+        m, v = m.astype(np.float64), v.astype(np.float64)
+        H.assert_bits_equal(H.host(opt.m_scale), ms, "m_scale")
+        H.assert_bits_equal(H.host(opt.v_scale), vs, "v_scale")
+        assert np.array_equal(H.host(opt.m)[:n], m) and np.array_equal(H.host(opt.v)[:n], v)
+
+
+def test_codes_of_equal_and_zero_gradients():
+    """Blocks whose largest magnitude is shared by many lanes, or is zero."""
+    H.require_gpu()
+    import torch
+    from quantized_halo_aggregation_amd import binding as B
+    g = np.zeros(1100, np.float32)
+    g[256:512] = -0.3
+    g[512:768:2] = 1e-3
+    g[768:] = np.repeat(np.float32([1.0, -1.0, 0.25, 1e-30]), 83)
+    H.note("adamw 8 equal gradients")
+    opt = B.AdamW([torch.ones(1100, device="cuda")], bits=8)
+    opt.step([H.dev(g)], 1e-3)
+    m, v = T.adam_moments(np.zeros(1100), np.zeros(1100), g, 0.9, 0.999)
+    for got, ref, top, power in ((opt.m, m, 127, 2), (opt.v, v, 255, 4)):
+        assert np.array_equal(H.host(got).astype(np.int64)[:1100], T.encode(ref, top, power)[0])
+
+
 @pytest.mark.parametrize("bits", [8, 32])
 def test_a_gradient_that_is_not_finite(bits):
     """Only its own parameter is touched in that step; with 8-bit moments its block reads as NaN after."""

@@ -26,7 +26,8 @@ KINDS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3}
 SHAPES = [(1, 1, 8, 1), (5, 1, 8, 8), (1001, 1, 128, 8), (300, 1, 256, 1), (77, 1, 40, 5), (33, 1, 1024, 32),
           (9, 1, 4096, 1), (5, 1, 2048, 64), (3, 1, 8192, 2), (7, 1, 1536, 3), (1, 1, 24, 24), (12, 1, 24, 4),
           (3, 97, 64, 8), (2, 1, 16, 2), (1, 3001, 128, 4), (17, 2, 40, 5), (2, 50, 2048, 16), (4, 9, 48, 12),
-          (2, 33, 4096, 2), (40, 5, 256, 256), (2, 11, 1032, 3)]
+          (2, 33, 4096, 2), (40, 5, 256, 256), (2, 11, 1032, 3), (2, 3, 8192, 8192),
+          (1, 3, 8192, 1)]
 
 
 def _data(rows, c, dtype, seed, shift=0.25, scale=1.5):
