@@ -18,6 +18,9 @@
 // 32 of Wu, so a wavefront holds G and U of the same columns and the activation and product happen in registers.
 // The matrix instruction's operands are swapped (C^T is formed), which leaves a lane four neighbouring
 // columns of a row to store at once.
+// Bound: the matrix cores for wide layers (16384 x 2048 -> 8192 bf16 with all three results stored, 1.06 ms, 1.03
+// PFLOP/s, where a plain library product of that size class reaches 1.25), the order of loads, products
+// and stores within a tile for narrow ones (300k x 128 -> 128 float32, 188 us against 123 us for its bytes).
 #include "act_common.hpp"
 #include "qha_internal.hpp"
 
@@ -574,7 +577,8 @@ __global__ __launch_bounds__(256) void gate_grad_kernel(GatedArgs p, T* out) {
 // Few rows (decoded tokens, queried nodes): the weights are read once at memory's rate and the tiles above
 // would leave most of the chip idle.  A block owns 16 columns of H and all rows (16 MB of them); its eight
 // wavefronts take every eighth 32-step piece of the reduction, read their 16 rows of Wg and Wu straight from
-// memory as matrix operands (16 bytes a lane, four pieces in flight), and meet in LDS.
+// memory as matrix operands (16 bytes a lane, four pieces in flight), and meet in LDS.  One row, 2048 -> 4096 bf16:
+// 7.3 us, 4.6 TB/s of weights.
 template <typename T, int MB>
 __global__ __launch_bounds__(512) void few_rows_kernel(GatedArgs p) {
   constexpr bool F32 = sizeof(T) == 4;
