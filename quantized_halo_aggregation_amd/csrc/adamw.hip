@@ -9,7 +9,7 @@
 // moments, 16-bit gradients and a 16-bit copy; the arithmetic hides behind it, which is why the 8-bit
 // form can afford float64 moments: a code is then the same whichever way its inputs were summed.
 //
-// 302M elements with float32 moments and gradients: 1.60 ms (5.3 TB/s; a large copy reaches 5.0).  201M with
+// 302M elements with float32 moments and gradients: 1.46 to 1.60 ms by card (5.3 to 5.8 TB/s; a large copy reaches 5.0).  201M with
 // 8-bit moments, bf16 gradients and copies: 0.68 ms (5.3 TB/s), and 0.35 ms to read the moments back (5.8 TB/s).
 //
 // Mapping: a block of 256 threads takes chunks of 1024 consecutive elements, four per thread (16-byte
