@@ -722,7 +722,7 @@ int64_t tiles_of(int64_t m, int64_t n, int64_t bm, int64_t bn) { return ((m + bm
 template <typename T, typename O, int PA, int PB, bool RA, bool RB, int OA, int OB, int OUT>
 hipError_t product(const ProductArgs& p, hipStream_t s) {
   const int64_t n = OUT == OUT_GATED ? 2 * p.n : p.n;       // rows of the B operand
-  const bool few = tiles_of(p.m, n, 128, 128) * p.splits <= kUnits / 2;
+  [[maybe_unused]] const bool few = tiles_of(p.m, n, 128, 128) * p.splits <= kUnits / 2;
   if constexpr (PA == 1) {
     if (tiles_of(p.m, n, 256, 256) * p.splits >= 2 * kUnits) return run_product<T, O, PA, PB, RA, RB, OA, OB, OUT, 256, 256, 64, 128, 64>(p, s);
     if (few) return run_product<T, O, PA, PB, RA, RB, OA, OB, OUT, 64, 64, 64, 32, 64>(p, s);

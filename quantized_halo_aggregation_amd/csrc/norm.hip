@@ -453,7 +453,7 @@ void go(const NormArgs& a, bool backward, hipStream_t s) {
   if (nvec <= NT) go<T, 1>(a, backward, s);
   else if (nvec <= 2 * NT) go<T, 2>(a, backward, s);
   else if (nvec <= 4 * NT) go<T, 4>(a, backward, s);
-  else go<T, 8>(a, backward, s);
+  else if constexpr (sizeof(T) == 4) go<T, 8>(a, backward, s);      // at most 8192 channels
 }
 
 hipError_t launch(const NormArgs& a, bool backward, hipStream_t s) {
