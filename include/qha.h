@@ -449,7 +449,7 @@ int qha_group_norm_bwd(int64_t n_samples, int64_t positions, int32_t c, int32_t 
                        int64_t lddy, const void* x, int64_t ldx, const float* mean, const float* rstd,
                        const float* weight, const float* bias, int32_t act, void* dx, int64_t lddx, float* dweight,
                        float* dbias, void* workspace, size_t workspace_bytes, void* stream);
-/* Bytes of workspace for either direction (0 where none is needed). */
+/* Bytes of workspace for either direction, enough for every type (0 where none is needed, and for sizes that the calls refuse). */
 size_t qha_group_norm_workspace(int64_t n_samples, int64_t positions, int32_t c, int32_t n_groups, int32_t backward);
 
 /* One AdamW step over a list of tensors.  With g = grad_scale * grad, for every element:

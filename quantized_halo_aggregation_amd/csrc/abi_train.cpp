@@ -185,7 +185,8 @@ int qha_gated_backward(int64_t m, int64_t n, int64_t k, int32_t type, const void
 size_t qha_group_norm_workspace(int64_t n_samples, int64_t positions, int32_t c, int32_t n_groups, int32_t backward) {
   if (n_samples <= 0 || positions <= 0 || n_samples > kMaxRows / positions || c <= 0 || c > 8192 || n_groups <= 0 || c % n_groups != 0) return 0;
   size_t need = 0;
-  for (int32_t type : {QHA_F32, QHA_BF16}) {       // the element type is not asked for: room for each
+  for (int32_t type : {QHA_F32, QHA_BF16}) {       // the element type is not asked for: room for each that c suits
+    if (c % static_cast<int32_t>(16 / type_bytes(type)) != 0) continue;
     qha::NormArgs a;
     std::memset(&a, 0, sizeof(a));
     a.samples = n_samples;

@@ -281,3 +281,15 @@ def test_graph_replays_equal_the_eager_call():
             torch.cuda.synchronize()
             for a, t in zip(want, out):
                 assert torch.equal(a, t), k
+
+
+@pytest.mark.parametrize("shape", [(700, 1, 4, 1), (33, 1, 4, 2), (50, 1, 4, 4), (3, 1000, 4, 1), (2, 3001, 4, 2), (5, 60, 4, 1),
+                                   (301, 1, 12, 3), (40, 1, 12, 2), (3, 500, 12, 3), (2, 1500, 12, 1)],
+                         ids=lambda s: "x".join(map(str, s)))
+def test_four_and_twelve_float32_channels(shape):
+    """Widths that only float32 has: one or three vectors a row, groups of whole vectors and groups that cut them."""
+    H.require_gpu()
+    for kind in ("relu", "silu"):
+        H.note(f"group norm narrow {shape} {kind}")
+        _check_fwd(shape, "float32", kind)
+        _check_bwd(shape, "float32", kind)

@@ -2,6 +2,10 @@
 
 Argument-error cases pass fake (never dereferenced) device addresses: the checks must fire first.
 """
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
@@ -9,6 +13,7 @@ import torch
 from quantized_halo_aggregation_amd import binding as B
 
 FAKE = 0x10000
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 
 def _adam(tensors=((10, FAKE, FAKE, 0, FAKE, FAKE, FAKE, FAKE),), n=None, bits=32, gt=B.F32, ct=B.F32, lr=1e-3, b1=0.9,
@@ -172,3 +177,26 @@ def test_gated_binding_refuses():
     a, w, h = torch.zeros(4, 16), torch.zeros(8, 16), torch.zeros(4, 8)
     with pytest.raises(ValueError, match="GPU"):
         B.gated_project(a, w, w, h)
+
+
+def test_group_norm_workspace_of_narrow_rows():
+    """Widths below a 16-bit vector: four float32 channels are legal, one to three and five to seven are not, and twelve suit
+    float32 alone.  In a process of its own, because a division by zero on the host would end this one."""
+    code = ("from quantized_halo_aggregation_amd import binding as B\n"
+            "for c in list(range(1, 9)) + [12]:\n"
+            "    for rows, positions in ((300, 1), (300, 100), (6000, 3000)):\n"
+            "        print(c, positions, *(B.group_norm_workspace(rows, positions, c, 1, b) for b in (False, True)))\n")
+    res = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300, cwd=ROOT)
+    assert res.returncode == 0, (res.returncode, res.stderr[-500:])
+    got = {tuple(map(int, line.split()[:2])): tuple(map(int, line.split()[2:])) for line in res.stdout.splitlines()}
+    assert len(got) == 27
+    for (c, positions), (fwd, bwd) in got.items():
+        if c % 4:
+            assert (fwd, bwd) == (0, 0), c
+            continue
+        assert bwd >= 2 * c * 4 and (fwd > 0 or positions < 3000), (c, positions, fwd, bwd)
+        if c % 8:        # float32 is the only type of these: the query gives exactly what the calls ask for
+            shape = dict(n={1: 300, 100: 3, 3000: 2}[positions], p=positions, c=c, g=1)
+            assert _norm_bwd(ldx=c, lddy=c, lddx=c, wsb=bwd - 1, **shape) == B.QHA_ERR_WORKSPACE
+            if fwd:
+                assert _norm_fwd(ldx=c, ldy=c, wsb=fwd - 1, **shape) == B.QHA_ERR_WORKSPACE
