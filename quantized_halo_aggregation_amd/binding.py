@@ -679,8 +679,9 @@ class AdamW:
     Moments are kept in flat tensors in which every parameter starts at a multiple of ADAMW_BLOCK
     elements (`starts`): m and v float32 (bits=32), or int8 / uint8 codes with one float32 scale per
     block in m_scale and v_scale (bits=8).  They and the step count t are all of the state: copy
-    them to save or resume.  `copies`, if given, are tensors of one 16-bit or float32 type that
-    receive the rounded parameters."""
+    them to save, and copy into them or assign tensors of the same size and type to resume.  `copies`,
+    if given, are tensors of one 16-bit or float32 type that receive the rounded parameters.  A tensor
+    that was replaced since the last step (also through its .data) is checked again and used from then on."""
 
     def __init__(self, params, bits: int = 32, betas=(0.9, 0.999), eps: float = 1e-8, weight_decay: float = 0.01,
                  copies=None):
@@ -688,7 +689,7 @@ class AdamW:
             raise ValueError(f"bits must be 8 or 32, got {bits}")
         self.params = list(params)
         self.copies = None if copies is None else list(copies)
-        self.bits, self.betas, self.eps, self.weight_decay = bits, tuple(betas), eps, weight_decay
+        self._bits, self.betas, self.eps, self.weight_decay = bits, tuple(betas), eps, weight_decay
         self.t = 0
         if self.copies is not None and len(self.copies) != len(self.params):
             raise ValueError(f"{len(self.copies)} copies for {len(self.params)} parameters")
@@ -698,16 +699,9 @@ class AdamW:
         at = 0
         for i, p in enumerate(self.params):
             _flat(p, f"params[{i}]", dtype=torch.float32)
-            if p.device != self.params[0].device:
-                raise ValueError("parameters must live on one GPU")
             self.sizes[i] = p.numel()
             self.starts.append(at)
             at += -(-p.numel() // ADAMW_BLOCK) * ADAMW_BLOCK
-        self._copy_type = F32
-        if self.copies:
-            self._copy_type = _type(self.copies[0].dtype, "copies")
-            for i, c in enumerate(self.copies):
-                _flat(c, f"copies[{i}]", self.sizes[i], self.copies[0].dtype)
         dev = self.params[0].device if n else "cuda"
         wide = bits == 32
         self.m = torch.zeros(at, dtype=torch.float32 if wide else torch.int8, device=dev)
@@ -716,26 +710,63 @@ class AdamW:
         self.v_scale = None if wide else torch.zeros(at // ADAMW_BLOCK, dtype=torch.float32, device=dev)
         # one qha_adamw_tensor per row: n, param, grad, copy, m, v, m_scale, v_scale
         self._table = np.zeros((max(n, 1), 8), dtype=np.int64)
-        for i, s in enumerate(self.starts):
-            e = 4 if wide else 1
-            self._table[i] = (self.sizes[i], self.params[i].data_ptr(), 0,
-                              self.copies[i].data_ptr() if self.copies else 0, self.m.data_ptr() + s * e,
-                              self.v.data_ptr() + s * e,
-                              0 if wide else self.m_scale.data_ptr() + s // ADAMW_BLOCK * 4,
-                              0 if wide else self.v_scale.data_ptr() + s // ADAMW_BLOCK * 4)
+        self._table[:n, 0] = self.sizes
         self._table_ptr = self._table.ctypes.data
+        self._total, self._seen = at, None
+        self._look()
+
+    @property
+    def bits(self):
+        return self._bits
+
+    def _tensors(self):
+        state = [self.m, self.v] if self._bits == 32 else [self.m, self.v, self.m_scale, self.v_scale]
+        return self.params + (self.copies or []) + state
+
+    def _look(self):
+        """Checks every tensor and writes its address into the table, if any address is another one than at
+        the last step.  `_held` aliases the tensors seen: while it does, their memory is not handed out again, so an
+        equal address is the same memory."""
+        seen = [t.data_ptr() for t in self._tensors()]
+        if seen == self._seen:
+            return
+        self._seen = None
+        n, wide, total = len(self.sizes), self._bits == 32, self._total
+        if len(self.params) != n or (self.copies is not None and len(self.copies) != n):
+            raise ValueError(f"{n} parameters were given, now there are {len(self.params)}")
+        table = self._table
+        for i, (p, size) in enumerate(zip(self.params, self.sizes)):
+            table[i, 1] = _flat(p, f"params[{i}]", size, torch.float32)
+        if len({t.device for t in self._tensors()}) > 1:
+            raise ValueError("parameters, copies and moments must live on one GPU")
+        self._copy_type = F32
+        if self.copies:
+            self._copy_type = _type(self.copies[0].dtype, "copies")
+            for i, c in enumerate(self.copies):
+                table[i, 3] = _flat(c, f"copies[{i}]", self.sizes[i], self.copies[0].dtype)
+        if n:
+            starts = np.array(self.starts, dtype=np.int64)
+            table[:n, 4] = _flat(self.m, "m", total, torch.float32 if wide else torch.int8) + starts * (4 if wide else 1)
+            table[:n, 5] = _flat(self.v, "v", total, torch.float32 if wide else torch.uint8) + starts * (4 if wide else 1)
+            if not wide:
+                blocks = total // ADAMW_BLOCK
+                table[:n, 6] = _flat(self.m_scale, "m_scale", blocks, torch.float32) + starts // ADAMW_BLOCK * 4
+                table[:n, 7] = _flat(self.v_scale, "v_scale", blocks, torch.float32) + starts // ADAMW_BLOCK * 4
+        self._held = [t.detach() for t in self._tensors()]
+        self._seen = seen
 
     def step(self, grads, lr: float, grad_scale: float = 1.0, stream=None):
         """One step with grads (one tensor per parameter, of one type; scaled by grad_scale)."""
-        n = len(self.params)
+        n = len(self.sizes)
         if len(grads) != n:
             raise ValueError(f"{len(grads)} gradients for {n} parameters")
         if n == 0:
             return
+        self._look()
         dtype = grads[0].dtype
         self._table[:n, 2] = [g.data_ptr() if g.dtype is dtype and g.numel() == size and g.is_cuda and g.is_contiguous()
                               else _flat(g, "a gradient", size, dtype) for g, size in zip(grads, self.sizes)]
-        status = _adamw_step(self._table_ptr, n, self.bits, _type(dtype, "grads"), self._copy_type, lr, *self.betas,
+        status = _adamw_step(self._table_ptr, n, self._bits, _type(dtype, "grads"), self._copy_type, lr, *self.betas,
                              self.eps, self.weight_decay, grad_scale, self.t + 1, _stream(stream))
         _check(status, "qha_adamw_step")
         self.t += 1
@@ -743,12 +774,13 @@ class AdamW:
     def values(self, m_out=None, v_out=None, stream=None):
         """The moments as flat float32 tensors (into m_out and v_out, or new ones; 32-bit moments are
         returned as they are)."""
-        if self.bits == 32:
+        if self._bits == 32:
             return self.m, self.v
-        n = self.m.numel()
+        n, blocks = self._total, self._total // ADAMW_BLOCK
         m_out = torch.empty(n, dtype=torch.float32, device=self.m.device) if m_out is None else m_out
         v_out = torch.empty(n, dtype=torch.float32, device=self.m.device) if v_out is None else v_out
-        _check(_adamw_values(self.m.data_ptr(), self.m_scale.data_ptr(), _flat(m_out, "m_out", n, torch.float32),
-                             self.v.data_ptr(), self.v_scale.data_ptr(), _flat(v_out, "v_out", n, torch.float32), n,
-                             _stream(stream)), "qha_adamw_values")
+        _check(_adamw_values(_flat(self.m, "m", n, torch.int8), _flat(self.m_scale, "m_scale", blocks, torch.float32),
+                             _flat(m_out, "m_out", n, torch.float32), _flat(self.v, "v", n, torch.uint8),
+                             _flat(self.v_scale, "v_scale", blocks, torch.float32),
+                             _flat(v_out, "v_out", n, torch.float32), n, _stream(stream)), "qha_adamw_values")
         return m_out, v_out

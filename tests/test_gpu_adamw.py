@@ -280,3 +280,32 @@ def test_binding_refuses_gradients_that_do_not_fit():
     with pytest.raises(ValueError, match="lr"):
         opt.step([p.clone()], -1.0)
     assert opt.t == 0
+
+
+@pytest.mark.parametrize("bits", [8, 32])
+def test_replaced_tensors_are_the_ones_updated(bits):
+    """A resume that assigns moments and replaces a parameter's .data goes on exactly as the run it came from, and
+    leaves the tensors that were replaced alone."""
+    H.require_gpu()
+    import torch
+    from quantized_halo_aggregation_amd import binding as B
+    H.note(f"adamw {bits} resume")
+    p, g, _, _ = _inputs([1000, 33], 9)
+    grads = [H.dev(x) for x in g]
+    names = ("m", "v") + (("m_scale", "v_scale") if bits == 8 else ())
+    run, resumed = (B.AdamW([H.dev(x) for x in p], bits=bits) for _ in range(2))
+    run.step(grads, 1e-2)
+    resumed.step(grads, 0.5)             # somewhere else: everything is replaced below
+    old = [resumed.params[0].detach()] + [getattr(resumed, k) for k in names]
+    kept = [t.clone() for t in old]
+    for a, b in zip(resumed.params, run.params):
+        a.data = b.clone()
+    for k in names:
+        setattr(resumed, k, getattr(run, k).clone())
+    for _ in range(2):
+        run.step(grads, 1e-2)
+        resumed.step(grads, 1e-2)
+    for a, b in zip(run.params + [getattr(run, k) for k in names], resumed.params + [getattr(resumed, k) for k in names]):
+        assert torch.equal(a, b)
+    for a, b in zip(old, kept):
+        assert torch.equal(a, b)

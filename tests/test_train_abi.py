@@ -200,3 +200,70 @@ def test_group_norm_workspace_of_narrow_rows():
             assert _norm_bwd(ldx=c, lddy=c, lddx=c, wsb=bwd - 1, **shape) == B.QHA_ERR_WORKSPACE
             if fwd:
                 assert _norm_fwd(ldx=c, ldy=c, wsb=fwd - 1, **shape) == B.QHA_ERR_WORKSPACE
+
+
+@pytest.fixture
+def adamw_calls(monkeypatch):
+    """AdamW over host tensors, with the tables that would reach qha_adamw_step recorded in its place."""
+    tables = []
+
+    def record(table, n, *rest):
+        import ctypes
+        tables.append(np.ctypeslib.as_array((ctypes.c_int64 * (8 * n)).from_address(table)).reshape(n, 8).copy())
+        return B.QHA_OK
+    check = B._flat
+
+    def on_host(t, name, n=None, dtype=None):
+        class Gpu(torch.Tensor):
+            is_cuda = True
+        return check(t.as_subclass(Gpu) if isinstance(t, torch.Tensor) else t, name, n, dtype)
+    monkeypatch.setattr(B, "_adamw_step", record)
+    monkeypatch.setattr(B, "_flat", on_host)
+    return tables
+
+
+@pytest.mark.parametrize("bits", [8, 32])
+def test_adamw_writes_where_its_tensors_are_now(adamw_calls, bits):
+    """Parameters whose .data was replaced, and moments, scales and copies that were assigned on resume."""
+    params = [torch.zeros(300), torch.zeros(5)]
+    opt = B.AdamW(params, bits=bits, copies=[torch.zeros(300, dtype=torch.bfloat16), torch.zeros(5, dtype=torch.bfloat16)])
+    grads = [torch.zeros(300), torch.zeros(5)]
+
+    def expect():
+        opt.step(grads, 1e-3, stream=0)
+        t, e = adamw_calls[-1], 4 if bits == 32 else 1
+        assert t[:, 0].tolist() == [300, 5]
+        assert t[:, 1].tolist() == [p.data_ptr() for p in params]
+        assert t[:, 2].tolist() == [g.data_ptr() for g in grads]
+        assert t[:, 3].tolist() == [c.data_ptr() for c in opt.copies]
+        assert t[:, 4].tolist() == [opt.m.data_ptr() + s * e for s in opt.starts]
+        assert t[:, 5].tolist() == [opt.v.data_ptr() + s * e for s in opt.starts]
+        if bits == 8:
+            assert t[:, 6].tolist() == [opt.m_scale.data_ptr() + s // 256 * 4 for s in opt.starts]
+            assert t[:, 7].tolist() == [opt.v_scale.data_ptr() + s // 256 * 4 for s in opt.starts]
+    expect()
+    params[1].data = torch.ones(5)
+    expect()
+    for name in ("m", "v") + (("m_scale", "v_scale") if bits == 8 else ()):
+        setattr(opt, name, getattr(opt, name).clone())
+        expect()
+    opt.copies[0] = opt.copies[0].clone()
+    expect()
+    opt.m.data = opt.m.clone()
+    expect()
+    # what does not fit is refused, and goes nowhere
+    calls, t = len(adamw_calls), opt.t
+    for name, bad in (("m", opt.m[:-1].clone()), ("v", opt.v.double()), ("m", opt.m.repeat(2)[::2])):
+        good = getattr(opt, name)
+        setattr(opt, name, bad)
+        with pytest.raises((ValueError, TypeError), match=name):
+            opt.step(grads, 1e-3, stream=0)
+        setattr(opt, name, good)
+    params[0].data = torch.zeros(299)
+    with pytest.raises(ValueError, match="params"):
+        opt.step(grads, 1e-3, stream=0)
+    assert len(adamw_calls) == calls and opt.t == t
+    params[0].data = torch.zeros(300)
+    expect()
+    with pytest.raises(AttributeError):
+        opt.bits = 40 - bits
