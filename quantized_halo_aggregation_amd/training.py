@@ -41,7 +41,6 @@ class GatedNormStack:
                         "norm_bias": torch.zeros(d, device=dev)} for _ in range(layers)]
         self.grads = [{k: torch.empty_like(v) for k, v in p.items()} for p in self.params]
         self.opt = B.AdamW([p[k] for p in self.params for k in NAMES], bits=state_bits, weight_decay=weight_decay)
-        self._grad_list = [g[k] for g in self.grads for k in NAMES]
         rows = lambda: torch.empty(n, d, dtype=torch.float32, device=dev)
         # kept for the backward, per layer: A, gate, up, H and the norm's statistics
         self.X = [rows() for _ in range(layers + 1)]
@@ -83,7 +82,9 @@ class GatedNormStack:
         return g
 
     def update(self, lr: float):
-        self.opt.step(self._grad_list, lr)
+        # as they are now: a caller may have put other tensors in their places
+        self.opt.params = [p[k] for p in self.params for k in NAMES]
+        self.opt.step([g[k] for g in self.grads for k in NAMES], lr)
 
     def step(self, x, loss_grad, lr: float, epoch: int = 0):
         """One training step; loss_grad maps the last layer's rows to their gradient.  Returns the rows."""

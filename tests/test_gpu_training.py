@@ -73,3 +73,28 @@ def test_the_example_learns(bits):
     H.note(f"training example, {bits}-bit moments")
     losses = train_nodes.train(25, bits, n_in=1200, n_h=400, nnz=15000, d=32)
     assert np.isfinite(losses).all() and losses[-1] < 0.5 * losses[0], losses[::6]
+
+
+def test_replaced_weights_are_the_ones_trained():
+    """Weights and gradient buffers put into the layers' dicts (a loaded checkpoint) train as the ones they replace."""
+    H.require_gpu()
+    import torch
+    from quantized_halo_aggregation_amd.pipeline import GpuPartition
+    from quantized_halo_aggregation_amd.training import GatedNormStack
+    part = synth.make_partition(synth.small_workload(500, 200, 5000, 32, bits=("const", 32)))
+    gp = GpuPartition(part)
+    x, grad = torch.from_numpy(part.x).cuda(), torch.from_numpy(part.grad_top).cuda()
+    H.note("training step with replaced weights")
+    stacks = [GatedNormStack(gp, 2, seed=5) for _ in range(2)]
+    old = stacks[1].params[0]["w_gate"]
+    kept = old.clone()
+    for d in stacks[1].params + stacks[1].grads:
+        for k in d:
+            d[k] = d[k].clone()
+    for _ in range(2):
+        for s in stacks:
+            s.step(x, lambda y: grad, 1e-2)
+    for a, b in zip(*(s.params for s in stacks)):
+        for k in a:
+            assert torch.equal(a[k], b[k]), k
+    assert torch.equal(old, kept) and not torch.equal(stacks[1].params[0]["w_gate"], kept)
