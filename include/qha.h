@@ -384,7 +384,7 @@ size_t qha_dense_backward_workspace(int64_t m, int64_t n, int64_t k);
 
 /* activations */
 #define QHA_ACT_NONE 0
-#define QHA_ACT_RELU 1          /* z > 0 ? z : 0 */
+#define QHA_ACT_RELU 1          /* z <= 0 ? 0 : z (NaN stays NaN, with slope 1) */
 #define QHA_ACT_SILU 2          /* z / (1 + exp(-z)) */
 #define QHA_ACT_GELU 3          /* z (1 + erf(z / sqrt 2)) / 2 */
 

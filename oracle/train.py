@@ -64,7 +64,7 @@ _erf = np.vectorize(math.erf, otypes=[np.float64])
 
 def act(z, kind):
     if kind == "relu":
-        return np.where(z > 0, z, 0.0)
+        return np.where(z <= 0, 0.0, z)          # NaN stays NaN
     if kind == "silu":
         return z / (1.0 + np.exp(-z))
     if kind == "gelu":
@@ -74,7 +74,7 @@ def act(z, kind):
 
 def act_slope(z, kind):
     if kind == "relu":
-        return (z > 0).astype(np.float64)
+        return np.where(z <= 0, 0.0, 1.0)
     if kind == "silu":
         s = 1.0 / (1.0 + np.exp(-z))
         return s + z * s * (1.0 - s)

@@ -15,9 +15,10 @@ namespace qha {
 __device__ __forceinline__ float exp_neg(float z) { return __builtin_amdgcn_exp2f(fminf(z * -1.44269504088896341f, 127.0f)); }
 __device__ __forceinline__ float sigmoid(float z) { return z == z ? __builtin_amdgcn_rcpf(1.0f + exp_neg(z)) : z; }
 
-// act(z); `act` is uniform over a launch, so the branch costs one scalar test.
+// act(z); `act` is uniform over a launch, so the branch costs one scalar test.  ReLU asks for z <= 0, which NaN is
+// not: it stays NaN, with slope 1.
 __device__ __forceinline__ float activate(float z, int32_t act) {
-  if (act == QHA_ACT_RELU) return z > 0.0f ? z : 0.0f;
+  if (act == QHA_ACT_RELU) return z <= 0.0f ? 0.0f : z;
   if (act == QHA_ACT_SILU) return z * sigmoid(z);
   if (act == QHA_ACT_GELU) return 0.5f * z * (1.0f + erff(z * 0.70710678118654752f));
   return z;
@@ -26,8 +27,8 @@ __device__ __forceinline__ float activate(float z, int32_t act) {
 // act(z) and act'(z).
 __device__ __forceinline__ float activate_both(float z, int32_t act, float* slope) {
   if (act == QHA_ACT_RELU) {
-    *slope = z > 0.0f ? 1.0f : 0.0f;
-    return z > 0.0f ? z : 0.0f;
+    *slope = z <= 0.0f ? 0.0f : 1.0f;
+    return z <= 0.0f ? 0.0f : z;
   }
   if (act == QHA_ACT_SILU) {
     const float s = sigmoid(z);
@@ -50,7 +51,7 @@ __device__ __forceinline__ float grad_z(float dy, float x, float mean, float rst
   if (act == QHA_ACT_RELU) {
     const double z = (static_cast<double>(x) - static_cast<double>(mean)) * static_cast<double>(rstd) *
                          static_cast<double>(w) + static_cast<double>(b);
-    return z > 0.0 ? dy : 0.0f;
+    return z <= 0.0 ? 0.0f : dy;
   }
   float slope;
   activate_both(xhat * w + b, act, &slope);

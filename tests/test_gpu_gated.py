@@ -275,3 +275,33 @@ def test_graph_replays_equal_the_eager_call(dtype):
             torch.cuda.synchronize()
             for x, y in zip(want, out):
                 assert torch.equal(x, y), i
+
+
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16", "float16"])
+@pytest.mark.parametrize("kind", list(KINDS))
+def test_every_activation_keeps_nan(kind, dtype):
+    """A row of A with a NaN has NaN in all of H, and a NaN among the kept gates makes that row's dA NaN, whatever the
+    activation; other rows are as without it."""
+    H.require_gpu()
+    import torch
+    from quantized_halo_aggregation_amd import binding as B
+    for m in (5, 200):
+        H.note(f"gated NaN {kind} {dtype} {m}")
+        a, wg, wu, dh = _data(m, 64, 40, dtype, 8)
+        clean = [t.clone() for t in _forward(a.cuda(), wg.cuda(), wu.cuda(), kind)]
+        a[m - 2, 3] = float("nan")
+        h, _, _ = _forward(a.cuda(), wg.cuda(), wu.cuda(), kind)
+        rows = np.arange(m) != m - 2
+        assert np.isnan(_np(h)[m - 2]).all() and np.array_equal(_np(h)[rows], _np(clean[0])[rows])
+        h, gate, up = clean
+        ws = _space(B.gated_backward_workspace(a.dtype, m, 64, 40))
+        da = [torch.zeros(m, 40, dtype=a.dtype, device="cuda") for _ in range(2)]
+        dws = [torch.zeros(64, 40, device="cuda") for _ in range(2)]
+        a[m - 2, 3] = 0.5
+        for out in da:
+            B.gated_backward(dh.cuda(), gate, up, a.cuda(), wg.cuda(), wu.cuda(), out, *dws, act=KINDS[kind], workspace=ws)
+            gate[m - 2, 5] = float("nan")
+        assert np.isfinite(_np(da[0])).all() and np.isnan(_np(da[1])[m - 2]).all()
+        assert np.array_equal(_np(da[1])[rows], _np(da[0])[rows])
+        # the gate's column is NaN in dup, and in dgate where the slope needs the gate
+        assert np.isnan(_np(dws[1])[5]).all() and np.isfinite(np.delete(_np(dws[1]), 5, 0)).all()

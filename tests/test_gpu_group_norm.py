@@ -293,3 +293,29 @@ def test_four_and_twelve_float32_channels(shape):
         H.note(f"group norm narrow {shape} {kind}")
         _check_fwd(shape, "float32", kind)
         _check_bwd(shape, "float32", kind)
+
+
+@pytest.mark.parametrize("kind", list(KINDS))
+def test_every_activation_keeps_nan(kind):
+    """A NaN in x reaches every y and dx of its sample's group, whatever the activation, in rows, small and large samples,
+    and no other; a NaN weight or bias reaches its channel."""
+    H.require_gpu()
+    import torch
+    from quantized_halo_aggregation_amd import binding as B
+    for s, p, c in ((6, 1, 32), (4, 6, 32), (3, 400, 32), (4, 1, 12), (3, 700, 12)):
+        H.note(f"group norm NaN {kind} {s}x{p}x{c}")
+        x, dy, w, b = _data(s * p, c, "float32", 3)
+        x[p, c // 2 + 1] = float("nan")
+        b[0] = float("nan")
+        y, mean, rstd = _run_fwd(x.cuda(), H.dev(w), H.dev(b), 2, p, kind)
+        bad = np.zeros((s * p, c), bool)
+        bad[p:2 * p, c // 2:] = True
+        hit = bad.copy()
+        hit[:, 0] = True
+        assert np.array_equal(np.isnan(_np(y)), hit)
+        dx = torch.zeros(s * p, c, device="cuda")
+        ws = torch.empty(max(B.group_norm_workspace(s * p, p, c, 2, True), 16), dtype=torch.uint8, device="cuda")
+        b[0] = 0.0
+        B.group_norm_bwd(dy.cuda(), x.cuda(), mean, rstd, dx, 2, weight=H.dev(w), bias=H.dev(b), act=KINDS[kind],
+                         positions=p, workspace=ws)
+        assert np.array_equal(np.isnan(_np(dx)), bad)

@@ -61,3 +61,12 @@ def test_code_blocks_with_zeros_and_values_that_are_not_finite():
     assert scale[0] == 0 and np.isnan(scale[1]) and scale[2] == 2.0
     assert (codes[:599] == 0).all() and codes[599] == -127
     assert np.isnan(T.decode(codes, scale, 127, 2)[256:512]).all()
+
+
+@pytest.mark.parametrize("kind", ["none", "relu", "silu", "gelu"])
+def test_activations_keep_nan(kind):
+    z = np.array([-1.0, np.nan, 0.0, 2.0])
+    assert np.array_equal(np.isnan(T.act(z, kind)), np.isnan(z))
+    assert np.isfinite(T.act_slope(z, kind)[[0, 2, 3]]).all()
+    if kind == "relu":
+        assert T.act(z, kind)[[0, 2, 3]].tolist() == [0.0, 0.0, 2.0] and T.act_slope(z, kind).tolist() == [0.0, 1.0, 0.0, 1.0]
