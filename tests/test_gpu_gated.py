@@ -305,3 +305,131 @@ def test_every_activation_keeps_nan(kind, dtype):
         assert np.array_equal(_np(da[1])[rows], _np(da[0])[rows])
         # the gate's column is NaN in dup, and in dgate where the slope needs the gate
         assert np.isnan(_np(dws[1])[5]).all() and np.isfinite(np.delete(_np(dws[1]), 5, 0)).all()
+
+
+def _check_f16_range(m, n, k, kind, rows, cols, weights):
+    """f16 gradients whose dH has the sizes `rows` and whose up has the sizes `cols` (cycled).
+
+    A term of [dG dU] carries 16 u of |dH U| (1 + |G|) or |dH| (1 + |G|) as above.  For dW it enters in two parts, scaled so that its
+    column's largest is in [2^14, 2^15): 2^-22 of itself, or half of f16's last step 2^-24 against 2^14 at least, 2^-39 of
+    that largest.  For dA in one, scaled by its row: 2^-11 of itself or 2^-39 of the row's largest."""
+    import torch
+    from quantized_halo_aggregation_amd import binding as B
+    rng = np.random.default_rng(m + n + k)
+    half = lambda x: torch.from_numpy(np.asarray(x, np.float32)).to(torch.float16)
+    fill = lambda sizes, count: np.resize(np.asarray(sizes, np.float64), count)
+    a, gate = half(rng.standard_normal((m, k))), half(rng.standard_normal((m, n)))
+    dh = half(rng.standard_normal((m, n)) * fill(rows, m)[:, None])
+    up = half(rng.standard_normal((m, n)) * fill(cols, n))
+    wg, wu = (half(rng.standard_normal((n, k)) * weights) for _ in range(2))
+    da = torch.full((m, k), float("nan"), dtype=torch.float16, device="cuda")
+    dw = [torch.full((n, k), float("nan"), device="cuda") for _ in range(2)]
+    B.gated_backward(*(x.cuda() for x in (dh, gate, up, a, wg, wu)), da, *dw, act=KINDS[kind],
+                     workspace=_space(B.gated_backward_workspace(torch.float16, m, n, k)))
+    fdh, fg, fu, fa, fwg, fwu = (_np(x) for x in (dh, gate, up, a, wg, wu))
+    rda, *rdw = T.gated_backward(fdh, fg, fu, fa, fwg, fwu, kind)
+    aa, aw = np.abs(fa), (np.abs(fwg), np.abs(fwu))
+    terms = np.abs(fdh * fu * T.act_slope(fg, kind)), np.abs(fdh * T.act(fg, kind))
+    own = 16 * U * np.abs(fdh * fu) * (1 + np.abs(fg)), 16 * U * np.abs(fdh) * (1 + np.abs(fg))
+    for name, got, ref, t, e in zip(("dwg", "dwu"), dw, rdw, terms, own):
+        e = e + 2.0 ** -22 * t + 2.0 ** -39 * t.max(0)
+        bound = e.T @ aa + 2 * (m + 8) * U * ((t + e).T @ aa)
+        err = np.abs(_np(got) - ref)
+        assert (err <= bound).all(), (name, float((err / bound).max()))
+    top = np.maximum(terms[0].max(1), terms[1].max(1))[:, None]
+    e = sum((o + 2.0 ** -11 * t + 2.0 ** -39 * top) @ w + 2 * (2 * n + 8) * U * (t @ w) for o, t, w in zip(own, terms, aw))
+    e = e + HALF["float16"] * (np.abs(rda) + e) + TINY["float16"]
+    fits = np.abs(rda) + e < 65504
+    err = np.abs(_np(da) - rda)
+    assert fits.mean() > 0.9 and (err <= e)[fits].all(), ("da", float((err / e)[fits].max()))
+
+
+@pytest.mark.parametrize("rows,cols,weights", [((1e-5,), (1.0,), 0.1), ((1e-3,), (1e-4,), 0.1), ((3e2,), (1e4,), 1e-4),
+                                               ((1e-6, 1.0, 1e4), (1e-4, 1.0, 1e3, 1e-2), 1e-4), ((1e4, 1e-7), (1.0,), 0.05)],
+                         ids=["small", "product_underflows", "product_overflows", "mixed", "rows_far_apart"])
+@pytest.mark.parametrize("shape", [(1, 8, 16), (33, 72, 40), (300, 520, 264), (2500, 64, 128), (700, 1032, 72)],
+                         ids=lambda s: "x".join(map(str, s)))
+def test_f16_gradients_of_any_size(shape, rows, cols, weights):
+    """dgate and dup leave f16's range in both directions; the weight gradients are float32 and stay exact to their terms."""
+    H.require_gpu()
+    kind = ["silu", "none", "gelu", "relu"][sum(shape) // 8 % 4]
+    H.note(f"gated f16 range {shape} {rows} {cols} {kind}")
+    _check_f16_range(*shape, kind, rows, cols, weights)
+
+
+def test_f16_gradients_that_are_not_finite():
+    """An infinite dH makes its columns' weight gradients infinite with A's signs and its row of dA not finite; all else is as
+    without it."""
+    H.require_gpu()
+    import torch
+    from quantized_halo_aggregation_amd import binding as B
+    m, n, k = 150, 72, 40
+    H.note("gated f16 infinite gradient")
+    a, wg, wu, dh = _data(m, n, k, "float16", 5)
+    a[7] = torch.where(a[7] == 0, torch.ones_like(a[7]), a[7])
+    gate, up = torch.full((m, n), 2.0, dtype=torch.float16), torch.full((m, n), 3.0, dtype=torch.float16)
+    ws = _space(B.gated_backward_workspace(torch.float16, m, n, k))
+    runs = []
+    for value in (0.0, float("inf")):
+        dh[7, 11] = value
+        out = [torch.zeros(m, k, dtype=torch.float16, device="cuda")] + [torch.zeros(n, k, device="cuda") for _ in range(2)]
+        B.gated_backward(*(x.cuda() for x in (dh, gate, up, a, wg, wu)), *out, act=0, workspace=ws)
+        runs.append([_np(x) for x in out])
+    for i, hit in ((0, 7), (1, 11), (2, 11)):
+        keep = np.arange(runs[0][i].shape[0]) != hit
+        assert np.array_equal(runs[0][i][keep], runs[1][i][keep])
+    assert not np.isfinite(runs[1][0][7]).any()
+    assert (runs[1][1][11] == np.inf * np.sign(_np(a)[7])).all() and (runs[1][2][11] == runs[1][1][11]).all()
+
+
+def test_f16_gradients_in_a_graph():
+    """The sizes are found again in every replay."""
+    H.require_gpu()
+    import torch
+    from quantized_halo_aggregation_amd import binding as B
+    m, n, k = 700, 136, 64
+    H.note("gated f16 graph")
+    a, wg, wu, dh = (x.cuda() for x in _data(m, n, k, "float16", 2))
+    _, gate, up = _forward(a, wg, wu, "silu")
+    out = [torch.zeros_like(a)] + [torch.zeros(n, k, device="cuda") for _ in range(2)]
+    ws = _space(B.gated_backward_workspace(torch.float16, m, n, k))
+    step = lambda: B.gated_backward(dh, gate, up, a, wg, wu, *out, workspace=ws)
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for scale in (1e-3, 1e-2, 1e4, 1e-4):
+        dh.mul_(scale)
+        step()
+        want = [x.clone() for x in out]
+        for x in out:
+            x.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        for x, y in zip(want, out):
+            assert torch.equal(x, y) and torch.isfinite(x).all() and x.abs().max() > 0
+
+
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16", "float16"])
+@pytest.mark.parametrize("shape", [(1, 8, 16), (150, 72, 40), (300, 520, 264), (2500, 64, 128)], ids=lambda s: "x".join(map(str, s)))
+def test_the_workspace_is_as_large_as_its_query_says(shape, dtype):
+    """Both directions with exactly the queried bytes, inside a larger buffer whose other bytes stay as they were."""
+    H.require_gpu()
+    import torch
+    from quantized_halo_aggregation_amd import binding as B
+    m, n, k = shape
+    H.note(f"gated workspace {shape} {dtype}")
+    a, wg, wu, dh = (x.cuda() for x in _data(m, n, k, dtype, 1))
+    out = [torch.zeros(m, n, dtype=a.dtype, device="cuda") for _ in range(3)]
+    grads = [torch.zeros_like(a)] + [torch.zeros(n, k, device="cuda") for _ in range(2)]
+    pad = 1 << 16
+    for backward in (False, True):
+        need = (B.gated_backward_workspace if backward else B.gated_project_workspace)(a.dtype, m, n, k)
+        buf = torch.full((pad + need + pad,), 0xA5, dtype=torch.uint8, device="cuda")
+        ws = buf[pad:pad + need] if need else None
+        if backward:
+            B.gated_backward(dh, out[1], out[2], a, wg, wu, *grads, workspace=ws)
+        else:
+            B.gated_project(a, wg, wu, out[0], gate=out[1], up=out[2], workspace=ws)
+        assert (buf[:pad] == 0xA5).all() and (buf[pad + need:] == 0xA5).all()
