@@ -408,7 +408,7 @@ int qha_gated_project(int64_t m, int64_t n, int64_t k, int32_t type, const void*
  *   dgate = dH up act'(gate),  dup = dH act(gate),   dA = dgate W_gate + dup W_up   (elements of type)
  *   dW_gate = dgate^T A,  dW_up = dup^T A            (float32 [n x k], overwritten; zeros when m = 0)
  * dgate and dup are the matrix cores' operands: float32 in three parts; in 16-bit types rounded once for
- * dA, which is rounded itself, and in two parts for the float32 weight gradients.  f16 values are scaled by
+ * dA, which is rounded itself, and for the float32 weight gradients in three parts of bf16 or two of f16.  f16 values are scaled by
  * powers of two to the largest finite one of their row (for dA) or column (for dW) first and the results scaled
  * back, so that gradients of any size keep f16's full precision: a part's subnormals are below 2^-39 of that largest value.
  * dA is nullable (a first layer needs none) and must not overlap the other arrays.  Long

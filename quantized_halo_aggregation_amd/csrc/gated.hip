@@ -339,7 +339,7 @@ __device__ __forceinline__ bool tile_of(const ProductArgs& p, int64_t b, int64_t
 }
 
 // T: 16-bit type of the planes; O: type of the stored result; PA, PB: parts of A's and B's values (1 and 1,
-// 2 and 1, or 3 and 3); RA, RB: they are split from float32 values in LDS (else stored as planes).
+// 2 and 1, 3 and 1, or 3 and 3); RA, RB: they are split from float32 values in LDS (else stored as planes).
 // BM x BN tile of C (forward: BN counts the rows of Wg and Wu together), wavefronts of WM x WN.
 template <typename T, typename O, int PA, int PB, bool RA, bool RB, int OA, int OB, int OUT, int BM, int BN, int BK, int WM, int WN>
 __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) void product_kernel(ProductArgs p) {
@@ -409,7 +409,8 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) void product_kernel(Pro
             c = mma<T>(fb[now][j][2], fa[now][i][0], c);
             c = mma<T>(fb[now][j][0], fa[now][i][1], c);
             c = mma<T>(fb[now][j][1], fa[now][i][0], c);
-          } else if constexpr (PA == 2) {
+          } else if constexpr (PA > 1) {
+            if constexpr (PA == 3) c = mma<T>(fb[now][j][0], fa[now][i][2], c);
             c = mma<T>(fb[now][j][0], fa[now][i][1], c);
           }
           acc[i][j] = mma<T>(fb[now][j][0], fa[now][i][0], c);
@@ -581,9 +582,10 @@ __device__ __forceinline__ void gate_terms_at(const GatedArgs& p, int64_t r, int
   gate_terms(dh, g, u, p.act, dg, du);
 }
 
-// [dG dU], 2n columns wide, as the products' operand: float32 values, or two parts of bf16 in two planes.  dA is
-// stored in bf16 and takes the first part alone (one rounding of each term, as its own result has); dW is
-// float32 and takes both, which leaves 2^-17 of a term.
+// [dG dU], 2n columns wide, as the products' operand: float32 values, or their three parts of bf16 in as many
+// planes.  dA is stored in bf16 and takes the first part alone (one rounding of each term, as its own result has); dW is
+// float32 and takes all three, which are the value exactly (two leave 2^-17 of a term: 2.6e-6 of dW at 8191 rows where
+// float32 operands leave 1.6e-6).
 template <typename T>
 __global__ __launch_bounds__(256) void gate_grad_kernel(GatedArgs p, T* out) {
   typedef T vec __attribute__((ext_vector_type(4)));
@@ -591,15 +593,29 @@ __global__ __launch_bounds__(256) void gate_grad_kernel(GatedArgs p, T* out) {
   for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < p.m * per;
        i += static_cast<int64_t>(gridDim.x) * 256) {
     const int64_t r = i / per, c = i % per * 4;
-    f32x4 dg, du;
-    gate_terms_at<T>(p, r, c, dg, du);
+    f32x4 d[2];
+    gate_terms_at<T>(p, r, c, d[0], d[1]);
     T* o = out + r * 2 * p.n + c;
-    const vec g1 = __builtin_convertvector(dg, vec), u1 = __builtin_convertvector(du, vec);
-    *reinterpret_cast<vec*>(o) = g1;
-    *reinterpret_cast<vec*>(o + p.n) = u1;
-    if constexpr (sizeof(T) == 2) {
-      store4<T>(o + plane, dg - __builtin_convertvector(g1, f32x4));
-      store4<T>(o + p.n + plane, du - __builtin_convertvector(u1, f32x4));
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      if constexpr (sizeof(T) == 4) {
+        *reinterpret_cast<vec*>(o + h * p.n) = d[h];
+      } else {
+        vec first, second, third;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          // finite values beyond bf16's largest start with it; an infinity is whole in its first part
+          constexpr float top = 0x1.FEp127f;
+          const float x = d[h][e], y = __builtin_isfinite(x) ? fminf(fmaxf(x, -top), top) : x;
+          first[e] = static_cast<T>(y);
+          const float rest = __builtin_isinf(x) ? 0.0f : x - static_cast<float>(first[e]);
+          second[e] = static_cast<T>(rest);
+          third[e] = static_cast<T>(rest - static_cast<float>(second[e]));
+        }
+        *reinterpret_cast<vec*>(o + h * p.n) = first;
+        *reinterpret_cast<vec*>(o + h * p.n + plane) = second;
+        *reinterpret_cast<vec*>(o + h * p.n + 2 * plane) = third;
+      }
     }
   }
 }
@@ -912,7 +928,8 @@ int64_t tiles_of(int64_t m, int64_t n, int64_t bm, int64_t bn) { return ((m + bm
 // Tile shapes.  Larger tiles read LDS less per product and need enough of them to occupy the compute
 // units: forward of 16384 x 2048 -> 8192 bf16, 1044 us in 256 x 256 tiles (4096 of them) against
 // 1335 us in 128 x 128; dA of 8191 x 8192 -> 1024, 212 us in 256 x 256 (128 tiles, half the chip) against
-// 152 us in 128 x 128; its dW 253 us in 256 x 128 against 331 us.  Three-part products: dA and dW of
+// 152 us in 128 x 128; its dW of two parts (f16) 253 us in 256 x 128 against 331 us, of three (bf16) 373 us in 128 x 128 with
+// steps of 32, two blocks to a compute unit, and as long in 256 x 128; steps of 64 take 470 us.  Three-part products: dA and dW of
 // 30k x 256 -> 256 in 128 x 256, 48 and 58 us, against 59 and 59 us in 128 x 128; the forward, with three results to
 // store, in 128 x 128, two blocks to a compute unit, so that one multiplies while the other stores: 300k x 128 -> 128
 // 172 against 184 us, 20k x 384 -> 512 105 against 121 us.  Where even tiles of
@@ -929,6 +946,8 @@ hipError_t product(const ProductArgs& p, hipStream_t s) {
   } else if constexpr (PA == 2) {
     if (p.m > 128 && tiles_of(p.m, n, 256, 128) * p.splits > kUnits / 2) return run_product<T, O, PA, PB, RA, RB, OA, OB, OUT, 256, 128, 64, 64, 64>(p, s);
     return run_product<T, O, PA, PB, RA, RB, OA, OB, OUT, 128, 128, 64, 64, 64>(p, s);
+  } else if constexpr (PB == 1) {
+    return run_product<T, O, PA, PB, RA, RB, OA, OB, OUT, 128, 128, 32, 64, 64>(p, s);
   } else {
     if constexpr (OUT != OUT_GATED) {
       if (n > 128 && tiles_of(p.m, n, 128, 256) * p.splits > kUnits / 2) return run_product<T, O, PA, PB, RA, RB, OA, OB, OUT, 128, 256, 32, 64, 64>(p, s);
@@ -1004,7 +1023,7 @@ Space gated_space(int32_t type, int64_t m, int64_t n, int64_t k, bool backward) 
   Space s = {0, 0, 0, 0};
   if (type == QHA_F32 && (backward || !few_rows(m, n))) s.w = up16(3 * 2 * up8(n) * up8(k) * 2);
   if (backward) {
-    s.grad = up16(m * 2 * n * (type == QHA_F16 ? 6 : 4));      // float32, two planes of bf16 or three of f16
+    s.grad = up16(m * 2 * n * (type == QHA_F32 ? 4 : 6));      // float32, or three planes of 16 bits
     if (type == QHA_F16) s.sizes = grad_tiles_space(m, n);
     const int64_t splits = dw_splits(m, n, k);
     s.partial = splits > 1 ? up16(splits * 2 * n * k * 4) : 0;
@@ -1126,7 +1145,8 @@ hipError_t bwd(const GatedArgs& g, hipStream_t s) {
   p.c1 = g.dwu;
   p.ldc1 = g.lddwu;
   p.partial = partial;
-  e = product<T, float, PL == 3 ? 3 : 2, PL, PL == 3, PL == 3, ORDER_CROSS, ORDER_CROSS, OUT_DW>(p, s);
+  constexpr int parts = std::is_same<T, _Float16>::value ? 2 : 3;
+  e = product<T, float, parts, PL, PL == 3, PL == 3, ORDER_CROSS, ORDER_CROSS, OUT_DW>(p, s);
   if (e == hipSuccess && p.splits > 1) e = sum_splits<float>(p, s);
   return e;
 }

@@ -433,3 +433,63 @@ def test_the_workspace_is_as_large_as_its_query_says(shape, dtype):
         else:
             B.gated_project(a, wg, wu, out[0], gate=out[1], up=out[2], workspace=ws)
         assert (buf[:pad] == 0xA5).all() and (buf[pad + need:] == 0xA5).all()
+
+
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16", "float16"])
+@pytest.mark.parametrize("shape", [(1, 64, 256), (3, 200, 72), (8, 72, 520)], ids=lambda s: "x".join(map(str, s)))
+def test_weight_gradients_are_float32_results(shape, dtype):
+    """With few rows the bound on a weight gradient is close enough to show a part of dG or dU that does not reach the products:
+    16 u of |dH U| (1 + |G|) or |dH| (1 + |G|) as above, 2^-23 for float32's dropped part products, 2^-22 of a term or 2^-39 of its
+    column's largest for f16's two scaled parts, and the sums' 2 (m + 8) u.  Two parts of bf16 break it."""
+    H.require_gpu()
+    import torch
+    from quantized_halo_aggregation_amd import binding as B
+    m, n, k = shape
+    H.note(f"gated float32 weight gradients {shape} {dtype}")
+    a, wg, wu, dh = _data(m, n, k, dtype, 21)
+    rng = np.random.default_rng(22)
+    gate, up = (torch.from_numpy((1 + np.abs(rng.standard_normal((m, n)))).astype(np.float32)).to(a.dtype) for _ in range(2))
+    dw = [torch.full((n, k), float("nan"), device="cuda") for _ in range(2)]
+    B.gated_backward(*(x.cuda() for x in (dh, gate, up, a, wg, wu)), None, *dw, act=2,
+                     workspace=_space(B.gated_backward_workspace(a.dtype, m, n, k)))
+    aa, fdh, fg, fu = (_np(x) for x in (a, dh, gate, up))
+    for name, got, d, own in (("dwg", dw[0], fdh * fu * T.act_slope(fg, "silu"), fdh * fu * (1 + fg)),
+                              ("dwu", dw[1], fdh * T.act(fg, "silu"), fdh * (1 + fg))):
+        t = np.abs(d)
+        e = 16 * U * np.abs(own) + (2 + 2 * (m + 8)) * U * t
+        if dtype == "float16":
+            e = e + 2.0 ** -22 * t + 2.0 ** -39 * t.max(0)
+        bound = e.T @ np.abs(aa)
+        err = np.abs(_np(got) - d.T @ aa)
+        assert (err <= bound).all(), (name, float((err / bound).max()))
+        if dtype == "bfloat16" and m == 1:
+            first = torch.from_numpy(d).to(torch.bfloat16).double()
+            two = (first + (torch.from_numpy(d) - first).to(torch.bfloat16).double()).numpy()
+            assert (np.abs(two.T @ aa - d.T @ aa) > bound).any()
+
+
+def test_bf16_gradients_at_the_end_of_the_range():
+    """An infinite dH makes its column's weight gradients infinite with A's signs; a dgate between bf16's and float32's
+    largest values stays finite."""
+    H.require_gpu()
+    import torch
+    from quantized_halo_aggregation_amd import binding as B
+    m, n, k = 5, 16, 8
+    H.note("gated bf16 range")
+    a, wg, wu, dh = _data(m, n, k, "bfloat16", 5)
+    a[2] = torch.tensor([0.25, -0.5, 0.125, -0.0625, 0.25, -0.25, 0.5, -0.125])
+    gate, up = torch.full((m, n), 2.0, dtype=torch.bfloat16), torch.full((m, n), 3.0, dtype=torch.bfloat16)
+    dh[2, 11] = float("inf")
+    dh[2, 9], up[2, 9], gate[2, 9] = 1.4140625 * 2.0 ** 64, 1.4140625 * 2.0 ** 63, 0.0    # dgate 1.99957 2^127, bf16 ends at 1.99219 2^127
+    dw = [torch.zeros(n, k, device="cuda") for _ in range(2)]
+    B.gated_backward(*(x.cuda() for x in (dh, gate, up, a, wg, wu)), None, *dw, act=0,
+                     workspace=_space(B.gated_backward_workspace(torch.bfloat16, m, n, k)))
+    got = _np(dw[0])
+    assert (got[11] == np.inf * np.sign(_np(a)[2])).all() and (_np(dw[1])[11] == got[11]).all()
+    with np.errstate(over="ignore", invalid="ignore"):
+        d = _np(dh) * _np(up)
+    rest = np.arange(n) != 11
+    assert d[2, 9] > 3.3895313892515355e38
+    ref = d[:, rest].T @ _np(a)
+    bound = (2 + 2 * (m + 8)) * U * (np.abs(d[:, rest]).T @ np.abs(_np(a)))
+    assert (np.abs(got[rest] - ref) <= bound).all()
