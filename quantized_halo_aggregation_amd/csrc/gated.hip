@@ -102,9 +102,11 @@ __device__ __forceinline__ void loads_done() { asm volatile("s_waitcnt vmcnt(0)"
 // 16 bytes a lane from memory to LDS, lane i of the wavefront to `to` + 16 i.  Written as assembly because
 // the compiler would wait for all such loads before any LDS read that it cannot tell apart from their
 // destination (the transposing reads), and so undo the double buffering; nothing comes back in a
-// register, and loads_done() waits.
+// vector register, and loads_done() waits.  m0, which holds the destination, is an output, so that the compiler
+// knows it to have changed (it takes no reserved register in a list of clobbers).
 __device__ __forceinline__ void load_to_lds(const uint16_t* from, uint32_t to) {
-  asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(from), "s"(to) : "memory");
+  uint32_t m0;
+  asm volatile("s_mov_b32 %0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" : "={m0}"(m0) : "v"(from), "s"(to) : "memory");
 }
 
 __device__ __forceinline__ uint32_t lds_address(const uint16_t* p) {
