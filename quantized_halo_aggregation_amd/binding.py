@@ -574,7 +574,7 @@ def _matrix(t, name, dtype, rows, cols):
     ld, one = t.stride()
     if one != 1 and cols > 1:
         raise ValueError(f"{name} must be a 2-D tensor with contiguous rows")
-    return t.data_ptr(), ld if rows > 1 else max(ld, cols)
+    return t.data_ptr(), ld if rows > 1 else cols
 
 
 def _vector(t, name, n):

@@ -493,3 +493,23 @@ def test_bf16_gradients_at_the_end_of_the_range():
     ref = d[:, rest].T @ _np(a)
     bound = (2 + 2 * (m + 8)) * U * (np.abs(d[:, rest]).T @ np.abs(_np(a)))
     assert (np.abs(got[rest] - ref) <= bound).all()
+
+
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
+def test_one_row_of_a_buffer_with_odd_rows(dtype):
+    """A single row may lie anywhere that is aligned: the stride to a next one that is not there does not count."""
+    H.require_gpu()
+    import torch
+    from quantized_halo_aggregation_amd import binding as B
+    H.note(f"gated one row of odd rows {dtype}")
+    a, wg, wu, _ = (x.cuda() for x in _data(1, 64, 72, dtype, 3))
+    h, _, _ = _forward(a, wg, wu, "silu", kept=False)
+    wide = torch.full((2, 79), 5.0, dtype=a.dtype, device="cuda")
+    wide[:1, :72] = a
+    out = torch.full((2, 67), 5.0, dtype=a.dtype, device="cuda")
+    B.gated_project(wide[:1, :72], wg, wu, out[:1, :64])
+    assert torch.equal(out[:1, :64], h) and (out[:, 64:] == 5).all() and (out[1] == 5).all()
+    y = torch.empty_like(h)
+    B.group_norm_fwd(h, y, 4)
+    B.group_norm_fwd(out[:1, :64], out[:1, :64], 4)
+    assert torch.equal(out[:1, :64], y)

@@ -267,3 +267,16 @@ def test_adamw_writes_where_its_tensors_are_now(adamw_calls, bits):
     expect()
     with pytest.raises(AttributeError):
         opt.bits = 40 - bits
+
+
+def test_the_stride_of_a_single_row_does_not_matter():
+    """One row of a buffer with odd rows (one token, one node) has no next row: its leading dimension is its width."""
+    class Gpu(torch.Tensor):
+        is_cuda = True
+    buf = torch.zeros(3, 67)
+    for view in (buf[:1, :64], buf[1:2, 1:65], torch.zeros(64).expand(1, 64)):
+        p, ld = B._matrix(view.as_subclass(Gpu), "a", torch.float32, 1, 64)
+        assert (p, ld) == (view.data_ptr(), 64)
+        assert _norm_fwd(n=1, p=1, ldx=ld, ldy=ld, mean=None, rstd=None, x=FAKE + 4, ws=None, wsb=0) == B.QHA_ERR_INVALID_ARG
+        assert b"aligned" in B._last_error()
+    assert B._matrix(buf[:2, :64].as_subclass(Gpu), "a", torch.float32, 2, 64)[1] == 67
