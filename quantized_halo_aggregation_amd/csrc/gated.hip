@@ -927,16 +927,18 @@ constexpr int64_t kUnits = 256;          // compute units; a block with a large 
 
 int64_t tiles_of(int64_t m, int64_t n, int64_t bm, int64_t bn) { return ((m + bm - 1) / bm) * ((n + bn - 1) / bn); }
 
-// Tile shapes.  Larger tiles read LDS less per product and need enough of them to occupy the compute
-// units: forward of 16384 x 2048 -> 8192 bf16, 1044 us in 256 x 256 tiles (4096 of them) against
-// 1335 us in 128 x 128; dA of 8191 x 8192 -> 1024, 212 us in 256 x 256 (128 tiles, half the chip) against
-// 152 us in 128 x 128; its dW of two parts (f16) 253 us in 256 x 128 against 331 us, of three (bf16) 373 us in 128 x 128 with
-// steps of 32, two blocks to a compute unit, and as long in 256 x 128; steps of 64 take 470 us.  Three-part products: dA and dW of
-// 30k x 256 -> 256 in 128 x 256, 48 and 58 us, against 59 and 59 us in 128 x 128; the forward, with three results to
-// store, in 128 x 128, two blocks to a compute unit, so that one multiplies while the other stores: 300k x 128 -> 128
-// 172 against 184 us, 20k x 384 -> 512 105 against 121 us.  Where even tiles of
-// 128 x 128 leave half the compute units idle, 64 x 64: forward of 512 x 1024 -> 2048 (128 tiles) bf16 11.9 against
-// 14.8 us, float32 54.8 against 59.6 us; of 1500 x 1136 -> 1224 (240 tiles) 21.1 against 18.9 us.
+// Tile shapes, with medians of a kernel trace of both sides on one card.  Larger tiles read LDS less per product and need
+// enough of them to occupy the compute units: forward of 16384 x 2048 -> 8192 bf16, 1044 us in 256 x 256 tiles (4096 of
+// them) against 1225 us in 128 x 128; dA of 8191 x 8192 -> 1024, 206 us in 256 x 256 (128 tiles, half the chip) against
+// 172 us in 128 x 128; its dW of two parts (f16) 261 us in 256 x 128 against 343 us, of three (bf16) 358 us in 128 x 128
+// with steps of 32, two blocks to a compute unit, against 361 us in 256 x 128 and 455 us with steps of 64.
+// Three-part products in 128 x 128, two blocks to a compute unit: forward, where one multiplies while the other stores,
+// of 300k x 128 -> 128 148 against 168 us in 128 x 256, 20k x 384 -> 512 92 against 107 us.  dA and dW in tiles twice as
+// large, one to a compute unit, where those make one round of blocks: of 4000 x 2048 -> 4096 652 and 758 us against 676
+// and 773 us; 20k x 384 -> 512 would take two rounds of 314 and 336 blocks, 159 and 188 us against 93 and 107 us,
+// and dA of 100k x 512 -> 512 seven, 584 against 549 us.  Where even tiles of 128 x 128 leave half the compute units idle, 64 x 64: forward of
+// 512 x 1024 -> 2048 (128 tiles) bf16 12.2 against 15.4 us, float32 40 against 46 us; of 1500 x 1136 -> 1224
+// (240 tiles) 21.1 against 18.9 us.
 template <typename T, typename O, int PA, int PB, bool RA, bool RB, int OA, int OB, int OUT>
 hipError_t product(const ProductArgs& p, hipStream_t s) {
   const int64_t n = OUT == OUT_GATED ? 2 * p.n : p.n;       // rows of the B operand
@@ -952,8 +954,12 @@ hipError_t product(const ProductArgs& p, hipStream_t s) {
     return run_product<T, O, PA, PB, RA, RB, OA, OB, OUT, 128, 128, 32, 64, 64>(p, s);
   } else {
     if constexpr (OUT != OUT_GATED) {
-      if (n > 128 && tiles_of(p.m, n, 128, 256) * p.splits > kUnits / 2) return run_product<T, O, PA, PB, RA, RB, OA, OB, OUT, 128, 256, 32, 64, 64>(p, s);
-      if (p.m > 128 && tiles_of(p.m, n, 256, 128) * p.splits > kUnits / 2) return run_product<T, O, PA, PB, RA, RB, OA, OB, OUT, 256, 128, 32, 64, 64>(p, s);
+      auto one_round = [&](int64_t bm, int64_t bn) {
+        const int64_t blocks = tiles_of(p.m, n, bm, bn) * p.splits;
+        return blocks > kUnits / 2 && blocks <= kUnits;
+      };
+      if (n > 128 && one_round(128, 256)) return run_product<T, O, PA, PB, RA, RB, OA, OB, OUT, 128, 256, 32, 64, 64>(p, s);
+      if (p.m > 128 && one_round(256, 128)) return run_product<T, O, PA, PB, RA, RB, OA, OB, OUT, 256, 128, 32, 64, 64>(p, s);
     }
     if constexpr (OUT != OUT_DW) {
       if (few) return run_product<T, O, PA, PB, RA, RB, OA, OB, OUT, 64, 64, 32, 32, 64>(p, s);
