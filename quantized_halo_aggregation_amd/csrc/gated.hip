@@ -993,8 +993,16 @@ int32_t da_splits(int64_t m, int64_t n, int64_t k) {
   return static_cast<int32_t>(s < 1 ? 1 : s);
 }
 
-// Rows that few_rows_kernel takes: up to 16 always, up to 128 while the tiles would not fill the chip.
-bool few_rows(int64_t m, int64_t n) { return m <= 16 || (m <= 128 && tiles_of(m, 2 * n, 128, 128) < kUnits); }
+// Rows that few_rows_kernel takes.  Each of its n / 16 blocks reads all rows, padded to 16, 32, 64 or 128, so its time grows with
+// both; the tiles' does not below 128 rows.  16-bit, few rows against tiles in us: 1 row of 2048 -> 4096 10.8 and 18.3,
+// 16 rows of 4096 -> 8192 28.1 and 34.7, 32 rows 33.5 and 34.9, 64 rows of 2048 -> 4096 14.9 and 19.2, of 4096 -> 8192 47.5
+// and 35.3, 128 rows of 1024 -> 2048 13.7 and 11.3.  float32, whose tiles split the weights first: 128 rows of
+// 4096 -> 8192 167 and 276.
+bool few_rows(int32_t type, int64_t m, int64_t n) {
+  if (m <= 16) return true;
+  if (type == QHA_F32) return m <= 128 && n < 16384;
+  return m <= 64 && (m <= 32 ? 32 : 64) * n <= 1 << 18;
+}
 
 struct Space {
   int64_t w, grad, sizes, partial;        // bytes
@@ -1029,7 +1037,7 @@ int64_t grad_tiles_space(int64_t m, int64_t n) {
 
 Space gated_space(int32_t type, int64_t m, int64_t n, int64_t k, bool backward) {
   Space s = {0, 0, 0, 0};
-  if (type == QHA_F32 && (backward || !few_rows(m, n))) s.w = up16(3 * 2 * up8(n) * up8(k) * 2);
+  if (type == QHA_F32 && (backward || !few_rows(type, m, n))) s.w = up16(3 * 2 * up8(n) * up8(k) * 2);
   if (backward) {
     s.grad = up16(m * 2 * n * (type == QHA_F32 ? 4 : 6));      // float32, or three planes of 16 bits
     if (type == QHA_F16) s.sizes = grad_tiles_space(m, n);
@@ -1058,7 +1066,7 @@ hipError_t fwd_few(const GatedArgs& g, hipStream_t s) {
   if (g.m <= 16) few_rows_kernel<T, 1><<<blocks, 512, 0, s>>>(g);
   else if (g.m <= 32) few_rows_kernel<T, 2><<<blocks, 512, 0, s>>>(g);
   else if (g.m <= 64) few_rows_kernel<T, 4><<<blocks, 512, 0, s>>>(g);
-  else few_rows_kernel<T, 8><<<blocks, 512, 0, s>>>(g);
+  else if constexpr (sizeof(T) == 4) few_rows_kernel<T, 8><<<blocks, 512, 0, s>>>(g);
   return hipGetLastError();
 }
 
@@ -1167,7 +1175,7 @@ size_t gated_workspace(int32_t type, int64_t m, int64_t n, int64_t k, bool backw
 }
 
 hipError_t launch_gated_fwd(const GatedArgs& g, hipStream_t s) {
-  if (few_rows(g.m, g.n)) return g.type == QHA_F32 ? fwd_few<float>(g, s) : g.type == QHA_BF16 ? fwd_few<__bf16>(g, s) : fwd_few<_Float16>(g, s);
+  if (few_rows(g.type, g.m, g.n)) return g.type == QHA_F32 ? fwd_few<float>(g, s) : g.type == QHA_BF16 ? fwd_few<__bf16>(g, s) : fwd_few<_Float16>(g, s);
   if (g.type == QHA_F32) return fwd<__bf16, float, 3>(g, s);
   return g.type == QHA_BF16 ? fwd<__bf16, __bf16, 1>(g, s) : fwd<_Float16, _Float16, 1>(g, s);
 }
