@@ -398,6 +398,8 @@ size_t qha_dense_backward_workspace(int64_t m, int64_t n, int64_t k);
  * dropped ones total below 2^-23 of the product); sums are float32, and H is formed from the float32
  * gate and up and rounded once.  H, gate and up must not overlap A or the weights.  workspace:
  * device, 16-byte aligned, qha_gated_workspace bytes (0 for 16-bit types).  m = 0 or n = 0 is a no-op.
+ * NaN and infinities of a row of A stay in its row of the results.  A float32 operand of 2^128 - 2^119 or more in
+ * magnitude has no finite first part: every result it enters is NaN, also where the formula is infinite.
  * Errors: INVALID_ARG, UNSUPPORTED (more than 2^22 tiles of 128 rows and 64 columns: cut the rows),
  * WORKSPACE, HIP. */
 int qha_gated_project(int64_t m, int64_t n, int64_t k, int32_t type, const void* a, int64_t lda, const void* w_gate,

@@ -18,7 +18,7 @@ BUILD_DIR = os.path.join(PKG, "_build")
 SOURCES = ["abi.cpp", "control.cpp", "quantize.hip", "gather.hip", "gemm.hip", "panel.hip",
            "abi_train.cpp", "adamw.hip", "norm.hip", "norm_rows.hip",
            "gated.hip"]
-HEADERS = ["qha_internal.hpp"]
+HEADERS = ["qha_internal.hpp", "act_common.hpp"]
 
 ARCH = "gfx950"
 FLAGS = [

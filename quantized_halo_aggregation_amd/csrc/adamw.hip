@@ -5,12 +5,12 @@
 // m = s sign(c) (c / 127)^2 and v = s (c / 255)^4, which spaces the codes by about 2 / c of the value, so
 // a small moment beside a large one keeps a code; s is the block's largest magnitude.
 //
-// Bound: memory.  Per element 28 bytes move with float32 moments and gradients, 18 with 8-bit
-// moments, 16-bit gradients and a 16-bit copy; the arithmetic hides behind it, which is why the 8-bit
-// form can afford float64 moments: a code is then the same whichever way its inputs were summed.
+// Bound: memory.  Per element 28 bytes move with float32 moments and gradients, 16 with 8-bit
+// moments, 16-bit gradients and a 16-bit copy.  The 8-bit form's arithmetic is float64, so that a code is the same
+// whichever way its inputs were summed; most of it hides behind memory, not all: it reaches 4.7 TB/s.
 //
 // 302M elements with float32 moments and gradients: 1.46 to 1.60 ms by card (5.3 to 5.8 TB/s; a large copy reaches 5.0).  201M with
-// 8-bit moments, bf16 gradients and copies: 0.68 ms (5.3 TB/s), and 0.35 ms to read the moments back (5.8 TB/s).
+// 8-bit moments, bf16 gradients and copies: 0.69 ms (4.7 TB/s), and 0.35 ms to read the moments back (5.8 TB/s).
 //
 // Mapping: a block of 256 threads takes chunks of 1024 consecutive elements, four per thread (16-byte
 // accesses), so that one wavefront holds exactly one 256-element code block and finds its largest

@@ -18,9 +18,9 @@
 // 32 of Wu, so a wavefront holds G and U of the same columns and the activation and product happen in registers.
 // The matrix instruction's operands are swapped (C^T is formed), which leaves a lane four neighbouring
 // columns of a row to store at once.
-// Bound: the matrix cores for wide layers (16384 x 2048 -> 8192 bf16 with all three results stored, 1.06 ms, 1.03
-// PFLOP/s, where a plain library product of that size class reaches 1.25), the order of loads, products
-// and stores within a tile for narrow ones (300k x 128 -> 128 float32, 188 us against 123 us for its bytes).
+// Bound: the matrix cores for wide layers (16384 x 2048 -> 8192 bf16 with all three results stored, 1.01 to 1.08 ms, 1.02 to
+// 1.09 PFLOP/s, where a plain library product of that size class reaches 1.25), the order of loads, products
+// and stores within a tile for narrow ones (300k x 128 -> 128 float32, 158 to 192 us against 123 us for its bytes).
 #include "act_common.hpp"
 #include "qha_internal.hpp"
 
@@ -290,7 +290,7 @@ __device__ __forceinline__ void store4<_Float16>(_Float16* p, f32x4 v) {
 }
 
 // 32 rows x CW columns of results on their way out through a wavefront's own piece of LDS, as streaming stores
-// (300k x 128 float32 forward 183 against 212 us: the operands stay in the caches).  Rows are 16 bytes
+// (300k x 128 float32 forward 183 against 212 us on one card: the operands stay in the caches).  Rows are 16 bytes
 // longer than their values, which spreads a column of lanes over the banks.
 template <typename O, int CW>
 struct RowWriter {

@@ -14,7 +14,7 @@
 // The second launch adds the pairs of its sample's chunks in order and applies.  Forward sums are
 // float64 (x and x^2: the float64 pipes idle in a memory-bound loop, and mean^2 >> variance costs
 // nothing there); the backward's per-channel sums run in float32 over a chunk and meet in float64.
-// 16 x 4096 x 512 bf16 in 32 groups, SiLU: 13 us for the sums (5.3 TB/s) and 32 us to apply (4.2 TB/s).
+// 16 x 4096 x 512 bf16 in 32 groups, SiLU: 13 us for the sums (5.2 TB/s) and 33 us to apply (4.1 TB/s).
 #include "act_common.hpp"
 #include "qha_internal.hpp"
 

@@ -12,7 +12,7 @@
 // one group by all of the team, others through LDS.  A block leaves one partial of dw and db, and a second small
 // launch adds those in float64.
 // 300k rows of 128 float32 in 8 groups: forward 55 us (5.9 TB/s; a large copy reaches 5.0), 300k rows of 256
-// backward 166 us (5.6 TB/s).
+// backward 162 to 178 us (5.2 to 5.7 TB/s).
 #include "act_common.hpp"
 #include "qha_internal.hpp"
 
