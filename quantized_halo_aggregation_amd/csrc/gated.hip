@@ -3,7 +3,8 @@
 // Mathematics: G = A Wg^T, U = A Wu^T, H = act(G) U.  Backward: dG = dH U act'(G), dU = dH act(G),
 // dA = [dG dU] [Wg; Wu], [dWg; dWu] = [dG dU]^T A.  16-bit types multiply as they are; float32
 // values are split exactly into three bf16 parts (hi, mid, lo) and a product is rebuilt from the six part
-// products of weight >= 2^-16 of it (the dropped ones total below 2^-23 of the product).  All sums
+// products of weight >= 2^-16 of it (the dropped ones total below 2^-23 of the product).  [dG dU] of 16-bit types enters the
+// float32 dW in three bf16 parts or two scaled f16 ones, and dA, a 16-bit result, in one.  All sums
 // are float32 in the matrix cores' accumulators; a reduction that is split leaves float32 partials that
 // are added in float64.
 //
