@@ -23,6 +23,8 @@
  *   qha_gated_backward        its gradients
  *   qha_group_norm_fwd        group normalisation with an activation, channels last
  *   qha_group_norm_bwd        its gradients
+ *   qha_residual_norm_fwd     the norms after and before a block fused with its gate and the residual stream
+ *   qha_residual_norm_bwd     its gradients
  *   qha_adamw_step            one AdamW step over many tensors, moments in float32 or 8-bit codes
  *   qha_adamw_values          8-bit moments read back as float32 values
  *
@@ -456,6 +458,55 @@ int qha_group_norm_bwd(int64_t n_samples, int64_t positions, int32_t c, int32_t 
                        float* dbias, void* workspace, size_t workspace_bytes, void* stream);
 /* Bytes of workspace for either direction, enough for every type (0 where none is needed, and for sizes that the calls refuse). */
 size_t qha_group_norm_workspace(int64_t n_samples, int64_t positions, int32_t c, int32_t n_groups, int32_t backward);
+
+/* The norms around a block, fused with its gate and the residual stream between blocks.  Per row:
+ *   z = post_weight hhat + post_bias,   x' = skip x + branch (gate z),   u = pre_weight xhat' + pre_bias
+ * h is a block's output, x the stream that it is added to, x' (written to y) the stream after it and u the next
+ * block's input.  hhat is h normalised by `post`, xhat' is x' (before it is rounded to its type) normalised by `pre`:
+ *   QHA_ROW_RMS    v / sqrt(mean of v^2 + eps)
+ *   QHA_ROW_LAYER  (v - mean of v) / sqrt(var of v + eps)
+ *   QHA_ROW_NONE   post: h itself (post_weight is then a scale per channel); pre: there is no u
+ * over the row's c channels.  x and y have elements of stream_type, which is QHA_F32 or type; h, gate and u of
+ * type.  Weights and biases: device float32[c], 16-byte aligned, each nullable (1 and 0).  gate: one row for each
+ * `positions` consecutive rows (their number must be a multiple), nullable (1).  post_stats and pre_stats: device
+ * float32[n_rows][2], 8-byte aligned, nullable: each row's mean (0 for RMS) and 1 / sqrt(..), for the backward.
+ * h may be NULL (the first block's input): then u is the norm of x itself, and gate, y, post_stats and the post vectors must be NULL.
+ * y may be x and u may be h (with the same leading dimension); otherwise outputs must not overlap inputs or each other.
+ * Sums over a row are float32, means before squares; results are deterministic.
+ * c is a multiple of 16 bytes of elements of type and at most 8192; leading dimensions are at least c and
+ * multiples of 16 bytes; rows are 16-byte aligned.  n_rows = 0 is a no-op.
+ * Errors: INVALID_ARG (an unknown type or norm; no u with a pre norm, or one without; neither norm nor block; skip,
+ * branch not finite, eps negative or not finite; n_rows of 2^31 or more), UNSUPPORTED (c above 8192), HIP. */
+#define QHA_ROW_NONE 0
+#define QHA_ROW_RMS 1
+#define QHA_ROW_LAYER 2
+int qha_residual_norm_fwd(int64_t n_rows, int64_t positions, int32_t c, int32_t stream_type, int32_t type,
+                          int32_t post, int32_t pre, const void* x, int64_t ldx, const void* h, int64_t ldh,
+                          const void* gate, int64_t ldg, const float* post_weight, const float* post_bias,
+                          const float* pre_weight, const float* pre_bias, double skip, double branch, double eps,
+                          void* y, int64_t ldy, void* u, int64_t ldu, float* post_stats, float* pre_stats,
+                          void* stream);
+
+/* Gradients of qha_residual_norm_fwd from its kept x' (y; without a block its x) and h and its statistics.  With
+ * t = dy + the gradient of x' through the pre norm (from du):
+ *   dx = skip t,   dgate = sum over the gate's rows of branch t z,   dh = the gradient of h through branch gate z,
+ *   d(weight) = sum of dz xhat, d(bias) = sum of dz over all rows, for either norm (dz: the norm's result's gradient)
+ * dy: the gradient of x' from elsewhere (stream_type; nullable with a pre norm: none).  du: elements of type, NULL
+ * without a pre norm.  dx has elements of stream_type, dh and dgate of type.  dgate and the four vectors' gradients
+ * (device float32[c], overwritten; zeros when there are no rows) are nullable.  dx may be dy or y, dh may be du or h
+ * (with the same leading dimension); otherwise outputs must not overlap inputs or each other.  workspace: device,
+ * 16-byte aligned, qha_residual_norm_workspace bytes (needed where a vector's gradient or that of a shared gate is asked
+ * for).  Partial sums are float32 in a team of threads and float64 over teams, in a fixed order.
+ * Other arguments, limits, determinism and errors as there; WORKSPACE. */
+int qha_residual_norm_bwd(int64_t n_rows, int64_t positions, int32_t c, int32_t stream_type, int32_t type,
+                          int32_t post, int32_t pre, const void* dy, int64_t lddy, const void* du, int64_t lddu,
+                          const void* y, int64_t ldy, const void* h, int64_t ldh, const void* gate, int64_t ldg,
+                          const float* post_weight, const float* post_bias, const float* pre_weight, double skip,
+                          double branch, const float* post_stats, const float* pre_stats, void* dx, int64_t lddx,
+                          void* dh, int64_t lddh, void* dgate, int64_t lddg, float* dpost_weight, float* dpost_bias,
+                          float* dpre_weight, float* dpre_bias, void* workspace, size_t workspace_bytes, void* stream);
+/* Bytes of workspace for the backward, enough for every type, with and without a gate (0 for sizes that the calls refuse). */
+size_t qha_residual_norm_workspace(int64_t n_rows, int64_t positions, int32_t c);
 
 /* One AdamW step over a list of tensors.  With g = grad_scale * grad, for every element:
  *   m = beta1 m + (1 - beta1) g,    v = beta2 v + (1 - beta2) g^2,

@@ -1,5 +1,6 @@
 """Float64 oracle of the training operators: AdamW with float32 or 8-bit moments, group norm with an
-activation, and the gated projection, each with its gradients.  Written from the formulas; shares no
+activation, the norms around a block with its gate and residual stream, and the gated projection, each with
+its gradients.  Written from the formulas; shares no
 code with the GPU path."""
 import math
 
@@ -112,6 +113,60 @@ def group_norm_backward(dy, x, mean, rstd, w, b, groups, positions, kind):
     xh = xhat.reshape(shape)
     dx = rstd[:, None, :, None] * (q - q.mean((1, 3), keepdims=True) - xh * (q * xh).mean((1, 3), keepdims=True))
     return dx.reshape(x.shape), (dz * xhat).sum(0), dz.sum(0)
+
+
+# ---------------------------------------------------------------------------------------------
+# the norms around a block: rows [rows, c], a gate row for `positions` of them
+# ---------------------------------------------------------------------------------------------
+
+def row_norm(v, kind, w, b, eps):
+    """(result, statistics [rows, 2]) of every row's norm: "none", "rms" or "layer"."""
+    v = np.asarray(v, np.float64)
+    mean = v.mean(1, keepdims=True) if kind == "layer" else np.zeros((v.shape[0], 1))
+    rstd = np.ones_like(mean) if kind == "none" else 1.0 / np.sqrt(((v - mean) ** 2).mean(1, keepdims=True) + eps)
+    return (v - mean) * rstd * (1.0 if w is None else w) + (0.0 if b is None else b), np.concatenate([mean, rstd], 1)
+
+
+def row_norm_backward(dz, v, kind, stats, w):
+    """(dv, dw, db) for given statistics."""
+    dz, v, stats = (np.asarray(t, np.float64) for t in (dz, v, stats))
+    xhat = (v - stats[:, :1]) * stats[:, 1:]
+    q = dz * (1.0 if w is None else np.asarray(w, np.float64))
+    dv = q.copy()
+    if kind != "none":
+        dv -= xhat * (q * xhat).mean(1, keepdims=True)
+    if kind == "layer":
+        dv -= q.mean(1, keepdims=True)
+    return dv * stats[:, 1:], (dz * xhat).sum(0), dz.sum(0)
+
+
+def residual_norm(x, h, gate, positions, post, pre, vectors, skip, branch, eps):
+    """(y, u, post statistics, pre statistics); vectors: post weight and bias, pre weight and bias; h may be None."""
+    y, post_stats = np.asarray(x, np.float64), None
+    if h is not None:
+        z, post_stats = row_norm(h, post, vectors[0], vectors[1], eps)
+        g = 1.0 if gate is None else np.repeat(np.asarray(gate, np.float64), positions, 0)
+        y = skip * y + branch * (g * z)
+    u, pre_stats = row_norm(y, pre, vectors[2], vectors[3], eps)
+    return y, u, post_stats, pre_stats
+
+
+def residual_norm_backward(dy, du, y, h, gate, positions, post, pre, vectors, post_stats, pre_stats, skip, branch):
+    """(dx, dh, dgate, [post weight's and bias's, pre weight's and bias's gradients]) for given statistics."""
+    t = np.zeros(np.shape(y)) if dy is None else np.asarray(dy, np.float64)
+    grads = [None] * 4
+    if pre != "none":
+        dv, grads[2], grads[3] = row_norm_backward(du, y, pre, pre_stats, vectors[2])
+        t = t + dv
+    if h is None:
+        return skip * t, None, None, grads
+    g = np.ones((t.shape[0] // positions, t.shape[1])) if gate is None else np.asarray(gate, np.float64)
+    h = np.asarray(h, np.float64)
+    z = (h - post_stats[:, :1]) * post_stats[:, 1:] * (1.0 if vectors[0] is None else vectors[0])
+    z = z + (0.0 if vectors[1] is None else vectors[1])
+    dgate = (branch * t * z).reshape(-1, positions, t.shape[1]).sum(1)
+    dh, grads[0], grads[1] = row_norm_backward(branch * t * np.repeat(g, positions, 0), h, post, post_stats, vectors[0])
+    return skip * t, dh, dgate, grads
 
 
 # ---------------------------------------------------------------------------------------------

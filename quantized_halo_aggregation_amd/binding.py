@@ -45,6 +45,7 @@ PRO_NONE, PRO_RELU_MASK = 0, 1
 EPI_NONE, EPI_RELU = 0, 1
 F32, BF16, F16 = 0, 1, 2
 ACT_NONE, ACT_RELU, ACT_SILU, ACT_GELU = 0, 1, 2, 3
+ROW_NONE, ROW_RMS, ROW_LAYER = 0, 1, 2
 ADAMW_BLOCK = 256
 DEFAULT_CHUNK = 512
 DEFAULT_GROUP_EDGES = 256
@@ -140,6 +141,13 @@ _gated_project = _sig("qha_gated_project", _i32, _i64, _i64, _i64, _i32, _vp, _i
 _gated_backward = _sig("qha_gated_backward", _i32, _i64, _i64, _i64, _i32, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _i64,
                        _vp, _i64, _vp, _i64, _i32, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _sz, _vp)
 _gated_ws = _sig("qha_gated_workspace", _sz, _i32, _i64, _i64, _i64, _i32)
+_residual_norm_fwd = _sig("qha_residual_norm_fwd", _i32, _i64, _i64, _i32, _i32, _i32, _i32, _i32, _vp, _i64, _vp, _i64,
+                          _vp, _i64, _vp, _vp, _vp, _vp, C.c_double, C.c_double, C.c_double, _vp, _i64, _vp, _i64, _vp,
+                          _vp, _vp)
+_residual_norm_bwd = _sig("qha_residual_norm_bwd", _i32, _i64, _i64, _i32, _i32, _i32, _i32, _i32, _vp, _i64, _vp, _i64,
+                          _vp, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _vp, C.c_double, C.c_double, _vp, _vp, _vp, _i64,
+                          _vp, _i64, _vp, _i64, _vp, _vp, _vp, _vp, _vp, _sz, _vp)
+_residual_norm_ws = _sig("qha_residual_norm_workspace", _sz, _i64, _i64, _i32)
 
 EXPORTED = ["qha_abi_version", "qha_status_string", "qha_last_error", "qha_pack_layout", "qha_pack_classes",
             "qha_edge_weights", "qha_validate_csr",
@@ -149,7 +157,8 @@ EXPORTED = ["qha_abi_version", "qha_status_string", "qha_last_error", "qha_pack_
             "qha_aggregate_bwd_quantize", "qha_dense_project", "qha_dense_project_workspace", "qha_dense_backward",
             "qha_dense_backward_workspace", "qha_mask_levels", "qha_node_bits", "qha_level_order",
             "qha_coordinator_init", "qha_coordinator_step", "qha_adamw_step", "qha_adamw_values",
-            "qha_gated_project", "qha_gated_backward", "qha_gated_workspace", "qha_group_norm_fwd", "qha_group_norm_bwd", "qha_group_norm_workspace"]
+            "qha_gated_project", "qha_gated_backward", "qha_gated_workspace", "qha_group_norm_fwd", "qha_group_norm_bwd", "qha_group_norm_workspace",
+            "qha_residual_norm_fwd", "qha_residual_norm_bwd", "qha_residual_norm_workspace"]
 
 
 class QhaError(RuntimeError):
@@ -572,7 +581,7 @@ def _matrix(t, name, dtype, rows, cols):
     if t.dim() != 2 or t.shape[0] != rows or t.shape[1] != cols:
         raise ValueError(f"{name} must be {rows} x {cols}, got {tuple(t.shape)}")
     ld, one = t.stride()
-    if one != 1 and cols > 1:
+    if one != 1 and cols > 1 and rows > 0:
         raise ValueError(f"{name} must be a 2-D tensor with contiguous rows")
     return t.data_ptr(), ld if rows > 1 else cols
 
@@ -587,6 +596,14 @@ def _space(workspace):
     if not workspace.is_cuda or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous GPU tensor")
     return workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
+def _on_current(*tensors):
+    """The calls enqueue on the current device: tensors of another one are refused."""
+    current = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.get_device() != current:
+            raise ValueError(f"a tensor lives on {t.device}, the current device is cuda:{current}")
 
 
 def gated_project_workspace(dtype, m: int, n: int, k: int) -> int:
@@ -671,6 +688,70 @@ def group_norm_bwd(dy, x, mean, rstd, dx, n_groups: int, weight=None, bias=None,
                            _flat(rstd, "rstd", n * n_groups, torch.float32), _vector(weight, "weight", c),
                            _vector(bias, "bias", c), act, pd, ldd, _vector(dweight, "dweight", c),
                            _vector(dbias, "dbias", c), ws, ws_bytes, _stream(stream)), "qha_group_norm_bwd")
+
+
+def residual_norm_workspace(rows: int, c: int, positions: int = 1) -> int:
+    return int(_residual_norm_ws(rows, positions, c))
+
+
+def _stats(t, name, rows):
+    return None if t is None else _flat(t, name, 2 * rows, torch.float32)
+
+
+def residual_norm_fwd(x, h, y, u, post: int = ROW_RMS, pre: int = ROW_RMS, post_weight=None, post_bias=None,
+                      pre_weight=None, pre_bias=None, gate=None, positions: int = 1, skip: float = 1.0,
+                      branch: float = 1.0, eps: float = 1e-6, post_stats=None, pre_stats=None, stream=None):
+    """y = skip x + branch gate post(h) and u = pre(y), row by row: the norms after and before a block.
+
+    x and y are the residual stream [rows, c] (float32, or the type of h); h, the block's output, gate [rows /
+    positions, c] and u have one type.  post_stats and pre_stats (float32 [rows, 2], if given) receive what the
+    backward needs.  With pre=ROW_NONE u is None; with h=None (post=ROW_NONE, y=None) u is pre(x)."""
+    rows, c = x.shape
+    t = x.dtype if h is None and u is None else (u if h is None else h).dtype
+    n = _samples(rows, positions)
+    px, ldx = _matrix(x, "x", x.dtype, rows, c)
+    ph, ldh = (None, 0) if h is None else _matrix(h, "h", t, rows, c)
+    py, ldy = (None, 0) if y is None else _matrix(y, "y", x.dtype, rows, c)
+    pu, ldu = (None, 0) if u is None else _matrix(u, "u", t, rows, c)
+    pg, ldg = (None, 0) if gate is None else _matrix(gate, "gate", t, n, c)
+    _on_current(x, h, y, u, gate, post_weight, post_bias, pre_weight, pre_bias, post_stats, pre_stats)
+    _check(_residual_norm_fwd(rows, positions, c, _type(x.dtype, "x"), _type(t, "h"), post, pre, px, ldx, ph, ldh, pg,
+                              ldg, _vector(post_weight, "post_weight", c), _vector(post_bias, "post_bias", c),
+                              _vector(pre_weight, "pre_weight", c), _vector(pre_bias, "pre_bias", c), skip, branch, eps,
+                              py, ldy, pu, ldu, _stats(post_stats, "post_stats", rows),
+                              _stats(pre_stats, "pre_stats", rows), _stream(stream)), "qha_residual_norm_fwd")
+
+
+def residual_norm_bwd(dy, du, y, h, dx, dh, post: int = ROW_RMS, pre: int = ROW_RMS, post_stats=None, pre_stats=None,
+                      post_weight=None, post_bias=None, pre_weight=None, pre_bias=None, gate=None, positions: int = 1,
+                      skip: float = 1.0, branch: float = 1.0, dgate=None, dpost_weight=None, dpost_bias=None,
+                      dpre_weight=None, dpre_bias=None, workspace=None, stream=None):
+    """Gradients of residual_norm_fwd from its kept y (its x where h was None; not read without a pre norm), h and
+    statistics: dx and dh, and dgate and those of the vectors (float32 [c]) where given.  dy, the gradient that
+    reaches y from elsewhere, may be None with a pre norm.  pre_bias is not needed."""
+    rows, c = dx.shape
+    s = dx.dtype
+    t = s if h is None and du is None else (du if h is None else h).dtype
+    n = _samples(rows, positions)
+    pdy, lddy = (None, 0) if dy is None else _matrix(dy, "dy", s, rows, c)
+    pdu, lddu = (None, 0) if du is None else _matrix(du, "du", t, rows, c)
+    py, ldy = (None, 0) if y is None else _matrix(y, "y", s, rows, c)
+    ph, ldh = (None, 0) if h is None else _matrix(h, "h", t, rows, c)
+    pdx, lddx = _matrix(dx, "dx", s, rows, c)
+    pdh, lddh = (None, 0) if dh is None else _matrix(dh, "dh", t, rows, c)
+    pg, ldg = (None, 0) if gate is None else _matrix(gate, "gate", t, n, c)
+    pdg, lddg = (None, 0) if dgate is None else _matrix(dgate, "dgate", t, n, c)
+    ws, ws_bytes = _space(workspace)
+    _on_current(dy, du, y, h, dx, dh, post_stats, pre_stats, post_weight, post_bias, pre_weight, gate, dgate, dpost_weight,
+                dpost_bias, dpre_weight, dpre_bias, workspace)
+    _check(_residual_norm_bwd(rows, positions, c, _type(s, "dx"), _type(t, "h"), post, pre, pdy, lddy, pdu, lddu, py, ldy,
+                              ph, ldh, pg, ldg, _vector(post_weight, "post_weight", c),
+                              _vector(post_bias, "post_bias", c), _vector(pre_weight, "pre_weight", c), skip, branch,
+                              _stats(post_stats, "post_stats", rows), _stats(pre_stats, "pre_stats", rows), pdx, lddx,
+                              pdh, lddh, pdg, lddg, _vector(dpost_weight, "dpost_weight", c),
+                              _vector(dpost_bias, "dpost_bias", c), _vector(dpre_weight, "dpre_weight", c),
+                              _vector(dpre_bias, "dpre_bias", c), ws, ws_bytes, _stream(stream)),
+           "qha_residual_norm_bwd")
 
 
 class AdamW:

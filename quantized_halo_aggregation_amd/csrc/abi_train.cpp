@@ -73,6 +73,36 @@ int take_norm_workspace(qha::NormArgs& a, bool backward, void* ws, size_t bytes)
   return QHA_OK;
 }
 
+// Checks the arguments both directions of the residual norm share and fills the kernel arguments.
+int take_residual(qha::ResidualArgs& a, int64_t n_rows, int64_t positions, int32_t c, int32_t stream_type, int32_t type,
+                  int32_t post, int32_t pre, const float* const (&vectors)[4], double skip, double branch) {
+  std::memset(&a, 0, sizeof(a));
+  if (n_rows < 0 || n_rows > kMaxRows || positions < 1 || n_rows % positions != 0) return fail(QHA_ERR_INVALID_ARG, "bad sizes");
+  if (!known_type(type)) return fail(QHA_ERR_INVALID_ARG, "unknown element type %d", type);
+  if (stream_type != type && stream_type != QHA_F32) return fail(QHA_ERR_INVALID_ARG, "the stream's type %d is neither float32 nor %d", stream_type, type);
+  if (post < QHA_ROW_NONE || post > QHA_ROW_LAYER || pre < QHA_ROW_NONE || pre > QHA_ROW_LAYER) return fail(QHA_ERR_INVALID_ARG, "unknown norm");
+  const int32_t vec = static_cast<int32_t>(16 / type_bytes(type));
+  if (c < 1 || c % vec != 0) return fail(QHA_ERR_INVALID_ARG, "c=%d must be a multiple of %d", c, vec);
+  if (c > 8192) return fail(QHA_ERR_UNSUPPORTED, "c=%d is above 8192", c);
+  if (!std::isfinite(static_cast<float>(skip)) || !std::isfinite(static_cast<float>(branch))) return fail(QHA_ERR_INVALID_ARG, "skip and branch must be finite in float32");
+  for (const float* v : vectors)
+    if (!aligned(v, 16)) return fail(QHA_ERR_INVALID_ARG, "a weight or bias is not 16-byte aligned");
+  a.rows = n_rows;
+  a.positions = positions;
+  a.c = c;
+  a.stream_type = stream_type;
+  a.type = type;
+  a.post = post;
+  a.pre = pre;
+  a.skip = static_cast<float>(skip);
+  a.branch = static_cast<float>(branch);
+  a.post_w = vectors[0];
+  a.post_b = vectors[1];
+  a.pre_w = vectors[2];
+  a.pre_b = vectors[3];
+  return QHA_OK;
+}
+
 }  // namespace
 
 namespace {
@@ -252,6 +282,131 @@ int qha_group_norm_bwd(int64_t n_samples, int64_t positions, int32_t c, int32_t 
   a.dw = dweight;
   a.db = dbias;
   return hip_status(qha::launch_norm_bwd(a, static_cast<hipStream_t>(stream)), "group_norm_bwd");
+}
+
+size_t qha_residual_norm_workspace(int64_t n_rows, int64_t positions, int32_t c) {
+  if (n_rows <= 0 || n_rows > kMaxRows || positions < 1 || n_rows % positions != 0 || c < 1 || c > 8192) return 0;
+  size_t need = 0;
+  for (int32_t type : {QHA_F32, QHA_BF16}) {       // the element type is not asked for: room for each that c suits
+    if (c % static_cast<int32_t>(16 / type_bytes(type)) != 0) continue;
+    for (int32_t gate = 0; gate < 2; ++gate) {
+      qha::ResidualArgs a;
+      std::memset(&a, 0, sizeof(a));
+      a.rows = n_rows;
+      a.positions = positions;
+      a.c = c;
+      a.type = type;
+      a.shared_gate = gate && positions > 1;
+      qha::residual_plan(a);
+      const size_t b = qha::residual_workspace(a);
+      need = b > need ? b : need;
+    }
+  }
+  return need;
+}
+
+int qha_residual_norm_fwd(int64_t n_rows, int64_t positions, int32_t c, int32_t stream_type, int32_t type,
+                          int32_t post, int32_t pre, const void* x, int64_t ldx, const void* h, int64_t ldh,
+                          const void* gate, int64_t ldg, const float* post_weight, const float* post_bias,
+                          const float* pre_weight, const float* pre_bias, double skip, double branch, double eps,
+                          void* y, int64_t ldy, void* u, int64_t ldu, float* post_stats, float* pre_stats,
+                          void* stream) {
+  qha::ResidualArgs a;
+  int st = take_residual(a, n_rows, positions, c, stream_type, type, post, pre, {post_weight, post_bias, pre_weight, pre_bias}, skip, branch);
+  if (st) return st;
+  if (!(eps >= 0.0) || !std::isfinite(static_cast<float>(eps))) return fail(QHA_ERR_INVALID_ARG, "eps must be finite in float32 and not negative");
+  if (!aligned(post_stats, 8) || !aligned(pre_stats, 8)) return fail(QHA_ERR_INVALID_ARG, "statistics are not 8-byte aligned");
+  if (pre == QHA_ROW_NONE && (u || pre_stats || pre_weight || pre_bias)) return fail(QHA_ERR_INVALID_ARG, "u, pre_stats or a pre vector without a pre norm");
+  if (post == QHA_ROW_NONE && post_stats) return fail(QHA_ERR_INVALID_ARG, "post_stats without a post norm");
+  if (!h && (post != QHA_ROW_NONE || pre == QHA_ROW_NONE || y || gate || post_weight || post_bias) && n_rows > 0)
+    return fail(QHA_ERR_INVALID_ARG, "without h there is a pre norm alone: no y, gate, post norm or post vectors");
+  if (n_rows == 0) return ok();
+  if ((st = check_rows("x", x, ldx, c, stream_type))) return st;
+  if (h && ((st = check_rows("h", h, ldh, c, type)) || (st = check_rows("y", y, ldy, c, stream_type)))) return st;
+  if (gate && (st = check_rows("gate", gate, ldg, c, type))) return st;
+  if (pre != QHA_ROW_NONE && (st = check_rows("u", u, ldu, c, type))) return st;
+  a.eps = static_cast<float>(eps);
+  a.x = x;
+  a.ldx = ldx;
+  a.h = h;
+  a.ldh = ldh;
+  a.gate = gate;
+  a.ldg = ldg;
+  a.y = y;
+  a.ldy = ldy;
+  a.u = u;
+  a.ldu = ldu;
+  a.post_stats = post_stats;
+  a.pre_stats = pre_stats;
+  return hip_status(qha::launch_residual(a, false, static_cast<hipStream_t>(stream)), "residual_norm_fwd");
+}
+
+int qha_residual_norm_bwd(int64_t n_rows, int64_t positions, int32_t c, int32_t stream_type, int32_t type,
+                          int32_t post, int32_t pre, const void* dy, int64_t lddy, const void* du, int64_t lddu,
+                          const void* y, int64_t ldy, const void* h, int64_t ldh, const void* gate, int64_t ldg,
+                          const float* post_weight, const float* post_bias, const float* pre_weight, double skip,
+                          double branch, const float* post_stats, const float* pre_stats, void* dx, int64_t lddx,
+                          void* dh, int64_t lddh, void* dgate, int64_t lddg, float* dpost_weight, float* dpost_bias,
+                          float* dpre_weight, float* dpre_bias, void* workspace, size_t workspace_bytes, void* stream) {
+  qha::ResidualArgs a;
+  int st = take_residual(a, n_rows, positions, c, stream_type, type, post, pre, {post_weight, post_bias, pre_weight, nullptr}, skip, branch);
+  if (st) return st;
+  float* const grads[4] = {dpost_weight, dpost_bias, dpre_weight, dpre_bias};
+  for (float* v : grads)
+    if (!aligned(v, 4)) return fail(QHA_ERR_INVALID_ARG, "a vector's gradient is misaligned");
+  if (pre == QHA_ROW_NONE && (du || pre_stats || pre_weight || dpre_weight || dpre_bias)) return fail(QHA_ERR_INVALID_ARG, "du, pre_stats or a pre vector without a pre norm");
+  if (post == QHA_ROW_NONE && post_stats) return fail(QHA_ERR_INVALID_ARG, "post_stats without a post norm");
+  if (n_rows > 0) {
+    if (!h && (post != QHA_ROW_NONE || pre == QHA_ROW_NONE || dh || gate || post_weight || post_bias || dpost_weight || dpost_bias))
+      return fail(QHA_ERR_INVALID_ARG, "without h there is a pre norm alone: no dh, gate, post norm or post vectors");
+    if (dgate && !gate) return fail(QHA_ERR_INVALID_ARG, "dgate without a gate");
+    if (!dy && pre == QHA_ROW_NONE) return fail(QHA_ERR_INVALID_ARG, "dy is NULL");
+    if (dy && (st = check_rows("dy", dy, lddy, c, stream_type))) return st;
+    if ((st = check_rows("dx", dx, lddx, c, stream_type))) return st;
+    if (h && ((st = check_rows("h", h, ldh, c, type)) || (st = check_rows("dh", dh, lddh, c, type)))) return st;
+    if (gate && (st = check_rows("gate", gate, ldg, c, type))) return st;
+    if (dgate && (st = check_rows("dgate", dgate, lddg, c, type))) return st;
+    if (pre != QHA_ROW_NONE) {
+      if ((st = check_rows("du", du, lddu, c, type)) || (st = check_rows("y", y, ldy, c, stream_type))) return st;
+      if (!pre_stats || !aligned(pre_stats, 8)) return fail(QHA_ERR_INVALID_ARG, "pre_stats out of contract");
+    }
+    if (post != QHA_ROW_NONE && (!post_stats || !aligned(post_stats, 8))) return fail(QHA_ERR_INVALID_ARG, "post_stats out of contract");
+  }
+  bool partials = false;
+  for (int i = 0; i < 4; ++i) {
+    a.dvec[i] = grads[i];
+    partials = partials || grads[i];
+  }
+  if (n_rows == 0 && !partials) return ok();
+  a.shared_gate = n_rows > 0 && gate && positions > 1;
+  qha::residual_plan(a);
+  partials = n_rows > 0 && (partials || (a.shared_gate && dgate && a.chunks > 1));
+  if (partials) {
+    const size_t need = qha::residual_workspace(a);
+    if (!workspace || workspace_bytes < need) return fail(QHA_ERR_WORKSPACE, "workspace of %zu bytes needed, %zu given", need, workspace ? workspace_bytes : (size_t)0);
+    if (!aligned(workspace, 16)) return fail(QHA_ERR_INVALID_ARG, "workspace is not 16-byte aligned");
+    a.vec_part = static_cast<float*>(workspace);
+    a.gate_part = a.vec_part + a.blocks * 4 * a.c;
+  }
+  a.dy = dy;
+  a.lddy = lddy;
+  a.du = du;
+  a.lddu = lddu;
+  a.x = y;
+  a.ldx = ldy;
+  a.h = h;
+  a.ldh = ldh;
+  a.gate = gate;
+  a.ldg = ldg;
+  a.post_stats = const_cast<float*>(post_stats);
+  a.pre_stats = const_cast<float*>(pre_stats);
+  a.dx = dx;
+  a.lddx = lddx;
+  a.dh = dh;
+  a.lddh = lddh;
+  a.dgate = dgate;
+  a.lddg = lddg;
+  return hip_status(qha::launch_residual(a, true, static_cast<hipStream_t>(stream)), "residual_norm_bwd");
 }
 
 int qha_adamw_step(const qha_adamw_tensor* tensors, int64_t n_tensors, int32_t state_bits, int32_t grad_type,

@@ -250,6 +250,49 @@ hipError_t launch_norm_rows(const NormArgs& a, bool backward, hipStream_t s);
 hipError_t launch_norm_fwd(const NormArgs& a, hipStream_t s);
 hipError_t launch_norm_bwd(const NormArgs& a, hipStream_t s);
 
+// The norms around a block with its gate and the residual stream: rows of c channels, the stream's of stream_type.
+struct ResidualArgs {
+  int64_t rows, positions;           // rows of a sample (they share a gate row)
+  int32_t c, type, stream_type, post, pre;
+  float skip, branch, eps;
+  const void* x;                     // forward: the stream before the block; backward: the one after it
+  int64_t ldx;
+  const void* h;
+  int64_t ldh;
+  const void* gate;
+  int64_t ldg;
+  void* y;
+  int64_t ldy;
+  void* u;
+  int64_t ldu;
+  const float* post_w;
+  const float* post_b;
+  const float* pre_w;
+  const float* pre_b;
+  float* post_stats;                 // [rows][2]: mean and 1 / deviation; written by the forward, read by the backward
+  float* pre_stats;
+  // backward
+  const void* dy;
+  int64_t lddy;
+  const void* du;
+  int64_t lddu;
+  void* dx;
+  int64_t lddx;
+  void* dh;
+  int64_t lddh;
+  void* dgate;
+  int64_t lddg;
+  float* dvec[4];                    // post weight and bias, pre weight and bias
+  int32_t shared_gate;               // a gate, and positions > 1
+  int64_t units, chunks, rows_each;  // pieces of rows; pieces of a sample and their rows
+  int64_t blocks;
+  float* vec_part;                   // [blocks][4][c]
+  float* gate_part;                  // [units][c]
+};
+void residual_plan(ResidualArgs& a);
+size_t residual_workspace(const ResidualArgs& a);
+hipError_t launch_residual(const ResidualArgs& a, bool backward, hipStream_t s);
+
 // AdamW over a batch of tensors, passed to the kernel by value.  Tensor i's chunks are
 // first[i] .. first[i + 1] - 1 of the grid.
 constexpr int kAdamBatch = 48;

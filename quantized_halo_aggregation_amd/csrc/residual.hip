@@ -1,0 +1,418 @@
+// The norms around a block fused with its gate and the residual stream, and their gradients.
+//
+// Mathematics, per row: z = w_p hhat + b_p with hhat = (h - mean) rstd (layer norm), h rstd (RMS) or h;
+//   x' = skip x + branch g z,   u = w_q xhat' + b_q with xhat' the same of x' (in float32, before it is rounded).
+// Backward, with q = w_q du and t = dy + rstd (q - mean q - xhat' mean(q xhat')) (no mean q for RMS):
+//   dx = skip t,  dg = sum of branch t z over the rows that share g,  dh the same form of q = w_p branch t g,
+//   dw = sum dz xhat and db = sum dz over all rows, for both norms.
+//
+// Bound: memory, every array once.  A row belongs to a team of L threads (8 to a wavefront's 64, or a block of 256 or
+// 512) that keeps it in registers, R vectors a thread (16 bytes of the branch's type), so that the statistics of both
+// norms and both outputs come from one read; a thread's places, its weights and its share of the weights' gradients stay with
+// it over many rows.  Sums over a row are float32 (at most 8192 values, means before squares).  Gradients of weights are
+// float32 in a team, one partial a block; those of a shared gate one partial for each piece of a sample's rows; a second launch
+// adds partials in float64 in a fixed order.
+#include "act_common.hpp"
+#include "qha_internal.hpp"
+
+namespace qha {
+namespace {
+
+// Rows as V values a vector, whatever their type.
+template <typename E, int V>
+struct Row {
+  typedef E vec __attribute__((ext_vector_type(V), aligned(16)));
+  typedef float wide __attribute__((ext_vector_type(V)));
+  static __device__ __forceinline__ wide load(const void* p, int64_t at) {
+    return __builtin_convertvector(*reinterpret_cast<const vec*>(static_cast<const E*>(p) + at), wide);
+  }
+  static __device__ __forceinline__ void store(void* p, int64_t at, wide x) {
+    __builtin_nontemporal_store(__builtin_convertvector(x, vec), reinterpret_cast<vec*>(static_cast<E*>(p) + at));
+  }
+};
+
+template <int L>
+constexpr int threads_of() { return L < 256 ? 256 : L; }
+
+// Sums over the team; every thread gets them.  Blocks alternate between two LDS buffers, so that one barrier a sum is enough: a
+// buffer is written again only after the barrier of the sum between.
+template <int L, int N>
+struct TeamSum {
+  static constexpr int W = L < 64 ? L : 64;
+  float (*lds)[8][N];
+  int parity = 0;
+  __device__ __forceinline__ void operator()(float (&s)[N]) {
+#pragma unroll
+    for (int o = W >> 1; o > 0; o >>= 1)
+#pragma unroll
+      for (int i = 0; i < N; ++i) s[i] += __shfl_xor(s[i], o, 64);
+    if constexpr (L > 64) {
+      if ((threadIdx.x & 63) == 0)
+#pragma unroll
+        for (int i = 0; i < N; ++i) lds[parity][threadIdx.x >> 6][i] = s[i];
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        s[i] = 0.0f;
+#pragma unroll
+        for (int k = 0; k < L / 64; ++k) s[i] += lds[parity][k][i];
+      }
+      parity ^= 1;
+    }
+  }
+};
+
+// Thread's places in a row.
+template <int L, int R, int V>
+struct Place {
+  int col[R];
+  bool in[R];
+  __device__ __forceinline__ explicit Place(int c) {
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      col[r] = (static_cast<int>(threadIdx.x) % L + r * L) * V;
+      in[r] = col[r] < c;
+    }
+  }
+  typedef float wide __attribute__((ext_vector_type(V)));
+  __device__ __forceinline__ void weights(const float* w, float other, wide (&to)[R]) const {
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      to[r] = other;
+      if (w && in[r]) to[r] = Row<float, V>::load(w, col[r]);
+    }
+  }
+};
+
+template <typename S, typename T, int L, int R>
+__global__ __launch_bounds__(threads_of<L>()) void residual_fwd_kernel(ResidualArgs a) {
+  constexpr int V = 16 / sizeof(T);
+  constexpr int TEAMS = threads_of<L>() / L;
+  typedef float wide __attribute__((ext_vector_type(V)));
+  __shared__ float lds[2][8][1];
+  TeamSum<L, 1> team_sum{lds};
+  const Place<L, R, V> at(a.c);
+  const float n = static_cast<float>(a.c), eps = a.eps;
+  wide pw[R], pb[R], qw[R], qb[R];
+  at.weights(a.post_w, 1.0f, pw);
+  at.weights(a.post_b, 0.0f, pb);
+  at.weights(a.pre_w, 1.0f, qw);
+  at.weights(a.pre_b, 0.0f, qb);
+  const int64_t step = static_cast<int64_t>(gridDim.x) * TEAMS;
+  wide next_x[R], next_h[R], next_g[R];
+  auto fetch = [&](int64_t row) {
+    const int64_t sample = a.positions == 1 ? row : static_cast<uint32_t>(row) / static_cast<uint32_t>(a.positions);
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      next_x[r] = next_h[r] = 0.0f;
+      next_g[r] = 1.0f;
+      if (row < a.rows && at.in[r]) {
+        next_x[r] = Row<S, V>::load(a.x, row * a.ldx + at.col[r]);
+        if (a.h) next_h[r] = Row<T, V>::load(a.h, row * a.ldh + at.col[r]);
+        if (a.gate) next_g[r] = Row<T, V>::load(a.gate, sample * a.ldg + at.col[r]);
+      }
+    }
+  };
+  // the norm's statistics of a row held as v[R]
+  auto row_stats = [&](const wide (&v)[R], int kind, float* mean, float* rstd) {
+    float s[1] = {0.0f};
+    *mean = 0.0f;
+    if (kind == QHA_ROW_LAYER) {
+#pragma unroll
+      for (int r = 0; r < R; ++r)
+#pragma unroll
+        for (int i = 0; i < V; ++i) s[0] += v[r][i];       // zeros past the row's end
+      team_sum(s);
+      *mean = s[0] / n;              // a quotient: rows of equal values have exactly that mean
+    }
+    s[0] = 0.0f;
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const float d = v[r][i] - *mean;
+        s[0] += at.in[r] ? d * d : 0.0f;
+      }
+    team_sum(s);
+    *rstd = 1.0f / sqrtf(s[0] / n + eps);
+  };
+  int64_t row = static_cast<int64_t>(blockIdx.x) * TEAMS + threadIdx.x / L;
+  fetch(row);
+  for (; row < a.rows; row += step) {
+    wide x[R], z[R], g[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      x[r] = next_x[r];
+      z[r] = next_h[r];
+      g[r] = next_g[r];
+    }
+    fetch(row + step);
+    if (a.h) {
+      float mean = 0.0f, rstd = 1.0f;
+      if (a.post != QHA_ROW_NONE) {
+        row_stats(z, a.post, &mean, &rstd);
+        if (a.post_stats && threadIdx.x % L == 0) *reinterpret_cast<float2*>(a.post_stats + 2 * row) = make_float2(mean, rstd);
+      }
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        x[r] = a.skip * x[r] + a.branch * (g[r] * ((z[r] - mean) * rstd * pw[r] + pb[r]));
+        if (!at.in[r]) x[r] = 0.0f;
+        else Row<S, V>::store(a.y, row * a.ldy + at.col[r], x[r]);
+      }
+    }
+    if (a.pre != QHA_ROW_NONE) {
+      float mean, rstd;
+      row_stats(x, a.pre, &mean, &rstd);
+      if (a.pre_stats && threadIdx.x % L == 0) *reinterpret_cast<float2*>(a.pre_stats + 2 * row) = make_float2(mean, rstd);
+#pragma unroll
+      for (int r = 0; r < R; ++r)
+        if (at.in[r]) Row<T, V>::store(a.u, row * a.ldu + at.col[r], (x[r] - mean) * rstd * qw[r] + qb[r]);
+    }
+  }
+}
+
+// A team's units of rows.  With a gate shared by the rows of a sample, a unit is `rows_each` consecutive rows of one sample (the last
+// one of a sample shorter) and ends with its partial of dg; otherwise a team takes every n-th row.
+template <typename S, typename T, int L, int R>
+__global__ __launch_bounds__(threads_of<L>()) void residual_bwd_kernel(ResidualArgs a) {
+  constexpr int V = 16 / sizeof(T);
+  constexpr int NT = threads_of<L>(), TEAMS = NT / L;
+  typedef float wide __attribute__((ext_vector_type(V)));
+  __shared__ float lds[2][8][2];
+  __shared__ float buf[L < 256 ? NT / 64 : 1][L < 256 ? L * R * V : 1];
+  TeamSum<L, 2> team_sum{lds};
+  const Place<L, R, V> at(a.c);
+  const float inv = 1.0f / static_cast<float>(a.c);
+  wide pw[R], pb[R], qw[R], dpw[R], dpb[R], dqw[R], dqb[R], dg[R];
+  at.weights(a.post_w, 1.0f, pw);
+  at.weights(a.post_b, 0.0f, pb);
+  at.weights(a.pre_w, 1.0f, qw);
+#pragma unroll
+  for (int r = 0; r < R; ++r) dpw[r] = dpb[r] = dqw[r] = dqb[r] = dg[r] = 0.0f;
+  const int64_t teams = static_cast<int64_t>(gridDim.x) * TEAMS;
+  const int64_t team = static_cast<int64_t>(blockIdx.x) * TEAMS + threadIdx.x / L;
+  const bool shared = a.shared_gate;
+  // q - mean q - xhat mean(q xhat), times rstd
+  auto through_norm = [&](wide (&q)[R], const wide (&xhat)[R], int kind, float rstd) {
+    float s[2] = {0.0f, 0.0f};
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        s[0] += q[r][i];
+        s[1] += q[r][i] * xhat[r][i];
+      }
+    team_sum(s);
+    const float level = kind == QHA_ROW_LAYER ? s[0] * inv : 0.0f, along = s[1] * inv;
+#pragma unroll
+    for (int r = 0; r < R; ++r) q[r] = rstd * (q[r] - level - xhat[r] * along);
+  };
+  for (int64_t unit = team; unit < a.units; unit += teams) {
+    int64_t row = unit, end = a.rows, sample = 0;
+    const int64_t step = shared ? 1 : teams;
+    if (shared) {
+      sample = unit / a.chunks;
+      const int64_t first = unit % a.chunks * a.rows_each;
+      row = sample * a.positions + first;
+      end = sample * a.positions + (first + a.rows_each < a.positions ? first + a.rows_each : a.positions);
+    }
+    for (; row < end; row += step) {
+      wide t[R], y[R], q[R], h[R], g[R];
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        t[r] = y[r] = q[r] = h[r] = 0.0f;
+        g[r] = 1.0f;
+        if (at.in[r]) {
+          if (a.pre != QHA_ROW_NONE) {
+            q[r] = Row<T, V>::load(a.du, row * a.lddu + at.col[r]);
+            y[r] = Row<S, V>::load(a.x, row * a.ldx + at.col[r]);
+          }
+          if (a.dy) t[r] = Row<S, V>::load(a.dy, row * a.lddy + at.col[r]);
+          if (a.h) h[r] = Row<T, V>::load(a.h, row * a.ldh + at.col[r]);
+          if (a.gate) g[r] = Row<T, V>::load(a.gate, (shared ? sample : row) * a.ldg + at.col[r]);
+        }
+      }
+      float2 ps = make_float2(0.0f, 1.0f);
+      if (a.post != QHA_ROW_NONE) ps = *reinterpret_cast<const float2*>(a.post_stats + 2 * row);
+      if (a.pre != QHA_ROW_NONE) {
+        const float2 qs = *reinterpret_cast<const float2*>(a.pre_stats + 2 * row);
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+          y[r] = at.in[r] ? (y[r] - qs.x) * qs.y : 0.0f;
+          dqw[r] += q[r] * y[r];
+          dqb[r] += q[r];
+          q[r] *= qw[r];
+        }
+        through_norm(q, y, a.pre, qs.y);
+#pragma unroll
+        for (int r = 0; r < R; ++r) t[r] += q[r];
+      }
+#pragma unroll
+      for (int r = 0; r < R; ++r)
+        if (at.in[r]) Row<S, V>::store(a.dx, row * a.lddx + at.col[r], a.skip * t[r]);
+      if (!a.h) continue;
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        t[r] = at.in[r] ? a.branch * t[r] : 0.0f;
+        h[r] = at.in[r] ? (h[r] - ps.x) * ps.y : 0.0f;
+        const wide e = t[r] * (h[r] * pw[r] + pb[r]);
+        if (shared) dg[r] += e;
+        else if (a.dgate && at.in[r]) Row<T, V>::store(a.dgate, row * a.lddg + at.col[r], e);
+        t[r] *= g[r];
+        dpw[r] += t[r] * h[r];
+        dpb[r] += t[r];
+        t[r] *= pw[r];
+      }
+      if (a.post != QHA_ROW_NONE) through_norm(t, h, a.post, ps.y);
+#pragma unroll
+      for (int r = 0; r < R; ++r)
+        if (at.in[r]) Row<T, V>::store(a.dh, row * a.lddh + at.col[r], t[r]);
+    }
+    if (shared) {
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        if (a.dgate && at.in[r]) {
+          if (a.chunks == 1) Row<T, V>::store(a.dgate, sample * a.lddg + at.col[r], dg[r]);
+          else Row<float, V>::store(a.gate_part, unit * a.c + at.col[r], dg[r]);
+        }
+        dg[r] = 0.0f;
+      }
+    }
+  }
+  // the block's partials: teams of a wavefront by exchanges, wavefronts through LDS
+  float* out = a.vec_part + static_cast<int64_t>(blockIdx.x) * 4 * a.c;
+  auto leave = [&](wide (&v)[R], int which) {
+    if constexpr (L >= 256) {
+#pragma unroll
+      for (int r = 0; r < R; ++r)
+        if (at.in[r]) *reinterpret_cast<typename Row<float, V>::vec*>(out + which * a.c + at.col[r]) = v[r];
+    } else {
+#pragma unroll
+      for (int o = L; o < 64; o <<= 1)
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+#pragma unroll
+          for (int i = 0; i < V; ++i) v[r][i] += __shfl_xor(v[r][i], o, 64);
+      __syncthreads();
+      if ((threadIdx.x & 63) < L)
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+#pragma unroll
+          for (int i = 0; i < V; ++i) buf[threadIdx.x >> 6][at.col[r] + i] = v[r][i];
+      __syncthreads();
+      for (int i = threadIdx.x; i < a.c; i += NT) {
+        float s = 0.0f;
+#pragma unroll
+        for (int k = 0; k < NT / 64; ++k) s += buf[k][i];
+        out[which * a.c + i] = s;
+      }
+    }
+  };
+  if (a.dvec[0]) leave(dpw, 0);
+  if (a.dvec[1]) leave(dpb, 1);
+  if (a.dvec[2]) leave(dqw, 2);
+  if (a.dvec[3]) leave(dqb, 3);
+}
+
+// Adds partials in float64: blocks below 4 * col_blocks those of the weights, 32 columns each, the others those of
+// a sample's gate.  Eight threads a column take every eighth partial and are added in order.
+template <typename T>
+__global__ __launch_bounds__(256) void residual_sums_kernel(ResidualArgs a, int32_t col_blocks) {
+  __shared__ double buf[8][32];
+  const int lane = static_cast<int>(threadIdx.x) & 31, k0 = static_cast<int>(threadIdx.x) >> 5;
+  const int64_t set = static_cast<int64_t>(blockIdx.x) / col_blocks;      // 0 .. 3 the weights' gradients, then the samples
+  const int col = static_cast<int>(static_cast<int64_t>(blockIdx.x) % col_blocks) * 32 + lane;
+  const bool weights = set < 4;
+  if (weights && !a.dvec[set]) return;
+  const float* part = weights ? a.vec_part + set * a.c : a.gate_part + (set - 4) * a.chunks * a.c;
+  const int64_t stride = weights ? 4LL * a.c : a.c, n = weights ? a.blocks : a.chunks;
+  double s = 0.0;
+  if (col < a.c) {
+#pragma unroll 8
+    for (int64_t k = k0; k < n; k += 8) s += static_cast<double>(part[k * stride + col]);
+  }
+  buf[k0][lane] = s;
+  __syncthreads();
+  if (k0 != 0 || col >= a.c) return;
+  for (int k = 1; k < 8; ++k) s += buf[k][lane];
+  if (weights) a.dvec[set][col] = static_cast<float>(s);
+  else static_cast<T*>(a.dgate)[(set - 4) * a.lddg + col] = static_cast<T>(static_cast<float>(s));
+}
+
+// lanes of a team and blocks of a launch, by the vectors of a row
+int team_of(int nvec) {
+  return nvec <= 8 ? 8 : nvec <= 16 ? 16 : nvec <= 32 ? 32 : nvec <= 128 ? 64 : nvec <= 512 ? 256 : 512;
+}
+int64_t most_blocks(int lanes) { return lanes == 512 ? 256 : lanes == 256 ? 512 : 1024; }
+
+template <typename S, typename T, int L, int R>
+void run(const ResidualArgs& a, bool backward, hipStream_t s) {
+  constexpr int TEAMS = threads_of<L>() / L;
+  if (!backward) {
+    const int64_t want = (a.rows + TEAMS - 1) / TEAMS;
+    residual_fwd_kernel<S, T, L, R><<<static_cast<uint32_t>(want < 2048 ? want : 2048), threads_of<L>(), 0, s>>>(a);
+    return;
+  }
+  residual_bwd_kernel<S, T, L, R><<<static_cast<uint32_t>(a.blocks), threads_of<L>(), 0, s>>>(a);
+}
+
+template <typename S, typename T>
+void run(const ResidualArgs& a, bool backward, hipStream_t s) {
+  const int nvec = a.rows > 0 ? a.c / (16 / static_cast<int>(sizeof(T))) : 0;
+  if (nvec == 0) {}                  // no rows: zeros alone
+  else if (nvec <= 8) run<S, T, 8, 1>(a, backward, s);
+  else if (nvec <= 16) run<S, T, 16, 1>(a, backward, s);
+  else if (nvec <= 32) run<S, T, 32, 1>(a, backward, s);
+  else if (nvec <= 64) run<S, T, 64, 1>(a, backward, s);
+  else if (nvec <= 128) run<S, T, 64, 2>(a, backward, s);
+  else if (nvec <= 256) run<S, T, 256, 1>(a, backward, s);
+  else if (nvec <= 512) run<S, T, 256, 2>(a, backward, s);
+  else if (nvec <= 1024) run<S, T, 512, 2>(a, backward, s);
+  else if constexpr (sizeof(T) == 4) run<S, T, 512, 4>(a, backward, s);      // at most 8192 values
+  if (!backward) return;
+  const bool gates = a.dgate && a.shared_gate && a.chunks > 1;
+  const bool vectors = a.dvec[0] || a.dvec[1] || a.dvec[2] || a.dvec[3];
+  if (!gates && !vectors) return;
+  const int32_t col_blocks = (a.c + 31) / 32;
+  const int64_t sets = 4 + (gates ? a.rows / a.positions : 0);
+  residual_sums_kernel<T><<<static_cast<uint32_t>(sets * col_blocks), 256, 0, s>>>(a, col_blocks);
+}
+
+}  // namespace
+
+// Blocks, units and pieces of samples of a backward, from a's rows, positions, c and type.
+void residual_plan(ResidualArgs& a) {
+  const int lanes = team_of(a.c / (a.type == QHA_F32 ? 4 : 8));
+  const int teams = lanes < 256 ? 256 / lanes : 1;
+  const int64_t samples = a.rows / a.positions, most = most_blocks(lanes);
+  a.chunks = 1;
+  a.rows_each = a.positions;
+  a.units = a.rows;
+  if (a.shared_gate) {
+    // whole samples where they fill the launch; otherwise pieces, one for each team
+    const int64_t pieces = (most * teams + samples - 1) / samples;
+    a.rows_each = pieces >= a.positions ? 1 : (a.positions + pieces - 1) / pieces;
+    a.chunks = (a.positions + a.rows_each - 1) / a.rows_each;
+    a.units = samples * a.chunks;
+  }
+  const int64_t want = (a.units + teams - 1) / teams;
+  a.blocks = want < most ? want : most;
+  if (!a.shared_gate) a.units = a.blocks * teams < a.rows ? a.blocks * teams : a.rows;
+}
+
+size_t residual_workspace(const ResidualArgs& a) {
+  size_t bytes = static_cast<size_t>(a.blocks) * 4 * static_cast<size_t>(a.c) * sizeof(float);
+  if (a.shared_gate && a.chunks > 1) bytes += static_cast<size_t>(a.units) * static_cast<size_t>(a.c) * sizeof(float);
+  return bytes;
+}
+
+hipError_t launch_residual(const ResidualArgs& a, bool backward, hipStream_t s) {
+  if (a.type == QHA_F32) run<float, float>(a, backward, s);
+  else if (a.type == QHA_BF16 && a.stream_type == QHA_F32) run<float, __bf16>(a, backward, s);
+  else if (a.type == QHA_BF16) run<__bf16, __bf16>(a, backward, s);
+  else if (a.stream_type == QHA_F32) run<float, _Float16>(a, backward, s);
+  else run<_Float16, _Float16>(a, backward, s);
+  return hipGetLastError();
+}
+
+}  // namespace qha

@@ -70,3 +70,40 @@ def test_activations_keep_nan(kind):
     assert np.isfinite(T.act_slope(z, kind)[[0, 2, 3]]).all()
     if kind == "relu":
         assert T.act(z, kind)[[0, 2, 3]].tolist() == [0.0, 0.0, 2.0] and T.act_slope(z, kind).tolist() == [0.0, 1.0, 0.0, 1.0]
+
+
+@pytest.mark.parametrize("post,pre", [("none", "rms"), ("rms", "layer"), ("layer", "none"), ("layer", "rms")])
+def test_residual_norm_gradients_match_central_differences(post, pre):
+    """Step and bound as above; two rows share a gate row, and both results enter the loss."""
+    rng = np.random.default_rng(11)
+    h_step, shape = 1e-5, (4, 6)
+    x, h, gate = rng.standard_normal(shape), rng.standard_normal(shape), rng.standard_normal((2, 6))
+    vectors = [1 + 0.3 * rng.standard_normal(6) for _ in range(4)]
+    dy, du = rng.standard_normal(shape), rng.standard_normal(shape) if pre != "none" else None
+
+    def loss(x_, h_, gate_, *v):
+        y, u, _, _ = T.residual_norm(x_, h_, gate_, 2, post, pre, v, 0.8, 1.3, 1e-3)
+        return float((y * dy).sum() + (0.0 if du is None else (u * du).sum()))
+    y, _, ps, qs = T.residual_norm(x, h, gate, 2, post, pre, vectors, 0.8, 1.3, 1e-3)
+    dx, dh, dgate, grads = T.residual_norm_backward(dy, du, y, h, gate, 2, post, pre, vectors, ps, qs, 0.8, 1.3)
+    args = [x, h, gate] + vectors
+    for k, grad in enumerate([dx, dh, dgate] + grads):
+        if grad is None:
+            continue
+        for i in np.ndindex(args[k].shape):
+            hi, lo = [t.copy() for t in args], [t.copy() for t in args]
+            hi[k][i] += h_step
+            lo[k][i] -= h_step
+            assert abs((loss(*hi) - loss(*lo)) / (2 * h_step) - grad[i]) < 1e-7
+
+
+def test_residual_norm_is_the_composition_of_its_parts():
+    rng = np.random.default_rng(12)
+    x, h, gate = rng.standard_normal((6, 8)), 3 + rng.standard_normal((6, 8)), rng.standard_normal((3, 8))
+    w, b = rng.standard_normal(8), rng.standard_normal(8)
+    y, u, ps, qs = T.residual_norm(x, h, gate, 2, "layer", "layer", (w, b, w, b), 1.0, 0.5, 1e-6)
+    z = T.group_norm(h, w, b, 1, 1, 1e-6, "none")[0]
+    assert np.allclose(y, x + 0.5 * np.repeat(gate, 2, 0) * z, atol=1e-12)
+    assert np.allclose(u, T.group_norm(y, w, b, 1, 1, 1e-6, "none")[0], atol=1e-12)
+    r = T.residual_norm(x, None, None, 1, "none", "rms", (None, None, None, None), 1.0, 1.0, 0.0)[1]
+    assert np.allclose((r ** 2).mean(1), 1.0)
