@@ -25,6 +25,8 @@
  *   qha_group_norm_bwd        its gradients
  *   qha_residual_norm_fwd     the norms after and before a block fused with its gate and the residual stream
  *   qha_residual_norm_bwd     its gradients
+ *   qha_newton_schulz         matrices orthogonalised by Newton-Schulz products
+ *   qha_muon_step             one step of the optimiser that applies such updates
  *   qha_adamw_step            one AdamW step over many tensors, moments in float32 or 8-bit codes
  *   qha_adamw_values          8-bit moments read back as float32 values
  *
@@ -507,6 +509,61 @@ int qha_residual_norm_bwd(int64_t n_rows, int64_t positions, int32_t c, int32_t 
                           float* dpre_weight, float* dpre_bias, void* workspace, size_t workspace_bytes, void* stream);
 /* Bytes of workspace for the backward, enough for every type, with and without a gate (0 for sizes that the calls refuse). */
 size_t qha_residual_norm_workspace(int64_t n_rows, int64_t positions, int32_t c);
+
+/* Orthogonalises matrices by Newton-Schulz products, each on its own: with X = x / (|x| + eps) (|.| the Frobenius norm),
+ * `steps` times
+ *   A = X X^T,   B = b A + c A^2,   X = a X + B X         (X^T X and X B where there are more rows than columns: the same)
+ * which takes every singular value s of X to a s + b s^3 + c s^5 and keeps the singular vectors.  out = X.
+ * coefficients: host, [steps][3], a, b and c of each step; 1 <= steps <= 16.  They must keep the singular values of X, which
+ * begin in [0, 1], small: INVALID_ARG if some s in [0, 1] can pass 3.8 in size (X's bound, A's its square) or b s^2 + c s^4
+ * 60 on the way, by the largest values that each step's polynomials take.  3.4445, -4.7750, 2.0315 in each of five steps take
+ * [0.002, 1] to about [0.7, 1.2].
+ * matrices: host array, read during the call.  x has elements of `type`, out of out_type, at least one element aligned, with
+ * leading dimensions of at least cols; any rows and cols up to 65536 (UNSUPPORTED above).  out may be x (with the same
+ * leading dimension and type); otherwise outputs must not overlap inputs or each other.  Accesses are of four elements where cols and the
+ * leading dimension are multiples of 4 and the pointer is aligned to four elements.  Matrices without elements are skipped.
+ * Products have float32's precision (two f16 parts of values scaled by powers of two, three products, float32
+ * sums); the norm is summed in float64.  A matrix with a value that is not finite gives NaN throughout; a zero matrix gives zeros.
+ * Results are deterministic and those of a matrix do not depend on the others in its call.
+ * workspace: device, 16-byte aligned, qha_newton_schulz_workspace bytes (0 where no matrix has more than 128 rows or columns:
+ * those stay on chip); calls that may overlap need one each.
+ * Errors: INVALID_ARG, UNSUPPORTED, WORKSPACE, HIP (also where the host has no memory for the list). */
+typedef struct qha_ns_matrix {
+  int64_t rows, cols;
+  const void* x;           /* device type[rows][ldx] */
+  int64_t ldx;
+  void* out;               /* device out_type[rows][ldo] */
+  int64_t ldo;
+} qha_ns_matrix;
+
+int qha_newton_schulz(const qha_ns_matrix* matrices, int64_t n_matrices, int32_t type, int32_t out_type, int32_t steps,
+                      const double* coefficients, double eps, void* workspace, size_t workspace_bytes, void* stream);
+/* Bytes of workspace for matrices of sizes[i][0] rows and sizes[i][1] columns (host), for this and the next call (0 for
+ * sizes or steps that the calls refuse). */
+size_t qha_newton_schulz_workspace(const int64_t* sizes, int64_t n_matrices, int32_t steps);
+
+/* One step of an optimiser with orthogonalised momentum over a list of matrices.  With g = grad_scale * grad:
+ *   momentum = beta momentum + g,   u = g + beta momentum (nesterov) or momentum,   O = Newton-Schulz of u (as above)
+ *   param = param (1 - lr weight_decay) - lr scale O
+ * all float32, param and momentum updated in place; copy (nullable) receives the new parameter rounded to copy_type.
+ * grad has elements of grad_type.  All arrays are rows x cols without gaps, aligned to one element (a matrix is accessed by
+ * four where cols is a multiple of 4 and its pointers are aligned to four elements), and must not overlap.  scale is the
+ * matrix's own factor, such as sqrt(max(1, rows / cols)).  A momentum whose values are not finite spoils its own matrix alone.
+ * lr and the other scalars are host values: a captured call replays the same ones.  steps, coefficients, eps, sizes, workspace,
+ * determinism and errors as there; INVALID_ARG also for lr, weight_decay or a scale that are negative or not finite, beta
+ * outside [0, 1), a grad_scale that is not finite. */
+typedef struct qha_muon_matrix {
+  int64_t rows, cols;
+  float* param;            /* device, updated */
+  const void* grad;        /* device grad_type */
+  void* copy;              /* device copy_type, written, or NULL */
+  float* momentum;         /* device, updated */
+  double scale;
+} qha_muon_matrix;
+
+int qha_muon_step(const qha_muon_matrix* matrices, int64_t n_matrices, int32_t grad_type, int32_t copy_type, double lr,
+                  double beta, int32_t nesterov, double weight_decay, double grad_scale, int32_t steps,
+                  const double* coefficients, double eps, void* workspace, size_t workspace_bytes, void* stream);
 
 /* One AdamW step over a list of tensors.  With g = grad_scale * grad, for every element:
  *   m = beta1 m + (1 - beta1) g,    v = beta2 v + (1 - beta2) g^2,

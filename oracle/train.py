@@ -1,6 +1,6 @@
 """Float64 oracle of the training operators: AdamW with float32 or 8-bit moments, group norm with an
 activation, the norms around a block with its gate and residual stream, and the gated projection, each with
-its gradients.  Written from the formulas; shares no
+its gradients, and Newton-Schulz products with the step that applies them.  Written from the formulas; shares no
 code with the GPU path."""
 import math
 
@@ -183,3 +183,28 @@ def gated_backward(dh, gate, up, a, wg, wu, kind):
     dh, gate, up, a, wg, wu = (np.asarray(t, np.float64) for t in (dh, gate, up, a, wg, wu))
     dg, du = dh * up * act_slope(gate, kind), dh * act(gate, kind)
     return dg @ wg + du @ wu, dg.T @ a, du.T @ a
+
+
+# ---------------------------------------------------------------------------------------------
+# Newton-Schulz products and the step that applies them
+# ---------------------------------------------------------------------------------------------
+
+def newton_schulz(x, coefficients, eps):
+    """X = x / (|x| + eps), whose singular values s go through a s + b s^3 + c s^5 for each (a, b, c)."""
+    x = np.asarray(x, np.float64)
+    size = np.sqrt((x * x).sum()) + eps
+    if size == 0.0:
+        return np.zeros_like(x)
+    u, s, vt = np.linalg.svd(x / size, full_matrices=False)
+    for a, b, c in coefficients:
+        s = a * s + b * s ** 3 + c * s ** 5
+    return (u * s) @ vt
+
+
+def muon(p, g, m, lr, beta, nesterov, weight_decay, scale, grad_scale, coefficients, eps):
+    """(new parameter, new momentum)."""
+    p, g, m = (np.asarray(t, np.float64) for t in (p, g, m))
+    g = grad_scale * g
+    m = beta * m + g
+    o = newton_schulz(g + beta * m if nesterov else m, coefficients, eps)
+    return p * (1.0 - lr * weight_decay) - lr * scale * o, m

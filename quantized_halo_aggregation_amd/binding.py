@@ -148,6 +148,10 @@ _residual_norm_bwd = _sig("qha_residual_norm_bwd", _i32, _i64, _i64, _i32, _i32,
                           _vp, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _vp, C.c_double, C.c_double, _vp, _vp, _vp, _i64,
                           _vp, _i64, _vp, _i64, _vp, _vp, _vp, _vp, _vp, _sz, _vp)
 _residual_norm_ws = _sig("qha_residual_norm_workspace", _sz, _i64, _i64, _i32)
+_newton_schulz = _sig("qha_newton_schulz", _i32, _vp, _i64, _i32, _i32, _i32, _vp, C.c_double, _vp, _sz, _vp)
+_newton_schulz_ws = _sig("qha_newton_schulz_workspace", _sz, _vp, _i64, _i32)
+_muon_step = _sig("qha_muon_step", _i32, _vp, _i64, _i32, _i32, C.c_double, C.c_double, _i32, C.c_double, C.c_double, _i32,
+                  _vp, C.c_double, _vp, _sz, _vp)
 
 EXPORTED = ["qha_abi_version", "qha_status_string", "qha_last_error", "qha_pack_layout", "qha_pack_classes",
             "qha_edge_weights", "qha_validate_csr",
@@ -158,7 +162,8 @@ EXPORTED = ["qha_abi_version", "qha_status_string", "qha_last_error", "qha_pack_
             "qha_dense_backward_workspace", "qha_mask_levels", "qha_node_bits", "qha_level_order",
             "qha_coordinator_init", "qha_coordinator_step", "qha_adamw_step", "qha_adamw_values",
             "qha_gated_project", "qha_gated_backward", "qha_gated_workspace", "qha_group_norm_fwd", "qha_group_norm_bwd", "qha_group_norm_workspace",
-            "qha_residual_norm_fwd", "qha_residual_norm_bwd", "qha_residual_norm_workspace"]
+            "qha_residual_norm_fwd", "qha_residual_norm_bwd", "qha_residual_norm_workspace",
+            "qha_newton_schulz", "qha_newton_schulz_workspace", "qha_muon_step"]
 
 
 class QhaError(RuntimeError):
@@ -865,3 +870,134 @@ class AdamW:
                              _flat(self.v_scale, "v_scale", blocks, torch.float32),
                              _flat(v_out, "v_out", n, torch.float32), n, _stream(stream)), "qha_adamw_values")
         return m_out, v_out
+
+
+# five steps of these take singular values of [0.002, 1] to about [0.7, 1.2]
+NS_COEFFICIENTS = (3.4445, -4.7750, 2.0315)
+
+
+def _ns_coefficients(coefficients, steps):
+    """[steps, 3] float64 from one triple or one for each step."""
+    k = np.asarray(coefficients, dtype=np.float64)
+    if k.shape == (3,):
+        k = np.tile(k, (max(int(steps), 0), 1))
+    if k.shape != (steps, 3):
+        raise ValueError(f"coefficients must be (a, b, c), or {steps} of them, got shape {k.shape}")
+    return np.ascontiguousarray(k)
+
+
+def newton_schulz_workspace(shapes, steps: int = 5) -> int:
+    sizes = np.array([tuple(s) for s in shapes], dtype=np.int64).reshape(-1, 2)
+    return int(_newton_schulz_ws(sizes.ctypes.data, len(sizes), steps))
+
+
+def newton_schulz(xs, outs, steps: int = 5, coefficients=NS_COEFFICIENTS, eps: float = 1e-7, workspace=None, stream=None):
+    """outs[i] = the Newton-Schulz iterate of xs[i] / |xs[i]| after `steps` steps of `coefficients` (a, b, c, or
+    one such triple for each step): lists of matrices, each list of one type, rows may be strided."""
+    n = len(xs)
+    if len(outs) != n:
+        raise ValueError(f"{len(outs)} results for {n} matrices")
+    k = _ns_coefficients(coefficients, steps)
+    if n == 0:
+        return
+    t, o = xs[0].dtype, outs[0].dtype
+    table = np.empty((n, 6), dtype=np.int64)
+    for i, (x, out) in enumerate(zip(xs, outs)):
+        if x.dim() != 2:
+            raise ValueError(f"xs[{i}] must be a matrix, got {tuple(x.shape)}")
+        rows, cols = x.shape
+        table[i] = rows, cols, *_matrix(x, "a matrix", t, rows, cols), *_matrix(out, "a result", o, rows, cols)
+    ws, ws_bytes = _space(workspace)
+    _on_current(*xs, *outs, workspace)
+    _check(_newton_schulz(table.ctypes.data, n, _type(t, "xs"), _type(o, "outs"), steps, k.ctypes.data, eps, ws, ws_bytes,
+                          _stream(stream)), "qha_newton_schulz")
+
+
+class Muon:
+    """Muon over a list of float32 weight matrices, updated in place by qha_muon_step: momentum, orthogonalised by
+    Newton-Schulz products.
+
+    scale: what a matrix's update is multiplied by beside lr, "spectral" for sqrt(max(1, rows / cols)), "rms" for
+    0.2 sqrt(max(rows, cols)) (the size of an AdamW update), or a number.  The momenta `m` (float32 tensors like the
+    parameters; zeros, or those given) are all of the state: copy them to save, and copy into them or put others
+    into the list to resume.  `copies`, if given, are tensors of one 16-bit or float32 type that receive the rounded
+    parameters.  Tensors that were replaced since the last step are checked again and used from then on.  Steps of one
+    optimiser share its workspace and must not overlap."""
+
+    def __init__(self, params, momentum: float = 0.95, nesterov: bool = True, weight_decay: float = 0.0,
+                 scale="spectral", steps: int = 5, coefficients=NS_COEFFICIENTS, eps: float = 1e-7, momenta=None,
+                 copies=None):
+        self.params = list(params)
+        self.momentum, self.nesterov, self.weight_decay, self.eps = momentum, nesterov, weight_decay, eps
+        self._steps, self._k = steps, _ns_coefficients(coefficients, steps)
+        n = len(self.params)
+        for i, p in enumerate(self.params):
+            _flat(p, f"params[{i}]", dtype=torch.float32)
+            if p.dim() != 2:
+                raise ValueError(f"params[{i}] must be a matrix, got {tuple(p.shape)}")
+        self.m = [torch.zeros_like(p) for p in self.params] if momenta is None else list(momenta)
+        self.copies = None if copies is None else list(copies)
+        self.shapes = [tuple(p.shape) for p in self.params]
+        # one qha_muon_matrix per row: rows, cols, param, grad, copy, momentum, scale
+        self._table = np.zeros((max(n, 1), 7), dtype=np.int64)
+        for i, (rows, cols) in enumerate(self.shapes):
+            self._table[i, :2] = rows, cols
+            self._table.view(np.float64)[i, 6] = self._scale(scale, rows, cols)
+        self._ws = None
+        self._seen = None
+        self._look()
+
+    @staticmethod
+    def _scale(scale, rows, cols):
+        if scale == "spectral":
+            return max(1.0, rows / max(cols, 1)) ** 0.5
+        if scale == "rms":
+            return 0.2 * max(rows, cols) ** 0.5
+        if isinstance(scale, str):
+            raise ValueError(f'scale must be "spectral", "rms" or a number, got "{scale}"')
+        return float(scale)
+
+    def _look(self):
+        """Checks every tensor and writes its address into the table, if any address is another one than at the last
+        step.  `_held` aliases the tensors seen, so an equal address is the same memory."""
+        tensors = self.params + self.m + (self.copies or [])
+        seen = [t.data_ptr() for t in tensors]
+        if seen == self._seen:
+            return
+        self._seen = None
+        n, table = len(self.shapes), self._table
+        if len(self.params) != n or len(self.m) != n or (self.copies is not None and len(self.copies) != n):
+            raise ValueError(f"{n} parameters were given, now there are {len(self.params)}, {len(self.m)} momenta and "
+                             f"{n if self.copies is None else len(self.copies)} copies")
+        self._copy_type = _type(self.copies[0].dtype, "copies") if self.copies else F32
+        for name, column, given in (("params", 2, self.params), ("copies", 4, self.copies), ("m", 5, self.m)):
+            for i, t in enumerate(given or ()):
+                if tuple(t.shape) != self.shapes[i]:
+                    raise ValueError(f"{name}[{i}] must be {self.shapes[i]}, got {tuple(t.shape)}")
+                table[i, column] = _flat(t, f"{name}[{i}]", dtype=self.copies[0].dtype if column == 4 else torch.float32)
+        if len({t.device for t in tensors}) > 1:
+            raise ValueError("parameters, momenta and copies must live on one GPU")
+        need = newton_schulz_workspace(self.shapes, self._steps)
+        if need and (self._ws is None or self._ws.device != self.params[0].device):
+            self._ws = torch.empty(need, dtype=torch.uint8, device=self.params[0].device)
+        self._held = [t.detach() for t in tensors]
+        self._seen = seen
+
+    def step(self, grads, lr: float, grad_scale: float = 1.0, stream=None):
+        """One step with grads (one tensor per parameter, of one type; scaled by grad_scale)."""
+        n = len(self.shapes)
+        if len(grads) != n:
+            raise ValueError(f"{len(grads)} gradients for {n} parameters")
+        if n == 0:
+            return
+        self._look()
+        dtype = grads[0].dtype
+        for i, (g, shape) in enumerate(zip(grads, self.shapes)):
+            if g.shape != shape:
+                raise ValueError(f"grads[{i}] must be {shape}, got {tuple(g.shape)}")
+            self._table[i, 3] = _flat(g, "a gradient", dtype=dtype)
+        _on_current(self.params[0], *grads)
+        ws, ws_bytes = _space(self._ws)
+        _check(_muon_step(self._table.ctypes.data, n, _type(dtype, "grads"), self._copy_type, lr, self.momentum,
+                          int(self.nesterov), self.weight_decay, grad_scale, self._steps, self._k.ctypes.data, self.eps,
+                          ws, ws_bytes, _stream(stream)), "qha_muon_step")

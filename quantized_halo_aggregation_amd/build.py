@@ -17,8 +17,8 @@ OUT = os.path.join(PKG, "libqha.so")
 BUILD_DIR = os.path.join(PKG, "_build")
 SOURCES = ["abi.cpp", "control.cpp", "quantize.hip", "gather.hip", "gemm.hip", "panel.hip",
            "abi_train.cpp", "adamw.hip", "norm.hip", "norm_rows.hip",
-           "gated.hip", "residual.hip"]
-HEADERS = ["qha_internal.hpp", "act_common.hpp"]
+           "gated.hip", "residual.hip", "ns.hip"]
+HEADERS = ["qha_internal.hpp", "act_common.hpp", "tile_common.hpp"]
 
 ARCH = "gfx950"
 FLAGS = [

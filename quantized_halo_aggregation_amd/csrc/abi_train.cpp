@@ -5,8 +5,11 @@
 
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstring>
+#include <memory>
+#include <new>
 
 using qha::fail;
 using qha::ok;
@@ -131,6 +134,62 @@ int take_gated_workspace(qha::GatedArgs& g, bool backward, void* ws, size_t byte
   if (!aligned(ws, 16)) return fail(QHA_ERR_INVALID_ARG, "workspace is not 16-byte aligned");
   g.ws = ws;
   return QHA_OK;
+}
+
+constexpr int64_t kMaxSide = 1 << 16;       // rows and columns of a matrix to orthogonalise
+
+// The largest magnitude of f(s) = s (a + b s^2 + c s^4) over [0, top]: at its ends or where f' = a + 3 b t + 5 c t^2 = 0, t = s^2.
+double largest_of(double a, double b, double c, double top) {
+  const auto f = [&](double s) { return std::fabs(s * (a + s * s * (b + s * s * c))); };
+  double most = f(top);
+  const double d = 9.0 * b * b - 20.0 * a * c;
+  double roots[3] = {-1.0, -1.0, -1.0};
+  if (c != 0.0 && d >= 0.0) {
+    roots[0] = (-3.0 * b + std::sqrt(d)) / (10.0 * c);
+    roots[1] = (-3.0 * b - std::sqrt(d)) / (10.0 * c);
+  }
+  if (b != 0.0) roots[2] = -a / (3.0 * b);      // also near it where c is tiny
+  for (double t : roots)
+    if (t > 0.0 && t < top * top) most = std::max(most, f(std::sqrt(t)));
+  return most;
+}
+
+// The polynomials must keep X, A and B within the scaled parts' range.
+int check_steps(int32_t steps, const double* coefficients, double eps) {
+  if (steps < 1 || steps > qha::kNsSteps) return fail(QHA_ERR_INVALID_ARG, "steps must lie in 1 .. %d, got %d", qha::kNsSteps, steps);
+  if (!coefficients) return fail(QHA_ERR_INVALID_ARG, "coefficients is NULL");
+  if (!(eps >= 0.0) || !std::isfinite(eps)) return fail(QHA_ERR_INVALID_ARG, "eps must be finite and not negative");
+  double top = 1.0;
+  for (int32_t i = 0; i < steps; ++i) {
+    const double a = coefficients[3 * i], b = coefficients[3 * i + 1], c = coefficients[3 * i + 2];
+    if (!std::isfinite(a) || !std::isfinite(b) || !std::isfinite(c)) return fail(QHA_ERR_INVALID_ARG, "a coefficient is not finite");
+    const double t = top * top;
+    double inner = std::fabs(t * (b + c * t));                       // |b t + c t^2| over [0, top^2]
+    if (c != 0.0 && -b / (2.0 * c) > 0.0 && -b / (2.0 * c) < t) inner = std::max(inner, std::fabs(b * b / (4.0 * c)));
+    if (!(inner <= 60.0)) return fail(QHA_ERR_INVALID_ARG, "step %d: b s^2 + c s^4 passes 60", i);
+    top = largest_of(a, b, c, top);
+    if (!(top <= 3.8)) return fail(QHA_ERR_INVALID_ARG, "step %d: singular values pass 3.8", i);
+  }
+  return QHA_OK;
+}
+
+int check_sides(int64_t rows, int64_t cols) {
+  if (rows < 0 || cols < 0) return fail(QHA_ERR_INVALID_ARG, "a negative size");
+  if (rows > kMaxSide || cols > kMaxSide) return fail(QHA_ERR_UNSUPPORTED, "%lld x %lld: more than 65536 rows or columns", (long long)rows, (long long)cols);
+  return QHA_OK;
+}
+
+int check_ns_workspace(const qha::NsMatrix* m, int64_t n, const void* ws, size_t bytes) {
+  const size_t need = qha::ns_workspace(m, n);
+  if (need == 0) return QHA_OK;
+  if (!ws || bytes < need) return fail(QHA_ERR_WORKSPACE, "workspace of %zu bytes needed, %zu given", need, ws ? bytes : (size_t)0);
+  if (!aligned(ws, 16)) return fail(QHA_ERR_INVALID_ARG, "workspace is not 16-byte aligned");
+  return QHA_OK;
+}
+
+// The library's list of a call's matrices; no exception crosses the C ABI.
+std::unique_ptr<qha::NsMatrix[]> ns_list(int64_t n) {
+  return std::unique_ptr<qha::NsMatrix[]>(n < (1LL << 32) ? new (std::nothrow) qha::NsMatrix[static_cast<size_t>(n)]() : nullptr);
 }
 
 }  // namespace
@@ -407,6 +466,99 @@ int qha_residual_norm_bwd(int64_t n_rows, int64_t positions, int32_t c, int32_t 
   a.dgate = dgate;
   a.lddg = lddg;
   return hip_status(qha::launch_residual(a, true, static_cast<hipStream_t>(stream)), "residual_norm_bwd");
+}
+
+size_t qha_newton_schulz_workspace(const int64_t* sizes, int64_t n_matrices, int32_t steps) {
+  if (!sizes || n_matrices <= 0 || steps < 1 || steps > qha::kNsSteps) return 0;
+  const auto list = ns_list(n_matrices);
+  if (!list) return 0;
+  for (int64_t i = 0; i < n_matrices; ++i) {
+    if (check_sides(sizes[2 * i], sizes[2 * i + 1])) return 0;
+    list[i].rows = sizes[2 * i];
+    list[i].cols = sizes[2 * i + 1];
+  }
+  return qha::ns_workspace(list.get(), n_matrices);
+}
+
+int qha_newton_schulz(const qha_ns_matrix* matrices, int64_t n_matrices, int32_t type, int32_t out_type, int32_t steps,
+                      const double* coefficients, double eps, void* workspace, size_t workspace_bytes, void* stream) {
+  if (n_matrices < 0) return fail(QHA_ERR_INVALID_ARG, "n_matrices < 0");
+  if (!known_type(type) || !known_type(out_type)) return fail(QHA_ERR_INVALID_ARG, "unknown element type");
+  int st = check_steps(steps, coefficients, eps);
+  if (st) return st;
+  if (n_matrices == 0) return ok();
+  if (!matrices) return fail(QHA_ERR_INVALID_ARG, "matrices is NULL");
+  const auto list = ns_list(n_matrices);
+  if (!list) return fail(QHA_ERR_HIP, "no memory for %lld matrices", (long long)n_matrices);
+  for (int64_t i = 0; i < n_matrices; ++i) {
+    const qha_ns_matrix& m = matrices[i];
+    if ((st = check_sides(m.rows, m.cols))) return st;
+    if (m.rows == 0 || m.cols == 0) continue;
+    if (!m.x || !m.out) return fail(QHA_ERR_INVALID_ARG, "matrix %lld: NULL pointer", (long long)i);
+    if (m.ldx < m.cols || m.ldo < m.cols) return fail(QHA_ERR_INVALID_ARG, "matrix %lld: leading dimension below its %lld columns", (long long)i, (long long)m.cols);
+    if (!aligned(m.x, type_bytes(type)) || !aligned(m.out, type_bytes(out_type))) return fail(QHA_ERR_INVALID_ARG, "matrix %lld: misaligned pointer", (long long)i);
+    list[i].rows = m.rows;
+    list[i].cols = m.cols;
+    list[i].src = m.x;
+    list[i].lds = m.ldx;
+    list[i].dst = m.out;
+    list[i].ldo = m.ldo;
+  }
+  if ((st = check_ns_workspace(list.get(), n_matrices, workspace, workspace_bytes))) return st;
+  qha::NsArgs a = {};
+  a.type = type;
+  a.out_type = out_type;
+  a.steps = steps;
+  a.eps = eps;
+  a.coefficients = coefficients;
+  return hip_status(qha::launch_ns(list.get(), n_matrices, a, workspace, static_cast<hipStream_t>(stream)), "newton_schulz");
+}
+
+int qha_muon_step(const qha_muon_matrix* matrices, int64_t n_matrices, int32_t grad_type, int32_t copy_type, double lr,
+                  double beta, int32_t nesterov, double weight_decay, double grad_scale, int32_t steps,
+                  const double* coefficients, double eps, void* workspace, size_t workspace_bytes, void* stream) {
+  if (n_matrices < 0) return fail(QHA_ERR_INVALID_ARG, "n_matrices < 0");
+  if (!known_type(grad_type) || !known_type(copy_type)) return fail(QHA_ERR_INVALID_ARG, "unknown element type");
+  if (!(lr >= 0.0) || !(weight_decay >= 0.0) || !std::isfinite(static_cast<float>(lr)) || !std::isfinite(static_cast<float>(lr * weight_decay)) ||
+      !std::isfinite(weight_decay) || !std::isfinite(static_cast<float>(grad_scale)))
+    return fail(QHA_ERR_INVALID_ARG, "lr and weight_decay must be finite and not negative, grad_scale finite");
+  if (!(beta >= 0.0 && beta < 1.0)) return fail(QHA_ERR_INVALID_ARG, "beta must lie in [0, 1)");
+  int st = check_steps(steps, coefficients, eps);
+  if (st) return st;
+  if (n_matrices == 0) return ok();
+  if (!matrices) return fail(QHA_ERR_INVALID_ARG, "matrices is NULL");
+  const auto list = ns_list(n_matrices);
+  if (!list) return fail(QHA_ERR_HIP, "no memory for %lld matrices", (long long)n_matrices);
+  for (int64_t i = 0; i < n_matrices; ++i) {
+    const qha_muon_matrix& m = matrices[i];
+    if ((st = check_sides(m.rows, m.cols))) return st;
+    if (!(m.scale >= 0.0) || !std::isfinite(static_cast<float>(lr * m.scale))) return fail(QHA_ERR_INVALID_ARG, "matrix %lld: scale must be finite and not negative", (long long)i);
+    if (m.rows == 0 || m.cols == 0) continue;
+    if (!m.param || !m.grad || !m.momentum) return fail(QHA_ERR_INVALID_ARG, "matrix %lld: NULL pointer", (long long)i);
+    if (!aligned(m.param, 4) || !aligned(m.momentum, 4) || !aligned(m.grad, type_bytes(grad_type)) || !aligned(m.copy, type_bytes(copy_type)))
+      return fail(QHA_ERR_INVALID_ARG, "matrix %lld: misaligned pointer", (long long)i);
+    list[i].rows = m.rows;
+    list[i].cols = m.cols;
+    list[i].src = m.grad;
+    list[i].lds = list[i].ldo = m.cols;
+    list[i].dst = m.param;
+    list[i].mom = m.momentum;
+    list[i].copy = m.copy;
+    list[i].step = static_cast<float>(lr * m.scale);
+  }
+  if ((st = check_ns_workspace(list.get(), n_matrices, workspace, workspace_bytes))) return st;
+  qha::NsArgs a = {};
+  a.type = grad_type;
+  a.out_type = copy_type;
+  a.muon = 1;
+  a.nesterov = nesterov != 0;
+  a.steps = steps;
+  a.mu = static_cast<float>(beta);
+  a.grad_scale = static_cast<float>(grad_scale);
+  a.decay = static_cast<float>(1.0 - lr * weight_decay);
+  a.eps = eps;
+  a.coefficients = coefficients;
+  return hip_status(qha::launch_ns(list.get(), n_matrices, a, workspace, static_cast<hipStream_t>(stream)), "muon_step");
 }
 
 int qha_adamw_step(const qha_adamw_tensor* tensors, int64_t n_tensors, int32_t state_bits, int32_t grad_type,

@@ -293,6 +293,59 @@ void residual_plan(ResidualArgs& a);
 size_t residual_workspace(const ResidualArgs& a);
 hipError_t launch_residual(const ResidualArgs& a, bool backward, hipStream_t s);
 
+// Newton-Schulz products of matrices: what a call gives of each of them ...
+struct NsMatrix {
+  int64_t rows, cols;
+  const void* src;                   // the matrix, or its gradient
+  int64_t lds;
+  void* dst;                         // the result, or the weights
+  int64_t ldo;                       // of dst, and of the momentum and the copy
+  float* mom;                        // the optimiser's, or null
+  void* copy;                        // the new weights' copy, or null
+  float step;                        // the learning rate times the matrix's scale
+};
+struct NsArgs {
+  int32_t type, out_type;            // of src; of dst, or of the copies
+  int32_t muon, nesterov, steps;
+  float mu, grad_scale, decay;       // decay: 1 - learning rate * weight decay
+  double eps;
+  const double* coefficients;        // [steps][3]
+};
+// ... and a batch of them, passed to the kernels by value.
+constexpr int kNsBatch = 24, kNsSteps = 16;
+struct NsMat {
+  const void* src;
+  int64_t lds;
+  void* dst;
+  int64_t ldo;
+  float* mom;
+  void* copy;
+  uint16_t* x[2];                    // pairs of parts: X and the next one, A and B
+  uint16_t* a;
+  uint16_t* b;
+  double* parts;                     // sums of squares
+  int32_t rows, cols, m_pad, n_pad;  // X's sizes (the shorter first), padded to 64
+  float step;
+  uint8_t tall, vec_src, vec_out, vec_mom, vec_copy;
+};
+struct NsTable {
+  NsMat m[kNsBatch];
+  uint32_t first_piece[kNsBatch], first_tile[kNsBatch];
+  int32_t n, type, out_type, muon, nesterov;
+  float mu, grad_scale, decay;
+  double eps;
+};
+struct NsCoef {
+  float product, own;                // C = product * acc + own * the matrix that is there
+};
+struct NsSteps {
+  int32_t steps;
+  NsCoef gram, square[kNsSteps], apply[kNsSteps];
+};
+static_assert(sizeof(NsTable) + sizeof(NsSteps) <= 4096, "kernel arguments");
+size_t ns_workspace(const NsMatrix* m, int64_t n);
+hipError_t launch_ns(const NsMatrix* m, int64_t n, const NsArgs& args, void* ws, hipStream_t s);
+
 // AdamW over a batch of tensors, passed to the kernel by value.  Tensor i's chunks are
 // first[i] .. first[i + 1] - 1 of the grid.
 constexpr int kAdamBatch = 48;

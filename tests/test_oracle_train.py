@@ -107,3 +107,31 @@ def test_residual_norm_is_the_composition_of_its_parts():
     assert np.allclose(u, T.group_norm(y, w, b, 1, 1, 1e-6, "none")[0], atol=1e-12)
     r = T.residual_norm(x, None, None, 1, "none", "rms", (None, None, None, None), 1.0, 1.0, 0.0)[1]
     assert np.allclose((r ** 2).mean(1), 1.0)
+
+
+@pytest.mark.parametrize("shape", [(5, 5), (3, 9), (9, 3), (1, 4), (4, 1)])
+def test_newton_schulz_is_the_iteration_of_its_products(shape):
+    rng = np.random.default_rng(13)
+    g = rng.standard_normal(shape)
+    steps = [(3.4445, -4.7750, 2.0315)] * 4 + [(15 / 8, -10 / 8, 3 / 8)]
+    x = g / (np.sqrt((g ** 2).sum()) + 1e-7)
+    for a, b, c in steps:
+        s = x @ x.T
+        x = a * x + (b * s + c * s @ s) @ x
+    assert np.allclose(T.newton_schulz(g, steps, 1e-7), x, atol=1e-12)
+    assert np.allclose(T.newton_schulz(g.T, steps, 1e-7), x.T, atol=1e-12)
+    assert not T.newton_schulz(0 * g, steps, 0.0).any()
+    # twenty steps of Newton's own cubic make the nearest matrix with orthonormal rows or columns
+    q = T.newton_schulz(g, [(1.5, -0.5, 0.0)] * 40, 0.0)
+    gram = q @ q.T if shape[0] <= shape[1] else q.T @ q
+    assert np.allclose(gram, np.eye(min(shape)), atol=1e-9)
+
+
+def test_muon_step_by_hand():
+    """One value: its own singular value, 1 after scaling, so O = a + b + c = 0.701 with the sign of u."""
+    k = [(3.4445, -4.7750, 2.0315)]
+    p, m = T.muon([[2.0]], [[0.5]], [[-1.0]], 0.1, 0.9, True, 0.01, 3.0, 2.0, k, 0.0)
+    assert np.allclose(m, 0.1)                   # 0.9 * -1 + 2 * 0.5
+    assert np.allclose(p, 2.0 * 0.999 - 0.1 * 3.0 * 0.701)          # u = 1 + 0.9 * 0.1 > 0
+    p, m = T.muon([[2.0]], [[0.5]], [[-1.0]], 0.1, 0.9, False, 0.0, 1.0, 1.0, k, 0.0)
+    assert np.allclose(m, -0.4) and np.allclose(p, 2.0 + 0.1 * 0.701)

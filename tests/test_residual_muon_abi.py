@@ -1,4 +1,4 @@
-"""Refusals of the residual norm's entry points and of their binding, without a GPU.
+"""Refusals of the entry points of the residual norm, Newton-Schulz and Muon, and of their binding, without a GPU.
 
 Argument-error cases pass fake (never dereferenced) device addresses: the checks must fire first.
 """
@@ -109,3 +109,185 @@ def test_residual_norm_binding_refuses(monkeypatch):
         B.residual_norm_fwd(x, _gpu(6, 64, cls=Other), x, x, stream=0)
     with pytest.raises(ValueError, match="current device is cuda:0"):
         B.residual_norm_bwd(x, x, x, x, x, x, post_stats=_gpu(6, 2), pre_stats=_gpu(6, 2, cls=Other), stream=0)
+
+
+def _coef(k=B.NS_COEFFICIENTS, steps=5):
+    return B._ns_coefficients(k, steps)
+
+
+def _table(rows):
+    import numpy as np
+    return np.array(rows, dtype=np.int64).reshape(len(rows), -1)
+
+
+GOOD_NS = (200, 300, FAKE, 300, FAKE, 300)
+
+
+def _ns(rows=(GOOD_NS,), n=None, t=B.F32, o=B.F32, steps=5, k=None, eps=1e-7, ws=FAKE, wsb=1 << 40):
+    table = _table(rows) if rows else None
+    k = _coef(steps=5) if k is None else k
+    return B._newton_schulz(None if table is None else table.ctypes.data, len(rows) if n is None else n, t, o, steps,
+                            k if isinstance(k, int) else k.ctypes.data, eps, ws, wsb, None)
+
+
+GOOD_MUON = (200, 300, FAKE, FAKE, FAKE, FAKE, 1.0)
+
+
+def _muon(rows=(GOOD_MUON,), n=None, gt=B.F32, ct=B.F32, lr=0.02, beta=0.95, wd=0.1, gs=1.0, steps=5, k=None, eps=1e-7,
+          ws=FAKE, wsb=1 << 40):
+    import numpy as np
+    table = np.zeros((max(len(rows), 1), 7), np.int64)
+    for i, r in enumerate(rows):
+        table[i, :6] = r[:6]
+        table.view(np.float64)[i, 6] = r[6]
+    k = _coef(steps=5) if k is None else k
+    return B._muon_step(table.ctypes.data if rows else None, len(rows) if n is None else n, gt, ct, lr, beta, 1, wd, gs, steps,
+                        k if isinstance(k, int) else k.ctypes.data, eps, ws, wsb, None)
+
+
+STEPS = [dict(n=-1), dict(steps=0), dict(steps=17), dict(steps=-1), dict(k=0), dict(eps=-1.0), dict(eps=NAN), dict(rows=(), n=1),
+         dict(k=_coef((40, 0, 0))), dict(k=_coef((4, -7, 4))), dict(k=_coef((NAN, 0, 0))), dict(k=_coef((1, float("inf"), 0))),
+         dict(k=_coef((0, 0, -70))),
+         # 1.99 after the first step, 6.9 - 37.8 + 64 after the second
+         dict(k=_coef([(8.2872, -23.5959, 17.3004)] + [(3.4445, -4.7750, 2.0315)] * 4)), dict(k=_coef((0, 240, -240))), dict(ws=FAKE + 8)]
+
+
+@pytest.mark.parametrize("bad", STEPS + [
+    dict(t=3), dict(o=-1), dict(rows=((-1, 300, FAKE, 300, FAKE, 300),)), dict(rows=((200, 300, 0, 300, FAKE, 300),)),
+    dict(rows=((200, 300, FAKE, 300, 0, 300),)), dict(rows=((200, 300, FAKE, 299, FAKE, 300),)),
+    dict(rows=((200, 300, FAKE, 300, FAKE, 0),)), dict(rows=((200, 300, FAKE + 2, 300, FAKE, 300),)),
+    dict(rows=((200, 300, FAKE + 1, 300, FAKE, 300),), t=B.BF16), dict(rows=((200, 300, FAKE, 300, FAKE + 1, 300),), o=B.F16),
+    dict(rows=(GOOD_NS, (4, 4, 0, 4, FAKE, 4)))])
+def test_newton_schulz_refuses(bad):
+    assert _ns(**bad) == B.QHA_ERR_INVALID_ARG
+    assert B._last_error()
+
+
+@pytest.mark.parametrize("bad", STEPS + [
+    dict(gt=3), dict(ct=-1), dict(lr=-1.0), dict(lr=NAN), dict(lr=1e300), dict(beta=1.0), dict(beta=-0.1), dict(beta=NAN),
+    dict(wd=-1.0), dict(wd=float("inf")), dict(gs=NAN), dict(gs=1e300),
+    dict(rows=((200, -3, FAKE, FAKE, 0, FAKE, 1.0),)), dict(rows=((200, 300, 0, FAKE, 0, FAKE, 1.0),)),
+    dict(rows=((200, 300, FAKE, 0, 0, FAKE, 1.0),)), dict(rows=((200, 300, FAKE, FAKE, 0, 0, 1.0),)),
+    dict(rows=((200, 300, FAKE + 2, FAKE, 0, FAKE, 1.0),)), dict(rows=((200, 300, FAKE, FAKE + 2, 0, FAKE, 1.0),)),
+    dict(rows=((200, 300, FAKE, FAKE, 0, FAKE + 2, 1.0),)), dict(rows=((200, 300, FAKE, FAKE, FAKE + 1, FAKE, 1.0),), ct=B.BF16),
+    dict(rows=((200, 300, FAKE, FAKE, 0, FAKE, -1.0),)), dict(rows=((200, 300, FAKE, FAKE, 0, FAKE, NAN),)),
+    dict(rows=(GOOD_MUON, (4, 4, FAKE, FAKE, 0, 0, 1.0)))])
+def test_muon_step_refuses(bad):
+    assert _muon(**bad) == B.QHA_ERR_INVALID_ARG
+    assert B._last_error()
+
+
+def test_newton_schulz_limits_and_workspace():
+    far = ((1 << 17, 4, FAKE, 4, FAKE, 4),)
+    assert _ns(rows=far) == B.QHA_ERR_UNSUPPORTED
+    assert _muon(rows=((4, 1 << 17, FAKE, FAKE, 0, FAKE, 1.0),)) == B.QHA_ERR_UNSUPPORTED
+    assert _ns(ws=None) == B.QHA_ERR_WORKSPACE and _muon(ws=None) == B.QHA_ERR_WORKSPACE
+    need = B.newton_schulz_workspace([(200, 300)])
+    assert need > 0 and _ns(wsb=need - 1) == B.QHA_ERR_WORKSPACE
+    # the same but for the sums of squares: 4 x 2 pieces of 64 x 256 against 5 x 1, eight bytes each and 16 in all
+    assert need - B.newton_schulz_workspace([(300, 200)]) == 8 * 8 - 6 * 8
+    assert B.newton_schulz_workspace([(128, 128), (1, 5), (0, 700), (700, 0)]) == 0      # on chip, or nothing to do
+    assert B.newton_schulz_workspace([(128, 129)]) > 0
+    assert B.newton_schulz_workspace([(200, 300), (1 << 17, 4)]) == 0
+    for steps in (0, 17):
+        assert B.newton_schulz_workspace([(200, 300)], steps) == 0
+    # a long list is worked off in batches that share the space
+    assert B.newton_schulz_workspace([(1024, 1024)] * 400) < 30 * B.newton_schulz_workspace([(1024, 1024)])
+    assert _ns(rows=()) == B.QHA_OK and _muon(rows=()) == B.QHA_OK
+    assert _ns(rows=((0, 5, 0, 0, 0, 0), (5, 0, 0, 0, 0, 0)), ws=None) == B.QHA_OK
+    assert _muon(rows=((0, 5, 0, 0, 0, 0, 1.0),), ws=None) == B.QHA_OK
+
+
+def test_coefficients_that_stay_in_range_are_taken():
+    for k, steps in ((B.NS_COEFFICIENTS, 16), ((1.5, -0.5, 0.0), 16), ((15 / 8, -10 / 8, 3 / 8), 9), ((0, 0, 0), 1), ((3.8, 0, 0), 1),
+                     ([(8.2872, -23.5959, 17.3004), (4.1071, -2.9478, 0.5448)], 2)):
+        assert B._newton_schulz(None, 0, B.F32, B.F32, steps, B._ns_coefficients(k, steps).ctypes.data, 0.0, None, 0, None) == B.QHA_OK
+    with pytest.raises(ValueError, match="coefficients"):
+        B._ns_coefficients([(1, 2, 3)] * 4, 5)
+    with pytest.raises(ValueError, match="coefficients"):
+        B._ns_coefficients((1, 2), 5)
+
+
+def test_newton_schulz_and_muon_binding_refuse(monkeypatch):
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    x = _gpu(4, 6)
+    with pytest.raises(ValueError, match="2 results for 1"):
+        B.newton_schulz([x], [x, x])
+    with pytest.raises(ValueError, match="matrix"):
+        B.newton_schulz([_gpu(4)], [x])
+    with pytest.raises(ValueError, match="4 x 6"):
+        B.newton_schulz([x], [_gpu(6, 4)])
+    with pytest.raises(TypeError, match="float32"):
+        B.newton_schulz([x, _gpu(4, 6, dtype=torch.bfloat16)], [x, x])
+    with pytest.raises(ValueError, match="GPU"):
+        B.newton_schulz([torch.zeros(4, 6)], [x])
+    with pytest.raises(ValueError, match="current device"):
+        B.newton_schulz([x], [_gpu(4, 6, cls=Other)], stream=0)
+    with pytest.raises(ValueError, match="passes 60|pass 3.8"):
+        B.newton_schulz([x], [x], coefficients=(40, 0, 0), stream=0)
+    with pytest.raises(ValueError, match="coefficients"):
+        B.newton_schulz([x], [x], coefficients=(1, 2))
+    with pytest.raises(TypeError, match="float32"):
+        B.Muon([_gpu(4, 6, dtype=torch.float16)])
+    with pytest.raises(ValueError, match="matrix"):
+        B.Muon([_gpu(24)])
+    with pytest.raises(ValueError, match="contiguous"):
+        B.Muon([_gpu(6, 4).T])
+    with pytest.raises(ValueError, match="scale"):
+        B.Muon([x], scale="spectrum")
+    with pytest.raises(ValueError, match="momenta"):
+        B.Muon([x], momenta=[])
+    with pytest.raises(ValueError, match=r"m\[0\] must be"):
+        B.Muon([x], momenta=[_gpu(6, 4)])
+    with pytest.raises(ValueError, match=r"copies\[0\] must be"):
+        B.Muon([x], copies=[_gpu(24)])
+    opt = B.Muon([x])
+    with pytest.raises(ValueError, match="2 gradients for 1"):
+        opt.step([x, x], 0.1)
+    with pytest.raises(ValueError, match=r"grads\[0\] must be"):
+        opt.step([_gpu(24)], 0.1)
+    with pytest.raises(TypeError, match="float32|float16"):
+        opt.step([_gpu(4, 6, dtype=torch.float64)], 0.1)
+    with pytest.raises(ValueError, match="current device"):
+        opt.step([_gpu(4, 6, cls=Other)], 0.1, stream=0)
+    B.Muon([]).step([], 0.1)
+
+
+def test_muon_table_follows_the_tensors(monkeypatch):
+    """The addresses that reach the library, after parameters and momenta were replaced, without a GPU."""
+    import numpy as np
+    seen = []
+
+    def fake(table, n, *rest):
+        import ctypes
+        seen.append(np.ctypeslib.as_array((ctypes.c_int64 * (7 * n)).from_address(table)).reshape(n, 7).copy())
+        return B.QHA_OK
+    monkeypatch.setattr(B, "_muon_step", fake)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    params = [_gpu(4, 6), _gpu(9, 3)]
+    copies = [_gpu(4, 6, dtype=torch.bfloat16), _gpu(9, 3, dtype=torch.bfloat16)]
+    grads = [_gpu(4, 6), _gpu(9, 3)]
+    opt = B.Muon(params, scale="spectral", copies=copies)
+
+    def expect():
+        opt.step(grads, 0.1, stream=0)
+        t = seen[-1]
+        assert t[:, :2].tolist() == [[4, 6], [9, 3]]
+        assert t[:, 2].tolist() == [p.data_ptr() for p in opt.params]
+        assert t[:, 3].tolist() == [g.data_ptr() for g in grads]
+        assert t[:, 4].tolist() == [c.data_ptr() for c in opt.copies]
+        assert t[:, 5].tolist() == [m.data_ptr() for m in opt.m]
+        assert t.view(np.float64)[:, 6].tolist() == [1.0, 3 ** 0.5]
+    expect()
+    opt.params[1] = _gpu(9, 3)
+    expect()
+    opt.m[0] = _gpu(4, 6)
+    expect()
+    grads[0] = _gpu(4, 6)
+    opt.copies[1] = _gpu(9, 3, dtype=torch.bfloat16)
+    expect()
+    opt.m.pop()
+    with pytest.raises(ValueError, match="momenta"):
+        opt.step(grads, 0.1, stream=0)
+    assert B.Muon(params, scale="rms")._table.view(np.float64)[0, 6] == 0.2 * 6 ** 0.5
+    assert B.Muon(params, scale=0.5)._table.view(np.float64)[0, 6] == 0.5
