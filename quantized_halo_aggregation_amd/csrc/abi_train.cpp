@@ -164,9 +164,9 @@ int check_steps(int32_t steps, const double* coefficients, double eps) {
     const double a = coefficients[3 * i], b = coefficients[3 * i + 1], c = coefficients[3 * i + 2];
     if (!std::isfinite(a) || !std::isfinite(b) || !std::isfinite(c)) return fail(QHA_ERR_INVALID_ARG, "a coefficient is not finite");
     const double t = top * top;
-    double inner = std::fabs(t * (b + c * t));                       // |b t + c t^2| over [0, top^2]
-    if (c != 0.0 && -b / (2.0 * c) > 0.0 && -b / (2.0 * c) < t) inner = std::max(inner, std::fabs(b * b / (4.0 * c)));
-    if (!(inner <= 60.0)) return fail(QHA_ERR_INVALID_ARG, "step %d: b s^2 + c s^4 passes 60", i);
+    double inner = std::max(std::fabs(a), std::fabs(a + t * (b + c * t)));       // |a + b t + c t^2| over [0, top^2]
+    if (c != 0.0 && -b / (2.0 * c) > 0.0 && -b / (2.0 * c) < t) inner = std::max(inner, std::fabs(a - b * b / (4.0 * c)));
+    if (!(inner <= 60.0)) return fail(QHA_ERR_INVALID_ARG, "step %d: a + b s^2 + c s^4 passes 60", i);
     top = largest_of(a, b, c, top);
     if (!(top <= 3.8)) return fail(QHA_ERR_INVALID_ARG, "step %d: singular values pass 3.8", i);
   }

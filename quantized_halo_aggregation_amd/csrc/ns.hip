@@ -1,7 +1,7 @@
 // Orthogonalised updates: Newton-Schulz products of many matrices, and the optimiser's step around them.
 //
 // Mathematics, for a matrix of m x n values with m <= n (a tall one is taken as its transpose):
-//   X = U / (|U| + eps),  then `steps` times  A = X X^T,  B = b A + c A^2,  X = a X + B X
+//   X = U / (|U| + eps),  then `steps` times  A = X X^T,  B = a I + b A + c A^2,  X = B X
 // which moves every singular value s of X to a s + b s^3 + c s^5 and keeps the singular vectors.  U is the input, or the step's
 // momentum: M = mu M + g, U = g + mu M (Nesterov) or M.  The step ends with p = decay p - step X.
 //
@@ -18,6 +18,8 @@
 #include "../../include/qha.h"
 #include "qha_internal.hpp"
 #include "tile_common.hpp"
+
+#include <cstring>
 
 namespace qha {
 namespace {
@@ -84,29 +86,57 @@ __device__ __forceinline__ void apply4(const NsTable& t, const NsMat& a, int64_t
 }
 
 // The matrix that a block works on, by the first blocks of each.
-__device__ __forceinline__ int matrix_of(const NsTable& t, const uint32_t* first, uint32_t block) {
+__device__ __forceinline__ int matrix_of(const NsFirst& first, uint32_t block) {
   int i = 0;
-  while (i + 1 < t.n && first[i + 1] <= block) ++i;
+#pragma unroll
+  for (int k = 1; k < kNsBatch; ++k) i += k < first.n && first.block[k] <= block;
   return i;
 }
 
-// Pairs of parts: value (r, c) of a matrix whose rows hold `cols` values.
-__device__ __forceinline__ int64_t pair_at(int64_t r, int64_t c, int64_t cols) {
-  return r * 2 * cols + (c >> 3) * 16 + (c & 7);
-}
 __device__ __forceinline__ void split2(f32x4 x, f16x4& hi, f16x4& lo) {
   hi = __builtin_convertvector(x, f16x4);
   lo = __builtin_convertvector(x - __builtin_convertvector(hi, f32x4), f16x4);
 }
-__device__ __forceinline__ void put_pair(uint16_t* p, int64_t at, f32x4 v) {
+
+// X, A and B in memory, in the order in which the matrix cores take them: blocks of 32 rows x 16 values along the reduction, 512 hi
+// values, then their 512 lo values, those of lane l (row l % 32, values 8 (l / 32) .. + 7) together.  So a wavefront's operand is
+// 1 KB without gaps, from memory or from LDS.  The rows of the four eights of 32 columns are turned by 0, 4, 8 and 12 places against
+// each other: the transposing read, which takes four rows of all four at a time, then meets different banks.
+// The place of value (r, c), hi, in rows of `cols` values:
+constexpr int kBlock = 1024, kLo = 512;
+__device__ __forceinline__ int64_t block_at(int64_t r, int64_t c, int64_t cols) {
+  return ((r >> 5) * (cols >> 4) + (c >> 4)) * kBlock + ((c >> 3) & 1) * 256 + ((r + ((c >> 3) & 3) * 4) & 31) * 8 + (c & 7);
+}
+// A lane's place in an operand along the reduction: in blocks of even (h = 0) and odd (1) number of a row.
+__device__ __forceinline__ int lane_at(int lane, int h) { return (lane >> 5) * 256 + ((lane + (lane >> 5) * 4 + h * 8) & 31) * 8; }
+// A matrix's part of the workspace: A, B, X and the next one, (their transposes,) and the pieces' sums of squares.
+struct NsParts {
+  char* ws;
+  int64_t mn, mm;                    // bytes of X and of A
+  __device__ __forceinline__ explicit NsParts(const NsMat& a)
+      : ws(a.ws), mn(4LL * a.m_pad * a.n_pad), mm(4LL * a.m_pad * a.m_pad) {}
+  __device__ __forceinline__ uint16_t* x(int which) const { return reinterpret_cast<uint16_t*>(ws + 2 * mm + which * mn); }
+  __device__ __forceinline__ uint16_t* xt(int which) const { return reinterpret_cast<uint16_t*>(ws + 2 * mm + (2 + which) * mn); }
+  __device__ __forceinline__ uint16_t* a() const { return reinterpret_cast<uint16_t*>(ws); }
+  __device__ __forceinline__ uint16_t* b() const { return reinterpret_cast<uint16_t*>(ws + mm); }
+  __device__ __forceinline__ double* squares(bool transposes) const { return reinterpret_cast<double*>(ws + 2 * mm + (transposes ? 4 : 2) * mn); }
+};
+__device__ __forceinline__ void put4(uint16_t* p, int64_t at, f32x4 v) {
   f16x4 hi, lo;
   split2(v, hi, lo);
   *reinterpret_cast<f16x4*>(p + at) = hi;
-  *reinterpret_cast<f16x4*>(p + at + 8) = lo;
+  *reinterpret_cast<f16x4*>(p + at + kLo) = lo;
 }
-__device__ __forceinline__ f32x4 get_pair(const uint16_t* p, int64_t at) {
+__device__ __forceinline__ void put8(uint16_t* p, int64_t at, f32x4 u, f32x4 v) {
+  f16x4 hi[2], lo[2];
+  split2(u, hi[0], lo[0]);
+  split2(v, hi[1], lo[1]);
+  *reinterpret_cast<f16x8*>(p + at) = __builtin_shufflevector(hi[0], hi[1], 0, 1, 2, 3, 4, 5, 6, 7);
+  *reinterpret_cast<f16x8*>(p + at + kLo) = __builtin_shufflevector(lo[0], lo[1], 0, 1, 2, 3, 4, 5, 6, 7);
+}
+__device__ __forceinline__ f32x4 get4(const uint16_t* p, int64_t at) {
   return __builtin_convertvector(*reinterpret_cast<const f16x4*>(p + at), f32x4) +
-         __builtin_convertvector(*reinterpret_cast<const f16x4*>(p + at + 8), f32x4);
+         __builtin_convertvector(*reinterpret_cast<const f16x4*>(p + at + kLo), f32x4);
 }
 
 __device__ __forceinline__ double block_sum(double s, double* buf) {
@@ -130,95 +160,124 @@ __device__ __forceinline__ double scale_of(double squares, double eps) {
 // from the inputs to X, and from X to the results
 // ---------------------------------------------------------------------------------------------
 
-constexpr int kPieceRows = 64, kPieceCols = 256;
+constexpr int kPieceCols = 256;
 
-// Sum of squares of U by pieces of 64 x 256 values, in float64; the optimiser's momentum is updated here.
-__global__ __launch_bounds__(256) void ns_measure_kernel(NsTable t) {
+// Sum of squares of U by pieces of piece_rows x 256 values, in float64; the optimiser's momentum is updated here.  The first
+// block leaves the table, which came with the arguments, in the workspace for the launches behind it.
+__global__ __launch_bounds__(256) void ns_measure_kernel(NsTable t, NsFirst first, uint32_t* table) {
   __shared__ double buf[4];
-  const int i = matrix_of(t, t.first_piece, blockIdx.x);
+  if (blockIdx.x == 0) {
+    const uint32_t* words = reinterpret_cast<const uint32_t*>(&t);
+    for (int i = threadIdx.x; i < static_cast<int>(sizeof(NsTable) / 4); i += 256) table[i] = words[i];
+  }
+  const int i = matrix_of(first, blockIdx.x);
   const NsMat& a = t.m[i];
-  const int piece = static_cast<int>(blockIdx.x - t.first_piece[i]);
+  const int piece = static_cast<int>(blockIdx.x - first.block[i]);
   const int col_pieces = (a.cols + kPieceCols - 1) / kPieceCols;
   const int c = piece % col_pieces * kPieceCols + (static_cast<int>(threadIdx.x) & 63) * 4;
-  const int r0 = piece / col_pieces * kPieceRows, r1 = r0 + kPieceRows < a.rows ? r0 + kPieceRows : a.rows;
+  const int r0 = piece / col_pieces * t.piece_rows, r1 = r0 + t.piece_rows < a.rows ? r0 + t.piece_rows : a.rows;
   double s = 0.0;
-#pragma unroll 4
-  for (int r = r0 + static_cast<int>(threadIdx.x >> 6); r < r1; r += 4) {
-    const f32x4 g = read4(a.src, a.lds, r, c, a.cols, t.type, a.vec_src);
-    f32x4 m = {0.0f, 0.0f, 0.0f, 0.0f};
-    if (t.muon) {
-      m = read4(a.mom, a.ldo, r, c, a.cols, QHA_F32, a.vec_mom) * t.mu + g * t.grad_scale;
-      write4(a.mom, a.ldo, r, c, a.cols, QHA_F32, a.vec_mom, m);
-    }
-    const f32x4 u = update_of(t, g, m);
+  for (int r = r0 + static_cast<int>(threadIdx.x >> 6); r < r1; r += 8) {      // two rows' loads at once
+    f32x4 g[2], m[2];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) s += static_cast<double>(u[e]) * static_cast<double>(u[e]);
+    for (int h = 0; h < 2; ++h) {
+      g[h] = m[h] = 0.0f;
+      if (r + 4 * h >= r1) continue;
+      g[h] = read4(a.src, a.lds, r + 4 * h, c, a.cols, t.type, a.vec_src);
+      if (t.muon) m[h] = read4(a.mom, a.ldo, r + 4 * h, c, a.cols, QHA_F32, a.vec_mom);
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      if (r + 4 * h >= r1) continue;
+      if (t.muon) {
+        m[h] = m[h] * t.mu + g[h] * t.grad_scale;
+        write4(a.mom, a.ldo, r + 4 * h, c, a.cols, QHA_F32, a.vec_mom, m[h]);
+      }
+      const f32x4 u = update_of(t, g[h], m[h]);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) s += static_cast<double>(u[e]) * static_cast<double>(u[e]);
+    }
   }
   s = block_sum(s, buf);
-  if (threadIdx.x == 0) a.parts[piece] = s;
+  if (threadIdx.x == 0) NsParts(a).squares(t.transposes)[piece] = s;
 }
 
-// X as pairs, by tiles of 64 x 64 of it, zero past the matrix's end.
-__global__ __launch_bounds__(256) void ns_split_kernel(NsTable t) {
+// X, and its transpose where the products read that, by tiles of 64 x 64, zero past the matrix's end.
+__global__ __launch_bounds__(256) void ns_split_kernel(const NsTable* table, NsFirst first) {
+  const NsTable& t = *table;
   __shared__ double buf[4];
   __shared__ float tile[64][68];
-  const int i = matrix_of(t, t.first_tile, blockIdx.x);
+  const int i = matrix_of(first, blockIdx.x);
   const NsMat& a = t.m[i];
-  const int at = static_cast<int>(blockIdx.x - t.first_tile[i]), wide = a.n_pad / 64;
+  const int at = static_cast<int>(blockIdx.x - first.block[i]), wide = (a.n_pad + 63) / 64;
   const int x0 = at / wide * 64, y0 = at % wide * 64;            // of X
   const int r0 = a.tall ? y0 : x0, c0 = a.tall ? x0 : y0;        // of the matrix
-  const int pieces = ((a.rows + kPieceRows - 1) / kPieceRows) * ((a.cols + kPieceCols - 1) / kPieceCols);
-  double s = 0.0;
-  for (int k = threadIdx.x; k < pieces; k += 256) s += a.parts[k];
-  const double by = scale_of(block_sum(s, buf), t.eps);
-  const int cl = (static_cast<int>(threadIdx.x) & 15) * 4;
+  const int cl = (static_cast<int>(threadIdx.x) & 15) * 4, rl = static_cast<int>(threadIdx.x >> 4);
+  f32x4 u[4];
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
-    const int rl = static_cast<int>(threadIdx.x >> 4) + 16 * k;
-    f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
-    if (r0 + rl < a.rows) {
-      const f32x4 g = read4(a.src, a.lds, r0 + rl, c0 + cl, a.cols, t.type, a.vec_src);
-      const f32x4 m = t.muon ? read4(a.mom, a.ldo, r0 + rl, c0 + cl, a.cols, QHA_F32, a.vec_mom) : g;
-      const f32x4 u = update_of(t, g, m);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) v[e] = c0 + cl + e < a.cols ? static_cast<float>(static_cast<double>(u[e]) * by) : 0.0f;
+    u[k] = 0.0f;
+    if (r0 + rl + 16 * k < a.rows) {
+      const f32x4 g = read4(a.src, a.lds, r0 + rl + 16 * k, c0 + cl, a.cols, t.type, a.vec_src);
+      const f32x4 m = t.muon ? read4(a.mom, a.ldo, r0 + rl + 16 * k, c0 + cl, a.cols, QHA_F32, a.vec_mom) : g;
+      u[k] = update_of(t, g, m);
     }
+  }
+  const int pieces = ((a.rows + t.piece_rows - 1) / t.piece_rows) * ((a.cols + kPieceCols - 1) / kPieceCols);
+  double s = 0.0;
+  const NsParts w(a);
+  for (int k = threadIdx.x; k < pieces; k += 256) s += w.squares(t.transposes)[k];
+  const double by = scale_of(block_sum(s, buf), t.eps);
+  // the tile as the matrix has it; a thread then takes four neighbours of X's rows, or of its transpose's
 #pragma unroll
-    for (int e = 0; e < 4; ++e)
-      if (a.tall) tile[cl + e][rl] = v[e];
-      else tile[rl][cl + e] = v[e];
+  for (int k = 0; k < 4; ++k) {
+    f32x4 v;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const bool in = r0 + rl + 16 * k < a.rows && c0 + cl + e < a.cols;
+      v[e] = in ? static_cast<float>(static_cast<double>(u[k][e]) * by) : 0.0f;
+    }
+    *reinterpret_cast<f32x4*>(&tile[rl + 16 * k][cl]) = v;
   }
   __syncthreads();
+  uint16_t* xt = t.transposes ? w.xt(0) : nullptr;
+  uint16_t* along = a.tall ? xt : w.x(0);                        // stored as the matrix is
+  uint16_t* across = a.tall ? w.x(0) : xt;
+  const int along_cols = a.tall ? a.m_pad : a.n_pad, across_cols = a.tall ? a.n_pad : a.m_pad;
+  const int q = static_cast<int>(threadIdx.x) & 63;
 #pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const int rl = static_cast<int>(threadIdx.x >> 4) + 16 * k;
-    put_pair(a.x[0], pair_at(x0 + rl, y0 + cl, a.n_pad), *reinterpret_cast<const f32x4*>(&tile[rl][cl]));
+  for (int k = 0; k < 2; ++k) {
+    const int c = (static_cast<int>(threadIdx.x >> 6) + 4 * k) * 8;
+    if (along && r0 + q < across_cols && c0 + c < along_cols)
+      put8(along, block_at(r0 + q, c0 + c, along_cols), *reinterpret_cast<const f32x4*>(&tile[q][c]), *reinterpret_cast<const f32x4*>(&tile[q][c + 4]));
+    if (across && c0 + q < along_cols && r0 + c < across_cols) {
+      f32x4 v[2];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e >> 2][e & 3] = tile[c + e][q];
+      put8(across, block_at(c0 + q, r0 + c, across_cols), v[0], v[1]);
+    }
   }
 }
 
-// The results from the last X, by the same tiles.
-__global__ __launch_bounds__(256) void ns_finish_kernel(NsTable t, int32_t which) {
-  __shared__ float tile[64][68];
-  const int i = matrix_of(t, t.first_tile, blockIdx.x);
-  const NsMat& a = t.m[i];
-  const int at = static_cast<int>(blockIdx.x - t.first_tile[i]), wide = a.n_pad / 64;
-  const int x0 = at / wide * 64, y0 = at % wide * 64;
-  const int r0 = a.tall ? y0 : x0, c0 = a.tall ? x0 : y0;
-  const int cl = (static_cast<int>(threadIdx.x) & 15) * 4;
+constexpr int kPartRow = 36;         // floats of a row of 32 in LDS, padded to spread columns over the banks
+
+// The results from a block of 32 x 32 of the last X (times kScaleX) in LDS, rows x0 .., columns y0 ..: thread `id` of N takes four
+// neighbours of the matrix's rows, so that eight threads write whole lines.  (Straight from the accumulators, 16 bytes of 32 rows
+// at a time, the last product of 4096 x 4096 took 1638 us, the others 372.)
+template <int N>
+__device__ __forceinline__ void finish_block(const NsTable& t, const NsMat& a, const float* v, int64_t x0, int64_t y0, int id) {
+#pragma unroll 1
+  for (int k = 0; k < 256 / N; ++k) {
+    const int r = (id + k * N) >> 3, c = ((id + k * N) & 7) * 4;
+    f32x4 o;
+    if (a.tall) {
 #pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const int rl = static_cast<int>(threadIdx.x >> 4) + 16 * k;
-    const f32x4 v = get_pair(a.x[which], pair_at(x0 + rl, y0 + cl, a.n_pad)) * (1.0f / kScaleX);
-#pragma unroll
-    for (int e = 0; e < 4; ++e)
-      if (a.tall) tile[cl + e][rl] = v[e];
-      else tile[rl][cl + e] = v[e];
-  }
-  __syncthreads();
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const int rl = static_cast<int>(threadIdx.x >> 4) + 16 * k;
-    if (r0 + rl < a.rows) apply4(t, a, r0 + rl, c0 + cl, *reinterpret_cast<const f32x4*>(&tile[rl][cl]));
+      for (int e = 0; e < 4; ++e) o[e] = v[(c + e) * kPartRow + r];
+    } else {
+      o = *reinterpret_cast<const f32x4*>(v + r * kPartRow + c);
+    }
+    const int64_t row = (a.tall ? y0 : x0) + r;
+    if (row < a.rows) apply4(t, a, row, static_cast<int>((a.tall ? x0 : y0) + c), o * (1.0f / kScaleX));
   }
 }
 
@@ -226,37 +285,27 @@ __global__ __launch_bounds__(256) void ns_finish_kernel(NsTable t, int32_t which
 // the products
 // ---------------------------------------------------------------------------------------------
 
-enum { NS_GRAM = 0, NS_SQUARE = 1, NS_APPLY = 2 };
+enum { NS_GRAM = 0, NS_SQUARE = 1, NS_APPLY = 2, NS_LAST = 3 };      // NS_LAST: apply, with results in X's place
 constexpr int BK = 32;               // steps of the reduction in LDS at once
 
-// Places of 16-byte chunks in a tile's LDS image.  LDS serves 256 bytes at a time, so reads that go together must fall on
-// different sixteenths of 256 bytes.  Along the reduction (rows of 128 bytes), 16 lanes read one chunk of as many rows.
-// Across it (rows of 256 bytes or a multiple), a transposing read takes every second chunk of four (hi or lo) of four rows.
-__device__ __forceinline__ int place_along(int row, int chunk) { return chunk ^ ((row >> 1) & 7); }
-__device__ __forceinline__ int place_cross(int k, int chunk) { return chunk ^ (k & 1) ^ ((k & 2) << 2); }
-
-// A thread's share of an operand's tile: EXTENT rows x 32 steps (along) or 32 steps x EXTENT columns (across), as pairs.
-template <bool CROSS, int EXTENT, int NT>
-struct PairStager {
-  static constexpr int PER = CROSS ? EXTENT / 4 : 2 * BK / 8;     // chunks of a row in LDS
+// A thread's share of the loads of an operand's tile of a step: EXTENT rows, two blocks of each 32 rows (4 KB without gaps), or, ACROSS
+// the reduction, 32 rows and EXTENT columns (without gaps in all).
+template <bool ACROSS, int EXTENT, int NT>
+struct Stager {
   static constexpr int N = EXTENT * 8 / NT;
-  static_assert(EXTENT * 8 % NT == 0, "whole chunks per thread");
+  static constexpr int PER = ACROSS ? 128 : 256, RUNS = NT / PER;      // 16-byte pieces of a run, and runs that the threads take at once
+  static_assert(EXTENT * 8 % NT == 0 && NT % PER == 0, "whole runs");
   const uint16_t* at[N];
   int64_t next_by;
-  // rows x cols values are stored (multiples of 64); the tile begins at row or column `first`.  Those past the
-  // end repeat the last ones; their results are not stored.
-  __device__ __forceinline__ PairStager(const uint16_t* base, int64_t rows, int64_t cols, int64_t first) {
-    next_by = CROSS ? BK * 2 * cols : BK * 2;
+  // The matrix has `rows` runs of 32 rows of `blocks` blocks; the tile begins at run (across: at block) `first`.  Those past the end
+  // repeat the last one, whose results are not stored.
+  __device__ __forceinline__ Stager(const uint16_t* base, int64_t rows, int64_t blocks, int64_t first) {
+    next_by = ACROSS ? blocks * kBlock : 2 * kBlock;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      const int q = i * NT + static_cast<int>(threadIdx.x), r = q / PER, place = q % PER;
-      if constexpr (CROSS) {
-        const int64_t chunk = first / 4 + place_cross(r, place), last = cols / 4 - 1;
-        at[i] = base + r * 2 * cols + (chunk < last ? chunk : last) * 8;
-      } else {
-        const int64_t row = first + r < rows ? first + r : rows - 1;
-        at[i] = base + row * 2 * cols + place_along(r, place) * 8;
-      }
+      const int64_t r = first + i * RUNS + static_cast<int>(threadIdx.x) / PER;
+      const int64_t run = ACROSS ? (r < blocks ? r : blocks - 1) : (r < rows ? r : rows - 1) * blocks;
+      at[i] = base + run * kBlock + (static_cast<int>(threadIdx.x) & (PER - 1)) * 8;
     }
   }
   __device__ __forceinline__ void load(const uint16_t* lds) {
@@ -269,52 +318,49 @@ struct PairStager {
   }
 };
 
-// A matrix operand: one part (0 hi, 1 lo) of 32 rows or columns from `from` on, 16 steps from ks on; lane l holds row
-// l % 32, steps 8 (l / 32) .. + 7.
-template <bool CROSS, int EXTENT>
-__device__ __forceinline__ s16x8 pair_fragment(const uint16_t* lds, int from, int ks, int part, int lane) {
-  if constexpr (CROSS) {
-    // the transposing read takes 4 steps x 16 columns per 16 lanes: lane j of them addresses step j / 4, columns
-    // 4 (j % 4), and receives four steps of column j
-    const int j = lane & 15;
-    const int col = from + ((lane >> 4) & 1) * 16 + 4 * (j & 3);
-    const int k = ks + (lane >> 5) * 8 + (j >> 2);              // k and k + 4 share their places
-    const uint16_t* lo = lds + k * 2 * EXTENT + place_cross(k, (col >> 3) * 2 + part) * 8 + (col & 7);
-    const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)lo);
-    const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)(lo + 8 * EXTENT));
-    return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
-  } else {
-    const int row = from + (lane & 31);
-    const int c = place_along(row, ((ks >> 3) + (lane >> 5)) * 2 + part);
-    return *reinterpret_cast<const s16x8*>(lds + row * 2 * BK + c * 8);
-  }
+// Four neighbours of a row of B = a I + b A + c A^2 from c A^2's and A's.  The unit matrix's a goes through the last product with the
+// rest: that product then reads X once and adds nothing to its results.
+__device__ __forceinline__ f32x4 square_terms(const NsCoef& k, f32x4 v, f32x4 of_a, int64_t row, int64_t col) {
+  v += of_a * k.own;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) v[e] += col + e == row ? k.unit : 0.0f;
+  return v;
 }
 
-// C = P Q^T (gram, square) or P Q (apply), with C's other terms: one tile of one matrix.  A wavefront owns MI x NI
-// blocks of 32 x 32.  The matrix instruction's operands are swapped (C^T is formed), which leaves a lane four neighbouring
-// columns of a row.
-template <int KIND, int MI, int NI, int WM, int WN>
-__global__ __launch_bounds__(WM * WN * 64) void ns_product_kernel(NsTable t, NsCoef k, int32_t from, uint32_t total) {
+// Tile of the lower triangle: row m of it begins at m (m + 1) / 2.
+__device__ __forceinline__ void triangle(int tile, int* mt, int* nt) {
+  int m = static_cast<int>((sqrtf(8.0f * static_cast<float>(tile) + 1.0f) - 1.0f) * 0.5f);
+  while (m * (m + 1) / 2 > tile) --m;
+  while ((m + 1) * (m + 2) / 2 <= tile) ++m;
+  *mt = m;
+  *nt = tile - m * (m + 1) / 2;
+}
+
+// A = X X^T (gram), B = a I + b A + c A A^T (square) or the next X = B X (apply): one tile of one matrix.  A wavefront owns MI x NI
+// blocks of 32 x 32; X's columns in the last product come through the transposing read.  The matrix instruction's operands are swapped (C^T is formed), which leaves a lane four
+// neighbouring columns of a row.
+template <int KIND, int MI, int NI, int WM, int WN, int STAGES>
+__global__ __launch_bounds__(WM * WN * 64) void ns_product_kernel(const NsTable* table, NsFirst first, NsCoef k, int32_t from, uint32_t total) {
   constexpr int BM = MI * 32 * WM, BN = NI * 32 * WN, NT = WM * WN * 64;
-  constexpr bool SYM = KIND != NS_APPLY, CROSS = KIND == NS_APPLY;
-  static_assert(!SYM || BM == BN, "square tiles of symmetric results");
+  constexpr bool SYM = KIND == NS_GRAM || KIND == NS_SQUARE;
+  static_assert(BM == BN, "square tiles, for symmetric results");
   constexpr int A_SIZE = BM * BK * 2, BUF = A_SIZE + BN * BK * 2;
-  __shared__ __attribute__((aligned(16))) uint16_t lds[2 * BUF];
+  static_assert(WM * WN * 32 * kPartRow * 4 <= STAGES * BUF * 2, "room for the transposes");
+  __shared__ __attribute__((aligned(16))) uint16_t lds[STAGES * BUF];
   // consecutive blocks go to the eight dies in turn: each takes a run of neighbouring tiles, which share operands
   const uint32_t band = (total + kXcds - 1) / kXcds;
   const uint32_t block = blockIdx.x % kXcds * band + blockIdx.x / kXcds;
   if (block >= total) return;
-  const int i = matrix_of(t, t.first_tile, block);
+  const NsTable& t = *table;
+  const int i = matrix_of(first, block);
   const NsMat& a = t.m[i];
-  const int tile = static_cast<int>(block - t.first_tile[i]);
+  const int tile = static_cast<int>(block - first.block[i]);
+  const int64_t m_pad = a.m_pad, n_pad = a.n_pad;
   int mt, nt;
-  if constexpr (SYM) {                         // row mt of the lower triangle begins at mt (mt + 1) / 2
-    mt = static_cast<int>((sqrtf(8.0f * static_cast<float>(tile) + 1.0f) - 1.0f) * 0.5f);
-    while (mt * (mt + 1) / 2 > tile) --mt;
-    while ((mt + 1) * (mt + 2) / 2 <= tile) ++mt;
-    nt = tile - mt * (mt + 1) / 2;
+  if constexpr (SYM) {
+    triangle(tile, &mt, &nt);
   } else {                                     // down groups of eight row tiles before the next column tile
-    const int m_tiles = (a.m_pad + BM - 1) / BM, n_tiles = (a.n_pad + BN - 1) / BN;
+    const int m_tiles = static_cast<int>((m_pad + BM - 1) / BM), n_tiles = static_cast<int>((n_pad + BN - 1) / BN);
     const int g = tile / (8 * n_tiles), in = tile % (8 * n_tiles);
     const int rows = m_tiles - 8 * g < 8 ? m_tiles - 8 * g : 8;
     mt = 8 * g + in % rows;
@@ -323,242 +369,658 @@ __global__ __launch_bounds__(WM * WN * 64) void ns_product_kernel(NsTable t, NsC
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave / WN, wn = wave % WN;
-  const uint16_t* x = a.x[from];
-  const uint16_t* P = KIND == NS_GRAM ? x : KIND == NS_SQUARE ? a.a : a.b;
-  const uint16_t* Q = KIND == NS_SQUARE ? a.a : x;
-  const int64_t depth = KIND == NS_GRAM ? a.n_pad : a.m_pad;
+  const NsParts w(a);
+  const uint16_t* x = w.x(from);
+  const uint16_t* P = KIND == NS_GRAM ? x : KIND == NS_SQUARE ? w.a() : w.b();
+  const uint16_t* Q = KIND == NS_SQUARE ? w.a() : x;
+  const int64_t depth = KIND == NS_GRAM ? n_pad : m_pad, cols = SYM ? m_pad : n_pad;
 
   f32x16 acc[MI][NI];
 #pragma unroll
   for (int ii = 0; ii < MI; ++ii)
 #pragma unroll
     for (int j = 0; j < NI; ++j) acc[ii][j] = 0.0f;
-  PairStager<false, BM, NT> sp(P, a.m_pad, depth, static_cast<int64_t>(mt) * BM);
-  PairStager<CROSS, BN, NT> sq(Q, a.m_pad, KIND == NS_SQUARE ? a.m_pad : a.n_pad, static_cast<int64_t>(nt) * BN);
+  Stager<false, BM, NT> sp(P, m_pad / 32, depth / 16, static_cast<int64_t>(mt) * (BM / 32));
+  Stager<!SYM, BN, NT> sq(Q, m_pad / 32, (SYM ? depth : n_pad) / 16, static_cast<int64_t>(nt) * (SYM ? BN / 32 : BN / 16));
   const int steps = static_cast<int>(depth / BK);
-  sp.load(lds);
-  sq.load(lds + A_SIZE);
-  for (int s = 0; s < steps; ++s) {
-    const uint16_t* at = lds + (s & 1) * BUF;
-    loads_done();
-    __syncthreads();                 // step s is there, and everyone has read step s - 1
-    if (s + 1 < steps) {
-      uint16_t* to = lds + ((s + 1) & 1) * BUF;
-      sp.load(to);
-      sq.load(to + A_SIZE);
-    }
+  constexpr int EACH = decltype(sp)::N + decltype(sq)::N;      // loads of a thread for a step
+  // A step's operands come out of LDS in two halves of 16.  The first half of step s + 1 is read while the second half of step s is
+  // multiplied: the wait for its loads and the barrier lie in the middle of step s, where they find the matrix cores busy.
+  const int along[2] = {lane_at(lane, 0), lane_at(lane, 1)};
+  // across: 16 lanes take 4 rows x 16 columns, lane j of them addresses row j / 4, columns 4 (j % 4), and receives four rows of
+  // column j; rows 8 (l / 32) .. + 3 and the four behind them, columns 16 (l / 16 % 2) ..
+  int across[2];
 #pragma unroll
-    for (int ks = 0; ks < BK; ks += 16) {
-      s16x8 fp[MI][2], fq[NI][2];
+  for (int g = 0; g < 2; ++g) {
+    const int j = lane & 15, r = (lane >> 5) * 8 + (j >> 2) + 4 * g, c = ((lane >> 4) & 1) * 16 + 4 * (j & 3);
+    across[g] = static_cast<int>(block_at(r, c, 32));
+  }
+  const auto fetch = [&](int buffer, int h, s16x8 (&fp)[MI][2], s16x8 (&fq)[NI][2]) {
+    const uint16_t* at = lds + buffer * BUF;
+#pragma unroll
+    for (int ii = 0; ii < MI; ++ii)
+#pragma unroll
+      for (int part = 0; part < 2; ++part)
+        fp[ii][part] = *reinterpret_cast<const s16x8*>(at + along[h] + ((wm * MI + ii) * 2 + h) * kBlock + part * kLo);
+#pragma unroll
+    for (int j = 0; j < NI; ++j)
+#pragma unroll
+      for (int part = 0; part < 2; ++part) {
+        const uint16_t* from_q = at + A_SIZE + (wn * NI + j) * 2 * kBlock + part * kLo;
+        if constexpr (SYM) {
+          fq[j][part] = *reinterpret_cast<const s16x8*>(from_q + along[h] + h * kBlock);
+        } else {                       // 16 rows on, a row's place changes by its fifth bit
+          const s16x4 u = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)(from_q + (across[0] ^ h * 128)));
+          const s16x4 v = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)(from_q + (across[1] ^ h * 128)));
+          fq[j][part] = __builtin_shufflevector(u, v, 0, 1, 2, 3, 4, 5, 6, 7);
+        }
+      }
+  };
+  const auto multiply = [&](const s16x8 (&fp)[MI][2], const s16x8 (&fq)[NI][2]) {
+#pragma unroll
+    for (int term = 0; term < 3; ++term)            // lo hi, hi lo, hi hi
 #pragma unroll
       for (int ii = 0; ii < MI; ++ii)
 #pragma unroll
-        for (int part = 0; part < 2; ++part) fp[ii][part] = pair_fragment<false, BM>(at, (wm * MI + ii) * 32, ks, part, lane);
-#pragma unroll
-      for (int j = 0; j < NI; ++j)
-#pragma unroll
-        for (int part = 0; part < 2; ++part) fq[j][part] = pair_fragment<CROSS, BN>(at + A_SIZE, (wn * NI + j) * 32, ks, part, lane);
-#pragma unroll
-      for (int term = 0; term < 3; ++term)            // lo hi, hi lo, hi hi
-#pragma unroll
-        for (int ii = 0; ii < MI; ++ii)
-#pragma unroll
-          for (int j = 0; j < NI; ++j)
-            acc[ii][j] = mma<_Float16>(fq[j][term == 0], fp[ii][term == 1], acc[ii][j]);
+        for (int j = 0; j < NI; ++j)
+          acc[ii][j] = mma<_Float16>(fq[j][term == 0], fp[ii][term == 1], acc[ii][j]);
+  };
+  const auto load = [&](int buffer) {
+    sp.load(lds + buffer * BUF);
+    sq.load(lds + buffer * BUF + A_SIZE);
+  };
+  for (int s = 0; s < STAGES && s < steps; ++s) load(s);
+  if (steps >= STAGES) loads_left<(STAGES - 1) * EACH>();
+  else loads_left<0>();
+  __syncthreads();
+  s16x8 p0[MI][2], q0[NI][2], p1[MI][2], q1[NI][2];
+  fetch(0, 0, p0, q0);
+  for (int s = 0, now = 0; s < steps; ++s) {
+    fetch(now, 1, p1, q1);
+    multiply(p0, q0);
+    const int next = now + 1 == STAGES ? 0 : now + 1;
+    if (s + 1 < steps) {
+      // loads return in order: step s + 1 is there when only those of the steps behind it are on their way
+      if (s + STAGES - 1 < steps) loads_left<(STAGES - 2) * EACH>();
+      else loads_left<0>();
+      __syncthreads();               // for every wavefront, and everyone has read step s
+      if (s + STAGES < steps) load(now);
+      fetch(next, 0, p0, q0);
     }
+    multiply(p1, q1);
+    now = next;
   }
 
-  // Element r of lane l: row l % 32, column 8 (r / 4) + 4 (l / 32) + r % 4 of its block.
-  uint16_t* out = KIND == NS_GRAM ? a.a : KIND == NS_SQUARE ? a.b : a.x[from ^ 1];
-  const int64_t cols = SYM ? a.m_pad : a.n_pad;
+  // Element r of lane l: row l % 32, column 8 (r / 4) + 4 (l / 32) + r % 4 of its block.  The mirror of a symmetric result and rows of
+  // the call's results pass through a piece of LDS of the wavefront's own.
+  const bool turned = SYM ? mt != nt : KIND == NS_LAST;
+  uint16_t* out = KIND == NS_GRAM ? w.a() : KIND == NS_SQUARE ? w.b() : w.x(from ^ 1);
+  float* turn = reinterpret_cast<float*>(lds) + wave * 32 * kPartRow;
+  if (turned) __syncthreads();         // everyone has read the last step
 #pragma unroll
   for (int ii = 0; ii < MI; ++ii) {
-    const int64_t row = static_cast<int64_t>(mt) * BM + (wm * MI + ii) * 32 + (lane & 31);
+    const int64_t row0 = static_cast<int64_t>(mt) * BM + (wm * MI + ii) * 32;
 #pragma unroll
     for (int j = 0; j < NI; ++j) {
       const int64_t col0 = static_cast<int64_t>(nt) * BN + (wn * NI + j) * 32;
-      if (row - (lane & 31) >= a.m_pad || col0 >= cols) continue;
+      if (row0 >= m_pad || col0 >= cols) continue;
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
-        const int64_t col = col0 + 8 * q + 4 * (lane >> 5);
-        f32x4 v;
+        const int64_t row = row0 + (lane & 31), col = col0 + 8 * q + 4 * (lane >> 5);
+        f32x4 v = {acc[ii][j][4 * q], acc[ii][j][4 * q + 1], acc[ii][j][4 * q + 2], acc[ii][j][4 * q + 3]};
+        v *= k.product;
+        if constexpr (KIND == NS_SQUARE) v = square_terms(k, v, get4(w.a(), block_at(row, col, cols)), row, col);
+        if constexpr (KIND != NS_LAST) put4(out, block_at(row, col, cols), v);
+        if (turned) *reinterpret_cast<f32x4*>(turn + (lane & 31) * kPartRow + 8 * q + 4 * (lane >> 5)) = v;
+      }
+      if (!turned) continue;
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      __builtin_amdgcn_wave_barrier();
+      if constexpr (KIND == NS_LAST) {
+        finish_block<64>(t, a, turn, row0, col0, lane);
+      } else {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) v[e] = acc[ii][j][4 * q + e] * k.product;
-        if constexpr (KIND == NS_SQUARE) v += get_pair(a.a, pair_at(row, col, cols)) * k.own;
-        if constexpr (KIND == NS_APPLY) v += get_pair(x, pair_at(row, col, cols)) * k.own;
-        f16x4 hi, lo;
-        split2(v, hi, lo);
-        uint16_t* o = out + pair_at(row, col, cols);
-        *reinterpret_cast<f16x4*>(o) = hi;
-        *reinterpret_cast<f16x4*>(o + 8) = lo;
-        if (SYM && mt != nt) {
+        for (int q = 0; q < 4; ++q) {
+          const int c = 8 * q + 4 * (lane >> 5);
+          f32x4 v;
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            _Float16* w = reinterpret_cast<_Float16*>(out + pair_at(col + e, row, cols));
-            w[0] = hi[e];
-            w[8] = lo[e];
-          }
+          for (int e = 0; e < 4; ++e) v[e] = turn[(c + e) * kPartRow + (lane & 31)];
+          put4(out, block_at(col0 + (lane & 31), row0 + c, cols), v);
         }
       }
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      __builtin_amdgcn_wave_barrier();
     }
   }
 }
 
 // ---------------------------------------------------------------------------------------------
-// small matrices
+// matrices that fit in LDS
 // ---------------------------------------------------------------------------------------------
 
-constexpr int kSmall = 128, kSmallThreads = 512;
+constexpr int kChipThreads = 512, kChipWaves = kChipThreads / 64;
 
-// Places of 16-byte chunks in rows of 512 bytes: rows r .. r + 15 fall on different sixteenths, and so do every second
-// chunk of four (hi or lo) of the rows 4 i .. 4 i + 3.
-__device__ __forceinline__ int place_small(int row, int chunk) {
+// MB: rows of X by 32.  X's columns are padded to 64, A's rows to 64 or 128 values.
+template <int MB>
+struct Chip {
+  static constexpr int CAP = MB == 1 ? 896 : MB == 2 ? 384 : MB == 3 ? 192 : 128;      // columns of X
+  static constexpr int LDA = MB < 3 ? 64 : 128;
+  static constexpr int X_SIZE = MB * 32 * CAP * 2, A_SIZE = MB * 32 * LDA * 2;         // 16-bit values
+  static constexpr int PARTS = MB == 4 ? 0 : kChipWaves * 32 * kPartRow;               // floats
+  static constexpr int BYTES = (X_SIZE + A_SIZE) * 2 + PARTS * 4;
+};
+constexpr int kChipBytes = Chip<1>::BYTES;
+static_assert(Chip<2>::BYTES <= kChipBytes && Chip<3>::BYTES <= kChipBytes && Chip<4>::BYTES <= kChipBytes && kChipBytes <= 160000, "LDS");
+
+// Places of 16-byte chunks in rows of a multiple of 256 bytes: rows r .. r + 15 fall on different sixteenths of 256 bytes, and so
+// do every second chunk of four (hi or lo) of the rows 4 i .. 4 i + 3.
+__device__ __forceinline__ int place_chip(int row, int chunk) {
   return chunk ^ ((row & 1) | ((row & 2) << 2) | ((row & 12) >> 1));
 }
-__device__ __forceinline__ uint16_t* small_at(uint16_t* lds, int row, int col, int part) {
-  return lds + row * 2 * kSmall + place_small(row, (col >> 3) * 2 + part) * 8 + (col & 7);
+__device__ __forceinline__ uint16_t* chip_at(uint16_t* lds, int ld, int row, int col, int part) {
+  return lds + row * 2 * ld + place_chip(row, (col >> 3) * 2 + part) * 8 + (col & 7);
 }
-__device__ __forceinline__ s16x8 small_along(const uint16_t* lds, int from, int ks, int part, int lane) {
-  const int row = from + (lane & 31);
-  return *reinterpret_cast<const s16x8*>(lds + row * 2 * kSmall + place_small(row, ((ks >> 3) + (lane >> 5)) * 2 + part) * 8);
+// A matrix in LDS as a lane reads operands of 32 rows or columns and 16 steps from it: lane l holds row (column) l % 32, steps
+// 8 (l / 32) .. + 7.  The permutation acts on the low four bits of a chunk's number, of which a lane's own part is fixed: an
+// address is one exclusive or and one addition away (addresses formed anew took longer than the products: 128 x 128 47 us).
+struct ChipMatrix {
+  const char* base;
+  int row_bytes;
+  int along_row, along_low;          // along the rows: byte of the lane's row, its bits of the place times 16
+  int cross_row[2], cross_low[2], cross_in;
+  __device__ __forceinline__ ChipMatrix(const uint16_t* lds, int ld, int lane) : base(reinterpret_cast<const char*>(lds)), row_bytes(4 * ld) {
+    along_row = (lane & 31) * row_bytes;
+    along_low = place_chip(lane & 31, (lane >> 5) * 2) * 16;
+    const int j = lane & 15;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int k = (lane >> 5) * 8 + (j >> 2) + 4 * h;
+      cross_row[h] = k * row_bytes + 8 * (j & 1);
+      cross_low[h] = place_chip(k, ((lane >> 4) & 1) * 4 + ((j & 3) >> 1) * 2) * 16;
+    }
+  }
+  // 32 steps from 32 kb on, as two times 16: rows 32 i .., as they are stored,
+  __device__ __forceinline__ void along(int i, int kb, s16x8 (&f)[2][2]) const {
+    const char* at = base + along_row + i * 32 * row_bytes + (kb >> 1) * 256;
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int part = 0; part < 2; ++part)
+        f[h][part] = *reinterpret_cast<const s16x8*>(at + (along_low ^ ((kb & 1) * 128 + h * 64 + part * 16)));
+  }
+  // columns 32 j .., across the rows,
+  __device__ __forceinline__ void cross(int j, int kb, s16x8 (&f)[2][2]) const {
+    const char* at = base + kb * 32 * row_bytes + (j >> 1) * 256;
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int part = 0; part < 2; ++part) {
+        const int low = (j & 1) * 128 + part * 16;
+        const char* p = at + h * 16 * row_bytes + cross_row[0] + (cross_low[0] ^ low);
+        const char* q = at + h * 16 * row_bytes + cross_row[1] + (cross_low[1] ^ low);
+        const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)p);
+        const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)q);
+        f[h][part] = __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
+      }
+  }
+  // and rows 32 i .. of a symmetric matrix of which the blocks on and below the diagonal are stored.
+  __device__ __forceinline__ void rows(int i, int kb, s16x8 (&f)[2][2]) const {
+    if (kb > i) cross(i, kb, f);
+    else along(i, kb, f);
+  }
+};
+__device__ __forceinline__ f32x16 three(const s16x8 (&q)[2], const s16x8 (&p)[2], f32x16 c) {
+  c = mma<_Float16>(q[1], p[0], c);
+  c = mma<_Float16>(q[0], p[1], c);
+  return mma<_Float16>(q[0], p[0], c);
 }
-__device__ __forceinline__ s16x8 small_cross(const uint16_t* lds, int from, int ks, int part, int lane) {
-  const int j = lane & 15;
-  const int col = from + ((lane >> 4) & 1) * 16 + 4 * (j & 3), chunk = (col >> 3) * 2 + part;
-  const int k = ks + (lane >> 5) * 8 + (j >> 2);
-  const uint16_t* p = lds + k * 2 * kSmall + place_small(k, chunk) * 8 + (col & 7);
-  const uint16_t* q = lds + (k + 4) * 2 * kSmall + place_small(k + 4, chunk) * 8 + (col & 7);
-  const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)p);
-  const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)q);
-  return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
+// A block's values to and from pairs: lane l has row l % 32, columns 8 g + 4 (l / 32) + e.
+__device__ __forceinline__ char* chip_block(uint16_t* lds, int ld, int bi, int bj, int lane) {
+  return reinterpret_cast<char*>(lds) + (bi * 32 + (lane & 31)) * 4 * ld + (bj >> 1) * 256 + (lane >> 5) * 8;
+}
+__device__ __forceinline__ void chip_put(uint16_t* lds, int ld, int bi, int bj, int lane, f32x16 v) {
+  char* at = chip_block(lds, ld, bi, bj, lane);
+  const int low = place_chip(lane & 31, 0) * 16 ^ (bj & 1) * 128;
+#pragma unroll
+  for (int g = 0; g < 4; ++g) {
+    f16x4 hi, lo;
+    split2(f32x4{v[4 * g], v[4 * g + 1], v[4 * g + 2], v[4 * g + 3]}, hi, lo);
+    *reinterpret_cast<f16x4*>(at + (low ^ (g * 32))) = hi;
+    *reinterpret_cast<f16x4*>(at + (low ^ (g * 32 + 16))) = lo;
+  }
+}
+__device__ __forceinline__ f32x4 chip_get4(uint16_t* lds, int ld, int row, int col) {
+  return __builtin_convertvector(*reinterpret_cast<const f16x4*>(chip_at(lds, ld, row, col, 0)), f32x4) +
+         __builtin_convertvector(*reinterpret_cast<const f16x4*>(chip_at(lds, ld, row, col, 1)), f32x4);
+}
+__device__ __forceinline__ f32x16 chip_get(uint16_t* lds, int ld, int bi, int bj, int lane) {
+  const char* at = chip_block(lds, ld, bi, bj, lane);
+  const int low = place_chip(lane & 31, 0) * 16 ^ (bj & 1) * 128;
+  f32x16 v;
+#pragma unroll
+  for (int g = 0; g < 4; ++g) {
+    const f32x4 w = __builtin_convertvector(*reinterpret_cast<const f16x4*>(at + (low ^ (g * 32))), f32x4) +
+                    __builtin_convertvector(*reinterpret_cast<const f16x4*>(at + (low ^ (g * 32 + 16))), f32x4);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[4 * g + e] = w[e];
+  }
+  return v;
 }
 
-// One matrix of at most 128 x 128 a block: X and, in turn, A and B as pairs in LDS.  Blocks of 32 x 32 of a result are dealt to
-// the eight wavefronts, two to each.
-__global__ __launch_bounds__(kSmallThreads) void ns_small_kernel(NsTable t, NsSteps k) {
-  __shared__ __attribute__((aligned(16))) uint16_t lds_x[kSmall * kSmall * 2];
-  __shared__ __attribute__((aligned(16))) uint16_t lds_a[kSmall * kSmall * 2];
-  __shared__ double buf[kSmallThreads / 64];
+// A block of B = a I + b A + c A^2 from c A^2's and A's.
+__device__ __forceinline__ f32x16 square_block(const NsCoef& k, f32x16 c, f32x16 a, bool diagonal, int lane) {
+  c += a * k.own;
+  if (diagonal)
+#pragma unroll
+    for (int e = 0; e < 16; ++e) c[e] += 8 * (e >> 2) + 4 * (lane >> 5) + (e & 3) == (lane & 31) ? k.unit : 0.0f;
+  return c;
+}
+
+// The steps of a matrix of 97 to 128 rows and columns.  The ten blocks of a symmetric result go to the eight wavefronts so that
+// each of the four SIMDs (wavefronts w and w + 4) has two or three; X's sixteen go two to each.  A wavefront keeps its blocks of
+// A in registers for the term b A.
+__device__ __forceinline__ void chip_steps_square(uint16_t* lx, uint16_t* la, const NsSteps& k, int lane, int wave) {
+  constexpr int LD = 128;
+  const ChipMatrix mx(lx, LD, lane), ma(la, LD, lane);
+  // (0,0) and (1,1); (2,2) and (3,3); (1,0); (2,0); (3,0); (2,1); (3,1); (3,2)
+  const int n_own = wave < 2 ? 2 : 1;
+  const int bi[2] = {0x33232120 >> 4 * wave & 15, 2 * wave + 1}, bj[2] = {0x21100020 >> 4 * wave & 15, 2 * wave + 1};
+  const int xi = (wave >> 2) * 2, xj = wave & 3;                     // X's blocks (xi, xj) and (xi + 1, xj)
+  for (int step = 0; step < k.steps; ++step) {
+    f32x16 a[2];
+#pragma unroll
+    for (int o = 0; o < 2; ++o) {
+      a[o] = 0.0f;
+      if (o >= n_own) continue;
+#pragma unroll
+      for (int kb = 0; kb < 4; ++kb) {
+        s16x8 p[2][2], q[2][2];
+        mx.along(bi[o], kb, p);
+        if (wave < 2) {              // diagonal blocks
+          a[o] = three(p[0], p[0], a[o]);
+          a[o] = three(p[1], p[1], a[o]);
+          continue;
+        }
+        mx.along(bj[o], kb, q);
+        a[o] = three(q[0], p[0], a[o]);
+        a[o] = three(q[1], p[1], a[o]);
+      }
+      a[o] *= k.gram.product;
+      chip_put(la, LD, bi[o], bj[o], lane, a[o]);
+    }
+    __syncthreads();
+#pragma unroll
+    for (int o = 0; o < 2; ++o) {
+      if (o >= n_own) continue;
+      f32x16 c = 0.0f;
+#pragma unroll
+      for (int kb = 0; kb < 4; ++kb) {
+        s16x8 p[2][2], q[2][2];
+        ma.rows(bi[o], kb, p);
+        if (wave < 2) {
+          c = three(p[0], p[0], c);
+          c = three(p[1], p[1], c);
+          continue;
+        }
+        ma.rows(bj[o], kb, q);
+        c = three(q[0], p[0], c);
+        c = three(q[1], p[1], c);
+      }
+      a[o] = square_block(k.square[step], c * k.square[step].product, a[o], bi[o] == bj[o], lane);
+    }
+    __syncthreads();                 // everyone has read A
+#pragma unroll
+    for (int o = 0; o < 2; ++o)
+      if (o < n_own) chip_put(la, LD, bi[o], bj[o], lane, a[o]);
+    __syncthreads();
+    f32x16 x[2];
+    x[0] = x[1] = 0.0f;
+#pragma unroll
+    for (int kb = 0; kb < 4; ++kb) {
+      s16x8 p[2][2][2], q[2][2];
+      mx.cross(xj, kb, q);
+      ma.rows(xi, kb, p[0]);
+      ma.rows(xi + 1, kb, p[1]);
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int o = 0; o < 2; ++o) x[o] = three(q[h], p[o][h], x[o]);
+    }
+    __syncthreads();                 // everyone has read X
+    chip_put(lx, LD, xi, xj, lane, x[0] * k.apply.product);
+    chip_put(lx, LD, xi + 1, xj, lane, x[1] * k.apply.product);
+    __syncthreads();
+  }
+}
+
+// The steps of a matrix of fewer rows and up to CAP columns: for A the wavefronts share out the columns and each forms every
+// block; a column block of X is a wavefront's own.
+template <int MB>
+__device__ __forceinline__ void chip_steps(uint16_t* lx, uint16_t* la, float* parts, int n64, const NsSteps& k, int lane, int wave) {
+  constexpr int LDA = Chip<MB>::LDA, S = MB * (MB + 1) / 2;
+  const ChipMatrix mx(lx, n64, lane), ma(la, LDA, lane);
+  for (int step = 0; step < k.steps; ++step) {
+    f32x16 a[S];
+#pragma unroll
+    for (int s = 0; s < S; ++s) a[s] = 0.0f;
+    for (int kb = wave; kb < n64 / 32; kb += kChipWaves) {
+      s16x8 p[MB][2][2];
+#pragma unroll
+      for (int i = 0; i < MB; ++i) mx.along(i, kb, p[i]);
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int i = 0, s = 0; i < MB; ++i)
+#pragma unroll
+          for (int j = 0; j <= i; ++j, ++s) a[s] = three(p[j][h], p[i][h], a[s]);
+    }
+    const int share = n64 / 32 < kChipWaves ? n64 / 32 : kChipWaves;       // wavefronts that have columns
+#pragma unroll
+    for (int i = 0, s = 0; i < MB; ++i)
+#pragma unroll
+      for (int j = 0; j <= i; ++j, ++s) {
+        if (s > 0) __syncthreads();
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          const f32x4 v = {a[s][4 * g], a[s][4 * g + 1], a[s][4 * g + 2], a[s][4 * g + 3]};
+          *reinterpret_cast<f32x4*>(parts + (wave * 32 + (lane & 31)) * kPartRow + 8 * g + 4 * (lane >> 5)) = v;
+        }
+        __syncthreads();
+        if (threadIdx.x < 256) {
+          const int r = static_cast<int>(threadIdx.x) >> 3, c = (static_cast<int>(threadIdx.x) & 7) * 4;
+          f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
+          for (int w = 0; w < share; ++w) v += *reinterpret_cast<const f32x4*>(parts + (w * 32 + r) * kPartRow + c);
+          f16x4 hi, lo;
+          split2(v * k.gram.product, hi, lo);
+          *reinterpret_cast<f16x4*>(chip_at(la, LDA, i * 32 + r, j * 32 + c, 0)) = hi;
+          *reinterpret_cast<f16x4*>(chip_at(la, LDA, i * 32 + r, j * 32 + c, 1)) = lo;
+        }
+      }
+    __syncthreads();
+    f32x16 b = 0.0f;
+    int bi = 0, bj = wave;           // block `wave` of the lower triangle
+    while (bj > bi) bj -= ++bi;
+    if (wave < S) {
+#pragma unroll
+      for (int kb = 0; kb < MB; ++kb) {
+        s16x8 p[2][2], q[2][2];
+        ma.rows(bi, kb, p);
+        ma.rows(bj, kb, q);
+        b = three(q[0], p[0], b);
+        b = three(q[1], p[1], b);
+      }
+      b = square_block(k.square[step], b * k.square[step].product, chip_get(la, LDA, bi, bj, lane), bi == bj, lane);
+    }
+    __syncthreads();
+    if (wave < S) chip_put(la, LDA, bi, bj, lane, b);
+    __syncthreads();
+    for (int xj = wave; xj < n64 / 32; xj += kChipWaves) {
+      f32x16 x[MB];
+#pragma unroll
+      for (int i = 0; i < MB; ++i) x[i] = 0.0f;
+#pragma unroll
+      for (int kb = 0; kb < MB; ++kb) {
+        s16x8 q[2][2];
+        mx.cross(xj, kb, q);
+#pragma unroll
+        for (int i = 0; i < MB; ++i) {
+          s16x8 p[2][2];
+          ma.rows(i, kb, p);
+          x[i] = three(q[0], p[0], x[i]);
+          x[i] = three(q[1], p[1], x[i]);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < MB; ++i) chip_put(lx, n64, i, xj, lane, x[i] * k.apply.product);
+    }
+    __syncthreads();
+  }
+}
+
+// One matrix a block, from the gradient to the updated weight: X and, in turn, A and B as pairs in LDS.  SQUARE: those of 97
+// to 128 rows and columns.
+template <bool SQUARE>
+__global__ __launch_bounds__(kChipThreads) void ns_chip_kernel(NsTable t, NsSteps k) {
+  __shared__ __attribute__((aligned(16))) char pool[SQUARE ? Chip<4>::BYTES : kChipBytes];
+  __shared__ double buf[kChipWaves];
   const NsMat& a = t.m[blockIdx.x];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int mb = (a.m_pad + 31) / 32, nb = (a.n_pad + 31) / 32;      // blocks of 32 (m_pad, n_pad: the sizes themselves here)
-  // U in registers, 4 neighbours of a row a turn: 32 lanes a row of up to 128 columns
-  constexpr int TURNS = kSmall / (kSmallThreads / 32);
-  f32x4 u[TURNS];
-  const int c = (static_cast<int>(threadIdx.x) & 31) * 4;
+  const int mb = a.m_pad / 32, n64 = a.n_pad;
+  uint16_t* lx = reinterpret_cast<uint16_t*>(pool);
+  // U as float32 in the places that its pairs will have: values 8 c .. + 3 of a row in its chunk 2 c, + 4 .. + 7 in the next
+  const auto raw_at = [&](int row, int col) {
+    return reinterpret_cast<float*>(lx + row * 2 * n64 + place_chip(row, (col >> 2)) * 8) + (col & 3);
+  };
+  if ((a.tall ? a.cols : a.rows) != mb * 32 || (a.tall ? a.rows : a.cols) != n64) {
+    for (int i = threadIdx.x; i < mb * 32 * n64 / 4; i += kChipThreads) reinterpret_cast<f32x4*>(pool)[i] = 0.0f;
+    __syncthreads();
+  }
+  const int groups = (a.cols + 3) / 4;                 // of four neighbours of the matrix's rows
+  constexpr int AHEAD = 4;                             // groups whose loads are on their way together
   double s = 0.0;
+  for (int i0 = threadIdx.x; i0 < a.rows * groups; i0 += AHEAD * kChipThreads) {
+    f32x4 g[AHEAD], m[AHEAD];
 #pragma unroll
-  for (int i = 0; i < TURNS; ++i) {
-    const int r = static_cast<int>(threadIdx.x >> 5) + i * (kSmallThreads / 32);
-    u[i] = 0.0f;
-    if (r < a.rows && c < a.cols) {
-      const f32x4 g = read4(a.src, a.lds, r, c, a.cols, t.type, a.vec_src);
-      f32x4 m = {0.0f, 0.0f, 0.0f, 0.0f};
+    for (int n = 0; n < AHEAD; ++n) {
+      const int i = i0 + n * kChipThreads, r = i / groups, c = i % groups * 4;
+      g[n] = m[n] = 0.0f;
+      if (i >= a.rows * groups) continue;
+      g[n] = read4(a.src, a.lds, r, c, a.cols, t.type, a.vec_src);
+      if (t.muon) m[n] = read4(a.mom, a.ldo, r, c, a.cols, QHA_F32, a.vec_mom);
+    }
+#pragma unroll
+    for (int n = 0; n < AHEAD; ++n) {
+      const int i = i0 + n * kChipThreads, r = i / groups, c = i % groups * 4;
+      if (i >= a.rows * groups) continue;
       if (t.muon) {
-        m = read4(a.mom, a.ldo, r, c, a.cols, QHA_F32, a.vec_mom) * t.mu + g * t.grad_scale;
-        write4(a.mom, a.ldo, r, c, a.cols, QHA_F32, a.vec_mom, m);
+        m[n] = m[n] * t.mu + g[n] * t.grad_scale;
+        write4(a.mom, a.ldo, r, c, a.cols, QHA_F32, a.vec_mom, m[n]);
       }
-      u[i] = update_of(t, g, m);
+      f32x4 u = update_of(t, g[n], m[n]);
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        if (c + e >= a.cols) u[i][e] = 0.0f;
-        s += static_cast<double>(u[i][e]) * static_cast<double>(u[i][e]);
+        if (c + e >= a.cols) u[e] = 0.0f;
+        s += static_cast<double>(u[e]) * static_cast<double>(u[e]);
+      }
+      if (a.tall) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (c + e < a.cols) *raw_at(c + e, r) = u[e];
+      } else {
+        *reinterpret_cast<f32x4*>(raw_at(r, c)) = u;
       }
     }
   }
-  const double by = scale_of(block_sum(s, buf), t.eps);
+  const double by = scale_of(block_sum(s, buf), t.eps);      // its barriers make U whole
+  for (int i = threadIdx.x; i < mb * 32 * n64 / 8; i += kChipThreads) {
+    const int row = i / (n64 / 8), col = i % (n64 / 8) * 8;
+    f32x4* at[2] = {reinterpret_cast<f32x4*>(raw_at(row, col)), reinterpret_cast<f32x4*>(raw_at(row, col + 4))};
+    f16x4 hi[2], lo[2];
 #pragma unroll
-  for (int i = 0; i < TURNS; ++i) {
-    const int r = static_cast<int>(threadIdx.x >> 5) + i * (kSmallThreads / 32);
-    f32x4 v;
+    for (int h = 0; h < 2; ++h) {
+      f32x4 v = *at[h];
 #pragma unroll
-    for (int e = 0; e < 4; ++e)
-      v[e] = r < a.rows && c + e < a.cols ? static_cast<float>(static_cast<double>(u[i][e]) * by) : 0.0f;
-    f16x4 hi, lo;
-    split2(v, hi, lo);
-    if (a.tall) {
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        *reinterpret_cast<_Float16*>(small_at(lds_x, c + e, r, 0)) = hi[e];
-        *reinterpret_cast<_Float16*>(small_at(lds_x, c + e, r, 1)) = lo[e];
-      }
-    } else {
-      *reinterpret_cast<f16x4*>(small_at(lds_x, r, c, 0)) = hi;
-      *reinterpret_cast<f16x4*>(small_at(lds_x, r, c, 1)) = lo;
+      for (int e = 0; e < 4; ++e) v[e] = static_cast<float>(static_cast<double>(v[e]) * by);
+      split2(v, hi[h], lo[h]);
     }
+    *reinterpret_cast<f16x8*>(at[0]) = __builtin_shufflevector(hi[0], hi[1], 0, 1, 2, 3, 4, 5, 6, 7);
+    *reinterpret_cast<f16x8*>(at[1]) = __builtin_shufflevector(lo[0], lo[1], 0, 1, 2, 3, 4, 5, 6, 7);
   }
   __syncthreads();
-
-  // one product: results in registers, a barrier, results to LDS (where an operand may have been), a barrier
-  auto product = [&](uint16_t* p, uint16_t* q, bool cross, int depth, int cols_b, uint16_t* own, uint16_t* out, NsCoef f) {
-    f32x16 acc[2];
+  if constexpr (SQUARE) {
+    chip_steps_square(lx, lx + Chip<4>::X_SIZE, k, lane, wave);
+  } else if (mb == 3) {
+    chip_steps<3>(lx, lx + Chip<3>::X_SIZE, reinterpret_cast<float*>(lx + Chip<3>::X_SIZE + Chip<3>::A_SIZE), n64, k, lane, wave);
+  } else if (mb == 2) {
+    chip_steps<2>(lx, lx + Chip<2>::X_SIZE, reinterpret_cast<float*>(lx + Chip<2>::X_SIZE + Chip<2>::A_SIZE), n64, k, lane, wave);
+  } else {
+    chip_steps<1>(lx, lx + Chip<1>::X_SIZE, reinterpret_cast<float*>(lx + Chip<1>::X_SIZE + Chip<1>::A_SIZE), n64, k, lane, wave);
+  }
+#pragma unroll 4
+  for (int i = threadIdx.x; i < a.rows * groups; i += kChipThreads) {
+    const int r = i / groups, c = i % groups * 4;
+    f32x4 v;
+    if (a.tall) {
 #pragma unroll
-    for (int w = 0; w < 2; ++w) {
-      acc[w] = 0.0f;
-      const int b = wave + 8 * w, bi = b / cols_b, bj = b % cols_b;
-      if (b >= mb * cols_b) continue;
-      for (int ks = 0; ks < depth; ks += 16) {
-        s16x8 fp[2], fq[2];
-#pragma unroll
-        for (int part = 0; part < 2; ++part) {
-          fp[part] = small_along(p, bi * 32, ks, part, lane);
-          fq[part] = cross ? small_cross(q, bj * 32, ks, part, lane) : small_along(q, bj * 32, ks, part, lane);
-        }
-        acc[w] = mma<_Float16>(fq[1], fp[0], acc[w]);
-        acc[w] = mma<_Float16>(fq[0], fp[1], acc[w]);
-        acc[w] = mma<_Float16>(fq[0], fp[0], acc[w]);
-      }
-#pragma unroll
-      for (int e = 0; e < 16; ++e) acc[w][e] *= f.product;
-      if (own) {
-#pragma unroll
-        for (int g = 0; g < 4; ++g) {
-          const int row = bi * 32 + (lane & 31), col = bj * 32 + 8 * g + 4 * (lane >> 5);
-          const f32x4 v = __builtin_convertvector(*reinterpret_cast<const f16x4*>(small_at(own, row, col, 0)), f32x4) +
-                          __builtin_convertvector(*reinterpret_cast<const f16x4*>(small_at(own, row, col, 1)), f32x4);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) acc[w][4 * g + e] += v[e] * f.own;
-        }
-      }
+      for (int e = 0; e < 4; ++e)
+        v[e] = c + e < a.cols ? static_cast<float>(*reinterpret_cast<const _Float16*>(chip_at(lx, n64, c + e, r, 0))) +
+                                    static_cast<float>(*reinterpret_cast<const _Float16*>(chip_at(lx, n64, c + e, r, 1)))
+                              : 0.0f;
+    } else {
+      v = chip_get4(lx, n64, r, c);
     }
-    __syncthreads();
+    apply4(t, a, r, c, v * (1.0f / kScaleX));
+  }
+}
+
+// ---------------------------------------------------------------------------------------------
+// products of few tiles
+// ---------------------------------------------------------------------------------------------
+
+constexpr int kDirectWaves = 4, kDirectChunks = 4, kFusedRows = 128, kFusedBlocks = 512;
+
+// Operands of 32 rows and 32 steps straight from memory: p points to the rows' first block.
+__device__ __forceinline__ void direct_load(const uint16_t* p, int lane, int64_t chunk, s16x8 (&f)[2][2]) {
 #pragma unroll
-    for (int w = 0; w < 2; ++w) {
-      const int b = wave + 8 * w, bi = b / cols_b, bj = b % cols_b;
-      if (b >= mb * cols_b) continue;
+  for (int h = 0; h < 2; ++h)
+#pragma unroll
+    for (int part = 0; part < 2; ++part) f[h][part] = *reinterpret_cast<const s16x8*>(p + (2 * chunk + h) * kBlock + part * kLo + lane_at(lane, h));
+}
+
+// The same products for a batch whose tiles would leave most of the chip idle, where a launch's time is that of its chain of loads
+// and barriers: a block owns 32 x 32 values, and its wavefronts share out the reduction by 32 steps, four of which they load at
+// once straight from memory (X's transpose is kept for the last product).  Their sums meet in LDS and are added in order.
+// FUSED (X of at most 256 rows): the last product's block forms its 32 rows of B itself, from A, which saves a launch.
+template <int KIND, bool FUSED>
+__global__ __launch_bounds__(kDirectWaves * 64) void ns_direct_kernel(const NsTable* table, NsFirst first, NsCoef sq, NsCoef k, int32_t from, uint32_t total) {
+  constexpr bool SYM = KIND == NS_GRAM || KIND == NS_SQUARE;
+  constexpr int W = kDirectWaves, CH = kDirectChunks;
+  static_assert(!FUSED || (!SYM && kFusedRows <= 32 * W), "a block of B's rows for each wavefront");
+  __shared__ float part[W][32][kPartRow];
+  __shared__ __attribute__((aligned(16))) uint16_t panel[FUSED ? 32 * kFusedRows * 2 : 8];
+  const uint32_t band = (total + kXcds - 1) / kXcds;
+  const uint32_t block = blockIdx.x % kXcds * band + blockIdx.x / kXcds;
+  if (block >= total) return;
+  const NsTable& t = *table;
+  const int i = matrix_of(first, block);
+  const NsMat& a = t.m[i];
+  const int tile = static_cast<int>(block - first.block[i]);
+  const int m_pad = a.m_pad;
+  int mt, nt;
+  if constexpr (SYM) {
+    triangle(tile, &mt, &nt);
+  } else {
+    mt = tile % (m_pad / 32);
+    nt = tile / (m_pad / 32);
+  }
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const NsParts w(a);
+  const uint16_t* x = w.x(from);
+  const int64_t depth = KIND == NS_GRAM ? a.n_pad : m_pad;
+  const auto rows_of = [&](const uint16_t* base, int block_row) {
+    return base + block_row * (depth >> 4) * kBlock;
+  };
+  const uint16_t* p = rows_of(KIND == NS_GRAM ? x : KIND == NS_SQUARE || FUSED ? w.a() : w.b(), mt);
+  const uint16_t* q = rows_of(KIND == NS_GRAM ? x : KIND == NS_SQUARE ? w.a() : w.xt(from), nt);
+  // four neighbours of a row a thread; A's for the square product are on their way early
+  const int r = static_cast<int>(threadIdx.x) & 31, c = (static_cast<int>(threadIdx.x >> 5) & 7) * 4;
+  const int64_t row = mt * 32 + r, col = nt * 32 + c, cols = SYM ? m_pad : a.n_pad;
+  const bool mine = threadIdx.x < 256;
+  f32x4 own = {0.0f, 0.0f, 0.0f, 0.0f};
+  if (KIND == NS_SQUARE && mine) own = get4(w.a(), block_at(row, col, cols));
+
+  f32x16 acc[3];
+#pragma unroll
+  for (int e = 0; e < 3; ++e) acc[e] = 0.0f;
+  const auto add = [&](const s16x8 (&fq)[2][2], const s16x8 (&fp)[2][2]) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      acc[0] = mma<_Float16>(fq[h][1], fp[h][0], acc[0]);
+      acc[1] = mma<_Float16>(fq[h][0], fp[h][1], acc[1]);
+      acc[2] = mma<_Float16>(fq[h][0], fp[h][0], acc[2]);
+    }
+  };
+  const int64_t chunks = depth / 32;
+  if constexpr (FUSED) {
+    s16x8 x_rows[2][2];
+    if (wave < chunks) direct_load(q, lane, wave, x_rows);
+    if (wave < chunks) {             // B's rows 32 mt .., columns 32 wave ..
+      const uint16_t* other = rows_of(w.a(), wave);
+      f32x4 a_own[4];
+#pragma unroll
+      for (int g = 0; g < 4; ++g) a_own[g] = get4(w.a(), block_at(mt * 32 + (lane & 31), wave * 32 + 8 * g + 4 * (lane >> 5), m_pad));
+      for (int64_t s = 0; s < chunks; s += CH) {
+        s16x8 fp[CH][2][2], fq[CH][2][2];
+#pragma unroll
+        for (int n = 0; n < CH; ++n)
+          if (s + n < chunks) {
+            direct_load(p, lane, s + n, fp[n]);
+            direct_load(other, lane, s + n, fq[n]);
+          }
+#pragma unroll
+        for (int n = 0; n < CH; ++n)
+          if (s + n < chunks) add(fq[n], fp[n]);
+      }
+      f32x16 b = (acc[0] + acc[1] + acc[2]) * sq.product;
 #pragma unroll
       for (int g = 0; g < 4; ++g) {
-        const int row = bi * 32 + (lane & 31), col = bj * 32 + 8 * g + 4 * (lane >> 5);
-        f32x4 v;
+        const f32x4 v = square_terms(sq, f32x4{b[4 * g], b[4 * g + 1], b[4 * g + 2], b[4 * g + 3]}, a_own[g],
+                                     mt * 32 + (lane & 31), wave * 32 + 8 * g + 4 * (lane >> 5));
 #pragma unroll
-        for (int e = 0; e < 4; ++e) v[e] = acc[w][4 * g + e];
-        f16x4 hi, lo;
-        split2(v, hi, lo);
-        *reinterpret_cast<f16x4*>(small_at(out, row, col, 0)) = hi;
-        *reinterpret_cast<f16x4*>(small_at(out, row, col, 1)) = lo;
+        for (int e = 0; e < 4; ++e) b[4 * g + e] = v[e];
       }
+      chip_put(panel, kFusedRows, 0, wave, lane, b);
     }
     __syncthreads();
-  };
-  for (int step = 0; step < k.steps; ++step) {
-    product(lds_x, lds_x, false, 32 * nb, mb, nullptr, lds_a, k.gram);
-    product(lds_a, lds_a, false, 32 * mb, mb, lds_a, lds_a, k.square[step]);
-    product(lds_a, lds_x, true, 32 * mb, nb, lds_x, lds_x, k.apply[step]);
-  }
-
 #pragma unroll
-  for (int i = 0; i < TURNS; ++i) {
-    const int r = static_cast<int>(threadIdx.x >> 5) + i * (kSmallThreads / 32);
-    if (r >= a.rows || c >= a.cols) continue;
-    f32x4 v;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const int xr = a.tall ? c + e : r, xc = a.tall ? r : c + e;
-      v[e] = (static_cast<float>(*reinterpret_cast<const _Float16*>(small_at(lds_x, xr, xc, 0))) +
-              static_cast<float>(*reinterpret_cast<const _Float16*>(small_at(lds_x, xr, xc, 1)))) * (1.0f / kScaleX);
+    for (int e = 0; e < 3; ++e) acc[e] = 0.0f;
+    if (wave < chunks) {
+      s16x8 b_rows[2][2];
+      ChipMatrix(panel, kFusedRows, lane).along(0, wave, b_rows);
+      add(x_rows, b_rows);
     }
-    apply4(t, a, r, c, v);
+  } else {
+    for (int64_t s = wave; s < chunks; s += W * CH) {
+      s16x8 fp[CH][2][2], fq[CH][2][2];
+#pragma unroll
+      for (int n = 0; n < CH; ++n)
+        if (s + n * W < chunks) {
+          direct_load(p, lane, s + n * W, fp[n]);
+          direct_load(q, lane, s + n * W, fq[n]);
+        }
+#pragma unroll
+      for (int n = 0; n < CH; ++n)
+        if (s + n * W < chunks) add(fq[n], fp[n]);
+    }
+  }
+  acc[2] += acc[0] + acc[1];
+#pragma unroll
+  for (int g = 0; g < 4; ++g) {
+    const f32x4 v = {acc[2][4 * g], acc[2][4 * g + 1], acc[2][4 * g + 2], acc[2][4 * g + 3]};
+    *reinterpret_cast<f32x4*>(&part[wave][lane & 31][8 * g + 4 * (lane >> 5)]) = v;
+  }
+  __syncthreads();
+  f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
+  if (mine) {
+#pragma unroll
+    for (int n = 0; n < W; ++n) v += *reinterpret_cast<const f32x4*>(&part[n][r][c]);
+    v *= k.product;
+    if constexpr (KIND == NS_SQUARE) v = square_terms(k, v, own, row, col);
+    if constexpr (KIND != NS_LAST) put4(KIND == NS_GRAM ? w.a() : KIND == NS_SQUARE ? w.b() : w.x(from ^ 1), block_at(row, col, cols), v);
+  }
+  // the mirror of a symmetric result, the transpose of X, or the rows of the result
+  if (SYM && mt == nt) return;
+  if (mine) *reinterpret_cast<f32x4*>(&part[0][r][c]) = v;         // each thread read its own four values of it alone
+  __syncthreads();
+  if (!mine) return;
+  if constexpr (KIND == NS_LAST) {
+    finish_block<256>(t, a, &part[0][0][0], mt * 32, nt * 32, threadIdx.x);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] = part[0][c + e][r];
+    put4(KIND == NS_GRAM ? w.a() : KIND == NS_SQUARE ? w.b() : w.xt(from ^ 1), block_at(nt * 32 + r, mt * 32 + c, m_pad), v);
   }
 }
 
@@ -566,60 +1028,157 @@ __global__ __launch_bounds__(kSmallThreads) void ns_small_kernel(NsTable t, NsSt
 // host
 // ---------------------------------------------------------------------------------------------
 
-constexpr int64_t kBatchValues = 1LL << 24;      // values of X in flight in a batch of several matrices
+constexpr int64_t kBatchValues = 1LL << 27;      // values of X in flight in a batch of several matrices
 
+constexpr size_t kTableBytes = (sizeof(NsTable) + 255) / 256 * 256;
+
+int64_t pad32(int64_t x) { return (x + 31) / 32 * 32; }
 int64_t pad64(int64_t x) { return (x + 63) / 64 * 64; }
-bool is_small(const NsMatrix& m) { return m.rows <= kSmall && m.cols <= kSmall; }
-int64_t piece_count(const NsMatrix& m) {
-  return (m.rows + kPieceRows - 1) / kPieceRows * ((m.cols + kPieceCols - 1) / kPieceCols);
+// Rows of X by 32 where the matrix fits in LDS, else 0.
+int chip_rows_of(const NsMatrix& m) {
+  const int64_t s = m.rows < m.cols ? m.rows : m.cols, l = pad64(m.rows < m.cols ? m.cols : m.rows);
+  if (s <= 32 && l <= Chip<1>::CAP) return 1;
+  if (s <= 64 && l <= Chip<2>::CAP) return 2;
+  if (s <= 96 && l <= Chip<3>::CAP) return 3;
+  return s <= 128 && l <= Chip<4>::CAP ? 4 : 0;
 }
-// X twice, A and B as pairs, and the pieces' sums of squares
-size_t bytes_of(const NsMatrix& m) {
-  const int64_t s = pad64(m.rows < m.cols ? m.rows : m.cols), l = pad64(m.rows < m.cols ? m.cols : m.rows);
-  return static_cast<size_t>(2 * s * l + 2 * s * s) * 4 + static_cast<size_t>((piece_count(m) + 1) / 2 * 16);
+int64_t piece_count(const NsMatrix& m, int64_t rows) {
+  return (m.rows + rows - 1) / rows * ((m.cols + kPieceCols - 1) / kPieceCols);
+}
+int64_t short_side(const NsMatrix& m) { return pad32(m.rows < m.cols ? m.rows : m.cols); }
+int64_t long_side(const NsMatrix& m) { return pad32(m.rows < m.cols ? m.cols : m.rows); }
+
+// How a batch is worked: by tiles or directly, and rows of a piece to measure.
+struct NsPlan {
+  bool direct, fused;
+  int piece_rows;
+};
+NsPlan plan_of(const NsMatrix* m, const int64_t* index, int count) {
+  int64_t pieces = 0, tiles = 0, blocks = 0, deepest = 0, values = 0;
+  bool fits = true;
+  for (int i = 0; i < count; ++i) {
+    const NsMatrix& x = m[index[i]];
+    const int64_t s = short_side(x), l = long_side(x), rows = s / 32, cols = l / 32;
+    pieces += piece_count(x, 8);
+    fits = fits && s <= kFusedRows;
+    tiles += (s + 63) / 64 * ((l + 63) / 64);
+    blocks += rows * cols;
+    deepest = l + 2 * s > deepest ? l + 2 * s : deepest;
+    values += 64 * (rows * (rows + 1) / 2 * (l + (s <= kFusedRows ? 0 : s)) + rows * cols * s);
+  }
+  // us of a step: the operands that direct blocks read, at 13 TB/s; the tiles' steps of 32, one after the other
+  const double direct = static_cast<double>(values) * 4.0 / 13e6;
+  const double tiled = 0.28 * static_cast<double>(deepest) / 32.0 * (tiles > 512 ? static_cast<double>(tiles) / 512.0 : 1.0);
+  // each block forms B's rows: many of them lose more by it than a launch costs (12 of 96 x 2848 265 us, 237 unfused)
+  NsPlan p = {direct < tiled, fits && blocks <= kFusedBlocks, 8};
+  while (p.piece_rows < 64 && pieces > 1024) {
+    p.piece_rows *= 2;
+    pieces /= 2;
+  }
+  return p;
+}
+// a matrix's part of the workspace (NsParts)
+size_t bytes_of(const NsMatrix& m, const NsPlan& p) {
+  const int64_t s = short_side(m), l = long_side(m);
+  return static_cast<size_t>((p.direct ? 4 : 2) * s * l + 2 * s * s) * 4 + static_cast<size_t>((piece_count(m, p.piece_rows) + 1) / 2 * 16);
 }
 
-// The next batch of large (or small) matrices from *at on: their indices, at most kNsBatch.
-int next_batch(const NsMatrix* m, int64_t n, bool small, int64_t* at, int64_t* index) {
+enum { IN_MEMORY = 0, ON_CHIP = 1, ON_CHIP_SQUARE = 2 };
+int place_of(const NsMatrix& m) {
+  const int rows = chip_rows_of(m);
+  return rows == 4 ? ON_CHIP_SQUARE : rows ? ON_CHIP : IN_MEMORY;
+}
+
+// The next batch of matrices of a place from *at on: their indices, at most kNsBatch.
+int next_batch(const NsMatrix* m, int64_t n, int place, int64_t* at, int64_t* index) {
   int count = 0;
   int64_t values = 0;
   for (; *at < n && count < kNsBatch; ++*at) {
     const NsMatrix& x = m[*at];
-    if (x.rows == 0 || x.cols == 0 || is_small(x) != small) continue;
-    if (!small && count > 0 && values + x.rows * x.cols > kBatchValues) break;
+    if (x.rows == 0 || x.cols == 0 || place_of(x) != place) continue;
+    if (place == IN_MEMORY && count > 0 && values + x.rows * x.cols > kBatchValues) break;
     values += x.rows * x.cols;
     index[count++] = *at;
   }
   return count;
 }
 
-template <int KIND, int MI, int NI, int WM, int WN>
-void run_product(NsTable& t, const NsCoef& k, int from, hipStream_t s) {
-  constexpr int BM = MI * 32 * WM, BN = NI * 32 * WN;
-  uint32_t total = 0;
-  for (int i = 0; i < t.n; ++i) {
-    t.first_tile[i] = total;
-    const uint32_t mt = (t.m[i].m_pad + BM - 1) / BM, nt = (t.m[i].n_pad + BN - 1) / BN;
-    total += KIND == NS_APPLY ? mt * nt : mt * (mt + 1) / 2;
-  }
-  const uint32_t grid = (total + static_cast<uint32_t>(kXcds) - 1) / static_cast<uint32_t>(kXcds) * static_cast<uint32_t>(kXcds);
-  ns_product_kernel<KIND, MI, NI, WM, WN><<<grid, WM * WN * 64, 0, s>>>(t, k, from, total);
-}
-
-template <int KIND>
-int64_t tiles_of(const NsTable& t, int64_t side) {
+// Tiles of `side` of a batch's symmetric results, or of its X.
+uint32_t tiles_of(const NsTable& t, bool sym, int side, NsFirst* first) {
   int64_t total = 0;
+  if (first) first->n = t.n;
   for (int i = 0; i < t.n; ++i) {
+    if (first) first->block[i] = static_cast<uint32_t>(total);
     const int64_t mt = (t.m[i].m_pad + side - 1) / side, nt = (t.m[i].n_pad + side - 1) / side;
-    total += KIND == NS_APPLY ? mt * nt : mt * (mt + 1) / 2;
+    total += sym ? mt * (mt + 1) / 2 : mt * nt;
   }
-  return total;
+  return static_cast<uint32_t>(total);
 }
 
+// The side of a launch's tiles, by the time that the busiest of the 256 compute units takes: its tiles' first loads and stores, and
+// their steps.  Measured (us): gram products of 4096 x 4096: 192 222, 128 277, 256 281, 64 324; of 2528 x 3008: 128 89, 64 104, 192 137;
+// of 24 of 1024 x 4096: 256 355, 128 393, 64 436, 192 447; of five of 544 x 1024: 64 14, 128 29.  Last products of the same: 256 335,
+// 128 386, 64 494; 128 128, 64 159, 256 172; 256 585, 128 632, 64 839; 64 17, 128 19.
+int side_of(const NsTable& t, bool sym, int64_t depth) {
+  struct Speed {
+    int side;
+    double once, tile, step;         // us of a launch, of a tile, and of a step of the reduction in it
+  };
+  constexpr Speed speeds[] = {{64, 5.0, 1.0, 0.0078}, {128, 4.0, 3.0, 0.0235}, {192, 0.0, 10.0, 0.052}, {256, 0.0, 12.0, 0.083}};
+  int best = 0;
+  double least = 0.0;
+  for (const Speed& v : speeds) {
+    if (v.side == 192 && !sym) continue;
+    const double most = static_cast<double>((tiles_of(t, sym, v.side, nullptr) + 255) / 256);
+    // a unit holds two tiles of 128: one by itself runs slower
+    const double step = v.side == 128 && most == 1.0 ? 0.0275 : v.step;
+    const double time = v.once + most * (v.tile + step * static_cast<double>(depth));
+    if (best == 0 || time < least) {
+      best = v.side;
+      least = time;
+    }
+  }
+  return best;
+}
+
+// A launch's tiles: their side, their number, and each matrix's first.
+struct NsTiles {
+  int side;
+  uint32_t total;
+  NsFirst first;
+  uint32_t grid() const { return (total + static_cast<uint32_t>(kXcds) - 1) / static_cast<uint32_t>(kXcds) * static_cast<uint32_t>(kXcds); }
+};
+
 template <int KIND>
-void run_product(NsTable& t, const NsCoef& k, int from, hipStream_t s) {
-  if (tiles_of<KIND>(t, 128) >= 256) run_product<KIND, 2, 2, 2, 2>(t, k, from, s);
-  else run_product<KIND, 1, 1, 2, 2>(t, k, from, s);
+void run_product(const NsTable* t, const NsTiles& b, const NsCoef& k, int from, hipStream_t s) {
+  constexpr bool SYM = KIND == NS_GRAM || KIND == NS_SQUARE;
+  const uint32_t g = b.grid();
+  if (b.side == 256) ns_product_kernel<KIND, 4, 2, 2, 4, 2><<<g, 512, 0, s>>>(t, b.first, k, from, b.total);
+  else if (b.side == 128) ns_product_kernel<KIND, 2, 2, 2, 2, 2><<<g, 256, 0, s>>>(t, b.first, k, from, b.total);
+  else if (b.side == 64) ns_product_kernel<KIND, 1, 1, 2, 2, 3><<<g, 256, 0, s>>>(t, b.first, k, from, b.total);
+  else if constexpr (SYM) ns_product_kernel<KIND, 3, 3, 2, 2, 2><<<g, 256, 0, s>>>(t, b.first, k, from, b.total);
+}
+
+// One step of a batch; the last one's results go where the call wants them.
+void run_step(const NsTable* t, const NsPlan& plan, const NsTiles& gram, const NsTiles& square, const NsTiles& all,
+              const NsSteps& k, int step, hipStream_t s) {
+  const int from = step & 1;
+  const bool last = step + 1 == k.steps;
+  if (plan.direct) {
+    const NsCoef &sq = k.square[step], &ap = k.apply;
+    constexpr int NT = kDirectWaves * 64;
+    ns_direct_kernel<NS_GRAM, false><<<gram.grid(), NT, 0, s>>>(t, gram.first, sq, k.gram, from, gram.total);
+    if (!plan.fused) ns_direct_kernel<NS_SQUARE, false><<<square.grid(), NT, 0, s>>>(t, square.first, sq, sq, from, square.total);
+    if (plan.fused && last) ns_direct_kernel<NS_LAST, true><<<all.grid(), NT, 0, s>>>(t, all.first, sq, ap, from, all.total);
+    else if (plan.fused) ns_direct_kernel<NS_APPLY, true><<<all.grid(), NT, 0, s>>>(t, all.first, sq, ap, from, all.total);
+    else if (last) ns_direct_kernel<NS_LAST, false><<<all.grid(), NT, 0, s>>>(t, all.first, sq, ap, from, all.total);
+    else ns_direct_kernel<NS_APPLY, false><<<all.grid(), NT, 0, s>>>(t, all.first, sq, ap, from, all.total);
+    return;
+  }
+  run_product<NS_GRAM>(t, gram, k.gram, from, s);
+  run_product<NS_SQUARE>(t, square, k.square[step], from, s);
+  if (last) run_product<NS_LAST>(t, all, k.apply, from, s);
+  else run_product<NS_APPLY>(t, all, k.apply, from, s);
 }
 
 }  // namespace
@@ -628,9 +1187,11 @@ size_t ns_workspace(const NsMatrix* m, int64_t n) {
   size_t most = 0;
   int64_t index[kNsBatch];
   for (int64_t at = 0; at < n;) {
-    const int count = next_batch(m, n, false, &at, index);
+    const int count = next_batch(m, n, IN_MEMORY, &at, index);
     size_t need = 0;
-    for (int i = 0; i < count; ++i) need += bytes_of(m[index[i]]);
+    const NsPlan plan = plan_of(m, index, count);
+    for (int i = 0; i < count; ++i) need += bytes_of(m[index[i]], plan);
+    if (count) need += kTableBytes;
     most = need > most ? need : most;
   }
   return most;
@@ -648,16 +1209,17 @@ hipError_t launch_ns(const NsMatrix* m, int64_t n, const NsArgs& args, void* ws,
   t.eps = args.eps;
   NsSteps k = {};
   k.steps = args.steps;
-  k.gram = {kScaleA / (kScaleX * kScaleX), 0.0f};
+  k.gram = {kScaleA / (kScaleX * kScaleX), 0.0f, 0.0f};
+  k.apply = {1.0f / kScaleB, 0.0f, 0.0f};
   for (int i = 0; i < args.steps; ++i) {
     const double a = args.coefficients[3 * i], b = args.coefficients[3 * i + 1], c = args.coefficients[3 * i + 2];
-    k.square[i] = {static_cast<float>(c * (kScaleB / (kScaleA * kScaleA))), static_cast<float>(b * (kScaleB / kScaleA))};
-    k.apply[i] = {1.0f / kScaleB, static_cast<float>(a)};
+    k.square[i] = {static_cast<float>(c * (kScaleB / (kScaleA * kScaleA))), static_cast<float>(b * (kScaleB / kScaleA)), static_cast<float>(a * kScaleB)};
   }
   int64_t index[kNsBatch];
   bool launched = false;
+  NsPlan plan = {};
   const auto fill = [&](int count, bool small) {
-    char* at = static_cast<char*>(ws);
+    char* at = static_cast<char*>(ws) + kTableBytes;
     t.n = count;
     launched = true;
     for (int i = 0; i < count; ++i) {
@@ -667,8 +1229,8 @@ hipError_t launch_ns(const NsMatrix* m, int64_t n, const NsArgs& args, void* ws,
       a.cols = static_cast<int32_t>(x.cols);
       a.tall = x.rows > x.cols;
       const int64_t sh = a.tall ? x.cols : x.rows, lo = a.tall ? x.rows : x.cols;
-      a.m_pad = static_cast<int32_t>(small ? sh : pad64(sh));
-      a.n_pad = static_cast<int32_t>(small ? lo : pad64(lo));
+      a.m_pad = static_cast<int32_t>(small ? 32 * chip_rows_of(x) : pad32(sh));
+      a.n_pad = static_cast<int32_t>(small ? pad64(lo) : pad32(lo));
       a.src = x.src;
       a.lds = x.lds;
       a.dst = x.dst;
@@ -684,49 +1246,51 @@ hipError_t launch_ns(const NsMatrix* m, int64_t n, const NsArgs& args, void* ws,
       a.vec_mom = whole(x.mom, x.ldo, QHA_F32);
       a.vec_copy = whole(x.copy, x.ldo, args.out_type);
       if (small) continue;
-      const int64_t mn = static_cast<int64_t>(a.m_pad) * a.n_pad, mm = static_cast<int64_t>(a.m_pad) * a.m_pad;
-      a.x[0] = reinterpret_cast<uint16_t*>(at);
-      a.x[1] = a.x[0] + 2 * mn;
-      a.a = a.x[1] + 2 * mn;
-      a.b = a.a + 2 * mm;
-      a.parts = reinterpret_cast<double*>(a.b + 2 * mm);
-      at += bytes_of(x);
+      a.ws = at;
+      at += bytes_of(x, plan);
     }
   };
+  for (int place : {ON_CHIP, ON_CHIP_SQUARE})
+    for (int64_t at = 0; at < n;) {
+      const int count = next_batch(m, n, place, &at, index);
+      if (count == 0) break;
+      fill(count, true);
+      if (place == ON_CHIP) ns_chip_kernel<false><<<count, kChipThreads, 0, s>>>(t, k);
+      else ns_chip_kernel<true><<<count, kChipThreads, 0, s>>>(t, k);
+    }
   for (int64_t at = 0; at < n;) {
-    const int count = next_batch(m, n, true, &at, index);
+    const int count = next_batch(m, n, IN_MEMORY, &at, index);
     if (count == 0) break;
-    fill(count, true);
-    ns_small_kernel<<<count, kSmallThreads, 0, s>>>(t, k);
-  }
-  for (int64_t at = 0; at < n;) {
-    const int count = next_batch(m, n, false, &at, index);
-    if (count == 0) break;
+    plan = plan_of(m, index, count);
     fill(count, false);
-    uint32_t pieces = 0, tiles = 0;
+    t.piece_rows = plan.piece_rows;
+    t.transposes = plan.direct;
+    NsFirst pieces = {};
+    pieces.n = count;
+    uint32_t n_pieces = 0;
     for (int i = 0; i < count; ++i) {
-      t.first_piece[i] = pieces;
-      pieces += static_cast<uint32_t>(piece_count(m[index[i]]));
+      pieces.block[i] = n_pieces;
+      n_pieces += static_cast<uint32_t>(piece_count(m[index[i]], plan.piece_rows));
     }
-    const auto tables = [&] {          // the products write first_tile for tiles of their own
-      tiles = 0;
-      for (int i = 0; i < count; ++i) {
-        t.first_tile[i] = tiles;
-        tiles += static_cast<uint32_t>(t.m[i].m_pad / 64) * static_cast<uint32_t>(t.m[i].n_pad / 64);
-      }
+    int64_t most_m = 0, most_n = 0;
+    for (int i = 0; i < count; ++i) {
+      most_m = t.m[i].m_pad > most_m ? t.m[i].m_pad : most_m;
+      most_n = t.m[i].n_pad > most_n ? t.m[i].n_pad : most_n;
+    }
+    const auto tiles = [&](bool symmetric, int side) {
+      NsTiles b;
+      b.side = side;
+      b.total = tiles_of(t, symmetric, side, &b.first);
+      return b;
     };
-    ns_measure_kernel<<<pieces, 256, 0, s>>>(t);
-    tables();
-    ns_split_kernel<<<tiles, 256, 0, s>>>(t);
-    int from = 0;
-    for (int i = 0; i < args.steps; ++i) {
-      run_product<NS_GRAM>(t, k.gram, from, s);
-      run_product<NS_SQUARE>(t, k.square[i], from, s);
-      run_product<NS_APPLY>(t, k.apply[i], from, s);
-      from ^= 1;
-    }
-    tables();
-    ns_finish_kernel<<<tiles, 256, 0, s>>>(t, from);
+    const NsTiles whole = tiles(false, 64);
+    const NsTiles gram = tiles(true, plan.direct ? 32 : side_of(t, true, most_n));
+    const NsTiles square = tiles(true, plan.direct ? 32 : side_of(t, true, most_m));
+    const NsTiles all = tiles(false, plan.direct ? 32 : side_of(t, false, most_m));
+    NsTable* table = static_cast<NsTable*>(ws);
+    ns_measure_kernel<<<n_pieces, 256, 0, s>>>(t, pieces, reinterpret_cast<uint32_t*>(table));
+    ns_split_kernel<<<whole.total, 256, 0, s>>>(table, whole.first);
+    for (int i = 0; i < args.steps; ++i) run_step(table, plan, gram, square, all, k, i, s);
   }
   return launched ? hipGetLastError() : hipSuccess;
 }

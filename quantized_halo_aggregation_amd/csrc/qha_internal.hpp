@@ -311,8 +311,8 @@ struct NsArgs {
   double eps;
   const double* coefficients;        // [steps][3]
 };
-// ... and a batch of them, passed to the kernels by value.
-constexpr int kNsBatch = 24, kNsSteps = 16;
+// ... and a batch of them, as the kernels read it.
+constexpr int kNsBatch = 40, kNsSteps = 16;
 struct NsMat {
   const void* src;
   int64_t lds;
@@ -320,29 +320,30 @@ struct NsMat {
   int64_t ldo;
   float* mom;
   void* copy;
-  uint16_t* x[2];                    // pairs of parts: X and the next one, A and B
-  uint16_t* a;
-  uint16_t* b;
-  double* parts;                     // sums of squares
-  int32_t rows, cols, m_pad, n_pad;  // X's sizes (the shorter first), padded to 64
+  char* ws;                          // the matrix's part of the workspace
+  int32_t rows, cols, m_pad, n_pad;  // X's sizes (the shorter first), padded to 32
   float step;
   uint8_t tall, vec_src, vec_out, vec_mom, vec_copy;
 };
 struct NsTable {
   NsMat m[kNsBatch];
-  uint32_t first_piece[kNsBatch], first_tile[kNsBatch];
-  int32_t n, type, out_type, muon, nesterov;
+  int32_t n, piece_rows, transposes, type, out_type, muon, nesterov;
   float mu, grad_scale, decay;
   double eps;
 };
+struct NsFirst {                       // the first blocks of a launch's matrices
+  int32_t n;
+  uint32_t block[kNsBatch];
+};
 struct NsCoef {
-  float product, own;                // C = product * acc + own * the matrix that is there
+  float product, own, unit;          // a result's: of the product, of A and of the unit matrix
 };
 struct NsSteps {
   int32_t steps;
-  NsCoef gram, square[kNsSteps], apply[kNsSteps];
+  NsCoef gram, apply, square[kNsSteps];
 };
-static_assert(sizeof(NsTable) + sizeof(NsSteps) <= 4096, "kernel arguments");
+static_assert(sizeof(NsTable) + sizeof(NsSteps) <= 4096 && sizeof(NsTable) + sizeof(NsFirst) <= 4096, "kernel arguments");
+static_assert(sizeof(NsTable) % 8 == 0, "copied by words");
 size_t ns_workspace(const NsMatrix* m, int64_t n);
 hipError_t launch_ns(const NsMatrix* m, int64_t n, const NsArgs& args, void* ws, hipStream_t s);
 

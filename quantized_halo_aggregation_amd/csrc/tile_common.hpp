@@ -45,6 +45,10 @@ __device__ __forceinline__ f32x4 mma16<_Float16>(s16x8 a, s16x8 b, f32x4 c) {
 // Waits for this wavefront's loads into LDS; a barrier after it makes them visible to the block.
 __device__ __forceinline__ void loads_done() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
 
+// Waits until at most N of them (of the last ones) are on their way.
+template <int N>
+__device__ __forceinline__ void loads_left() { asm volatile("s_waitcnt vmcnt(%0)" : : "n"(N) : "memory"); }
+
 // 16 bytes a lane from memory to LDS, lane i of the wavefront to `to` + 16 i.  Written as assembly because
 // the compiler would wait for all such loads before any LDS read that it cannot tell apart from their
 // destination (the transposing reads), and so undo the double buffering; nothing comes back in a

@@ -23,9 +23,10 @@ TINY = {"float32": 0.0, "bfloat16": 0.0, "float16": 2.0 ** -25}
 FIVE = [(3.4445, -4.7750, 2.0315)] * 5
 L = 4.3
 
-# one block: a value, a row, a column, odd sizes, whole blocks of 32; tiles: just over it, odd, whole, long, tall
-SMALL = [(1, 1), (1, 7), (7, 1), (16, 16), (33, 20), (31, 128), (128, 100), (97, 97), (128, 128), (128, 1), (64, 127)]
-LARGE = [(129, 1), (1, 129), (130, 64), (64, 200), (193, 193), (256, 256), (333, 777), (1000, 520), (5, 3001), (700, 12), (512, 512)]
+# on chip: a value, a row, a column, odd sizes, whole blocks of 32, the longest; tiles: just over it, odd, whole, long, tall
+SMALL = [(1, 1), (1, 7), (7, 1), (16, 16), (33, 20), (31, 128), (128, 100), (97, 97), (128, 128), (128, 1), (64, 127),
+         (129, 1), (1, 129), (130, 64), (32, 896), (895, 3), (33, 384), (380, 64), (65, 65), (96, 192), (190, 70), (5, 65)]
+LARGE = [(897, 1), (1, 900), (385, 64), (64, 200), (193, 193), (256, 256), (333, 777), (1000, 520), (5, 3001), (700, 12), (512, 512)]
 
 
 def _draw(shape, seed, scale=1.0):
