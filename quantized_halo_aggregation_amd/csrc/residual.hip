@@ -18,18 +18,41 @@
 namespace qha {
 namespace {
 
-// Rows as V values a vector, whatever their type.
+// Rows as V values a vector, whatever their type; loads ahead of their use stay in that type (half the registers).
 template <typename E, int V>
 struct Row {
   typedef E vec __attribute__((ext_vector_type(V), aligned(16)));
   typedef float wide __attribute__((ext_vector_type(V)));
-  static __device__ __forceinline__ wide load(const void* p, int64_t at) {
-    return __builtin_convertvector(*reinterpret_cast<const vec*>(static_cast<const E*>(p) + at), wide);
-  }
+  static __device__ __forceinline__ vec raw(const void* p, int64_t at) { return *reinterpret_cast<const vec*>(static_cast<const E*>(p) + at); }
+  static __device__ __forceinline__ wide value(vec x) { return __builtin_convertvector(x, wide); }
   static __device__ __forceinline__ void store(void* p, int64_t at, wide x) {
     __builtin_nontemporal_store(__builtin_convertvector(x, vec), reinterpret_cast<vec*>(static_cast<E*>(p) + at));
   }
 };
+
+// The sum over W neighbouring lanes, in each of them: pairs, quads, halves and rows of 16 by the data paths of the vector
+// unit, then the two swaps of rows and halves.
+template <int CTRL>
+__device__ __forceinline__ float moved(float x) {
+  return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(x), CTRL, 0xF, 0xF, true));
+}
+template <int W>
+__device__ __forceinline__ float lanes_sum(float x) {
+  static_assert(W >= 8 && W <= 64, "teams");
+  x += moved<0xB1>(x);               // lanes 1 0 3 2
+  x += moved<0x4E>(x);               // 2 3 0 1
+  x += moved<0x141>(x);              // 7 .. 0
+  if constexpr (W >= 16) x += moved<0x140>(x);      // 15 .. 0
+  if constexpr (W >= 32) {
+    const auto p = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    x = __uint_as_float(p[0]) + __uint_as_float(p[1]);
+  }
+  if constexpr (W >= 64) {
+    const auto p = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    x = __uint_as_float(p[0]) + __uint_as_float(p[1]);
+  }
+  return x;
+}
 
 template <int L>
 constexpr int threads_of() { return L < 256 ? 256 : L; }
@@ -43,9 +66,7 @@ struct TeamSum {
   int parity = 0;
   __device__ __forceinline__ void operator()(float (&s)[N]) {
 #pragma unroll
-    for (int o = W >> 1; o > 0; o >>= 1)
-#pragma unroll
-      for (int i = 0; i < N; ++i) s[i] += __shfl_xor(s[i], o, 64);
+    for (int i = 0; i < N; ++i) s[i] = lanes_sum<W>(s[i]);
     if constexpr (L > 64) {
       if ((threadIdx.x & 63) == 0)
 #pragma unroll
@@ -75,12 +96,14 @@ struct Place {
     }
   }
   typedef float wide __attribute__((ext_vector_type(V)));
+  __device__ __forceinline__ wide weight(const float* w, float other, int r) const {
+    wide x = other;
+    if (w && in[r]) x = Row<float, V>::value(Row<float, V>::raw(w, col[r]));
+    return x;
+  }
   __device__ __forceinline__ void weights(const float* w, float other, wide (&to)[R]) const {
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
-      to[r] = other;
-      if (w && in[r]) to[r] = Row<float, V>::load(w, col[r]);
-    }
+    for (int r = 0; r < R; ++r) to[r] = weight(w, other, r);
   }
 };
 
@@ -99,17 +122,19 @@ __global__ __launch_bounds__(threads_of<L>()) void residual_fwd_kernel(ResidualA
   at.weights(a.pre_w, 1.0f, qw);
   at.weights(a.pre_b, 0.0f, qb);
   const int64_t step = static_cast<int64_t>(gridDim.x) * TEAMS;
-  wide next_x[R], next_h[R], next_g[R];
+  typename Row<S, V>::vec next_x[R];
+  typename Row<T, V>::vec next_h[R], next_g[R];
   auto fetch = [&](int64_t row) {
     const int64_t sample = a.positions == 1 ? row : static_cast<uint32_t>(row) / static_cast<uint32_t>(a.positions);
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      next_x[r] = next_h[r] = 0.0f;
-      next_g[r] = 1.0f;
+      next_x[r] = static_cast<S>(0.0f);
+      next_h[r] = static_cast<T>(0.0f);
+      next_g[r] = static_cast<T>(1.0f);
       if (row < a.rows && at.in[r]) {
-        next_x[r] = Row<S, V>::load(a.x, row * a.ldx + at.col[r]);
-        if (a.h) next_h[r] = Row<T, V>::load(a.h, row * a.ldh + at.col[r]);
-        if (a.gate) next_g[r] = Row<T, V>::load(a.gate, sample * a.ldg + at.col[r]);
+        next_x[r] = Row<S, V>::raw(a.x, row * a.ldx + at.col[r]);
+        if (a.h) next_h[r] = Row<T, V>::raw(a.h, row * a.ldh + at.col[r]);
+        if (a.gate) next_g[r] = Row<T, V>::raw(a.gate, sample * a.ldg + at.col[r]);
       }
     }
   };
@@ -142,9 +167,9 @@ __global__ __launch_bounds__(threads_of<L>()) void residual_fwd_kernel(ResidualA
     wide x[R], z[R], g[R];
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      x[r] = next_x[r];
-      z[r] = next_h[r];
-      g[r] = next_g[r];
+      x[r] = Row<S, V>::value(next_x[r]);
+      z[r] = Row<T, V>::value(next_h[r]);
+      g[r] = Row<T, V>::value(next_g[r]);
     }
     fetch(row + step);
     if (a.h) {
@@ -183,10 +208,18 @@ __global__ __launch_bounds__(threads_of<L>()) void residual_bwd_kernel(ResidualA
   TeamSum<L, 2> team_sum{lds};
   const Place<L, R, V> at(a.c);
   const float inv = 1.0f / static_cast<float>(a.c);
-  wide pw[R], pb[R], qw[R], dpw[R], dpb[R], dqw[R], dqb[R], dg[R];
-  at.weights(a.post_w, 1.0f, pw);
-  at.weights(a.post_b, 0.0f, pb);
-  at.weights(a.pre_w, 1.0f, qw);
+  // 16 values a thread and array in blocks of 512 leave no registers for the next row's, and rows of 8192 float32 none for the
+  // weights, which are then read again for every row
+  constexpr bool AHEAD = L < 512 || R * V < 16, KEEP = AHEAD || sizeof(T) < 4;
+  wide kept_pw[R], kept_pb[R], kept_qw[R], dpw[R], dpb[R], dqw[R], dqb[R], dg[R];
+  if (KEEP) {
+    at.weights(a.post_w, 1.0f, kept_pw);
+    at.weights(a.post_b, 0.0f, kept_pb);
+    at.weights(a.pre_w, 1.0f, kept_qw);
+  }
+  const auto pw = [&](int r) { return KEEP ? kept_pw[r] : at.weight(a.post_w, 1.0f, r); };
+  const auto pb = [&](int r) { return KEEP ? kept_pb[r] : at.weight(a.post_b, 0.0f, r); };
+  const auto qw = [&](int r) { return KEEP ? kept_qw[r] : at.weight(a.pre_w, 1.0f, r); };
 #pragma unroll
   for (int r = 0; r < R; ++r) dpw[r] = dpb[r] = dqw[r] = dqb[r] = dg[r] = 0.0f;
   const int64_t teams = static_cast<int64_t>(gridDim.x) * TEAMS;
@@ -207,77 +240,112 @@ __global__ __launch_bounds__(threads_of<L>()) void residual_bwd_kernel(ResidualA
 #pragma unroll
     for (int r = 0; r < R; ++r) q[r] = rstd * (q[r] - level - xhat[r] * along);
   };
-  for (int64_t unit = team; unit < a.units; unit += teams) {
-    int64_t row = unit, end = a.rows, sample = 0;
-    const int64_t step = shared ? 1 : teams;
-    if (shared) {
-      sample = unit / a.chunks;
-      const int64_t first = unit % a.chunks * a.rows_each;
-      row = sample * a.positions + first;
-      end = sample * a.positions + (first + a.rows_each < a.positions ? first + a.rows_each : a.positions);
+  // where a team is: a row of a unit
+  struct Walk {
+    int64_t unit, row, end, sample;
+  };
+  const int64_t step = shared ? 1 : teams;
+  const auto begin = [&](Walk& w) {
+    w.row = w.unit;
+    w.end = w.unit < a.units ? a.rows : 0;
+    w.sample = 0;
+    if (shared && w.unit < a.units) {
+      w.sample = static_cast<uint32_t>(w.unit) / static_cast<uint32_t>(a.chunks);
+      const int64_t first = (w.unit - w.sample * a.chunks) * a.rows_each;
+      w.row = w.sample * a.positions + first;
+      w.end = w.sample * a.positions + (first + a.rows_each < a.positions ? first + a.rows_each : a.positions);
     }
-    for (; row < end; row += step) {
-      wide t[R], y[R], q[R], h[R], g[R];
+  };
+  typename Row<S, V>::vec next_t[R], next_y[R];
+  typename Row<T, V>::vec next_q[R], next_h[R], next_g[R];
+  float2 next_ps = make_float2(0.0f, 1.0f), next_qs = next_ps;
+  const auto fetch = [&](const Walk& w) {
+    const int64_t row = w.row;
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      next_t[r] = next_y[r] = static_cast<S>(0.0f);
+      next_q[r] = next_h[r] = static_cast<T>(0.0f);
+      next_g[r] = static_cast<T>(1.0f);
+      if (!at.in[r]) continue;
+      if (a.pre != QHA_ROW_NONE) {
+        next_q[r] = Row<T, V>::raw(a.du, row * a.lddu + at.col[r]);
+        next_y[r] = Row<S, V>::raw(a.x, row * a.ldx + at.col[r]);
+      }
+      if (a.dy) next_t[r] = Row<S, V>::raw(a.dy, row * a.lddy + at.col[r]);
+      if (a.h) next_h[r] = Row<T, V>::raw(a.h, row * a.ldh + at.col[r]);
+      if (a.gate) next_g[r] = Row<T, V>::raw(a.gate, (shared ? w.sample : row) * a.ldg + at.col[r]);
+    }
+    if (a.post != QHA_ROW_NONE) next_ps = *reinterpret_cast<const float2*>(a.post_stats + 2 * row);
+    if (a.pre != QHA_ROW_NONE) next_qs = *reinterpret_cast<const float2*>(a.pre_stats + 2 * row);
+  };
+  Walk now;
+  now.unit = team;
+  begin(now);
+  if (AHEAD && now.row < now.end) fetch(now);
+  while (now.row < now.end) {
+    const int64_t row = now.row;
+    Walk after = now;
+    after.row += step;
+    if (after.row >= after.end) {
+      after.unit = shared ? after.unit + teams : a.units;
+      begin(after);
+    }
+    if (!AHEAD) fetch(now);
+    wide t[R], y[R], q[R], h[R], g[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      t[r] = Row<S, V>::value(next_t[r]);
+      y[r] = Row<S, V>::value(next_y[r]);
+      q[r] = Row<T, V>::value(next_q[r]);
+      h[r] = Row<T, V>::value(next_h[r]);
+      g[r] = Row<T, V>::value(next_g[r]);
+    }
+    const float2 ps = next_ps, qs = next_qs;
+    if (AHEAD && after.row < after.end) fetch(after);
+    if (a.pre != QHA_ROW_NONE) {
 #pragma unroll
       for (int r = 0; r < R; ++r) {
-        t[r] = y[r] = q[r] = h[r] = 0.0f;
-        g[r] = 1.0f;
-        if (at.in[r]) {
-          if (a.pre != QHA_ROW_NONE) {
-            q[r] = Row<T, V>::load(a.du, row * a.lddu + at.col[r]);
-            y[r] = Row<S, V>::load(a.x, row * a.ldx + at.col[r]);
-          }
-          if (a.dy) t[r] = Row<S, V>::load(a.dy, row * a.lddy + at.col[r]);
-          if (a.h) h[r] = Row<T, V>::load(a.h, row * a.ldh + at.col[r]);
-          if (a.gate) g[r] = Row<T, V>::load(a.gate, (shared ? sample : row) * a.ldg + at.col[r]);
-        }
+        y[r] = at.in[r] ? (y[r] - qs.x) * qs.y : 0.0f;
+        dqw[r] += q[r] * y[r];
+        dqb[r] += q[r];
+        q[r] *= qw(r);
       }
-      float2 ps = make_float2(0.0f, 1.0f);
-      if (a.post != QHA_ROW_NONE) ps = *reinterpret_cast<const float2*>(a.post_stats + 2 * row);
-      if (a.pre != QHA_ROW_NONE) {
-        const float2 qs = *reinterpret_cast<const float2*>(a.pre_stats + 2 * row);
+      through_norm(q, y, a.pre, qs.y);
 #pragma unroll
-        for (int r = 0; r < R; ++r) {
-          y[r] = at.in[r] ? (y[r] - qs.x) * qs.y : 0.0f;
-          dqw[r] += q[r] * y[r];
-          dqb[r] += q[r];
-          q[r] *= qw[r];
-        }
-        through_norm(q, y, a.pre, qs.y);
+      for (int r = 0; r < R; ++r) t[r] += q[r];
+    }
 #pragma unroll
-        for (int r = 0; r < R; ++r) t[r] += q[r];
-      }
-#pragma unroll
-      for (int r = 0; r < R; ++r)
-        if (at.in[r]) Row<S, V>::store(a.dx, row * a.lddx + at.col[r], a.skip * t[r]);
-      if (!a.h) continue;
+    for (int r = 0; r < R; ++r)
+      if (at.in[r]) Row<S, V>::store(a.dx, row * a.lddx + at.col[r], a.skip * t[r]);
+    if (a.h) {
 #pragma unroll
       for (int r = 0; r < R; ++r) {
         t[r] = at.in[r] ? a.branch * t[r] : 0.0f;
         h[r] = at.in[r] ? (h[r] - ps.x) * ps.y : 0.0f;
-        const wide e = t[r] * (h[r] * pw[r] + pb[r]);
+        const wide e = t[r] * (h[r] * pw(r) + pb(r));
         if (shared) dg[r] += e;
         else if (a.dgate && at.in[r]) Row<T, V>::store(a.dgate, row * a.lddg + at.col[r], e);
         t[r] *= g[r];
         dpw[r] += t[r] * h[r];
         dpb[r] += t[r];
-        t[r] *= pw[r];
+        t[r] *= pw(r);
       }
       if (a.post != QHA_ROW_NONE) through_norm(t, h, a.post, ps.y);
 #pragma unroll
       for (int r = 0; r < R; ++r)
         if (at.in[r]) Row<T, V>::store(a.dh, row * a.lddh + at.col[r], t[r]);
     }
-    if (shared) {
+    if (shared && after.unit != now.unit) {
 #pragma unroll
       for (int r = 0; r < R; ++r) {
         if (a.dgate && at.in[r]) {
-          if (a.chunks == 1) Row<T, V>::store(a.dgate, sample * a.lddg + at.col[r], dg[r]);
-          else Row<float, V>::store(a.gate_part, unit * a.c + at.col[r], dg[r]);
+          if (a.chunks == 1) Row<T, V>::store(a.dgate, now.sample * a.lddg + at.col[r], dg[r]);
+          else Row<float, V>::store(a.gate_part, now.unit * a.c + at.col[r], dg[r]);
         }
         dg[r] = 0.0f;
       }
     }
+    now = after;
   }
   // the block's partials: teams of a wavefront by exchanges, wavefronts through LDS
   float* out = a.vec_part + static_cast<int64_t>(blockIdx.x) * 4 * a.c;
@@ -339,18 +407,22 @@ __global__ __launch_bounds__(256) void residual_sums_kernel(ResidualArgs a, int3
   else static_cast<T*>(a.dgate)[(set - 4) * a.lddg + col] = static_cast<T>(static_cast<float>(s));
 }
 
-// lanes of a team and blocks of a launch, by the vectors of a row
+// lanes of a team, by the vectors of a row
 int team_of(int nvec) {
   return nvec <= 8 ? 8 : nvec <= 16 ? 16 : nvec <= 32 ? 32 : nvec <= 128 ? 64 : nvec <= 512 ? 256 : 512;
 }
-int64_t most_blocks(int lanes) { return lanes == 512 ? 256 : lanes == 256 ? 512 : 1024; }
+// Blocks of a launch: two a compute unit backward (its registers leave room for two or three: 300k x 256 float32 with 1024 blocks
+// 400 us, with 512 322), four forward, more of the larger ones (300k x 128 float32 with 2048 blocks, which seven a unit
+// do not divide, 122 us, with 1024 108; 4000 x 8192 float32 84 and 76).
+int64_t most_blocks(int lanes) { return lanes == 512 ? 256 : 512; }
+int64_t most_blocks_fwd(int lanes) { return lanes < 256 ? 1024 : 2048; }
 
 template <typename S, typename T, int L, int R>
 void run(const ResidualArgs& a, bool backward, hipStream_t s) {
   constexpr int TEAMS = threads_of<L>() / L;
   if (!backward) {
     const int64_t want = (a.rows + TEAMS - 1) / TEAMS;
-    residual_fwd_kernel<S, T, L, R><<<static_cast<uint32_t>(want < 2048 ? want : 2048), threads_of<L>(), 0, s>>>(a);
+    residual_fwd_kernel<S, T, L, R><<<static_cast<uint32_t>(want < most_blocks_fwd(L) ? want : most_blocks_fwd(L)), threads_of<L>(), 0, s>>>(a);
     return;
   }
   residual_bwd_kernel<S, T, L, R><<<static_cast<uint32_t>(a.blocks), threads_of<L>(), 0, s>>>(a);
