@@ -498,7 +498,7 @@ int qha_residual_norm_fwd(int64_t n_rows, int64_t positions, int32_t c, int32_t 
  * (device float32[c], overwritten; zeros when there are no rows) are nullable.  dx may be dy or y, dh may be du or h
  * (with the same leading dimension); otherwise outputs must not overlap inputs or each other.  workspace: device,
  * 16-byte aligned, qha_residual_norm_workspace bytes (needed where a vector's gradient or that of a shared gate is asked
- * for).  Partial sums are float32 in a team of threads and float64 over teams, in a fixed order.
+ * for).  Partial sums are float32 in a block and float64 over blocks, in a fixed order.
  * Other arguments, limits, determinism and errors as there; WORKSPACE. */
 int qha_residual_norm_bwd(int64_t n_rows, int64_t positions, int32_t c, int32_t stream_type, int32_t type,
                           int32_t post, int32_t pre, const void* dy, int64_t lddy, const void* du, int64_t lddu,

@@ -575,8 +575,8 @@ def _matrix(t, name, dtype, rows, cols):
     """(pointer, leading dimension) of a rows x cols matrix of dtype whose rows may be strided."""
     if type(t) is torch.Tensor and t.dtype is dtype and t.is_cuda and t.shape == (rows, cols):
         ld, one = t.stride()
-        if one == 1 and rows > 1:
-            return t.data_ptr(), ld
+        if one == 1 and rows > 0:
+            return t.data_ptr(), ld if rows > 1 else cols
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch tensor")
     if t.dtype != dtype:
@@ -609,6 +609,35 @@ def _on_current(*tensors):
     for t in tensors:
         if t is not None and t.get_device() != current:
             raise ValueError(f"a tensor lives on {t.device}, the current device is cuda:{current}")
+
+
+def _matrix_here(current, t, name, dtype, rows, cols):
+    """_matrix on the current device, (None, 0) for None."""
+    if t is None:
+        return None, 0
+    if type(t) is torch.Tensor and t.dtype is dtype and t.get_device() == current and t.shape == (rows, cols):
+        ld, one = t.stride()
+        if one == 1 and rows > 0:
+            return t.data_ptr(), ld if rows > 1 else cols
+    found = _matrix(t, name, dtype, rows, cols)
+    _on_current(t)
+    return found
+
+
+def _vector_here(current, t, name, n):
+    """A contiguous float32 tensor of n elements on the current device, or None."""
+    if t is None:
+        return None
+    if type(t) is torch.Tensor and t.dtype is torch.float32 and t.get_device() == current and t.numel() == n \
+            and t.is_contiguous():
+        return t.data_ptr()
+    found = _flat(t, name, n, torch.float32)
+    _on_current(t)
+    return found
+
+
+def _stream_here(current, stream):
+    return torch._C._cuda_getCurrentRawStream(current) if stream is None else int(stream)
 
 
 def gated_project_workspace(dtype, m: int, n: int, k: int) -> int:
@@ -699,10 +728,6 @@ def residual_norm_workspace(rows: int, c: int, positions: int = 1) -> int:
     return int(_residual_norm_ws(rows, positions, c))
 
 
-def _stats(t, name, rows):
-    return None if t is None else _flat(t, name, 2 * rows, torch.float32)
-
-
 def residual_norm_fwd(x, h, y, u, post: int = ROW_RMS, pre: int = ROW_RMS, post_weight=None, post_bias=None,
                       pre_weight=None, pre_bias=None, gate=None, positions: int = 1, skip: float = 1.0,
                       branch: float = 1.0, eps: float = 1e-6, post_stats=None, pre_stats=None, stream=None):
@@ -712,19 +737,23 @@ def residual_norm_fwd(x, h, y, u, post: int = ROW_RMS, pre: int = ROW_RMS, post_
     positions, c] and u have one type.  post_stats and pre_stats (float32 [rows, 2], if given) receive what the
     backward needs.  With pre=ROW_NONE u is None; with h=None (post=ROW_NONE, y=None) u is pre(x)."""
     rows, c = x.shape
-    t = x.dtype if h is None and u is None else (u if h is None else h).dtype
+    s = x.dtype
+    t = s if h is None and u is None else (u if h is None else h).dtype
     n = _samples(rows, positions)
-    px, ldx = _matrix(x, "x", x.dtype, rows, c)
-    ph, ldh = (None, 0) if h is None else _matrix(h, "h", t, rows, c)
-    py, ldy = (None, 0) if y is None else _matrix(y, "y", x.dtype, rows, c)
-    pu, ldu = (None, 0) if u is None else _matrix(u, "u", t, rows, c)
-    pg, ldg = (None, 0) if gate is None else _matrix(gate, "gate", t, n, c)
-    _on_current(x, h, y, u, gate, post_weight, post_bias, pre_weight, pre_bias, post_stats, pre_stats)
-    _check(_residual_norm_fwd(rows, positions, c, _type(x.dtype, "x"), _type(t, "h"), post, pre, px, ldx, ph, ldh, pg,
-                              ldg, _vector(post_weight, "post_weight", c), _vector(post_bias, "post_bias", c),
-                              _vector(pre_weight, "pre_weight", c), _vector(pre_bias, "pre_bias", c), skip, branch, eps,
-                              py, ldy, pu, ldu, _stats(post_stats, "post_stats", rows),
-                              _stats(pre_stats, "pre_stats", rows), _stream(stream)), "qha_residual_norm_fwd")
+    here = torch.cuda.current_device()
+    px, ldx = _matrix_here(here, x, "x", s, rows, c)
+    ph, ldh = _matrix_here(here, h, "h", t, rows, c)
+    py, ldy = _matrix_here(here, y, "y", s, rows, c)
+    pu, ldu = _matrix_here(here, u, "u", t, rows, c)
+    pg, ldg = _matrix_here(here, gate, "gate", t, n, c)
+    _check(_residual_norm_fwd(rows, positions, c, _type(s, "x"), _type(t, "h"), post, pre, px, ldx, ph, ldh, pg, ldg,
+                              _vector_here(here, post_weight, "post_weight", c),
+                              _vector_here(here, post_bias, "post_bias", c),
+                              _vector_here(here, pre_weight, "pre_weight", c),
+                              _vector_here(here, pre_bias, "pre_bias", c), skip, branch, eps, py, ldy, pu, ldu,
+                              _vector_here(here, post_stats, "post_stats", 2 * rows),
+                              _vector_here(here, pre_stats, "pre_stats", 2 * rows), _stream_here(here, stream)),
+           "qha_residual_norm_fwd")
 
 
 def residual_norm_bwd(dy, du, y, h, dx, dh, post: int = ROW_RMS, pre: int = ROW_RMS, post_stats=None, pre_stats=None,
@@ -738,24 +767,28 @@ def residual_norm_bwd(dy, du, y, h, dx, dh, post: int = ROW_RMS, pre: int = ROW_
     s = dx.dtype
     t = s if h is None and du is None else (du if h is None else h).dtype
     n = _samples(rows, positions)
-    pdy, lddy = (None, 0) if dy is None else _matrix(dy, "dy", s, rows, c)
-    pdu, lddu = (None, 0) if du is None else _matrix(du, "du", t, rows, c)
-    py, ldy = (None, 0) if y is None else _matrix(y, "y", s, rows, c)
-    ph, ldh = (None, 0) if h is None else _matrix(h, "h", t, rows, c)
-    pdx, lddx = _matrix(dx, "dx", s, rows, c)
-    pdh, lddh = (None, 0) if dh is None else _matrix(dh, "dh", t, rows, c)
-    pg, ldg = (None, 0) if gate is None else _matrix(gate, "gate", t, n, c)
-    pdg, lddg = (None, 0) if dgate is None else _matrix(dgate, "dgate", t, n, c)
+    here = torch.cuda.current_device()
+    pdy, lddy = _matrix_here(here, dy, "dy", s, rows, c)
+    pdu, lddu = _matrix_here(here, du, "du", t, rows, c)
+    py, ldy = _matrix_here(here, y, "y", s, rows, c)
+    ph, ldh = _matrix_here(here, h, "h", t, rows, c)
+    pdx, lddx = _matrix_here(here, dx, "dx", s, rows, c)
+    pdh, lddh = _matrix_here(here, dh, "dh", t, rows, c)
+    pg, ldg = _matrix_here(here, gate, "gate", t, n, c)
+    pdg, lddg = _matrix_here(here, dgate, "dgate", t, n, c)
     ws, ws_bytes = _space(workspace)
-    _on_current(dy, du, y, h, dx, dh, post_stats, pre_stats, post_weight, post_bias, pre_weight, gate, dgate, dpost_weight,
-                dpost_bias, dpre_weight, dpre_bias, workspace)
+    if workspace is not None and workspace.get_device() != here:
+        _on_current(workspace)
     _check(_residual_norm_bwd(rows, positions, c, _type(s, "dx"), _type(t, "h"), post, pre, pdy, lddy, pdu, lddu, py, ldy,
-                              ph, ldh, pg, ldg, _vector(post_weight, "post_weight", c),
-                              _vector(post_bias, "post_bias", c), _vector(pre_weight, "pre_weight", c), skip, branch,
-                              _stats(post_stats, "post_stats", rows), _stats(pre_stats, "pre_stats", rows), pdx, lddx,
-                              pdh, lddh, pdg, lddg, _vector(dpost_weight, "dpost_weight", c),
-                              _vector(dpost_bias, "dpost_bias", c), _vector(dpre_weight, "dpre_weight", c),
-                              _vector(dpre_bias, "dpre_bias", c), ws, ws_bytes, _stream(stream)),
+                              ph, ldh, pg, ldg, _vector_here(here, post_weight, "post_weight", c),
+                              _vector_here(here, post_bias, "post_bias", c),
+                              _vector_here(here, pre_weight, "pre_weight", c), skip, branch,
+                              _vector_here(here, post_stats, "post_stats", 2 * rows),
+                              _vector_here(here, pre_stats, "pre_stats", 2 * rows), pdx, lddx, pdh, lddh, pdg, lddg,
+                              _vector_here(here, dpost_weight, "dpost_weight", c),
+                              _vector_here(here, dpost_bias, "dpost_bias", c),
+                              _vector_here(here, dpre_weight, "dpre_weight", c),
+                              _vector_here(here, dpre_bias, "dpre_bias", c), ws, ws_bytes, _stream_here(here, stream)),
            "qha_residual_norm_bwd")
 
 

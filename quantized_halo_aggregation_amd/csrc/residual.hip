@@ -10,8 +10,8 @@
 // 512) that keeps it in registers, R vectors a thread (16 bytes of the branch's type), so that the statistics of both
 // norms and both outputs come from one read; a thread's places, its weights and its share of the weights' gradients stay with
 // it over many rows.  Sums over a row are float32 (at most 8192 values, means before squares).  Gradients of weights are
-// float32 in a team, one partial a block; those of a shared gate one partial for each piece of a sample's rows; a second launch
-// adds partials in float64 in a fixed order.
+// float32 in a block, which leaves one partial; those of a shared gate one partial for each piece of a sample's rows; a second launch
+// adds partials in float64 in a fixed order (a block by itself needs none).
 #include "act_common.hpp"
 #include "qha_internal.hpp"
 
@@ -348,12 +348,15 @@ __global__ __launch_bounds__(threads_of<L>()) void residual_bwd_kernel(ResidualA
     now = after;
   }
   // the block's partials: teams of a wavefront by exchanges, wavefronts through LDS
-  float* out = a.vec_part + static_cast<int64_t>(blockIdx.x) * 4 * a.c;
+  const bool alone = gridDim.x == 1;
   auto leave = [&](wide (&v)[R], int which) {
+    float* out = alone ? a.dvec[which] : a.vec_part + (static_cast<int64_t>(blockIdx.x) * 4 + which) * a.c;
     if constexpr (L >= 256) {
 #pragma unroll
       for (int r = 0; r < R; ++r)
-        if (at.in[r]) *reinterpret_cast<typename Row<float, V>::vec*>(out + which * a.c + at.col[r]) = v[r];
+        if (at.in[r])
+#pragma unroll
+          for (int i = 0; i < V; ++i) out[at.col[r] + i] = v[r][i];
     } else {
 #pragma unroll
       for (int o = L; o < 64; o <<= 1)
@@ -372,7 +375,7 @@ __global__ __launch_bounds__(threads_of<L>()) void residual_bwd_kernel(ResidualA
         float s = 0.0f;
 #pragma unroll
         for (int k = 0; k < NT / 64; ++k) s += buf[k][i];
-        out[which * a.c + i] = s;
+        out[i] = s;
       }
     }
   };
@@ -380,6 +383,17 @@ __global__ __launch_bounds__(threads_of<L>()) void residual_bwd_kernel(ResidualA
   if (a.dvec[1]) leave(dpb, 1);
   if (a.dvec[2]) leave(dqw, 2);
   if (a.dvec[3]) leave(dqb, 3);
+  if (!alone || !shared || !a.dgate || a.chunks == 1) return;
+  // a block by itself adds the pieces of a sample's gate, too
+  __syncthreads();
+  for (int64_t i = threadIdx.x; i < a.rows / a.positions * a.c; i += NT) {
+    const int64_t sample = i / a.c, col = i % a.c;
+    const float* part = a.gate_part + sample * a.chunks * a.c + col;
+    double s = 0.0;
+#pragma unroll 8
+    for (int64_t k = 0; k < a.chunks; ++k) s += static_cast<double>(part[k * a.c]);
+    static_cast<T*>(a.dgate)[sample * a.lddg + col] = static_cast<T>(static_cast<float>(s));
+  }
 }
 
 // Adds partials in float64: blocks below 4 * col_blocks those of the weights, 32 columns each, the others those of
@@ -441,7 +455,7 @@ void run(const ResidualArgs& a, bool backward, hipStream_t s) {
   else if (nvec <= 512) run<S, T, 256, 2>(a, backward, s);
   else if (nvec <= 1024) run<S, T, 512, 2>(a, backward, s);
   else if constexpr (sizeof(T) == 4) run<S, T, 512, 4>(a, backward, s);      // at most 8192 values
-  if (!backward) return;
+  if (!backward || a.blocks == 1) return;
   const bool gates = a.dgate && a.shared_gate && a.chunks > 1;
   const bool vectors = a.dvec[0] || a.dvec[1] || a.dvec[2] || a.dvec[3];
   if (!gates && !vectors) return;
@@ -456,14 +470,16 @@ void run(const ResidualArgs& a, bool backward, hipStream_t s) {
 void residual_plan(ResidualArgs& a) {
   const int lanes = team_of(a.c / (a.type == QHA_F32 ? 4 : 8));
   const int teams = lanes < 256 ? 256 / lanes : 1;
-  const int64_t samples = a.rows / a.positions, most = most_blocks(lanes);
+  // one block alone, without a second launch, where its teams take at most three rows each (97 rows of 64 in three samples, ten each,
+  // 17.6 us, with two launches 15; 4 rows of 64 12 and 15)
+  const int64_t samples = a.rows / a.positions, most = a.rows <= 3 * teams ? 1 : most_blocks(lanes);
   a.chunks = 1;
   a.rows_each = a.positions;
   a.units = a.rows;
   if (a.shared_gate) {
-    // whole samples where they fill the launch; otherwise pieces, one for each team
-    const int64_t pieces = (most * teams + samples - 1) / samples;
-    a.rows_each = pieces >= a.positions ? 1 : (a.positions + pieces - 1) / pieces;
+    // whole samples where they fill the launch; otherwise pieces, at most one for each team
+    const int64_t pieces = samples < most * teams ? most * teams / samples : 1;
+    a.rows_each = (a.positions + pieces - 1) / pieces;
     a.chunks = (a.positions + a.rows_each - 1) / a.rows_each;
     a.units = samples * a.chunks;
   }
