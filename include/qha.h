@@ -516,17 +516,19 @@ size_t qha_residual_norm_workspace(int64_t n_rows, int64_t positions, int32_t c)
  * which takes every singular value s of X to a s + b s^3 + c s^5 and keeps the singular vectors.  out = X.
  * coefficients: host, [steps][3], a, b and c of each step; 1 <= steps <= 16.  They must keep the singular values of X, which
  * begin in [0, 1], small: INVALID_ARG if some s in [0, 1] can pass 3.8 in size (X's bound, A's its square) or a + b s^2 + c s^4
- * 60 on the way, by the largest values that each step's polynomials take.  3.4445, -4.7750, 2.0315 in each of five steps take
- * [0.002, 1] to about [0.7, 1.2].
+ * 60 on the way, by the largest values that each step's polynomials take and what rounding adds to them (2e-6 of the sizes of
+ * a step's terms: steps that grow it without bound, from a fixed point that is steep, are refused).  3.4445, -4.7750, 2.0315 in
+ * each of five steps take [0.002, 1] to about [0.7, 1.2].
  * matrices: host array, read during the call.  x has elements of `type`, out of out_type, at least one element aligned, with
  * leading dimensions of at least cols; any rows and cols up to 65536 (UNSUPPORTED above).  out may be x (with the same
  * leading dimension and type); otherwise outputs must not overlap inputs or each other.  Accesses are of four elements where cols and the
  * leading dimension are multiples of 4 and the pointer is aligned to four elements.  Matrices without elements are skipped.
  * Products have float32's precision (two f16 parts of values scaled by powers of two, three products, float32
  * sums); the norm is summed in float64.  A matrix with a value that is not finite gives NaN throughout; a zero matrix gives zeros.
- * Results are deterministic and those of a matrix do not depend on the others in its call.
- * workspace: device, 16-byte aligned, qha_newton_schulz_workspace bytes (0 where no matrix has more than 128 rows or columns:
- * those stay on chip); calls that may overlap need one each.
+ * Results are deterministic.  Those of a matrix do not depend on the other matrices' values, and on their sizes only in the
+ * last bits (the list as a whole decides how the sums of those that do not stay on chip are cut).
+ * workspace: device, 16-byte aligned, qha_newton_schulz_workspace bytes (0 where every matrix stays on chip: those of up to
+ * 32 x 896, 64 x 384, 96 x 192 or 128 x 128, either way round); calls that may overlap need one each.
  * Errors: INVALID_ARG, UNSUPPORTED, WORKSPACE, HIP (also where the host has no memory for the list). */
 typedef struct qha_ns_matrix {
   int64_t rows, cols;

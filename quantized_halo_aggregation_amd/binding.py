@@ -919,6 +919,13 @@ def _ns_coefficients(coefficients, steps):
     return np.ascontiguousarray(k)
 
 
+def _apart(pointers, what):
+    """Refuses a list that names one tensor twice (tensors without elements have no address)."""
+    some = [p for p in pointers if p]
+    if len(set(some)) < len(some):
+        raise ValueError(f"two of the {what} are the same memory")
+
+
 def newton_schulz_workspace(shapes, steps: int = 5) -> int:
     sizes = np.array([tuple(s) for s in shapes], dtype=np.int64).reshape(-1, 2)
     return int(_newton_schulz_ws(sizes.ctypes.data, len(sizes), steps))
@@ -926,7 +933,8 @@ def newton_schulz_workspace(shapes, steps: int = 5) -> int:
 
 def newton_schulz(xs, outs, steps: int = 5, coefficients=NS_COEFFICIENTS, eps: float = 1e-7, workspace=None, stream=None):
     """outs[i] = the Newton-Schulz iterate of xs[i] / |xs[i]| after `steps` steps of `coefficients` (a, b, c, or
-    one such triple for each step): lists of matrices, each list of one type, rows may be strided."""
+    one such triple for each step): lists of matrices, each list of one type, rows may be strided.  outs[i] may be xs[i];
+    otherwise results must not overlap each other or the xs."""
     n = len(xs)
     if len(outs) != n:
         raise ValueError(f"{len(outs)} results for {n} matrices")
@@ -942,6 +950,7 @@ def newton_schulz(xs, outs, steps: int = 5, coefficients=NS_COEFFICIENTS, eps: f
         table[i] = rows, cols, *_matrix(x, "a matrix", t, rows, cols), *_matrix(out, "a result", o, rows, cols)
     ws, ws_bytes = _space(workspace)
     _on_current(*xs, *outs, workspace)
+    _apart([o.data_ptr() for o in outs], "results")
     _check(_newton_schulz(table.ctypes.data, n, _type(t, "xs"), _type(o, "outs"), steps, k.ctypes.data, eps, ws, ws_bytes,
                           _stream(stream)), "qha_newton_schulz")
 
@@ -1010,6 +1019,7 @@ class Muon:
                 table[i, column] = _flat(t, f"{name}[{i}]", dtype=self.copies[0].dtype if column == 4 else torch.float32)
         if len({t.device for t in tensors}) > 1:
             raise ValueError("parameters, momenta and copies must live on one GPU")
+        _apart(seen, "parameters, momenta and copies")
         need = newton_schulz_workspace(self.shapes, self._steps)
         if need and (self._ws is None or self._ws.device != self.params[0].device):
             self._ws = torch.empty(need, dtype=torch.uint8, device=self.params[0].device)

@@ -154,7 +154,8 @@ double largest_of(double a, double b, double c, double top) {
   return most;
 }
 
-// The polynomials must keep X, A and B within the scaled parts' range.
+// The polynomials must keep X, A and B within the scaled parts' range, also where rounding takes a singular value past what the
+// exact ones reach: a step's is below 2e-6 (16 units of float32) of its terms, and the next steps may grow it.
 int check_steps(int32_t steps, const double* coefficients, double eps) {
   if (steps < 1 || steps > qha::kNsSteps) return fail(QHA_ERR_INVALID_ARG, "steps must lie in 1 .. %d, got %d", qha::kNsSteps, steps);
   if (!coefficients) return fail(QHA_ERR_INVALID_ARG, "coefficients is NULL");
@@ -167,8 +168,9 @@ int check_steps(int32_t steps, const double* coefficients, double eps) {
     double inner = std::max(std::fabs(a), std::fabs(a + t * (b + c * t)));       // |a + b t + c t^2| over [0, top^2]
     if (c != 0.0 && -b / (2.0 * c) > 0.0 && -b / (2.0 * c) < t) inner = std::max(inner, std::fabs(a - b * b / (4.0 * c)));
     if (!(inner <= 60.0)) return fail(QHA_ERR_INVALID_ARG, "step %d: a + b s^2 + c s^4 passes 60", i);
-    top = largest_of(a, b, c, top);
-    if (!(top <= 3.8)) return fail(QHA_ERR_INVALID_ARG, "step %d: singular values pass 3.8", i);
+    const double most = largest_of(a, b, c, top);
+    if (!(most <= 3.8)) return fail(QHA_ERR_INVALID_ARG, "step %d: singular values pass 3.8", i);
+    top = most + 2e-6 * top * (std::fabs(a) + t * (std::fabs(b) + t * std::fabs(c)));
   }
   return QHA_OK;
 }

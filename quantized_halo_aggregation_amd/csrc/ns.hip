@@ -921,7 +921,7 @@ __device__ __forceinline__ void direct_load(const uint16_t* p, int lane, int64_t
 // The same products for a batch whose tiles would leave most of the chip idle, where a launch's time is that of its chain of loads
 // and barriers: a block owns 32 x 32 values, and its wavefronts share out the reduction by 32 steps, four of which they load at
 // once straight from memory (X's transpose is kept for the last product).  Their sums meet in LDS and are added in order.
-// FUSED (X of at most 256 rows): the last product's block forms its 32 rows of B itself, from A, which saves a launch.
+// FUSED (X of at most 128 rows): the last product's block forms its 32 rows of B itself, from A, which saves a launch.
 template <int KIND, bool FUSED>
 __global__ __launch_bounds__(kDirectWaves * 64) void ns_direct_kernel(const NsTable* table, NsFirst first, NsCoef sq, NsCoef k, int32_t from, uint32_t total) {
   constexpr bool SYM = KIND == NS_GRAM || KIND == NS_SQUARE;
@@ -954,12 +954,12 @@ __global__ __launch_bounds__(kDirectWaves * 64) void ns_direct_kernel(const NsTa
   };
   const uint16_t* p = rows_of(KIND == NS_GRAM ? x : KIND == NS_SQUARE || FUSED ? w.a() : w.b(), mt);
   const uint16_t* q = rows_of(KIND == NS_GRAM ? x : KIND == NS_SQUARE ? w.a() : w.xt(from), nt);
+  static_assert(W * 64 == 256, "four of a block's values a thread");
   // four neighbours of a row a thread; A's for the square product are on their way early
-  const int r = static_cast<int>(threadIdx.x) & 31, c = (static_cast<int>(threadIdx.x >> 5) & 7) * 4;
+  const int r = static_cast<int>(threadIdx.x) & 31, c = static_cast<int>(threadIdx.x >> 5) * 4;
   const int64_t row = mt * 32 + r, col = nt * 32 + c, cols = SYM ? m_pad : a.n_pad;
-  const bool mine = threadIdx.x < 256;
   f32x4 own = {0.0f, 0.0f, 0.0f, 0.0f};
-  if (KIND == NS_SQUARE && mine) own = get4(w.a(), block_at(row, col, cols));
+  if (KIND == NS_SQUARE) own = get4(w.a(), block_at(row, col, cols));
 
   f32x16 acc[3];
 #pragma unroll
@@ -1033,18 +1033,15 @@ __global__ __launch_bounds__(kDirectWaves * 64) void ns_direct_kernel(const NsTa
   }
   __syncthreads();
   f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
-  if (mine) {
 #pragma unroll
-    for (int n = 0; n < W; ++n) v += *reinterpret_cast<const f32x4*>(&part[n][r][c]);
-    v *= k.product;
-    if constexpr (KIND == NS_SQUARE) v = square_terms(k, v, own, row, col);
-    if constexpr (KIND != NS_LAST) put4(KIND == NS_GRAM ? w.a() : KIND == NS_SQUARE ? w.b() : w.x(from ^ 1), block_at(row, col, cols), v);
-  }
+  for (int n = 0; n < W; ++n) v += *reinterpret_cast<const f32x4*>(&part[n][r][c]);
+  v *= k.product;
+  if constexpr (KIND == NS_SQUARE) v = square_terms(k, v, own, row, col);
+  if constexpr (KIND != NS_LAST) put4(KIND == NS_GRAM ? w.a() : KIND == NS_SQUARE ? w.b() : w.x(from ^ 1), block_at(row, col, cols), v);
   // the mirror of a symmetric result, the transpose of X, or the rows of the result
   if (SYM && mt == nt) return;
-  if (mine) *reinterpret_cast<f32x4*>(&part[0][r][c]) = v;         // each thread read its own four values of it alone
+  *reinterpret_cast<f32x4*>(&part[0][r][c]) = v;         // each thread read its own four values of it alone
   __syncthreads();
-  if (!mine) return;
   if constexpr (KIND == NS_LAST) {
     finish_block<256>(t, a, &part[0][0][0], mt * 32, nt * 32, threadIdx.x);
   } else {

@@ -56,32 +56,33 @@ def _run(xs, steps, out_dtype="float32", eps=1e-7, outs=None):
 
 
 def _one_step(got, x, abc, eps):
+    """Every value of one step's result `got` for x: float64 tensors on the GPU."""
     a, b, c = abc
-    x = x / (np.sqrt((x * x).sum()) + eps)
-    x = x if x.shape[0] <= x.shape[1] else x.T
+    x = x / ((x * x).sum().sqrt() + eps)
+    x = x if x.shape[0] <= x.shape[1] else x.T.contiguous()
     got = got if got.shape == x.shape else got.T
     m, n = x.shape
     g = lambda k: (3 * k + 20) * U          # the additions, and the dropped product of second parts
     tiny = 2.0 ** -37                       # half a step of subnormal second parts, after scaling by 4096
-    ax = np.abs(x)
+    ax = x.abs()
     # a stored value is off by 4 u of itself and by `tiny` where it is small: x enters a x, the gram product (twice)
     # and B x with that error
     dx = 4 * U * ax + tiny
     s, ms = x @ x.T, ax @ ax.T
-    es = 2 * dx @ (ax + dx).T + g(n) * ms + 4 * U * np.abs(s) + tiny
-    es = np.maximum(es, es.T)
-    w, ma = b * s + c * s @ s, np.abs(s) + es
+    es = 2 * dx @ (ax + dx).T + g(n) * ms + 4 * U * s.abs() + tiny
+    es = es.maximum(es.T)
+    w, ma = b * s + c * s @ s, s.abs() + es
     mw = abs(b) * ma + abs(c) * ma @ ma
     ew = abs(b) * es + abs(c) * (2 * es @ ma + g(m) * ma @ ma) + 8 * U * mw + 4 * tiny
     ref = a * x + w @ x
-    bound = abs(a) * dx + ew @ (ax + dx) + mw @ dx + g(m) * mw @ ax + 8 * U * (abs(a) * ax + np.abs(ref)) + tiny
-    err = np.abs(got - ref)
-    assert (err <= bound).all(), float((err / bound).max())
+    bound = abs(a) * dx + ew @ (ax + dx) + mw @ dx + g(m) * mw @ ax + 8 * U * (abs(a) * ax + ref.abs()) + tiny
+    err = (got - ref).abs()
+    assert bool((err <= bound).all()), float((err / bound).max())
     # magnitudes of the whole step, with which errors that do not cancel would grow; x and the result are also off by up to
     # `tiny` each, whatever their size, which would be any share of a value near zero: that much is not counted
     size = abs(a) * ax + mw @ ax
-    err = np.maximum(err - (abs(a) + 1) * tiny, 0)
-    assert np.sqrt(((err / size) ** 2).mean()) <= 16 * U * (1 + (b != 0) + 3 * (c != 0))
+    err = (err - (abs(a) + 1) * tiny).clamp(min=0)
+    assert float(((err / size) ** 2).mean()) ** 0.5 <= 16 * U * (1 + (b != 0) + 3 * (c != 0))
 
 
 def _five_steps(got, x, dtype, eps=1e-7, steps=FIVE):
@@ -107,7 +108,7 @@ def test_one_step_value_by_value(shape, abc):
     H.note(f"newton-schulz one step {shape} {abc}")
     x = _draw(shape, 1, 1e-3)
     out, = _run([_t(x)], [abc])
-    _one_step(_np(out), x.astype(np.float64), abc, 1e-7)
+    _one_step(out.double(), _t(x).double(), abc, 1e-7)
 
 
 @pytest.mark.parametrize("types", [("float32", "float32"), ("bfloat16", "float32"), ("float16", "float16"),
@@ -137,14 +138,94 @@ def test_many_tiles():
     assert bool((wide == tall.T).all())
 
 
+def _products(got, x, dtype="float32", eps=1e-7):
+    """_five_steps for large matrices: the same bound, with the steps as products in float64 on the GPU in the
+    place of singular values (their sum of squares is X's)."""
+    x = x.double()
+    got = got.double() if x.shape[0] <= x.shape[1] else got.double().T
+    x = x if x.shape[0] <= x.shape[1] else x.T.contiguous()
+    x = x / ((x * x).sum().sqrt() + eps)
+    bound = 0.0
+    for k, (a, b, c) in enumerate(FIVE):
+        bound += L ** (4 - k) * 20 * np.sqrt(3 * x.shape[1] / 16 + 16) * U * float((x * x).sum()) ** 0.5
+        s = x @ x.T
+        x = a * x + (b * s + c * s @ s) @ x
+    off = (got - x).abs()
+    assert bool(got.isfinite().all())
+    assert float(((off - HALF[dtype] * got.abs() * (1 + HALF[dtype]) - TINY[dtype]).clamp(min=0) ** 2).sum()) ** 0.5 <= bound
+    if dtype == "float32":
+        assert float((off * off).sum()) <= 2.0 ** -24 * float((x * x).sum())
+
+
+# the rule on tiles takes sides of 128 (one of 2501 x 3001), 192 and 256 (one of 4001 x 4090) and 256 (24 of 1000 x 4070)
+LARGER = [[(2501, 3001)], [(3001, 2501)], [(4001, 4090)], [(4090, 4001)], [(1000, 4070), (4070, 1000)] * 12, [(1024, 4096)] * 24]
+
+
+def _on_gpu(shapes, seed, dtype="float32", scale=1.0):
+    import torch
+    gen = torch.Generator(device="cuda").manual_seed(seed)
+    return [(torch.randn(s, generator=gen, device="cuda") * scale).to(getattr(torch, dtype)) for s in shapes]
+
+
+@pytest.mark.parametrize("shapes", LARGER, ids=lambda s: f"{len(s)}of" + "x".join(map(str, s[0])))
+def test_larger_tiles(shapes):
+    """One step value by value, and five."""
+    H.require_gpu()
+    H.note(f"newton-schulz larger tiles {len(shapes)} of {shapes[0]}")
+    xs = _on_gpu(shapes, 5)
+    outs = _run(xs, FIVE[:1])
+    for i in sorted({0, len(xs) // 2 + 1 if len(xs) > 1 else 0, len(xs) - 1}):
+        _one_step(outs[i].double(), xs[i].double(), FIVE[0], 1e-7)
+    outs = _run(xs, FIVE, "float16")
+    for i in sorted({0, len(xs) - 1}):
+        _products(outs[i], xs[i], "float16")
+
+
+@pytest.mark.parametrize("shapes", [[(96, 2848)] * 12, [(100, 1000), (1000, 90)], [(130, 150), (40, 2000), (300, 20)],
+                                    [(33 + i, 901 - i) for i in range(45)]],
+                         ids=["many-96", "two-of-128-rows", "mixed", "more-than-a-batch"])
+def test_blocks_straight_from_memory(shapes):
+    """B's rows formed by the last product's blocks or by a launch of its own, and lists of more than one batch."""
+    H.require_gpu()
+    H.note(f"newton-schulz from memory {len(shapes)} of {shapes[0]}")
+    xs = _on_gpu(shapes, 6)
+    one, five = _run(xs, FIVE[:1]), _run(xs, FIVE)
+    for x, o, f in zip(xs, one, five):
+        _one_step(o.double(), x.double(), FIVE[0], 1e-7)
+        _products(f, x)
+
+
+def test_rows_far_apart():
+    """Offsets past 2^31 elements, of the source and of the result: on chip (800 x 30) and tiled (1100 x 300)."""
+    import torch
+    H.require_gpu()
+    H.note("newton-schulz rows far apart")
+    for rows, cols in ((800, 30), (1100, 300)):
+        ld = (2 ** 31 + 2 ** 28) // rows
+        x, = _on_gpu([(rows, cols)], 8, "bfloat16")
+        want, = _run([x], FIVE, "bfloat16")
+        buf = torch.empty(rows * ld, dtype=torch.bfloat16, device="cuda")
+        view = buf.view(rows, ld)[:, ld - cols:]
+        view.copy_(x)
+        _run([view], FIVE, outs=[view])
+        assert torch.equal(view, want)
+        del buf, view
+
+
 def test_a_matrix_does_not_depend_on_its_neighbours():
+    """Bit by bit on what the others hold; on their sizes only by how its sums are cut, and not at all on chip."""
     import torch
     H.require_gpu()
     H.note("newton-schulz alone and among others")
-    xs = [_t(_draw(s, 60 + i)) for i, s in enumerate([(100, 90), (200, 300), (300, 200), (64, 64), (400, 130)])]
+    shapes = [(100, 90), (200, 300), (300, 200), (64, 64), (400, 130)]
+    xs = [_t(_draw(s, 60 + i)) for i, s in enumerate(shapes)]
     together = _run(xs, FIVE)
-    for x, o in zip(xs, together):
-        assert torch.equal(_run([x], FIVE)[0], o)
+    for i, (x, o) in enumerate(zip(xs, together)):
+        others = [x if k == i else _t(_draw(s, 160 + k)) for k, s in enumerate(shapes)]
+        assert torch.equal(_run(others, FIVE)[i], o)
+        alone, = _run([x], FIVE)
+        _five_steps(_np(alone), _np(x), "float32")
+        assert max(x.shape) > 128 or torch.equal(alone, o)
     assert all(torch.equal(a, b) for a, b in zip(_run(xs, FIVE), together))
 
 
@@ -282,6 +363,27 @@ def test_muon_is_the_same_as_its_parts():
     before = [p.clone() for p in opt.params]
     opt.step([torch.zeros_like(p) for p in before], 0.0)
     assert all(torch.equal(p, q) for p, q in zip(before, opt.params))
+
+
+@pytest.mark.parametrize("shapes,copy", [([(1024, 4096), (4096, 1024)] * 6, "bfloat16"), ([(1000, 4070)] * 3, "float16"),
+                                         ([(2496, 3008)], None), ([(2501, 3004)], "float32")],
+                         ids=["whole-blocks", "odd-rows", "one", "ragged"])
+def test_muon_at_larger_tiles(shapes, copy):
+    """As above, for the weights' and the copies' paths out of the tiled products."""
+    import torch
+    from quantized_halo_aggregation_amd import binding as B
+    H.require_gpu()
+    H.note(f"muon larger tiles {len(shapes)} of {shapes[0]} {copy}")
+    params, grads = _on_gpu(shapes, 11, scale=0.1), _on_gpu(shapes, 12, "bfloat16", 0.01)
+    copies = [torch.full_like(p, float("nan"), dtype=getattr(torch, copy)) for p in params] if copy else None
+    opt = B.Muon(params, nesterov=False, scale=0.5, weight_decay=0.25, copies=copies)
+    before = [p.clone() for p in params]
+    opt.step(grads, 0.5)
+    assert all(torch.equal(m, g.float()) for m, g in zip(opt.m, grads))
+    for i, (p, q, o) in enumerate(zip(before, opt.params, _run(opt.m, FIVE))):
+        want = p.double() * (1 - 0.125) - o.double() * 0.25
+        assert bool(((want - q).abs() <= 3 * U * (p.abs() + o.abs())).all())
+        assert copy is None or torch.equal(copies[i], q.to(copies[i].dtype))
 
 
 def test_a_bad_gradient_spoils_its_own_matrix_alone():

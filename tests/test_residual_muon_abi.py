@@ -202,6 +202,9 @@ def test_coefficients_that_stay_in_range_are_taken():
     for k, steps in ((B.NS_COEFFICIENTS, 16), ((1.5, -0.5, 0.0), 16), ((15 / 8, -10 / 8, 3 / 8), 9), ((0, 0, 0), 1), ((3.8, 0, 0), 1),
                      ([(8.2872, -23.5959, 17.3004), (4.1071, -2.9478, 0.5448)], 2)):
         assert B._newton_schulz(None, 0, B.F32, B.F32, steps, B._ns_coefficients(k, steps).ctypes.data, 0.0, None, 0, None) == B.QHA_OK
+    # |5 s - 20 s^3 + 16 s^5| <= 1 on [0, 1], but its slope at 1 is 25: a rounding there grows 25-fold a step
+    five_fold = lambda n: B._newton_schulz(None, 0, B.F32, B.F32, n, B._ns_coefficients((5, -20, 16), n).ctypes.data, 0.0, None, 0, None)
+    assert five_fold(2) == B.QHA_OK and five_fold(5) == B.QHA_ERR_INVALID_ARG
     with pytest.raises(ValueError, match="coefficients"):
         B._ns_coefficients([(1, 2, 3)] * 4, 5)
     with pytest.raises(ValueError, match="coefficients"):
@@ -219,6 +222,8 @@ def test_newton_schulz_and_muon_binding_refuse(monkeypatch):
         B.newton_schulz([x], [_gpu(6, 4)])
     with pytest.raises(TypeError, match="float32"):
         B.newton_schulz([x, _gpu(4, 6, dtype=torch.bfloat16)], [x, x])
+    with pytest.raises(ValueError, match="two of the results"):
+        B.newton_schulz([x, _gpu(4, 6)], [x, x])
     with pytest.raises(ValueError, match="GPU"):
         B.newton_schulz([torch.zeros(4, 6)], [x])
     with pytest.raises(ValueError, match="current device"):
@@ -241,6 +246,10 @@ def test_newton_schulz_and_muon_binding_refuse(monkeypatch):
         B.Muon([x], momenta=[_gpu(6, 4)])
     with pytest.raises(ValueError, match=r"copies\[0\] must be"):
         B.Muon([x], copies=[_gpu(24)])
+    for again in ({"params": [x, x]}, {"params": [x], "momenta": [x]}, {"params": [x], "copies": [x]}):
+        with pytest.raises(ValueError, match="same memory"):
+            B.Muon(**again)
+    B.Muon([_gpu(0, 6), _gpu(0, 6)])
     opt = B.Muon([x])
     with pytest.raises(ValueError, match="2 gradients for 1"):
         opt.step([x, x], 0.1)
