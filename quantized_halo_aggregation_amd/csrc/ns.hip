@@ -10,11 +10,15 @@
 // of itself.  A product is rebuilt from hi hi, hi lo and lo hi (the dropped lo lo is below 2^-22 of a term, 2^-25 on the root mean
 // square), summed in float32 by the matrix cores: half of what three bf16 parts would cost (six products), at
 // float32's error, which the smallest singular values amplify by up to a^steps either way.
-// X, A and B are stored as pairs: 8 hi values, then their 8 lo values, so that a step of 32 is one 128-byte line of a row.
-//
-// A and B are symmetric: tiles on and below the diagonal are formed, and the others stored as their mirror.  The three
-// products take the tables of many matrices at once, three launches a step.  Matrices of at most 128 x 128 (the weights of
-// node layers) stay in one block's LDS from the gradient to the updated weight: one launch in all.
+// What bounds it, and the forms that follow from it (five steps, float32, us a call):
+//   - Large matrices: the matrix cores.  Tiles through LDS, A and B by their tiles on and below the diagonal (the others are stored
+//     as their mirror), three launches a step for a batch of up to 40 matrices, whose tables the launches share.  4096 x 4096 3580:
+//     B X 326 (1.27 PFLOP/s of part products, a plain library product in f16 reaches 1.39), A and B 190 to 200 each (1.2).  What is lost
+//     is a step's wait and barrier, and the stores of a tile, with which nothing overlaps at one block a compute unit.
+//   - Lists too small to fill the chip with tiles: the chain of loads and barriers of a launch.  Blocks of 32 x 32 whose wavefronts
+//     share out the reduction, straight from memory, two or three launches a step: 8 of 256 x 256 100 in 17 launches of 5 to 6.
+//   - Matrices that fit in one block's LDS (up to 32 x 896, 64 x 384, 96 x 192 and 128 x 128): one launch from the gradient to the updated
+//     weight.  8 of 128 x 128 42, of which 6 a step: latency of LDS reads and of five barriers, the matrix cores are mostly idle.
 #include "../../include/qha.h"
 #include "qha_internal.hpp"
 #include "tile_common.hpp"
@@ -358,8 +362,10 @@ __device__ __forceinline__ void triangle(int tile, int* mt, int* nt) {
 }
 
 // A = X X^T (gram), B = a I + b A + c A A^T (square) or the next X = B X (apply): one tile of one matrix.  A wavefront owns MI x NI
-// blocks of 32 x 32; X's columns in the last product come through the transposing read.  The matrix instruction's operands are swapped (C^T is formed), which leaves a lane four
-// neighbouring columns of a row.
+// blocks of 32 x 32; X's columns in the last product come through the transposing read.  The matrix instruction's
+// operands are swapped (C^T is formed), which leaves a lane four neighbouring columns of a row.  Bound by the matrix cores at 256 x 256 (63% of all cycles busy at 4096 x 4096, at the clock that their
+// power leaves), by loads and barriers at 64 x 64 (19% at five of 1000 x 520), where three buffers of 32 steps were the best
+// number (five of 1000 x 520 with three of 333 x 777, all steps: 269 us; two 286, four 275, five 277).
 template <int KIND, int MI, int NI, int WM, int WN, int STAGES>
 __global__ __launch_bounds__(WM * WN * 64) void ns_product_kernel(const NsTable* table, NsFirst first, NsCoef k, int32_t from, uint32_t total) {
   constexpr int BM = MI * 32 * WM, BN = NI * 32 * WN, NT = WM * WN * 64;
@@ -808,7 +814,8 @@ __device__ __forceinline__ void chip_steps(uint16_t* lx, uint16_t* la, float* pa
 }
 
 // One matrix a block, from the gradient to the updated weight: X and, in turn, A and B as pairs in LDS.  SQUARE: those of 97
-// to 128 rows and columns.
+// to 128 rows and columns.  Measured (us a call, five steps): 128 x 128 40 (5.5 a step), 64 x 64 23, 32 x 32 13.6, 22 x 840 35,
+// 96 x 192 57, 64 x 384 44.
 template <bool SQUARE>
 __global__ __launch_bounds__(kChipThreads) void ns_chip_kernel(NsTable t, NsSteps k) {
   __shared__ __attribute__((aligned(16))) char pool[SQUARE ? Chip<4>::BYTES : kChipBytes];
@@ -1061,7 +1068,8 @@ constexpr size_t kTableBytes = (sizeof(NsTable) + 255) / 256 * 256;
 
 int64_t pad32(int64_t x) { return (x + 31) / 32 * 32; }
 int64_t pad64(int64_t x) { return (x + 63) / 64 * 64; }
-// Rows of X by 32 where the matrix fits in LDS, else 0.
+// Rows of X by 32 where the matrix fits in LDS, else 0.  (From memory, us for five steps: 128 x 128 73, on chip 40; 40 of them 108, 63;
+// 96 x 192 69, 56; 64 x 384 70, 43; 22 x 840 72, 34; 32 x 32 55, 13.)
 int chip_rows_of(const NsMatrix& m) {
   const int64_t s = m.rows < m.cols ? m.rows : m.cols, l = pad64(m.rows < m.cols ? m.cols : m.rows);
   if (s <= 32 && l <= Chip<1>::CAP) return 1;
@@ -1093,7 +1101,9 @@ NsPlan plan_of(const NsMatrix* m, const int64_t* index, int count) {
     deepest = l + 2 * s > deepest ? l + 2 * s : deepest;
     values += 64 * (rows * (rows + 1) / 2 * (l + (s <= kFusedRows ? 0 : s)) + rows * cols * s);
   }
-  // us of a step: the operands that direct blocks read, at 13 TB/s; the tiles' steps of 32, one after the other
+  // us of a step: the operands that direct blocks read, at 13 TB/s; the tiles' steps of 32, one after the other.  Measured, direct and
+  // tiled (us, five steps): 256 x 256 92, 104; 8 of them 102, 106; 16 148, 110; 512 x 512 116, 144; four 192, 154; 700 x 700 146, 171;
+  // 1000 x 1000 270, 204; 39 x 3035 110, 182; 200 x 2000 129, 171; four 182, 187; 12 of 96 x 2848 (taken for direct) 234, 222
   const double direct = static_cast<double>(values) * 4.0 / 13e6;
   const double tiled = 0.28 * static_cast<double>(deepest) / 32.0 * (tiles > 512 ? static_cast<double>(tiles) / 512.0 : 1.0);
   // each block forms B's rows: many of them lose more by it than a launch costs (12 of 96 x 2848 265 us, 237 unfused)
