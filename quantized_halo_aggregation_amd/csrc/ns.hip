@@ -324,17 +324,20 @@ struct Stager {
   int64_t next_by;
   // The matrix has `rows` runs of 32 rows of `blocks` blocks; the tile begins at run (across: at block) `first`.  Those past the end
   // repeat the last one, whose results are not stored.
-  __device__ __forceinline__ Stager(const uint16_t* base, int64_t rows, int64_t blocks, int64_t first) {
+  // `id`: the thread's number of NT; the reduction begins at step `begin`.
+  __device__ __forceinline__ Stager(const uint16_t* base, int64_t rows, int64_t blocks, int64_t first, int id, int64_t begin) {
     next_by = ACROSS ? blocks * kBlock : 2 * kBlock;
+    base += begin * next_by;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      const int64_t r = first + i * RUNS + static_cast<int>(threadIdx.x) / PER;
+      const int64_t r = first + i * RUNS + id / PER;
       const int64_t run = ACROSS ? (r < blocks ? r : blocks - 1) : (r < rows ? r : rows - 1) * blocks;
-      at[i] = base + run * kBlock + (static_cast<int>(threadIdx.x) & (PER - 1)) * 8;
+      at[i] = base + run * kBlock + (id & (PER - 1)) * 8;
     }
   }
+  // `lds`: the wavefront's part of the buffer
   __device__ __forceinline__ void load(const uint16_t* lds) {
-    const uint32_t to = lds_address(lds) + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) * 1024;
+    const uint32_t to = __builtin_amdgcn_readfirstlane(lds_address(lds));
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       load_to_lds(at[i], to + i * NT * 16);
@@ -363,17 +366,20 @@ __device__ __forceinline__ void triangle(int tile, int* mt, int* nt) {
 
 // A = X X^T (gram), B = a I + b A + c A A^T (square) or the next X = B X (apply): one tile of one matrix.  A wavefront owns MI x NI
 // blocks of 32 x 32; X's columns in the last product come through the transposing read.  The matrix instruction's
-// operands are swapped (C^T is formed), which leaves a lane four neighbouring columns of a row.  Bound by the matrix cores at 256 x 256 (63% of all cycles busy at 4096 x 4096, at the clock that their
+// operands are swapped (C^T is formed), which leaves a lane four neighbouring columns of a row.  KS groups of WM x WN wavefronts share
+// out the reduction, each with buffers of its own, and the first adds the second's sums to its own.  Bound by the matrix cores at 256 x 256 (63% of all cycles busy at 4096 x 4096, at the clock that their
 // power leaves), by loads and barriers at 64 x 64 (19% at five of 1000 x 520), where three buffers of 32 steps were the best
 // number (five of 1000 x 520 with three of 333 x 777, all steps: 269 us; two 286, four 275, five 277).
-template <int KIND, int MI, int NI, int WM, int WN, int STAGES>
-__global__ __launch_bounds__(WM * WN * 64) void ns_product_kernel(const NsTable* table, NsFirst first, NsCoef k, int32_t from, uint32_t total) {
+template <int KIND, int MI, int NI, int WM, int WN, int STAGES, int KS>
+__global__ __launch_bounds__(WM * WN * KS * 64) void ns_product_kernel(const NsTable* table, NsFirst first, NsCoef k, int32_t from, uint32_t total) {
   constexpr int BM = MI * 32 * WM, BN = NI * 32 * WN, NT = WM * WN * 64;
   constexpr bool SYM = KIND == NS_GRAM || KIND == NS_SQUARE;
   static_assert(BM == BN, "square tiles, for symmetric results");
   constexpr int A_SIZE = BM * BK * 2, BUF = A_SIZE + BN * BK * 2;
-  static_assert(WM * WN * 32 * kPartRow * 4 <= STAGES * BUF * 2, "room for the transposes");
-  __shared__ __attribute__((aligned(16))) uint16_t lds[STAGES * BUF];
+  constexpr int PARTS = WM * WN * 32 * kPartRow;                     // floats: a block of 32 x 32 of each wavefront
+  static_assert(KS == 1 || (KS == 2 && MI == 1 && NI == 1), "halves of the reduction in tiles of one block a wavefront");
+  static_assert(PARTS * 4 * KS <= KS * STAGES * BUF * 2, "room for the transposes and for the other half's sums");
+  __shared__ __attribute__((aligned(16))) uint16_t pool[KS * STAGES * BUF];
   // consecutive blocks go to the eight dies in turn: each takes a run of neighbouring tiles, which share operands
   const uint32_t band = (total + kXcds - 1) / kXcds;
   const uint32_t block = blockIdx.x % kXcds * band + blockIdx.x / kXcds;
@@ -394,8 +400,11 @@ __global__ __launch_bounds__(WM * WN * 64) void ns_product_kernel(const NsTable*
     nt = in / rows;
   }
   const int lane = threadIdx.x & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int group = KS == 1 ? 0 : __builtin_amdgcn_readfirstlane(threadIdx.x / NT);      // of the reduction's halves
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) - group * (NT / 64);
+  const int id = static_cast<int>(threadIdx.x) - group * NT;
   const int wm = wave / WN, wn = wave % WN;
+  uint16_t* lds = pool + group * STAGES * BUF;
   const NsParts w(a);
   const uint16_t* x = w.x(from);
   const uint16_t* P = KIND == NS_GRAM ? x : KIND == NS_SQUARE ? w.a() : w.b();
@@ -407,9 +416,11 @@ __global__ __launch_bounds__(WM * WN * 64) void ns_product_kernel(const NsTable*
   for (int ii = 0; ii < MI; ++ii)
 #pragma unroll
     for (int j = 0; j < NI; ++j) acc[ii][j] = 0.0f;
-  Stager<false, BM, NT> sp(P, m_pad / 32, depth / 16, static_cast<int64_t>(mt) * (BM / 32));
-  Stager<!SYM, BN, NT> sq(Q, m_pad / 32, (SYM ? depth : n_pad) / 16, static_cast<int64_t>(nt) * (SYM ? BN / 32 : BN / 16));
-  const int steps = static_cast<int>(depth / BK);
+  const int whole = static_cast<int>(depth / BK), steps = (whole + KS - 1) / KS;
+  const int64_t begin = static_cast<int64_t>(group) * steps;
+  const bool blank = KS == 2 && group == 1 && (whole & 1);           // a second half of one step fewer begins with zeros
+  Stager<false, BM, NT> sp(P, m_pad / 32, depth / 16, static_cast<int64_t>(mt) * (BM / 32), id, begin);
+  Stager<!SYM, BN, NT> sq(Q, m_pad / 32, (SYM ? depth : n_pad) / 16, static_cast<int64_t>(nt) * (SYM ? BN / 32 : BN / 16), id, begin);
   constexpr int EACH = decltype(sp)::N + decltype(sq)::N;      // loads of a thread for a step
   // A step's operands come out of LDS in two halves of 16.  The first half of step s + 1 is read while the second half of step s is
   // multiplied: the wait for its loads and the barrier lie in the middle of step s, where they find the matrix cores busy.
@@ -453,11 +464,13 @@ __global__ __launch_bounds__(WM * WN * 64) void ns_product_kernel(const NsTable*
 #pragma unroll
     for (int term = 0; term < 3; ++term) multiply_term(fp, fq, term);
   };
-  const auto load = [&](int buffer) {
-    sp.load(lds + buffer * BUF);
-    sq.load(lds + buffer * BUF + A_SIZE);
-  };
-  for (int s = 0; s < STAGES && s < steps; ++s) load(s);
+  uint16_t* to = lds + wave * 512;
+  if (blank)
+    for (int i = id * 8; i < BUF; i += NT * 8) *reinterpret_cast<s16x8*>(lds + i) = 0;
+  for (int s = blank ? 1 : 0; s < STAGES && s < steps; ++s) {
+    sp.load(to + s * BUF);
+    sq.load(to + s * BUF + A_SIZE);
+  }
   if (steps >= STAGES) loads_left<(STAGES - 1) * EACH>();
   else loads_left<0>();
   __syncthreads();
@@ -477,9 +490,9 @@ __global__ __launch_bounds__(WM * WN * 64) void ns_product_kernel(const NsTable*
     // the loads of a later step go out between the products, which would otherwise wait for their issue
     const bool more = s + STAGES < steps;
     multiply_term(p1, q1, 0);
-    if (more) sp.load(lds + now * BUF);
+    if (more) sp.load(to + now * BUF);
     multiply_term(p1, q1, 1);
-    if (more) sq.load(lds + now * BUF + A_SIZE);
+    if (more) sq.load(to + now * BUF + A_SIZE);
     multiply_term(p1, q1, 2);
     now = next;
   }
@@ -491,8 +504,21 @@ __global__ __launch_bounds__(WM * WN * 64) void ns_product_kernel(const NsTable*
   // the call's results pass through a piece of LDS of the wavefront's own.
   const bool turned = SYM ? mt != nt : KIND == NS_LAST;
   uint16_t* out = KIND == NS_GRAM ? w.a() : KIND == NS_SQUARE ? w.b() : w.x(from ^ 1);
-  float* turn = reinterpret_cast<float*>(lds) + wave * 32 * kPartRow;
-  if (turned) __syncthreads();         // everyone has read the last step
+  float* turn = reinterpret_cast<float*>(pool) + wave * 32 * kPartRow;
+  if (KS == 2 || turned) __syncthreads();        // everyone has read the last step
+  if constexpr (KS == 2) {
+    f32x4* sums = reinterpret_cast<f32x4*>(reinterpret_cast<float*>(pool) + PARTS) + wave * 256 + lane;
+    if (group == 1) {
+#pragma unroll
+      for (int q = 0; q < 4; ++q) sums[64 * q] = f32x4{acc[0][0][4 * q], acc[0][0][4 * q + 1], acc[0][0][4 * q + 2], acc[0][0][4 * q + 3]};
+    }
+    __syncthreads();
+    if (group == 1) return;
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) acc[0][0][4 * q + e] += sums[64 * q][e];
+  }
 #pragma unroll
   for (int ii = 0; ii < MI; ++ii) {
     const int64_t row0 = static_cast<int64_t>(mt) * BM + (wm * MI + ii) * 32;
@@ -1187,18 +1213,21 @@ struct NsTiles {
 };
 
 template <int KIND>
-void run_product(const NsTable* t, const NsTiles& b, const NsCoef& k, int from, hipStream_t s) {
+void run_product(const NsTable* t, const NsTiles& b, int64_t depth, const NsCoef& k, int from, hipStream_t s) {
   constexpr bool SYM = KIND == NS_GRAM || KIND == NS_SQUARE;
   const uint32_t g = b.grid();
-  if (b.side == 256) ns_product_kernel<KIND, 4, 2, 2, 4, 2><<<g, 512, 0, s>>>(t, b.first, k, from, b.total);
-  else if (b.side == 128) ns_product_kernel<KIND, 2, 2, 2, 2, 2><<<g, 256, 0, s>>>(t, b.first, k, from, b.total);
-  else if (b.side == 64) ns_product_kernel<KIND, 1, 1, 2, 2, 3><<<g, 256, 0, s>>>(t, b.first, k, from, b.total);
-  else if constexpr (SYM) ns_product_kernel<KIND, 3, 3, 2, 2, 2><<<g, 256, 0, s>>>(t, b.first, k, from, b.total);
+  if (b.side == 256) ns_product_kernel<KIND, 4, 2, 2, 4, 2, 1><<<g, 512, 0, s>>>(t, b.first, k, from, b.total);
+  else if (b.side == 128) ns_product_kernel<KIND, 2, 2, 2, 2, 2, 1><<<g, 256, 0, s>>>(t, b.first, k, from, b.total);
+  // two halves of the reduction where a compute unit has one tile at most, and steps enough (us, five steps, whole and halved:
+  // 1024 x 4096 410, 362; 1300 x 1300 282, 268; 1000 x 1000 202, 189; four of 512 x 512 154, 158, 16 of 256 x 256 110, 118)
+  else if (b.side == 64 && b.total <= 256 && depth > 512) ns_product_kernel<KIND, 1, 1, 2, 2, 3, 2><<<g, 512, 0, s>>>(t, b.first, k, from, b.total);
+  else if (b.side == 64) ns_product_kernel<KIND, 1, 1, 2, 2, 3, 1><<<g, 256, 0, s>>>(t, b.first, k, from, b.total);
+  else if constexpr (SYM) ns_product_kernel<KIND, 3, 3, 2, 2, 2, 1><<<g, 256, 0, s>>>(t, b.first, k, from, b.total);
 }
 
 // One step of a batch; the last one's results go where the call wants them.
 void run_step(const NsTable* t, const NsPlan& plan, const NsTiles& gram, const NsTiles& square, const NsTiles& all,
-              const NsSteps& k, int step, hipStream_t s) {
+              int64_t most_m, int64_t most_n, const NsSteps& k, int step, hipStream_t s) {
   const int from = step & 1;
   const bool last = step + 1 == k.steps;
   if (plan.direct) {
@@ -1212,10 +1241,10 @@ void run_step(const NsTable* t, const NsPlan& plan, const NsTiles& gram, const N
     else ns_direct_kernel<NS_APPLY, false><<<all.grid(), NT, 0, s>>>(t, all.first, sq, ap, from, all.total);
     return;
   }
-  run_product<NS_GRAM>(t, gram, k.gram, from, s);
-  run_product<NS_SQUARE>(t, square, k.square[step], from, s);
-  if (last) run_product<NS_LAST>(t, all, k.apply, from, s);
-  else run_product<NS_APPLY>(t, all, k.apply, from, s);
+  run_product<NS_GRAM>(t, gram, most_n, k.gram, from, s);
+  run_product<NS_SQUARE>(t, square, most_m, k.square[step], from, s);
+  if (last) run_product<NS_LAST>(t, all, most_m, k.apply, from, s);
+  else run_product<NS_APPLY>(t, all, most_m, k.apply, from, s);
 }
 
 }  // namespace
@@ -1327,7 +1356,7 @@ hipError_t launch_ns(const NsMatrix* m, int64_t n, const NsArgs& args, void* ws,
     NsTable* table = static_cast<NsTable*>(ws);
     ns_measure_kernel<<<n_pieces, 256, 0, s>>>(t, pieces, reinterpret_cast<uint32_t*>(table));
     ns_split_kernel<<<whole.total, 256, 0, s>>>(table, whole.first);
-    for (int i = 0; i < args.steps; ++i) run_step(table, plan, gram, square, all, k, i, s);
+    for (int i = 0; i < args.steps; ++i) run_step(table, plan, gram, square, all, most_m, most_n, k, i, s);
   }
   return launched ? hipGetLastError() : hipSuccess;
 }

@@ -157,8 +157,10 @@ def _products(got, x, dtype="float32", eps=1e-7):
         assert float((off * off).sum()) <= 2.0 ** -24 * float((x * x).sum())
 
 
-# the rule on tiles takes sides of 128 (one of 2501 x 3001), 192 and 256 (one of 4001 x 4090) and 256 (24 of 1000 x 4070)
-LARGER = [[(2501, 3001)], [(3001, 2501)], [(4001, 4090)], [(4090, 4001)], [(1000, 4070), (4070, 1000)] * 12, [(1024, 4096)] * 24]
+# the rule on tiles takes sides of 64, of which each half of the reduction is a group's own (one of 1001 x 1300 in its A; 1000 x 900 with
+# 29 steps, and 30 x 1000 with one beside it), of 128 (one of 2501 x 3001), 192 and 256 (one of 4001 x 4090) and 256 (24 of 1000 x 4070)
+LARGER = [[(1001, 1300)], [(1000, 900), (30, 1000)], [(2501, 3001)], [(3001, 2501)], [(4001, 4090)], [(4090, 4001)], [(1000, 4070), (4070, 1000)] * 12,
+          [(1024, 4096)] * 24]
 
 
 def _on_gpu(shapes, seed, dtype="float32", scale=1.0):
@@ -174,7 +176,7 @@ def test_larger_tiles(shapes):
     H.note(f"newton-schulz larger tiles {len(shapes)} of {shapes[0]}")
     xs = _on_gpu(shapes, 5)
     outs = _run(xs, FIVE[:1])
-    for i in sorted({0, len(xs) // 2 + 1 if len(xs) > 1 else 0, len(xs) - 1}):
+    for i in sorted({0, len(xs) // 2, len(xs) - 1}):
         _one_step(outs[i].double(), xs[i].double(), FIVE[0], 1e-7)
     outs = _run(xs, FIVE, "float16")
     for i in sorted({0, len(xs) - 1}):
