@@ -1128,10 +1128,11 @@ NsPlan plan_of(const NsMatrix* m, const int64_t* index, int count) {
     values += 64 * (rows * (rows + 1) / 2 * (l + (s <= kFusedRows ? 0 : s)) + rows * cols * s);
   }
   // us of a step: the operands that direct blocks read, at 13 TB/s; the tiles' steps of 32, one after the other.  Measured, direct and
-  // tiled (us, five steps): 256 x 256 92, 104; 8 of them 102, 106; 16 148, 110; 512 x 512 116, 144; four 192, 154; 700 x 700 146, 171;
-  // 1000 x 1000 270, 204; 39 x 3035 110, 182; 200 x 2000 129, 171; four 182, 187; 12 of 96 x 2848 (taken for direct) 234, 222
+  // tiled (us, five steps): 256 x 256 92, 104; 8 of them 102, 106; 16 148, 110; 512 x 512 115, 144; four 192, 154; 700 x 700 146, 162;
+  // 800 x 800 183, 173; 1000 x 1000 270, 189; 39 x 3035 110, 161; 128 x 8000 235, 309; 300 x 8000 312, 345; 256 x 16000 488, 562; near each
+  // other, and taken for direct: 520 x 4000 278, 268, four of 200 x 2000 182, 175, 12 of 96 x 2848 234, 222
   const double direct = static_cast<double>(values) * 4.0 / 13e6;
-  const double tiled = 0.28 * static_cast<double>(deepest) / 32.0 * (tiles > 512 ? static_cast<double>(tiles) / 512.0 : 1.0);
+  const double tiled = 0.26 * static_cast<double>(deepest) / 32.0 * (tiles > 512 ? static_cast<double>(tiles) / 512.0 : 1.0);
   // each block forms B's rows: many of them lose more by it than a launch costs (12 of 96 x 2848 265 us, 237 unfused)
   NsPlan p = {direct < tiled, fits && blocks <= kFusedBlocks, 8};
   while (p.piece_rows < 64 && pieces > 1024) {
