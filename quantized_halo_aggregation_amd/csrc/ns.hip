@@ -61,6 +61,18 @@ __device__ __forceinline__ f32x4 read4(const void* p, int64_t ld, int64_t row, i
     if (c + e < cols) v[e] = load1(p, row * ld + c + e, type);
   return v;
 }
+// Four of 16 rows apart at once, from matrices whose rows are aligned to four values: all loads go out before the first is converted.
+// Places past the end hold others' values.
+template <typename E>
+__device__ __forceinline__ void read_rows(const void* p, int64_t ld, int r, int rows, int c, int cols, f32x4 (&v)[4]) {
+  typedef E vec __attribute__((ext_vector_type(4)));
+  vec raw[4];
+  const E* at = static_cast<const E*>(p) + (c < cols ? c : 0);
+#pragma unroll
+  for (int k = 0; k < 4; ++k) raw[k] = *reinterpret_cast<const vec*>(at + (r + 16 * k < rows ? r + 16 * k : rows - 1) * ld);
+#pragma unroll
+  for (int k = 0; k < 4; ++k) v[k] = __builtin_convertvector(raw[k], f32x4);
+}
 __device__ __forceinline__ void write4(void* p, int64_t ld, int64_t row, int c, int cols, int32_t type, bool vec, f32x4 v) {
   if (vec && c < cols) {
     store4(p, row * ld + c, type, v);
@@ -206,7 +218,8 @@ __global__ __launch_bounds__(256) void ns_measure_kernel(NsTable t, NsFirst firs
   if (threadIdx.x == 0) NsParts(a).squares(t.transposes)[piece] = s;
 }
 
-// X, and its transpose where the products read that, by tiles of 64 x 64, zero past the matrix's end.
+// X, and its transpose where the products read that, by tiles of 64 x 64, zero past the matrix's end.  Bound
+// by memory: 24 of 4096 x 1024 with bf16 gradients and momentum 220 us, 1.0 GB at 4.6 TB/s (a row's loads after another's 265)
 __global__ __launch_bounds__(256) void ns_split_kernel(const NsTable* table, NsFirst first) {
   const NsTable& t = *table;
   __shared__ double buf[4];
@@ -217,16 +230,23 @@ __global__ __launch_bounds__(256) void ns_split_kernel(const NsTable* table, NsF
   const int x0 = at / wide * 64, y0 = at % wide * 64;            // of X
   const int r0 = a.tall ? y0 : x0, c0 = a.tall ? x0 : y0;        // of the matrix
   const int cl = (static_cast<int>(threadIdx.x) & 15) * 4, rl = static_cast<int>(threadIdx.x >> 4);
-  f32x4 u[4];
+  f32x4 u[4], m[4];
+  if (a.vec_src && (!t.muon || a.vec_mom)) {
+    if (t.muon) read_rows<float>(a.mom, a.ldo, r0 + rl, a.rows, c0 + cl, a.cols, m);
+    if (t.type == QHA_F32) read_rows<float>(a.src, a.lds, r0 + rl, a.rows, c0 + cl, a.cols, u);
+    else if (t.type == QHA_BF16) read_rows<__bf16>(a.src, a.lds, r0 + rl, a.rows, c0 + cl, a.cols, u);
+    else read_rows<_Float16>(a.src, a.lds, r0 + rl, a.rows, c0 + cl, a.cols, u);
+  } else {
 #pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    u[k] = 0.0f;
-    if (r0 + rl + 16 * k < a.rows) {
-      const f32x4 g = read4(a.src, a.lds, r0 + rl + 16 * k, c0 + cl, a.cols, t.type, a.vec_src);
-      const f32x4 m = t.muon ? read4(a.mom, a.ldo, r0 + rl + 16 * k, c0 + cl, a.cols, QHA_F32, a.vec_mom) : g;
-      u[k] = update_of(t, g, m);
+    for (int k = 0; k < 4; ++k) {
+      u[k] = m[k] = 0.0f;
+      if (r0 + rl + 16 * k >= a.rows) continue;
+      u[k] = read4(a.src, a.lds, r0 + rl + 16 * k, c0 + cl, a.cols, t.type, a.vec_src);
+      if (t.muon) m[k] = read4(a.mom, a.ldo, r0 + rl + 16 * k, c0 + cl, a.cols, QHA_F32, a.vec_mom);
     }
   }
+#pragma unroll
+  for (int k = 0; k < 4; ++k) u[k] = update_of(t, u[k], m[k]);
   const int pieces = ((a.rows + t.piece_rows - 1) / t.piece_rows) * ((a.cols + kPieceCols - 1) / kPieceCols);
   double s = 0.0;
   const NsParts w(a);
