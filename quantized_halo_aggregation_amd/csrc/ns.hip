@@ -12,11 +12,11 @@
 // float32's error, which the smallest singular values amplify by up to a^steps either way.
 // What bounds it, and the forms that follow from it (five steps, float32, us a call):
 //   - Large matrices: the matrix cores.  Tiles through LDS, A and B by their tiles on and below the diagonal (the others are stored
-//     as their mirror), three launches a step for a batch of up to 40 matrices, whose tables the launches share.  4096 x 4096 3580:
-//     B X 326 (1.27 PFLOP/s of part products, a plain library product in f16 reaches 1.39), A and B 190 to 200 each (1.2).  What is lost
+//     as their mirror), three launches a step for a batch of up to 40 matrices, whose tables the launches share.  4096 x 4096 3490 to 3680:
+//     B X 326 (1.27 PFLOP/s of part products, a plain library product in f16 reaches 1.39), A and B 190 to 206 each (1.1 to 1.2).  What is lost
 //     is a step's wait and barrier, and the stores of a tile, with which nothing overlaps at one block a compute unit.
 //   - Lists too small to fill the chip with tiles: the chain of loads and barriers of a launch.  Blocks of 32 x 32 whose wavefronts
-//     share out the reduction, straight from memory, two or three launches a step: 8 of 256 x 256 100 in 17 launches of 5 to 6.
+//     share out the reduction, straight from memory, two or three launches a step: 8 of 256 x 256 98 in 17 launches of 5 to 7.
 //   - Matrices that fit in one block's LDS (up to 32 x 896, 64 x 384, 96 x 192 and 128 x 128): one launch from the gradient to the updated
 //     weight.  8 of 128 x 128 42, of which 6 a step: latency of LDS reads and of five barriers, the matrix cores are mostly idle.
 #include "../../include/qha.h"
