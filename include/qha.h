@@ -472,7 +472,8 @@ size_t qha_group_norm_workspace(int64_t n_samples, int64_t positions, int32_t c,
  * type.  Weights and biases: device float32[c], 16-byte aligned, each nullable (1 and 0).  gate: one row for each
  * `positions` consecutive rows (their number must be a multiple), nullable (1).  post_stats and pre_stats: device
  * float32[n_rows][2], 8-byte aligned, nullable: each row's mean (0 for RMS) and 1 / sqrt(..), for the backward.
- * h may be NULL (the first block's input): then u is the norm of x itself, and gate, y, post_stats and the post vectors must be NULL.
+ * h may be NULL (the first block's input): then u is the norm of x itself, skip and branch have no part, and gate, y, post_stats
+ * and the post vectors must be NULL.
  * y may be x and u may be h (with the same leading dimension); otherwise outputs must not overlap inputs or each other.
  * Sums over a row are float32, means before squares; results are deterministic.
  * c is a multiple of 16 bytes of elements of type and at most 8192; leading dimensions are at least c and
@@ -491,7 +492,7 @@ int qha_residual_norm_fwd(int64_t n_rows, int64_t positions, int32_t c, int32_t 
 
 /* Gradients of qha_residual_norm_fwd from its kept x' (y; without a block its x) and h and its statistics.  With
  * t = dy + the gradient of x' through the pre norm (from du):
- *   dx = skip t,   dgate = sum over the gate's rows of branch t z,   dh = the gradient of h through branch gate z,
+ *   dx = skip t (t without a block),   dgate = sum over the gate's rows of branch t z,   dh = the gradient of h through branch gate z,
  *   d(weight) = sum of dz xhat, d(bias) = sum of dz over all rows, for either norm (dz: the norm's result's gradient)
  * dy: the gradient of x' from elsewhere (stream_type; nullable with a pre norm: none).  du: elements of type, NULL
  * without a pre norm.  dx has elements of stream_type, dh and dgate of type.  dgate and the four vectors' gradients

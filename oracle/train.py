@@ -158,8 +158,8 @@ def residual_norm_backward(dy, du, y, h, gate, positions, post, pre, vectors, po
     if pre != "none":
         dv, grads[2], grads[3] = row_norm_backward(du, y, pre, pre_stats, vectors[2])
         t = t + dv
-    if h is None:
-        return skip * t, None, None, grads
+    if h is None:                                # u is the norm of x itself: skip has no part
+        return t, None, None, grads
     g = np.ones((t.shape[0] // positions, t.shape[1])) if gate is None else np.asarray(gate, np.float64)
     h = np.asarray(h, np.float64)
     z = (h - post_stats[:, :1]) * post_stats[:, 1:] * (1.0 if vectors[0] is None else vectors[0])

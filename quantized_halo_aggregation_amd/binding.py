@@ -735,7 +735,8 @@ def residual_norm_fwd(x, h, y, u, post: int = ROW_RMS, pre: int = ROW_RMS, post_
 
     x and y are the residual stream [rows, c] (float32, or the type of h); h, the block's output, gate [rows /
     positions, c] and u have one type.  post_stats and pre_stats (float32 [rows, 2], if given) receive what the
-    backward needs.  With pre=ROW_NONE u is None; with h=None (post=ROW_NONE, y=None) u is pre(x)."""
+    backward needs.  With pre=ROW_NONE u is None; with h=None (post=ROW_NONE, y=None) u is pre(x), whatever skip
+    and branch are."""
     rows, c = x.shape
     s = x.dtype
     t = s if h is None and u is None else (u if h is None else h).dtype

@@ -449,6 +449,7 @@ int qha_residual_norm_bwd(int64_t n_rows, int64_t positions, int32_t c, int32_t 
     a.vec_part = static_cast<float*>(workspace);
     a.gate_part = a.vec_part + a.blocks * 4 * a.c;
   }
+  if (!h) a.skip = 1.0f;             // without a block the forward's u is the norm of x itself, whatever skip is
   a.dy = dy;
   a.lddy = lddy;
   a.du = du;

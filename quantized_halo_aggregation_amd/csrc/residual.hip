@@ -3,7 +3,7 @@
 // Mathematics, per row: z = w_p hhat + b_p with hhat = (h - mean) rstd (layer norm), h rstd (RMS) or h;
 //   x' = skip x + branch g z,   u = w_q xhat' + b_q with xhat' the same of x' (in float32, before it is rounded).
 // Backward, with q = w_q du and t = dy + rstd (q - mean q - xhat' mean(q xhat')) (no mean q for RMS):
-//   dx = skip t,  dg = sum of branch t z over the rows that share g,  dh the same form of q = w_p branch t g,
+//   dx = skip t (the host sets skip to 1 where there is no block),  dg = sum of branch t z over the rows that share g,  dh the same form of q = w_p branch t g,
 //   dw = sum dz xhat and db = sum dz over all rows, for both norms.
 //
 // Bound: memory, every array once.  A row belongs to a team of L threads (8 to a wavefront's 64, or a block of 256 or

@@ -251,6 +251,26 @@ def test_the_first_norm_of_a_stack_has_no_block(types, pre):
         case.check_bwd(case.run_bwd())
 
 
+@pytest.mark.parametrize("pre", ["rms", "layer"])
+@pytest.mark.parametrize("types", TYPES, ids="-".join)
+def test_skip_has_no_part_without_a_block(types, pre):
+    """The forward's u is the norm of x itself, so its gradient is that of skip 1, which the oracle and differences
+    of it confirm, bit for bit whatever skip and branch are."""
+    import torch
+    H.require_gpu()
+    H.note(f"residual norm without a block, other skips {types} {pre}")
+    case = Case((37, 1, 264), types, "none", pre, block=False)
+    case.kept()
+    fwd, bwd = case.run_fwd(), case.run_bwd()
+    case.check_bwd(bwd)
+    for skip, branch in ((0.5, 1.0), (0.0, 0.0), (-2.0, 3.0)):
+        case.skip, case.branch = np.float32(skip), np.float32(branch)
+        assert torch.equal(case.run_fwd()["u"], fwd["u"]), skip
+        out = case.run_bwd()
+        assert torch.equal(out["dx"], bwd["dx"]), skip
+        assert all(torch.equal(a, b) for a, b in zip(out["vectors"][2:], bwd["vectors"][2:])), skip
+
+
 def test_a_large_mean_keeps_the_variance():
     """A mean 100 times the deviation."""
     H.require_gpu()

@@ -97,6 +97,27 @@ def test_residual_norm_gradients_match_central_differences(post, pre):
             assert abs((loss(*hi) - loss(*lo)) / (2 * h_step) - grad[i]) < 1e-7
 
 
+@pytest.mark.parametrize("pre", ["rms", "layer"])
+def test_gradients_without_a_block_match_central_differences(pre):
+    """The stream reaches the norm as it is there, so skip scales neither u nor the gradient; step and bound as above."""
+    rng = np.random.default_rng(14)
+    h_step, x = 1e-5, rng.standard_normal((4, 6))
+    w, b = 1 + 0.3 * rng.standard_normal(6), rng.standard_normal(6)
+    dy, du = rng.standard_normal((4, 6)), rng.standard_normal((4, 6))
+
+    def forward(x_, skip):
+        return T.residual_norm(x_, None, None, 1, "none", pre, (None, None, w, b), skip, 1.3, 1e-3)
+    for skip in (1.0, 0.5, 0.0, -2.0):
+        y, _, _, qs = forward(x, skip)
+        dx = T.residual_norm_backward(dy, du, y, None, None, 1, "none", pre, (None, None, w, b), None, qs, skip, 1.3)[0]
+        for i in np.ndindex(x.shape):
+            hi, lo = x.copy(), x.copy()
+            hi[i] += h_step
+            lo[i] -= h_step
+            loss = [float((y * dy).sum() + (u * du).sum()) for y, u, _, _ in (forward(hi, skip), forward(lo, skip))]
+            assert abs((loss[0] - loss[1]) / (2 * h_step) - dx[i]) < 1e-7
+
+
 def test_residual_norm_is_the_composition_of_its_parts():
     rng = np.random.default_rng(12)
     x, h, gate = rng.standard_normal((6, 8)), 3 + rng.standard_normal((6, 8)), rng.standard_normal((3, 8))
