@@ -860,6 +860,7 @@ class AdamW:
         if len({t.device for t in self._tensors()}) > 1:
             raise ValueError("parameters, copies and moments must live on one GPU")
         self._copy_type = F32
+        table[:, 3] = 0                              # of copies that were given up
         if self.copies:
             self._copy_type = _type(self.copies[0].dtype, "copies")
             for i, c in enumerate(self.copies):
@@ -1013,6 +1014,7 @@ class Muon:
             raise ValueError(f"{n} parameters were given, now there are {len(self.params)}, {len(self.m)} momenta and "
                              f"{n if self.copies is None else len(self.copies)} copies")
         self._copy_type = _type(self.copies[0].dtype, "copies") if self.copies else F32
+        table[:, 4] = 0                              # of copies that were given up
         for name, column, given in (("params", 2, self.params), ("copies", 4, self.copies), ("m", 5, self.m)):
             for i, t in enumerate(given or ()):
                 if tuple(t.shape) != self.shapes[i]:

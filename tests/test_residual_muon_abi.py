@@ -262,6 +262,35 @@ def test_newton_schulz_and_muon_binding_refuse(monkeypatch):
     B.Muon([]).step([], 0.1)
 
 
+@pytest.fixture
+def muon_calls(monkeypatch):
+    """The (table, gradients' type, copies' type) of every qha_muon_step, recorded in its place."""
+    import numpy as np
+    calls = []
+
+    def record(table, n, grad_type, copy_type, *rest):
+        import ctypes
+        rows = np.ctypeslib.as_array((ctypes.c_int64 * (7 * n)).from_address(table)).reshape(n, 7).copy()
+        calls.append((rows, grad_type, copy_type))
+        return B.QHA_OK
+    monkeypatch.setattr(B, "_muon_step", record)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    return calls
+
+
+def test_muon_without_its_copies_writes_none(muon_calls):
+    """Copies that were given up are not written any more, and are again when they come back."""
+    copies = [_gpu(4, 6, dtype=torch.bfloat16), _gpu(9, 3, dtype=torch.bfloat16)]
+    opt = B.Muon([_gpu(4, 6), _gpu(9, 3)], copies=copies)
+    grads = [_gpu(4, 6), _gpu(9, 3)]
+    for now in (copies, None, copies, None):
+        opt.copies = now
+        opt.step(grads, 0.1, stream=0)
+        rows, _, copy_type = muon_calls[-1]
+        assert rows[:, 4].tolist() == ([0, 0] if now is None else [c.data_ptr() for c in copies])
+        assert copy_type == (B.F32 if now is None else B.BF16)
+
+
 def test_muon_table_follows_the_tensors(monkeypatch):
     """The addresses that reach the library, after parameters and momenta were replaced, without a GPU."""
     import numpy as np

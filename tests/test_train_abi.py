@@ -269,6 +269,17 @@ def test_adamw_writes_where_its_tensors_are_now(adamw_calls, bits):
         opt.bits = 40 - bits
 
 
+@pytest.mark.parametrize("bits", [8, 32])
+def test_adamw_without_its_copies_writes_none(adamw_calls, bits):
+    """Copies that were given up are not written any more, and are again when they come back."""
+    copies = [torch.zeros(300, dtype=torch.bfloat16), torch.zeros(5, dtype=torch.bfloat16)]
+    opt = B.AdamW([torch.zeros(300), torch.zeros(5)], bits=bits, copies=copies)
+    for now in (copies, None, copies, None):
+        opt.copies = now
+        opt.step([torch.zeros(300), torch.zeros(5)], 1e-3, stream=0)
+        assert adamw_calls[-1][:, 3].tolist() == ([0, 0] if now is None else [c.data_ptr() for c in copies])
+
+
 def test_the_stride_of_a_single_row_does_not_matter():
     """One row of a buffer with odd rows (one token, one node) has no next row: its leading dimension is its width."""
     class Gpu(torch.Tensor):
