@@ -8,6 +8,7 @@ no fallback path -- importing this module fails loudly if libqha.so has not been
 from __future__ import annotations
 
 import ctypes as C
+import operator
 import os
 
 import numpy as np
@@ -793,6 +794,13 @@ def residual_norm_bwd(dy, du, y, h, dx, dh, post: int = ROW_RMS, pre: int = ROW_
            "qha_residual_norm_bwd")
 
 
+def _addresses(tensors):
+    return list(map(torch.Tensor.data_ptr, tensors))
+
+
+_dtype_of, _shape_of, _on_gpu = (operator.attrgetter(name) for name in ("dtype", "shape", "is_cuda"))
+
+
 class AdamW:
     """AdamW over a list of float32 parameter tensors, updated in place by qha_adamw_step.
 
@@ -844,10 +852,12 @@ class AdamW:
         return self.params + (self.copies or []) + state
 
     def _look(self):
-        """Checks every tensor and writes its address into the table, if any address is another one than at
-        the last step.  `_held` aliases the tensors seen: while it does, their memory is not handed out again, so an
-        equal address is the same memory."""
-        seen = [t.data_ptr() for t in self._tensors()]
+        """Checks every tensor and writes its address into the table, if any has another address, type, size or
+        order than at the last step.  `_held` aliases the tensors seen: while it does, their memory is not handed out
+        again, so an equal address is the same memory."""
+        tensors = self._tensors()
+        seen = (_addresses(tensors), list(map(_dtype_of, tensors)), list(map(torch.Tensor.numel, tensors)),
+                list(map(torch.Tensor.is_contiguous, tensors)))
         if seen == self._seen:
             return
         self._seen = None
@@ -857,7 +867,7 @@ class AdamW:
         table = self._table
         for i, (p, size) in enumerate(zip(self.params, self.sizes)):
             table[i, 1] = _flat(p, f"params[{i}]", size, torch.float32)
-        if len({t.device for t in self._tensors()}) > 1:
+        if len({t.device for t in tensors}) > 1:
             raise ValueError("parameters, copies and moments must live on one GPU")
         self._copy_type = F32
         table[:, 3] = 0                              # of copies that were given up
@@ -873,7 +883,7 @@ class AdamW:
                 blocks = total // ADAMW_BLOCK
                 table[:n, 6] = _flat(self.m_scale, "m_scale", blocks, torch.float32) + starts // ADAMW_BLOCK * 4
                 table[:n, 7] = _flat(self.v_scale, "v_scale", blocks, torch.float32) + starts // ADAMW_BLOCK * 4
-        self._held = [t.detach() for t in self._tensors()]
+        self._held = [t.detach() for t in tensors]
         self._seen = seen
 
     def step(self, grads, lr: float, grad_scale: float = 1.0, stream=None):
@@ -885,8 +895,11 @@ class AdamW:
             return
         self._look()
         dtype = grads[0].dtype
-        self._table[:n, 2] = [g.data_ptr() if g.dtype is dtype and g.numel() == size and g.is_cuda and g.is_contiguous()
-                              else _flat(g, "a gradient", size, dtype) for g, size in zip(grads, self.sizes)]
+        if set(map(_dtype_of, grads)) == {dtype} and all(map(_on_gpu, grads)) and all(map(torch.Tensor.is_contiguous, grads)) \
+                and list(map(torch.Tensor.numel, grads)) == self.sizes:
+            self._table[:n, 2] = _addresses(grads)
+        else:
+            self._table[:n, 2] = [_flat(g, "a gradient", size, dtype) for g, size in zip(grads, self.sizes)]
         status = _adamw_step(self._table_ptr, n, self._bits, _type(dtype, "grads"), self._copy_type, lr, *self.betas,
                              self.eps, self.weight_decay, grad_scale, self.t + 1, _stream(stream))
         _check(status, "qha_adamw_step")
@@ -1002,10 +1015,12 @@ class Muon:
         return float(scale)
 
     def _look(self):
-        """Checks every tensor and writes its address into the table, if any address is another one than at the last
-        step.  `_held` aliases the tensors seen, so an equal address is the same memory."""
+        """Checks every tensor and writes its address into the table, if any has another address, type, shape or
+        order than at the last step.  `_held` aliases the tensors seen, so an equal address is the same memory."""
         tensors = self.params + self.m + (self.copies or [])
-        seen = [t.data_ptr() for t in tensors]
+        addresses = _addresses(tensors)
+        seen = (addresses, list(map(_dtype_of, tensors)), list(map(_shape_of, tensors)),
+                list(map(torch.Tensor.stride, tensors)))
         if seen == self._seen:
             return
         self._seen = None
@@ -1022,7 +1037,7 @@ class Muon:
                 table[i, column] = _flat(t, f"{name}[{i}]", dtype=self.copies[0].dtype if column == 4 else torch.float32)
         if len({t.device for t in tensors}) > 1:
             raise ValueError("parameters, momenta and copies must live on one GPU")
-        _apart(seen, "parameters, momenta and copies")
+        _apart(addresses, "parameters, momenta and copies")
         need = newton_schulz_workspace(self.shapes, self._steps)
         if need and (self._ws is None or self._ws.device != self.params[0].device):
             self._ws = torch.empty(need, dtype=torch.uint8, device=self.params[0].device)
@@ -1038,11 +1053,17 @@ class Muon:
             return
         self._look()
         dtype = grads[0].dtype
-        for i, (g, shape) in enumerate(zip(grads, self.shapes)):
-            if g.shape != shape:
-                raise ValueError(f"grads[{i}] must be {shape}, got {tuple(g.shape)}")
-            self._table[i, 3] = _flat(g, "a gradient", dtype=dtype)
-        _on_current(self.params[0], *grads)
+        if set(map(_dtype_of, grads)) == {dtype} and list(map(_shape_of, grads)) == self.shapes \
+                and all(map(torch.Tensor.is_contiguous, grads)) \
+                and set(map(torch.Tensor.get_device, grads)) == {torch.cuda.current_device()}:
+            self._table[:n, 3] = _addresses(grads)
+        else:
+            for i, (g, shape) in enumerate(zip(grads, self.shapes)):
+                if g.shape != shape:
+                    raise ValueError(f"grads[{i}] must be {shape}, got {tuple(g.shape)}")
+                self._table[i, 3] = _flat(g, "a gradient", dtype=dtype)
+            _on_current(*grads)
+        _on_current(self.params[0])
         ws, ws_bytes = _space(self._ws)
         _check(_muon_step(self._table.ctypes.data, n, _type(dtype, "grads"), self._copy_type, lr, self.momentum,
                           int(self.nesterov), self.weight_decay, grad_scale, self._steps, self._k.ctypes.data, self.eps,

@@ -291,6 +291,40 @@ def test_muon_without_its_copies_writes_none(muon_calls):
         assert copy_type == (B.F32 if now is None else B.BF16)
 
 
+def test_muon_checks_what_stands_at_a_known_address(muon_calls):
+    """Views of the memory that was there at the last step, with another type, shape or order of their elements."""
+    copies = [_gpu(4, 4, dtype=torch.bfloat16)]
+    opt = B.Muon([_gpu(4, 4)], copies=copies)
+    step = lambda: opt.step([_gpu(4, 4)], 0.1, stream=0)
+    step()
+    assert muon_calls[-1][2] == B.BF16
+    opt.copies = [copies[0].view(torch.float16)]
+    step()
+    assert muon_calls[-1][2] == B.F16
+    calls = len(muon_calls)
+    opt.copies = [copies[0].view(torch.int16)]
+    with pytest.raises(TypeError):
+        step()
+    opt.copies = copies
+    for name in ("params", "m", "copies"):
+        own = getattr(opt, name)
+        for bad, what in ((own[0].t(), "contiguous"), (own[0].view(2, 8), "must be"), (own[0][:3], "must be"),
+                          (own[0].as_strided((4, 4), (2, 1)), "contiguous")):
+            assert bad.data_ptr() == own[0].data_ptr()
+            setattr(opt, name, [bad])
+            with pytest.raises(ValueError, match=what):
+                step()
+        setattr(opt, name, own)
+    # the same object, turned in its place
+    opt.params[0].t_()
+    with pytest.raises(ValueError, match="contiguous"):
+        step()
+    assert len(muon_calls) == calls
+    opt.params[0].t_()
+    step()
+    assert len(muon_calls) == calls + 1
+
+
 def test_muon_table_follows_the_tensors(monkeypatch):
     """The addresses that reach the library, after parameters and momenta were replaced, without a GPU."""
     import numpy as np

@@ -280,6 +280,47 @@ def test_adamw_without_its_copies_writes_none(adamw_calls, bits):
         assert adamw_calls[-1][:, 3].tolist() == ([0, 0] if now is None else [c.data_ptr() for c in copies])
 
 
+@pytest.mark.parametrize("bits", [8, 32])
+def test_adamw_checks_what_stands_at_a_known_address(adamw_calls, bits, monkeypatch):
+    """Views of the memory that was there at the last step, with another type, size or order of their elements."""
+    types, record = [], B._adamw_step
+
+    def with_type(table, n, state_bits, grad_type, copy_type, *rest):
+        types.append(copy_type)
+        return record(table, n, state_bits, grad_type, copy_type, *rest)
+    monkeypatch.setattr(B, "_adamw_step", with_type)
+    copies = [torch.zeros(16, 16, dtype=torch.bfloat16)]
+    opt = B.AdamW([torch.zeros(16, 16)], bits=bits, copies=copies)
+    step = lambda: opt.step([torch.zeros(16, 16)], 1e-3, stream=0)
+    step()
+    opt.copies = [copies[0].view(torch.float16)]
+    step()
+    assert types == [B.BF16, B.F16]
+    opt.copies = copies
+    for name in ("params", "copies"):
+        own = getattr(opt, name)
+        for bad, what in ((own[0].t(), "contiguous"), (own[0][:3], "elements")):
+            assert bad.data_ptr() == own[0].data_ptr()
+            setattr(opt, name, [bad])
+            with pytest.raises(ValueError, match=what):
+                step()
+        setattr(opt, name, own)
+    for name in ("m", "v"):
+        own = getattr(opt, name)
+        for bad in (own.view(torch.float16 if bits == 32 else torch.bool), own[:128]):
+            setattr(opt, name, bad)
+            with pytest.raises((ValueError, TypeError), match=name):
+                step()
+        setattr(opt, name, own)
+    opt.params[0].t_()                   # the same object, turned in its place
+    with pytest.raises(ValueError, match="contiguous"):
+        step()
+    assert len(types) == 2
+    opt.params[0].t_()
+    step()
+    assert len(types) == 3
+
+
 def test_the_stride_of_a_single_row_does_not_matter():
     """One row of a buffer with odd rows (one token, one node) has no next row: its leading dimension is its width."""
     class Gpu(torch.Tensor):
