@@ -965,7 +965,14 @@ def newton_schulz(xs, outs, steps: int = 5, coefficients=NS_COEFFICIENTS, eps: f
         table[i] = rows, cols, *_matrix(x, "a matrix", t, rows, cols), *_matrix(out, "a result", o, rows, cols)
     ws, ws_bytes = _space(workspace)
     _on_current(*xs, *outs, workspace)
-    _apart([o.data_ptr() for o in outs], "results")
+    sources, results = table[:, 2].tolist(), table[:, 4].tolist()
+    _apart(results, "results")
+    own = [i for i in range(n) if results[i] and results[i] == sources[i]]
+    taken = set(results) - {0}
+    if len(own) < sum(p in taken for p in sources):
+        raise ValueError("a result is the memory of another matrix")
+    if any(t != o or table[i, 3] != table[i, 5] for i in own):
+        raise ValueError("a result in place must have its matrix's type and leading dimension")
     _check(_newton_schulz(table.ctypes.data, n, _type(t, "xs"), _type(o, "outs"), steps, k.ctypes.data, eps, ws, ws_bytes,
                           _stream(stream)), "qha_newton_schulz")
 
@@ -1041,6 +1048,7 @@ class Muon:
         need = newton_schulz_workspace(self.shapes, self._steps)
         if need and (self._ws is None or self._ws.device != self.params[0].device):
             self._ws = torch.empty(need, dtype=torch.uint8, device=self.params[0].device)
+        self._memory = set(addresses) - {0}          # tensors without elements have no address
         self._held = [t.detach() for t in tensors]
         self._seen = seen
 
@@ -1064,6 +1072,8 @@ class Muon:
                 self._table[i, 3] = _flat(g, "a gradient", dtype=dtype)
             _on_current(*grads)
         _on_current(self.params[0])
+        if not self._memory.isdisjoint(self._table[:n, 3].tolist()):
+            raise ValueError("a gradient is the memory of a parameter, momentum or copy")
         ws, ws_bytes = _space(self._ws)
         _check(_muon_step(self._table.ctypes.data, n, _type(dtype, "grads"), self._copy_type, lr, self.momentum,
                           int(self.nesterov), self.weight_decay, grad_scale, self._steps, self._k.ctypes.data, self.eps,

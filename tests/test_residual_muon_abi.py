@@ -325,6 +325,31 @@ def test_muon_checks_what_stands_at_a_known_address(muon_calls):
     assert len(muon_calls) == calls + 1
 
 
+def test_results_over_inputs_of_others_are_refused(monkeypatch):
+    """Matrices of one launch are read and written at once, so a result may lie over its own input alone, place by place;
+    gradients are read again after the momenta were written."""
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    done = []
+    monkeypatch.setattr(B, "_newton_schulz", lambda *args: done.append(args) or B.QHA_OK)
+    monkeypatch.setattr(B, "_muon_step", lambda *args: done.append(args) or B.QHA_OK)
+    x, y, z = _gpu(4, 4), _gpu(4, 4), _gpu(4, 4)
+    buf = _gpu(8, 8)
+    for xs, outs in (([x, y], [y, x]), ([x, y], [z, x]), ([x, x], [x, z]), ([buf[:4, :4]], [buf.view(-1)[:16].view(4, 4)]),
+                     ([x], [x.view(torch.float16).view(-1)[:16].view(4, 4)])):
+        with pytest.raises(ValueError, match="another matrix|in place"):
+            B.newton_schulz(xs, outs, stream=0)
+    opt = B.Muon([x, y], copies=[z, _gpu(4, 4)])
+    for grads in ([opt.m[1], z], [x, _gpu(4, 4)], [opt.copies[1], _gpu(4, 4)]):
+        with pytest.raises(ValueError, match="gradient"):
+            opt.step(grads, 0.1, stream=0)
+    assert not done
+    empty = _gpu(0, 4)
+    B.newton_schulz([x, x, buf[:4, :4], empty, empty], [y, z, buf[:4, :4], empty, _gpu(0, 4)], stream=0)
+    opt.step([_gpu(4, 4)] * 2, 0.1, stream=0)              # gradients that are read alone may be the same
+    B.Muon([empty]).step([empty], 0.1, stream=0)
+    assert len(done) == 3
+
+
 def test_muon_table_follows_the_tensors(monkeypatch):
     """The addresses that reach the library, after parameters and momenta were replaced, without a GPU."""
     import numpy as np
