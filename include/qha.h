@@ -515,7 +515,7 @@ size_t qha_residual_norm_workspace(int64_t n_rows, int64_t positions, int32_t c)
  * `steps` times
  *   A = X X^T,   B = a I + b A + c A^2,   X = B X         (X^T X and X B where there are more rows than columns: the same)
  * which takes every singular value s of X to a s + b s^3 + c s^5 and keeps the singular vectors.  out = X.
- * coefficients: host, [steps][3], a, b and c of each step; 1 <= steps <= 16.  They must keep the singular values of X, which
+ * coefficients: host, [steps][3], a, b and c of each step, of at most 1e30; 1 <= steps <= 16.  They must keep the singular values of X, which
  * begin in [0, 1], small: INVALID_ARG if some s in [0, 1] can pass 3.8 in size (X's bound, A's its square) or a + b s^2 + c s^4
  * 60 on the way, by the largest values that each step's polynomials take and what rounding adds to them (2e-6 of the sizes of
  * a step's terms: steps that grow it without bound, from a fixed point that is steep, are refused).  3.4445, -4.7750, 2.0315 in

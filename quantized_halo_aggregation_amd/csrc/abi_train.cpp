@@ -137,20 +137,17 @@ int take_gated_workspace(qha::GatedArgs& g, bool backward, void* ws, size_t byte
 }
 
 constexpr int64_t kMaxSide = 1 << 16;       // rows and columns of a matrix to orthogonalise
+constexpr double kMostCoefficient = 1e30;   // of a Newton-Schulz step: its products with the scales stay in float32's range
 
-// The largest magnitude of f(s) = s (a + b s^2 + c s^4) over [0, top]: at its ends or where f' = a + 3 b t + 5 c t^2 = 0, t = s^2.
-double largest_of(double a, double b, double c, double top) {
-  const auto f = [&](double s) { return std::fabs(s * (a + s * s * (b + s * s * c))); };
-  double most = f(top);
+// The largest magnitude of f(r) = r (a + b r^2 + c r^4) on [0, 1]: at its end or where f' = a + 3 b t + 5 c t^2 = 0, t = r^2.
+double largest_of(double a, double b, double c) {
+  const auto f = [&](double r) { return std::fabs(r * (a + r * r * (b + r * r * c))); };
+  double most = f(1.0);
   const double d = 9.0 * b * b - 20.0 * a * c;
-  double roots[3] = {-1.0, -1.0, -1.0};
-  if (c != 0.0 && d >= 0.0) {
-    roots[0] = (-3.0 * b + std::sqrt(d)) / (10.0 * c);
-    roots[1] = (-3.0 * b - std::sqrt(d)) / (10.0 * c);
-  }
-  if (b != 0.0) roots[2] = -a / (3.0 * b);      // also near it where c is tiny
-  for (double t : roots)
-    if (t > 0.0 && t < top * top) most = std::max(most, f(std::sqrt(t)));
+  if (d < 0.0) return most;
+  const double q = -0.5 * (3.0 * b + std::copysign(std::sqrt(d), b));      // no difference of equals, whichever root is small
+  for (double t : {q / (5.0 * c), a / q})
+    if (t > 0.0 && t < 1.0) most = std::max(most, f(std::sqrt(t)));          // 0 / 0 and x / 0 are not
   return most;
 }
 
@@ -162,15 +159,17 @@ int check_steps(int32_t steps, const double* coefficients, double eps) {
   if (!(eps >= 0.0) || !std::isfinite(eps)) return fail(QHA_ERR_INVALID_ARG, "eps must be finite and not negative");
   double top = 1.0;
   for (int32_t i = 0; i < steps; ++i) {
-    const double a = coefficients[3 * i], b = coefficients[3 * i + 1], c = coefficients[3 * i + 2];
-    if (!std::isfinite(a) || !std::isfinite(b) || !std::isfinite(c)) return fail(QHA_ERR_INVALID_ARG, "a coefficient is not finite");
-    const double t = top * top;
-    double inner = std::max(std::fabs(a), std::fabs(a + t * (b + c * t)));       // |a + b t + c t^2| over [0, top^2]
-    if (c != 0.0 && -b / (2.0 * c) > 0.0 && -b / (2.0 * c) < t) inner = std::max(inner, std::fabs(a - b * b / (4.0 * c)));
+    for (int32_t e = 0; e < 3; ++e)
+      if (!(std::fabs(coefficients[3 * i + e]) <= kMostCoefficient)) return fail(QHA_ERR_INVALID_ARG, "step %d: a coefficient is not finite or passes 1e30", i);
+    // in units of top: with s = top r, a + b s^2 + c s^4 = a + (b top^2) r^2 + (c top^4) r^4
+    const double t = top * top, a = coefficients[3 * i], b = coefficients[3 * i + 1] * t, c = coefficients[3 * i + 2] * t * t;
+    double inner = std::max(std::fabs(a), std::fabs(a + b + c));
+    const double turn = -0.5 * (b / c);
+    if (turn > 0.0 && turn < 1.0) inner = std::max(inner, std::fabs(a + 0.5 * b * turn));
     if (!(inner <= 60.0)) return fail(QHA_ERR_INVALID_ARG, "step %d: a + b s^2 + c s^4 passes 60", i);
-    const double most = largest_of(a, b, c, top);
+    const double most = top * largest_of(a, b, c);
     if (!(most <= 3.8)) return fail(QHA_ERR_INVALID_ARG, "step %d: singular values pass 3.8", i);
-    top = most + 2e-6 * top * (std::fabs(a) + t * (std::fabs(b) + t * std::fabs(c)));
+    top = most + 2e-6 * top * (std::fabs(a) + std::fabs(b) + std::fabs(c));
   }
   return QHA_OK;
 }

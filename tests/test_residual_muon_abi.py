@@ -211,6 +211,25 @@ def test_coefficients_that_stay_in_range_are_taken():
         B._ns_coefficients((1, 2), 5)
 
 
+def test_coefficients_of_any_size_are_checked():
+    """The bounds are formed in float64, whose squares and sums of the largest coefficients are infinite, and the steps in float32,
+    which ends at 3.4e38."""
+    def status(k, steps=1):
+        return B._newton_schulz(None, 0, B.F32, B.F32, steps, B._ns_coefficients(k, steps).ctypes.data, 0.0, None, 0, None)
+    big = 1.7e308
+    # at s^2 = 1/2 the first is 1 - 2.5e307; the others pass at the end, or inside [0, 1]
+    for k in ((1, -1e308, 1e308), (1, -big, big), (0, big, -big), (1, 0, big), (big, -big, 0), (-big, big, 1), (1, -1e154, 1e154),
+              (1, 1e300, -1e300), (0, 0, -big)):
+        assert status(k) == B.QHA_ERR_INVALID_ARG, k
+        assert status([B.NS_COEFFICIENTS, k], 2) == B.QHA_ERR_INVALID_ARG, k
+    # singular values of up to 1e-3, 1e-150 and 0 would bear these, float32 does not
+    for first, k in ((1e-3, (1, -1e300, 0)), (1e-150, (1, 1e299, 0)), (1e-150, (1, 0, 1e300)), (0, (1, 1e300, -1e300)), (0, (0, 0, 1e39))):
+        assert status([(first, 0, 0), k], 2) == B.QHA_ERR_INVALID_ARG, k
+    # and these it does: 3 - 3 + 3 at s = 1e-3
+    assert status([(1e-3, 0, 0), (3, -3e6, 3e12)], 2) == B.QHA_OK
+    assert status([(1e-3, 0, 0), (3, -3e6, 70e12)], 2) == B.QHA_ERR_INVALID_ARG
+
+
 def test_newton_schulz_and_muon_binding_refuse(monkeypatch):
     monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
     x = _gpu(4, 6)
