@@ -153,11 +153,15 @@ double largest_of(double a, double b, double c) {
 
 // The polynomials must keep X, A and B within the scaled parts' range, also where rounding takes a singular value past what the
 // exact ones reach: a step's is below 2e-6 (16 units of float32) of its terms, and the next steps may grow it.
-int check_steps(int32_t steps, const double* coefficients, double eps) {
+int check_steps(qha::NsArgs& args, int32_t steps, const double* coefficients, double eps) {
+  args.steps = steps;
+  args.eps = eps;
+  args.coefficients = coefficients;
   if (steps < 1 || steps > qha::kNsSteps) return fail(QHA_ERR_INVALID_ARG, "steps must lie in 1 .. %d, got %d", qha::kNsSteps, steps);
   if (!coefficients) return fail(QHA_ERR_INVALID_ARG, "coefficients is NULL");
   if (!(eps >= 0.0) || !std::isfinite(eps)) return fail(QHA_ERR_INVALID_ARG, "eps must be finite and not negative");
   double top = 1.0;
+  args.most_x[0] = top;
   for (int32_t i = 0; i < steps; ++i) {
     for (int32_t e = 0; e < 3; ++e)
       if (!(std::fabs(coefficients[3 * i + e]) <= kMostCoefficient)) return fail(QHA_ERR_INVALID_ARG, "step %d: a coefficient is not finite or passes 1e30", i);
@@ -169,7 +173,9 @@ int check_steps(int32_t steps, const double* coefficients, double eps) {
     if (!(inner <= 60.0)) return fail(QHA_ERR_INVALID_ARG, "step %d: a + b s^2 + c s^4 passes 60", i);
     const double most = top * largest_of(a, b, c);
     if (!(most <= 3.8)) return fail(QHA_ERR_INVALID_ARG, "step %d: singular values pass 3.8", i);
-    top = most + 2e-6 * top * (std::fabs(a) + std::fabs(b) + std::fabs(c));
+    const double rounding = 2e-6 * (std::fabs(a) + std::fabs(b) + std::fabs(c));
+    args.most_b[i] = inner + rounding;
+    args.most_x[i + 1] = top = most + top * rounding;
   }
   return QHA_OK;
 }
@@ -486,7 +492,8 @@ int qha_newton_schulz(const qha_ns_matrix* matrices, int64_t n_matrices, int32_t
                       const double* coefficients, double eps, void* workspace, size_t workspace_bytes, void* stream) {
   if (n_matrices < 0) return fail(QHA_ERR_INVALID_ARG, "n_matrices < 0");
   if (!known_type(type) || !known_type(out_type)) return fail(QHA_ERR_INVALID_ARG, "unknown element type");
-  int st = check_steps(steps, coefficients, eps);
+  qha::NsArgs a = {};
+  int st = check_steps(a, steps, coefficients, eps);
   if (st) return st;
   if (n_matrices == 0) return ok();
   if (!matrices) return fail(QHA_ERR_INVALID_ARG, "matrices is NULL");
@@ -507,12 +514,8 @@ int qha_newton_schulz(const qha_ns_matrix* matrices, int64_t n_matrices, int32_t
     list[i].ldo = m.ldo;
   }
   if ((st = check_ns_workspace(list.get(), n_matrices, workspace, workspace_bytes))) return st;
-  qha::NsArgs a = {};
   a.type = type;
   a.out_type = out_type;
-  a.steps = steps;
-  a.eps = eps;
-  a.coefficients = coefficients;
   return hip_status(qha::launch_ns(list.get(), n_matrices, a, workspace, static_cast<hipStream_t>(stream)), "newton_schulz");
 }
 
@@ -525,7 +528,8 @@ int qha_muon_step(const qha_muon_matrix* matrices, int64_t n_matrices, int32_t g
       !std::isfinite(weight_decay) || !std::isfinite(static_cast<float>(grad_scale)))
     return fail(QHA_ERR_INVALID_ARG, "lr and weight_decay must be finite and not negative, grad_scale finite");
   if (!(beta >= 0.0 && beta < 1.0)) return fail(QHA_ERR_INVALID_ARG, "beta must lie in [0, 1)");
-  int st = check_steps(steps, coefficients, eps);
+  qha::NsArgs a = {};
+  int st = check_steps(a, steps, coefficients, eps);
   if (st) return st;
   if (n_matrices == 0) return ok();
   if (!matrices) return fail(QHA_ERR_INVALID_ARG, "matrices is NULL");
@@ -549,17 +553,13 @@ int qha_muon_step(const qha_muon_matrix* matrices, int64_t n_matrices, int32_t g
     list[i].step = static_cast<float>(lr * m.scale);
   }
   if ((st = check_ns_workspace(list.get(), n_matrices, workspace, workspace_bytes))) return st;
-  qha::NsArgs a = {};
   a.type = grad_type;
   a.out_type = copy_type;
   a.muon = 1;
   a.nesterov = nesterov != 0;
-  a.steps = steps;
   a.mu = static_cast<float>(beta);
   a.grad_scale = static_cast<float>(grad_scale);
   a.decay = static_cast<float>(1.0 - lr * weight_decay);
-  a.eps = eps;
-  a.coefficients = coefficients;
   return hip_status(qha::launch_ns(list.get(), n_matrices, a, workspace, static_cast<hipStream_t>(stream)), "muon_step");
 }
 

@@ -5,11 +5,16 @@
 // which moves every singular value s of X to a s + b s^3 + c s^5 and keeps the singular vectors.  U is the input, or the step's
 // momentum: M = mu M + g, U = g + mu M (Nesterov) or M.  The step ends with p = decay p - step X.
 //
-// Singular values of X stay below a few units (the host checks the polynomials), so its entries and those of A and B do, too:
-// a power of two puts them where half precision has all its bits, and a float32 value is two f16 parts, hi + lo, to 2^-23
-// of itself.  A product is rebuilt from hi hi, hi lo and lo hi (the dropped lo lo is below 2^-22 of a term, 2^-25 on the root mean
-// square), summed in float32 by the matrix cores: half of what three bf16 parts would cost (six products), at
-// float32's error, which the smallest singular values amplify by up to a^steps either way.
+// The host follows the largest singular value through the polynomials, which bounds X's entries and those of A and B: a power of two
+// a step takes each bound to the end of half precision's range, and a float32 value is two f16 parts, hi + lo, to 2^-23 of
+// itself above 2^-17 of the bound, below that to 2^-40 of the bound.  A product is rebuilt from hi hi, hi lo and lo hi (the dropped
+// lo lo is below 2^-22 of a term, 2^-25 on the root mean square), summed in float32 by the matrix cores: half of what three bf16
+// parts would cost (six products).  So a result has float32's precision with respect to its norm, which the smallest singular
+// values amplify by up to a^steps either way, but not each row or column that is small by itself.  Measured, off by this share of the
+// norm after five steps, in brackets the same with float32 products: noise of 256 x 256 6e-7 (1.7e-6), of 4096 x 4096 3.3e-6 (4.8e-6); singular
+// values falling to 1e-4, 128 x 128 5.0e-6 (3.6e-6), 1024 x 1024 5.5e-6 (4.6e-6).  The worst row's share of itself where rows fade
+// to 1e-6: 256 x 256 2.8e-5 (5e-6), 1024 x 1024 1.1e-4 (1.8e-5), 4096 x 4096 4.3e-4 (3.6e-5); with one scale for any
+// coefficients 2.2e-4, 8.6e-4 and 3.5e-3.  Second parts with a scale of their own would need accumulators of their own, twice as many.
 // What bounds it, and the forms that follow from it (five steps, float32, us a call):
 //   - Large matrices: the matrix cores.  Tiles through LDS, A and B by their tiles on and below the diagonal (the others are stored
 //     as their mirror), three launches a step for a batch of up to 40 matrices, whose tables the launches share.  4096 x 4096 3490 to 3680:
@@ -23,13 +28,13 @@
 #include "qha_internal.hpp"
 #include "tile_common.hpp"
 
-#include <cstring>
+#include <cmath>
 
 namespace qha {
 namespace {
 
-// What X, A and B are multiplied by: their entries stay below 16, 16 and 64.
-constexpr float kScaleX = 4096.0f, kScaleA = 4096.0f, kScaleB = 1024.0f;
+// What the first X is multiplied by, whose values are at most 1 (see half_scale).
+constexpr float kScaleX = 32768.0f;
 
 __device__ __forceinline__ f32x4 load4(const void* p, int64_t at, int32_t type) {
   if (type == QHA_F32) return *reinterpret_cast<const f32x4*>(static_cast<const float*>(p) + at);
@@ -285,7 +290,7 @@ __global__ __launch_bounds__(256) void ns_split_kernel(const NsTable* table, NsF
 
 constexpr int kPartRow = 36;         // floats of a row of 32 in LDS, padded to spread columns over the banks
 
-// The results from a block of 32 x 32 of the last X (times kScaleX) in LDS, rows x0 .., columns y0 ..: thread `id` of N takes four
+// The results from a block of 32 x 32 of the last X (times its scale) in LDS, rows x0 .., columns y0 ..: thread `id` of N takes four
 // neighbours of the matrix's rows, so that eight threads write whole lines.  (Straight from the accumulators, 16 bytes of 32 rows
 // at a time, the last product of 4096 x 4096 took 1638 us, the others 372.)
 template <int N>
@@ -301,7 +306,7 @@ __device__ __forceinline__ void finish_block(const NsTable& t, const NsMat& a, c
     } else {
       o = *reinterpret_cast<const f32x4*>(v + r * kPartRow + c);
     }
-    return o * (1.0f / kScaleX);
+    return o * t.result;
   };
   if (t.muon && a.vec_out && (!a.copy || a.vec_copy) && r0 + 32 <= a.rows && c0 + 32 <= a.cols) {
     // whole blocks of aligned weights: every weight on its way before the first is needed (24 of 4096 x 1024 with a copy,
@@ -727,7 +732,7 @@ __device__ __forceinline__ void chip_steps_square(uint16_t* lx, uint16_t* la, co
         a[o] = three(q[0], p[0], a[o]);
         a[o] = three(q[1], p[1], a[o]);
       }
-      a[o] *= k.gram.product;
+      a[o] *= k.gram[step];
       chip_put(la, LD, bi[o], bj[o], lane, a[o]);
     }
     __syncthreads();
@@ -769,8 +774,8 @@ __device__ __forceinline__ void chip_steps_square(uint16_t* lx, uint16_t* la, co
         for (int o = 0; o < 2; ++o) x[o] = three(q[h], p[o][h], x[o]);
     }
     __syncthreads();                 // everyone has read X
-    chip_put(lx, LD, xi, xj, lane, x[0] * k.apply.product);
-    chip_put(lx, LD, xi + 1, xj, lane, x[1] * k.apply.product);
+    chip_put(lx, LD, xi, xj, lane, x[0] * k.apply[step]);
+    chip_put(lx, LD, xi + 1, xj, lane, x[1] * k.apply[step]);
     __syncthreads();
   }
 }
@@ -813,7 +818,7 @@ __device__ __forceinline__ void chip_steps(uint16_t* lx, uint16_t* la, float* pa
           f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
           for (int w = 0; w < share; ++w) v += *reinterpret_cast<const f32x4*>(parts + (w * 32 + r) * kPartRow + c);
           f16x4 hi, lo;
-          split2(v * k.gram.product, hi, lo);
+          split2(v * k.gram[step], hi, lo);
           *reinterpret_cast<f16x4*>(chip_at(la, LDA, i * 32 + r, j * 32 + c, 0)) = hi;
           *reinterpret_cast<f16x4*>(chip_at(la, LDA, i * 32 + r, j * 32 + c, 1)) = lo;
         }
@@ -853,7 +858,7 @@ __device__ __forceinline__ void chip_steps(uint16_t* lx, uint16_t* la, float* pa
         }
       }
 #pragma unroll
-      for (int i = 0; i < MB; ++i) chip_put(lx, n64, i, xj, lane, x[i] * k.apply.product);
+      for (int i = 0; i < MB; ++i) chip_put(lx, n64, i, xj, lane, x[i] * k.apply[step]);
     }
     __syncthreads();
   }
@@ -953,7 +958,7 @@ __global__ __launch_bounds__(kChipThreads) void ns_chip_kernel(NsTable t, NsStep
     } else {
       v = chip_get4(lx, n64, r, c);
     }
-    apply4(t, a, r, c, v * (1.0f / kScaleX));
+    apply4(t, a, r, c, v * t.result);
   }
 }
 
@@ -1173,6 +1178,13 @@ int place_of(const NsMatrix& m) {
   return rows == 4 ? ON_CHIP_SQUARE : rows ? ON_CHIP : IN_MEMORY;
 }
 
+// The power of two that takes values of at most `most` to the end of half precision's range (65504, less what rounding may add), at most
+// 2^largest, where steps have shrunk X to nothing.
+double half_scale(double most, int largest) {
+  const double bound = std::ldexp(1.0, largest);
+  return most * bound > 60000.0 ? std::ldexp(1.0, std::ilogb(60000.0 / most)) : bound;
+}
+
 // The next batch of matrices of a place from *at on: their indices, at most kNsBatch.
 int next_batch(const NsMatrix* m, int64_t n, int place, int64_t* at, int64_t* index) {
   int count = 0;
@@ -1251,10 +1263,11 @@ void run_step(const NsTable* t, const NsPlan& plan, const NsTiles& gram, const N
               int64_t most_m, int64_t most_n, const NsSteps& k, int step, hipStream_t s) {
   const int from = step & 1;
   const bool last = step + 1 == k.steps;
+  const NsCoef gr = {k.gram[step], 0.0f, 0.0f}, ap = {k.apply[step], 0.0f, 0.0f};
   if (plan.direct) {
-    const NsCoef &sq = k.square[step], &ap = k.apply;
+    const NsCoef& sq = k.square[step];
     constexpr int NT = kDirectWaves * 64;
-    ns_direct_kernel<NS_GRAM, false><<<gram.grid(), NT, 0, s>>>(t, gram.first, sq, k.gram, from, gram.total);
+    ns_direct_kernel<NS_GRAM, false><<<gram.grid(), NT, 0, s>>>(t, gram.first, sq, gr, from, gram.total);
     if (!plan.fused) ns_direct_kernel<NS_SQUARE, false><<<square.grid(), NT, 0, s>>>(t, square.first, sq, sq, from, square.total);
     if (plan.fused && last) ns_direct_kernel<NS_LAST, true><<<all.grid(), NT, 0, s>>>(t, all.first, sq, ap, from, all.total);
     else if (plan.fused) ns_direct_kernel<NS_APPLY, true><<<all.grid(), NT, 0, s>>>(t, all.first, sq, ap, from, all.total);
@@ -1262,10 +1275,10 @@ void run_step(const NsTable* t, const NsPlan& plan, const NsTiles& gram, const N
     else ns_direct_kernel<NS_APPLY, false><<<all.grid(), NT, 0, s>>>(t, all.first, sq, ap, from, all.total);
     return;
   }
-  run_product<NS_GRAM>(t, gram, most_n, k.gram, from, s);
+  run_product<NS_GRAM>(t, gram, most_n, gr, from, s);
   run_product<NS_SQUARE>(t, square, most_m, k.square[step], from, s);
-  if (last) run_product<NS_LAST>(t, all, most_m, k.apply, from, s);
-  else run_product<NS_APPLY>(t, all, most_m, k.apply, from, s);
+  if (last) run_product<NS_LAST>(t, all, most_m, ap, from, s);
+  else run_product<NS_APPLY>(t, all, most_m, ap, from, s);
 }
 
 }  // namespace
@@ -1296,12 +1309,18 @@ hipError_t launch_ns(const NsMatrix* m, int64_t n, const NsArgs& args, void* ws,
   t.eps = args.eps;
   NsSteps k = {};
   k.steps = args.steps;
-  k.gram = {kScaleA / (kScaleX * kScaleX), 0.0f, 0.0f};
-  k.apply = {1.0f / kScaleB, 0.0f, 0.0f};
+  double scale_x = kScaleX;
   for (int i = 0; i < args.steps; ++i) {
     const double a = args.coefficients[3 * i], b = args.coefficients[3 * i + 1], c = args.coefficients[3 * i + 2];
-    k.square[i] = {static_cast<float>(c * (kScaleB / (kScaleA * kScaleA))), static_cast<float>(b * (kScaleB / kScaleA)), static_cast<float>(a * kScaleB)};
+    // X's and B's scales are float32 values, as are all ratios, which differ from their bounds' by less than 2^17
+    const double scale_a = half_scale(args.most_x[i] * args.most_x[i], 240), scale_b = half_scale(args.most_b[i], 120);
+    const double next = half_scale(args.most_x[i + 1], 120);
+    k.gram[i] = static_cast<float>(scale_a / (scale_x * scale_x));
+    k.square[i] = {static_cast<float>(c * (scale_b / (scale_a * scale_a))), static_cast<float>(b * (scale_b / scale_a)), static_cast<float>(a * scale_b)};
+    k.apply[i] = static_cast<float>(next / (scale_b * scale_x));
+    scale_x = next;
   }
+  t.result = static_cast<float>(1.0 / scale_x);
   int64_t index[kNsBatch];
   bool launched = false;
   NsPlan plan = {};

@@ -294,6 +294,7 @@ size_t residual_workspace(const ResidualArgs& a);
 hipError_t launch_residual(const ResidualArgs& a, bool backward, hipStream_t s);
 
 // Newton-Schulz products of matrices: what a call gives of each of them ...
+constexpr int kNsBatch = 40, kNsSteps = 16;
 struct NsMatrix {
   int64_t rows, cols;
   const void* src;                   // the matrix, or its gradient
@@ -310,9 +311,9 @@ struct NsArgs {
   float mu, grad_scale, decay;       // decay: 1 - learning rate * weight decay
   double eps;
   const double* coefficients;        // [steps][3]
+  double most_x[kNsSteps + 1], most_b[kNsSteps];      // what X's and B's values cannot pass before each step and in it
 };
 // ... and a batch of them, as the kernels read it.
-constexpr int kNsBatch = 40, kNsSteps = 16;
 struct NsMat {
   const void* src;
   int64_t lds;
@@ -329,6 +330,7 @@ struct NsTable {
   NsMat m[kNsBatch];
   int32_t n, piece_rows, transposes, type, out_type, muon, nesterov;
   float mu, grad_scale, decay;
+  float result;                      // the results are the last X's values times this
   double eps;
 };
 struct NsFirst {                       // the first blocks of a launch's matrices
@@ -340,7 +342,8 @@ struct NsCoef {
 };
 struct NsSteps {
   int32_t steps;
-  NsCoef gram, apply, square[kNsSteps];
+  float gram[kNsSteps], apply[kNsSteps];
+  NsCoef square[kNsSteps];
 };
 static_assert(sizeof(NsTable) + sizeof(NsSteps) <= 4096 && sizeof(NsTable) + sizeof(NsFirst) <= 4096, "kernel arguments");
 static_assert(sizeof(NsTable) % 8 == 0, "copied by words");
