@@ -10,11 +10,15 @@
 // itself above 2^-17 of the bound, below that to 2^-40 of the bound.  A product is rebuilt from hi hi, hi lo and lo hi (the dropped
 // lo lo is below 2^-22 of a term, 2^-25 on the root mean square), summed in float32 by the matrix cores: half of what three bf16
 // parts would cost (six products).  So a result has float32's precision with respect to its norm, which the smallest singular
-// values amplify by up to a^steps either way, but not each row or column that is small by itself.  Measured, off by this share of the
-// norm after five steps, in brackets the same with float32 products: noise of 256 x 256 6e-7 (1.7e-6), of 4096 x 4096 3.3e-6 (4.8e-6); singular
-// values falling to 1e-4, 128 x 128 5.0e-6 (3.6e-6), 1024 x 1024 5.5e-6 (4.6e-6).  The worst row's share of itself where rows fade
-// to 1e-6: 256 x 256 2.8e-5 (5e-6), 1024 x 1024 1.1e-4 (1.8e-5), 4096 x 4096 4.3e-4 (3.6e-5); with one scale for any
-// coefficients 2.2e-4, 8.6e-4 and 3.5e-3.  Second parts with a scale of their own would need accumulators of their own, twice as many.
+// values amplify by up to a^steps either way, but not each row or column that is small by itself.  a X, the largest term of most values, is
+// added to a product's result (on chip, where X's blocks stay in registers) or goes through the last product as B's diagonal, where
+// it passes few additions: tiles take their own rows' steps last, and blocks straight from memory add that wavefront's sum last.  (Reading
+// X for it instead took 3 to 6 % of a step in memory; the steps in their places left 5.0e-6 for the second 2.8e-6 below, 5.5e-6 for the third.)
+// Measured, off by this share of the norm after five steps, in brackets the same with a library's float32 products: noise of 256 x 256
+// 6e-7 (1.7e-6), of 4096 x 4096 2.5e-6 (4.8e-6); singular values falling to 1e-4, 128 x 128 2.8e-6 (3.6e-6), 1024 x 1024 2.8e-6
+// (4.6e-6).  The worst row's share of itself where rows fade to 1e-6: 256 x 256 2.8e-5 (5e-6), 1024 x 1024 1.1e-4 (1.8e-5),
+// 4096 x 4096 4.3e-4 (3.6e-5); with one scale for any coefficients 2.2e-4, 8.6e-4 and 3.5e-3.  Second parts with a scale of their own would
+// need accumulators of their own, twice as many.
 // What bounds it, and the forms that follow from it (five steps, float32, us a call):
 //   - Large matrices: the matrix cores.  Tiles through LDS, A and B by their tiles on and below the diagonal (the others are stored
 //     as their mirror), three launches a step for a batch of up to 40 matrices, whose tables the launches share.  4096 x 4096 3490 to 3680:
@@ -360,6 +364,10 @@ struct Stager {
       at[i] = base + run * kBlock + (id & (PER - 1)) * 8;
     }
   }
+  __device__ __forceinline__ void move(int steps) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) at[i] += steps * next_by;
+  }
   // `lds`: the wavefront's part of the buffer
   __device__ __forceinline__ void load(const uint16_t* lds) {
     const uint32_t to = __builtin_amdgcn_readfirstlane(lds_address(lds));
@@ -371,8 +379,7 @@ struct Stager {
   }
 };
 
-// Four neighbours of a row of B = a I + b A + c A^2 from c A^2's and A's.  The unit matrix's a goes through the last product with the
-// rest: that product then reads X once and adds nothing to its results.
+// Four neighbours of a row of B = a I + b A + c A^2 from c A^2's and A's.
 __device__ __forceinline__ f32x4 square_terms(const NsCoef& k, f32x4 v, f32x4 of_a, int64_t row, int64_t col) {
   v += of_a * k.own;
 #pragma unroll
@@ -442,10 +449,36 @@ __global__ __launch_bounds__(WM * WN * KS * 64) void ns_product_kernel(const NsT
 #pragma unroll
     for (int j = 0; j < NI; ++j) acc[ii][j] = 0.0f;
   const int whole = static_cast<int>(depth / BK), steps = (whole + KS - 1) / KS;
-  const int64_t begin = static_cast<int64_t>(group) * steps;
   const bool blank = KS == 2 && group == 1 && (whole & 1);           // a second half of one step fewer begins with zeros
-  Stager<false, BM, NT> sp(P, m_pad / 32, depth / 16, static_cast<int64_t>(mt) * (BM / 32), id, begin);
-  Stager<!SYM, BN, NT> sq(Q, m_pad / 32, (SYM ? depth : n_pad) / 16, static_cast<int64_t>(nt) * (SYM ? BN / 32 : BN / 16), id, begin);
+  // In B X the steps of the tile's own rows, where B's diagonal brings a X in, come last: two jumps over the reduction's steps.  (A
+  // reduction that begins behind them and turns took 2 % more: blocks beside each other then read X at different places.)
+  const int mine = blank ? steps - 1 : steps;                        // of this group
+  int first_step = group * steps, left = 0, jump = 0;      // loads left to the next jump, and its steps
+  int after = 0, back = 0;             // the same of the jump behind it
+  if constexpr (!SYM) {
+    const int end = first_step + mine, own_end = (mt + 1) * (BM / BK);
+    const int own_begin = mt * (BM / BK) > first_step ? mt * (BM / BK) : first_step;
+    if (own_begin < own_end && own_end < end) {
+      left = own_begin - first_step;
+      jump = own_end - own_begin;
+      after = end - own_end;
+      back = own_begin - end;
+      if (left == 0) {                 // they are the first ones
+        first_step = own_end;
+        left = after;
+        jump = back;
+      }
+    }
+  }
+  Stager<false, BM, NT> sp(P, m_pad / 32, depth / 16, static_cast<int64_t>(mt) * (BM / 32), id, first_step);
+  Stager<!SYM, BN, NT> sq(Q, m_pad / 32, (SYM ? depth : n_pad) / 16, static_cast<int64_t>(nt) * (SYM ? BN / 32 : BN / 16), id, first_step);
+  const auto jump_over = [&] {
+    if (SYM || --left != 0) return;
+    sp.move(jump);
+    sq.move(jump);
+    left = jump == back ? 0 : after;
+    jump = back;
+  };
   constexpr int EACH = decltype(sp)::N + decltype(sq)::N;      // loads of a thread for a step
   // A step's operands come out of LDS in two halves of 16.  The first half of step s + 1 is read while the second half of step s is
   // multiplied: the wait for its loads and the barrier lie in the middle of step s, where they find the matrix cores busy.
@@ -495,6 +528,7 @@ __global__ __launch_bounds__(WM * WN * KS * 64) void ns_product_kernel(const NsT
   for (int s = blank ? 1 : 0; s < STAGES && s < steps; ++s) {
     sp.load(to + s * BUF);
     sq.load(to + s * BUF + A_SIZE);
+    jump_over();
   }
   if (steps >= STAGES) loads_left<(STAGES - 1) * EACH>();
   else loads_left<0>();
@@ -517,7 +551,10 @@ __global__ __launch_bounds__(WM * WN * KS * 64) void ns_product_kernel(const NsT
     multiply_term(p1, q1, 0);
     if (more) sp.load(to + now * BUF);
     multiply_term(p1, q1, 1);
-    if (more) sq.load(to + now * BUF + A_SIZE);
+    if (more) {
+      sq.load(to + now * BUF + A_SIZE);
+      jump_over();
+    }
     multiply_term(p1, q1, 2);
     now = next;
   }
@@ -694,14 +731,8 @@ __device__ __forceinline__ f32x16 chip_get(uint16_t* lds, int ld, int bi, int bj
   return v;
 }
 
-// A block of B = a I + b A + c A^2 from c A^2's and A's.
-__device__ __forceinline__ f32x16 square_block(const NsCoef& k, f32x16 c, f32x16 a, bool diagonal, int lane) {
-  c += a * k.own;
-  if (diagonal)
-#pragma unroll
-    for (int e = 0; e < 16; ++e) c[e] += 8 * (e >> 2) + 4 * (lane >> 5) + (e & 3) == (lane & 31) ? k.unit : 0.0f;
-  return c;
-}
+// On chip B is b A + c A^2: the wavefronts keep their blocks of X in registers as float32 from step to step, and a X is added to a
+// product's result.
 
 // The steps of a matrix of 97 to 128 rows and columns.  The ten blocks of a symmetric result go to the eight wavefronts so that
 // each of the four SIMDs (wavefronts w and w + 4) has two or three; X's sixteen go two to each.  A wavefront keeps its blocks of
@@ -713,6 +744,7 @@ __device__ __forceinline__ void chip_steps_square(uint16_t* lx, uint16_t* la, co
   const int n_own = wave < 2 ? 2 : 1;
   const int bi[2] = {0x33232120 >> 4 * wave & 15, 2 * wave + 1}, bj[2] = {0x21100020 >> 4 * wave & 15, 2 * wave + 1};
   const int xi = (wave >> 2) * 2, xj = wave & 3;                     // X's blocks (xi, xj) and (xi + 1, xj)
+  f32x16 own[2] = {chip_get(lx, LD, xi, xj, lane), chip_get(lx, LD, xi + 1, xj, lane)};
   for (int step = 0; step < k.steps; ++step) {
     f32x16 a[2];
 #pragma unroll
@@ -753,7 +785,7 @@ __device__ __forceinline__ void chip_steps_square(uint16_t* lx, uint16_t* la, co
         c = three(q[0], p[0], c);
         c = three(q[1], p[1], c);
       }
-      a[o] = square_block(k.square[step], c * k.square[step].product, a[o], bi[o] == bj[o], lane);
+      a[o] = c * k.square[step].product + a[o] * k.square[step].own;
     }
     __syncthreads();                 // everyone has read A
 #pragma unroll
@@ -774,8 +806,11 @@ __device__ __forceinline__ void chip_steps_square(uint16_t* lx, uint16_t* la, co
         for (int o = 0; o < 2; ++o) x[o] = three(q[h], p[o][h], x[o]);
     }
     __syncthreads();                 // everyone has read X
-    chip_put(lx, LD, xi, xj, lane, x[0] * k.apply[step]);
-    chip_put(lx, LD, xi + 1, xj, lane, x[1] * k.apply[step]);
+#pragma unroll
+    for (int o = 0; o < 2; ++o) {
+      own[o] = x[o] * k.apply[step] + own[o] * k.own[step];
+      chip_put(lx, LD, xi + o, xj, lane, own[o]);
+    }
     __syncthreads();
   }
 }
@@ -784,8 +819,16 @@ __device__ __forceinline__ void chip_steps_square(uint16_t* lx, uint16_t* la, co
 // block; a column block of X is a wavefront's own.
 template <int MB>
 __device__ __forceinline__ void chip_steps(uint16_t* lx, uint16_t* la, float* parts, int n64, const NsSteps& k, int lane, int wave) {
-  constexpr int LDA = Chip<MB>::LDA, S = MB * (MB + 1) / 2;
+  constexpr int LDA = Chip<MB>::LDA, S = MB * (MB + 1) / 2, COLS = (Chip<MB>::CAP / 32 + kChipWaves - 1) / kChipWaves;
   const ChipMatrix mx(lx, n64, lane), ma(la, LDA, lane);
+  f32x16 own[COLS][MB];              // column blocks wave, wave + 8 ..
+#pragma unroll
+  for (int c = 0; c < COLS; ++c)
+#pragma unroll
+    for (int i = 0; i < MB; ++i) {
+      own[c][i] = 0.0f;
+      if (wave + c * kChipWaves < n64 / 32) own[c][i] = chip_get(lx, n64, i, wave + c * kChipWaves, lane);
+    }
   for (int step = 0; step < k.steps; ++step) {
     f32x16 a[S];
 #pragma unroll
@@ -836,12 +879,15 @@ __device__ __forceinline__ void chip_steps(uint16_t* lx, uint16_t* la, float* pa
         b = three(q[0], p[0], b);
         b = three(q[1], p[1], b);
       }
-      b = square_block(k.square[step], b * k.square[step].product, chip_get(la, LDA, bi, bj, lane), bi == bj, lane);
+      b = b * k.square[step].product + chip_get(la, LDA, bi, bj, lane) * k.square[step].own;
     }
     __syncthreads();
     if (wave < S) chip_put(la, LDA, bi, bj, lane, b);
     __syncthreads();
-    for (int xj = wave; xj < n64 / 32; xj += kChipWaves) {
+#pragma unroll
+    for (int col = 0; col < COLS; ++col) {
+      const int xj = wave + col * kChipWaves;
+      if (xj >= n64 / 32) break;
       f32x16 x[MB];
 #pragma unroll
       for (int i = 0; i < MB; ++i) x[i] = 0.0f;
@@ -858,7 +904,10 @@ __device__ __forceinline__ void chip_steps(uint16_t* lx, uint16_t* la, float* pa
         }
       }
 #pragma unroll
-      for (int i = 0; i < MB; ++i) chip_put(lx, n64, i, xj, lane, x[i] * k.apply[step]);
+      for (int i = 0; i < MB; ++i) {
+        own[col][i] = x[i] * k.apply[step] + own[col][i] * k.own[step];
+        chip_put(lx, n64, i, xj, lane, own[col][i]);
+      }
     }
     __syncthreads();
   }
@@ -1092,7 +1141,7 @@ __global__ __launch_bounds__(kDirectWaves * 64) void ns_direct_kernel(const NsTa
   __syncthreads();
   f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-  for (int n = 0; n < W; ++n) v += *reinterpret_cast<const f32x4*>(&part[n][r][c]);
+  for (int n = 1; n <= W; ++n) v += *reinterpret_cast<const f32x4*>(&part[((SYM ? 0u : static_cast<uint32_t>(mt)) + n) % W][r][c]);      // a X's last
   v *= k.product;
   if constexpr (KIND == NS_SQUARE) v = square_terms(k, v, own, row, col);
   if constexpr (KIND != NS_LAST) put4(KIND == NS_GRAM ? w.a() : KIND == NS_SQUARE ? w.b() : w.x(from ^ 1), block_at(row, col, cols), v);
@@ -1318,6 +1367,7 @@ hipError_t launch_ns(const NsMatrix* m, int64_t n, const NsArgs& args, void* ws,
     k.gram[i] = static_cast<float>(scale_a / (scale_x * scale_x));
     k.square[i] = {static_cast<float>(c * (scale_b / (scale_a * scale_a))), static_cast<float>(b * (scale_b / scale_a)), static_cast<float>(a * scale_b)};
     k.apply[i] = static_cast<float>(next / (scale_b * scale_x));
+    k.own[i] = static_cast<float>(a * (next / scale_x));
     scale_x = next;
   }
   t.result = static_cast<float>(1.0 / scale_x);

@@ -342,7 +342,7 @@ struct NsCoef {
 };
 struct NsSteps {
   int32_t steps;
-  float gram[kNsSteps], apply[kNsSteps];
+  float gram[kNsSteps], apply[kNsSteps], own[kNsSteps];      // own: the next X's, of X itself
   NsCoef square[kNsSteps];
 };
 static_assert(sizeof(NsTable) + sizeof(NsSteps) <= 4096 && sizeof(NsTable) + sizeof(NsFirst) <= 4096, "kernel arguments");

@@ -97,6 +97,44 @@ def test_five_steps_of_a_steep_spectrum(shape, fall):
     _products(_run([x], FIVE)[0], x)
 
 
+def _term_by_term(x, steps):
+    """The steps in float32, sums of products that are exact added one term after another."""
+    import torch
+    x = x if x.shape[0] <= x.shape[1] else x.T.contiguous()
+    x = (x.double() / ((x.double() ** 2).sum().sqrt() + 1e-7)).float()
+
+    def product(p, q):
+        total = torch.zeros(p.shape[0], q.shape[1], device="cuda")
+        for k in range(p.shape[1]):
+            total = torch.addr(total.double(), p[:, k].double(), q[k].double()).float()
+        return total
+    for a, b, c in steps:
+        s = product(x, x.T.contiguous())
+        x = a * x + product(b * s + c * product(s, s), x)
+    return x
+
+
+@pytest.mark.parametrize("shape", SHAPES[:7], ids=lambda s: "x".join(map(str, s)))
+def test_a_steep_spectrum_is_as_precise_as_float32(shape):
+    """Singular values from 1 to 1e-4, where a X is most of most values: in norm no further off than float32 products
+    that add one term after another, and a quarter of that for what two parts drop of each product."""
+    import torch
+    H.require_gpu()
+    H.note(f"newton-schulz against float32 {shape}")
+    k = min(shape)
+    u, v = (torch.linalg.qr(t.double())[0] for t in _on_gpu([(shape[0], k), (shape[1], k)], 8))
+    x = ((u * torch.logspace(0, -4, k, dtype=torch.float64, device="cuda")) @ v.T.contiguous()).float()
+    got = _run([x], FIVE)[0]
+    plain = _term_by_term(x, FIVE)
+    y, got = (x, got) if shape[0] <= shape[1] else (x.T.contiguous(), got.T)
+    y = y.double() / ((y.double() ** 2).sum().sqrt() + 1e-7)
+    for a, b, c in FIVE:
+        s = y @ y.T.contiguous()
+        y = a * y + (b * s + c * s @ s) @ y
+    off = lambda z: float((z.double() - y).norm() / y.norm())
+    assert off(got) <= 1.25 * off(plain), (off(got), off(plain))
+
+
 @pytest.mark.parametrize("shape", [(20, 50), (128, 100), (200, 300), (1000, 1100)], ids=lambda s: "x".join(map(str, s)))
 def test_steps_that_shrink_x_keep_its_bits(shape):
     """X a_1 a_2 ..: every step has a bound of its own.  A step rounds twice, within 4 u, and drops as much; values are off by FLOOR of the
