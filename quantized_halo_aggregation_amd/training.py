@@ -28,6 +28,13 @@ from . import pipeline
 NAMES = ("w_gate", "w_up", "norm_weight", "norm_bias")
 
 
+def _take_rows(held, x):
+    """Copies x into `held`; rows that a copy would broadcast are refused."""
+    if x.shape != held.shape:
+        raise ValueError(f"x must be {held.shape[0]} x {held.shape[1]}, got {tuple(x.shape)}")
+    held.copy_(x)
+
+
 class GatedNormStack:
     """`layers` layers of width gp.d on a GCN partition, their gradients and an AdamW optimiser.
 
@@ -64,7 +71,7 @@ class GatedNormStack:
         """The last layer's rows for the inner rows x [n_in, d] (halo rows quantised at the partition's
         widths)."""
         gp = self.gp
-        self.X[0].copy_(x)
+        _take_rows(self.X[0], x)
         for l, p in enumerate(self.params):
             gp.quantize_send(self.X[l], gp.mirror, self.msg_f, epoch, 2 * l)
             gp.aggregate_fwd(self.X[l], self.msg_f, self.A[l])
@@ -154,7 +161,7 @@ class ResidualStack:
         """The last layer's normalised rows for the inner rows x [n_in, d] (halo rows quantised at the
         partition's widths)."""
         gp = self.gp
-        self.X[0].copy_(x)
+        _take_rows(self.X[0], x)
         B.residual_norm_fwd(self.X[0], None, None, self.U, post=B.ROW_NONE, pre=self.norm, pre_weight=self.first_weight,
                             eps=self.eps, pre_stats=self.pre_stats[0])
         for l, p in enumerate(self.params):

@@ -111,6 +111,18 @@ def test_residual_norm_binding_refuses(monkeypatch):
         B.residual_norm_bwd(x, x, x, x, x, x, post_stats=_gpu(6, 2), pre_stats=_gpu(6, 2, cls=Other), stream=0)
 
 
+def test_stacks_refuse_rows_that_would_be_broadcast():
+    """The gradient of x that backward returns has a row for every node, so x must have them, too."""
+    from types import SimpleNamespace
+    from quantized_halo_aggregation_amd.training import GatedNormStack, ResidualStack
+    held = torch.zeros(6, 8)
+    for stack in (GatedNormStack, ResidualStack):
+        for shape in ((8,), (1, 8), (6, 1), (), (6, 8, 1), (5, 8)):
+            with pytest.raises(ValueError, match="6 x 8"):
+                stack.forward(SimpleNamespace(gp=None, X=[held], layers=1), torch.ones(shape))
+    assert not held.any()
+
+
 def _coef(k=B.NS_COEFFICIENTS, steps=5):
     return B._ns_coefficients(k, steps)
 
