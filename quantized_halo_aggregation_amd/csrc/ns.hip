@@ -21,13 +21,13 @@
 // need accumulators of their own, twice as many.
 // What bounds it, and the forms that follow from it (five steps, float32, us a call):
 //   - Large matrices: the matrix cores.  Tiles through LDS, A and B by their tiles on and below the diagonal (the others are stored
-//     as their mirror), three launches a step for a batch of up to 40 matrices, whose tables the launches share.  4096 x 4096 3490 to 3680:
-//     B X 326 (1.27 PFLOP/s of part products, a plain library product in f16 reaches 1.39), A and B 190 to 206 each (1.1 to 1.2).  What is lost
+//     as their mirror), three launches a step for a batch of up to 40 matrices, whose tables the launches share.  4096 x 4096 3570 to 3790,
+//     on a card where a plain library product in f16 reaches 1.31 PFLOP/s 3788, B X 343 (1.20 of part products), A and B 203 and 212 (1.1).  What is lost
 //     is a step's wait and barrier, and the stores of a tile, with which nothing overlaps at one block a compute unit.
 //   - Lists too small to fill the chip with tiles: the chain of loads and barriers of a launch.  Blocks of 32 x 32 whose wavefronts
-//     share out the reduction, straight from memory, two or three launches a step: 8 of 256 x 256 98 in 17 launches of 5 to 7.
+//     share out the reduction, straight from memory, two or three launches a step: 8 of 256 x 256 98 to 100 in 17 launches of 5 to 8.
 //   - Matrices that fit in one block's LDS (up to 32 x 896, 64 x 384, 96 x 192 and 128 x 128): one launch from the gradient to the updated
-//     weight.  8 of 128 x 128 42, of which 6 a step: latency of LDS reads and of five barriers, the matrix cores are mostly idle.
+//     weight.  8 of 128 x 128 42, of which 5.5 a step: latency of LDS reads and of five barriers, the matrix cores are mostly idle.
 #include "../../include/qha.h"
 #include "qha_internal.hpp"
 #include "tile_common.hpp"
@@ -451,7 +451,8 @@ __global__ __launch_bounds__(WM * WN * KS * 64) void ns_product_kernel(const NsT
   const int whole = static_cast<int>(depth / BK), steps = (whole + KS - 1) / KS;
   const bool blank = KS == 2 && group == 1 && (whole & 1);           // a second half of one step fewer begins with zeros
   // In B X the steps of the tile's own rows, where B's diagonal brings a X in, come last: two jumps over the reduction's steps.  (A
-  // reduction that begins behind them and turns took 2 % more: blocks beside each other then read X at different places.)
+  // reduction that begins behind them and turns took 2 % more.)  Tiles beside each other are then up to a tile's steps apart in X: at
+  // 4096 x 4096 520 MB from memory instead of 403, and 0.7 % more time.
   const int mine = blank ? steps - 1 : steps;                        // of this group
   int first_step = group * steps, left = 0, jump = 0;      // loads left to the next jump, and its steps
   int after = 0, back = 0;             // the same of the jump behind it
@@ -637,7 +638,8 @@ constexpr int kChipBytes = Chip<1>::BYTES;
 static_assert(Chip<2>::BYTES <= kChipBytes && Chip<3>::BYTES <= kChipBytes && Chip<4>::BYTES <= kChipBytes && kChipBytes <= 160000, "LDS");
 
 // Places of 16-byte chunks in rows of a multiple of 256 bytes: rows r .. r + 15 fall on different sixteenths of 256 bytes, and so
-// do every second chunk of four (hi or lo) of the rows 4 i .. 4 i + 3.
+// do every second chunk of four (hi or lo) of the rows 4 i .. 4 i + 3.  Rows 16 apart share a place, so that stores of 8 bytes by 32
+// rows (chip_put) meet in pairs: 21 % of the LDS cycles of 8 of 128 x 128 are counted as conflicts.
 __device__ __forceinline__ int place_chip(int row, int chunk) {
   return chunk ^ ((row & 1) | ((row & 2) << 2) | ((row & 12) >> 1));
 }
@@ -914,8 +916,8 @@ __device__ __forceinline__ void chip_steps(uint16_t* lx, uint16_t* la, float* pa
 }
 
 // One matrix a block, from the gradient to the updated weight: X and, in turn, A and B as pairs in LDS.  SQUARE: those of 97
-// to 128 rows and columns.  Measured (us a call, five steps): 128 x 128 40 (5.5 a step), 64 x 64 23, 32 x 32 13.6, 22 x 840 35,
-// 96 x 192 57, 64 x 384 44.
+// to 128 rows and columns.  Measured (us a call, five steps): 128 x 128 39.5 (5.5 a step), 64 x 64 23.7, 32 x 32 13.2, 22 x 840 33.5,
+// 96 x 192 57, 64 x 384 43.
 template <bool SQUARE>
 __global__ __launch_bounds__(kChipThreads) void ns_chip_kernel(NsTable t, NsSteps k) {
   __shared__ __attribute__((aligned(16))) char pool[SQUARE ? Chip<4>::BYTES : kChipBytes];

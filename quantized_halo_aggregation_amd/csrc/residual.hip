@@ -14,9 +14,10 @@
 // adds partials in float64 in a fixed order (a block by itself needs none).  A team loads its next row before it works on the
 // present one, in the row's own type, and outputs are stored past the caches.
 //
-// Measured (kernel alone): forward, 300k x 128 float32, both layer norms, 108 to 112 us (619 MB, 5.5 TB/s; a large copy here reaches 4.7);
-// 16384 x 2048 bf16 on a float32 stream, four gates, 66 us (6.1 TB/s); one row of 4096 3.4 us (8.4 a call: host).  Backward, 300001 x 256
-// float32 326 us and 6 for the partials (5.6 TB/s); 8191 x 2048 bf16, a gate a row, 46 and 5 (269 MB, 5.3 TB/s).
+// Measured (kernel alone, in a loop over the same inputs): forward, 300k x 128 float32, both layer norms, 104 to 120 us (619 MB, 5.1 to 5.9 TB/s;
+// a large copy here reaches 4.7); 16384 x 2048 bf16 on a float32 stream, four gates, 68 us (a call on new inputs 80, 5.0 TB/s); one row of
+// 4096 3.4 us (8.5 a call: host).  Backward, 300001 x 256 float32 326 us and 6 for the partials (5.6 TB/s); 8191 x 2048 bf16, a gate a row,
+// 46 and 5 (269 MB, 5.2 TB/s; a call on new inputs 58).
 #include "act_common.hpp"
 #include "qha_internal.hpp"
 
