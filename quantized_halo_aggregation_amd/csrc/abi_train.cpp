@@ -151,31 +151,43 @@ double largest_of(double a, double b, double c) {
   return most;
 }
 
+// What a step (a, b, c) makes of singular values up to top: the largest |a + b s^2 + c s^4|, the largest value behind it, and the sum of
+// its terms' sizes.
+struct Reach {
+  double inner, most, terms;
+};
+Reach reach_of(const double* k, double top) {
+  // in units of top: with s = top r, a + b s^2 + c s^4 = a + (b top^2) r^2 + (c top^4) r^4
+  const double t = top * top, a = k[0], b = k[1] * t, c = k[2] * t * t;
+  Reach r = {std::max(std::fabs(a), std::fabs(a + b + c)), top * largest_of(a, b, c), std::fabs(a) + std::fabs(b) + std::fabs(c)};
+  const double turn = -0.5 * (b / c);
+  if (turn > 0.0 && turn < 1.0) r.inner = std::max(r.inner, std::fabs(a + 0.5 * b * turn));
+  return r;
+}
+
 // The polynomials must keep X, A and B within the scaled parts' range, also where rounding takes a singular value past what the
-// exact ones reach: a step's is below 2e-6 (16 units of float32) of its terms, and the next steps may grow it.
+// exact ones reach: a step's is taken for 2e-6 (16 units of float32) of its terms, and the next steps may grow it.  The bounds that X, A
+// and B are scaled by allow for 16 times as much, or all that this check lets pass: steep steps of the largest matrices cannot overflow.
 int check_steps(qha::NsArgs& args, int32_t steps, const double* coefficients, double eps) {
+  constexpr double kRounding = 2e-6, kFar = 16.0, kMostX = 3.8, kMostB = 60.0;
   args.steps = steps;
   args.eps = eps;
   args.coefficients = coefficients;
   if (steps < 1 || steps > qha::kNsSteps) return fail(QHA_ERR_INVALID_ARG, "steps must lie in 1 .. %d, got %d", qha::kNsSteps, steps);
   if (!coefficients) return fail(QHA_ERR_INVALID_ARG, "coefficients is NULL");
   if (!(eps >= 0.0) || !std::isfinite(eps)) return fail(QHA_ERR_INVALID_ARG, "eps must be finite and not negative");
-  double top = 1.0;
-  args.most_x[0] = top;
+  double top = 1.0, far = 1.0;
+  args.most_x[0] = far;
   for (int32_t i = 0; i < steps; ++i) {
+    const double* k = coefficients + 3 * i;
     for (int32_t e = 0; e < 3; ++e)
-      if (!(std::fabs(coefficients[3 * i + e]) <= kMostCoefficient)) return fail(QHA_ERR_INVALID_ARG, "step %d: a coefficient is not finite or passes 1e30", i);
-    // in units of top: with s = top r, a + b s^2 + c s^4 = a + (b top^2) r^2 + (c top^4) r^4
-    const double t = top * top, a = coefficients[3 * i], b = coefficients[3 * i + 1] * t, c = coefficients[3 * i + 2] * t * t;
-    double inner = std::max(std::fabs(a), std::fabs(a + b + c));
-    const double turn = -0.5 * (b / c);
-    if (turn > 0.0 && turn < 1.0) inner = std::max(inner, std::fabs(a + 0.5 * b * turn));
-    if (!(inner <= 60.0)) return fail(QHA_ERR_INVALID_ARG, "step %d: a + b s^2 + c s^4 passes 60", i);
-    const double most = top * largest_of(a, b, c);
-    if (!(most <= 3.8)) return fail(QHA_ERR_INVALID_ARG, "step %d: singular values pass 3.8", i);
-    const double rounding = 2e-6 * (std::fabs(a) + std::fabs(b) + std::fabs(c));
-    args.most_b[i] = inner + rounding;
-    args.most_x[i + 1] = top = most + top * rounding;
+      if (!(std::fabs(k[e]) <= kMostCoefficient)) return fail(QHA_ERR_INVALID_ARG, "step %d: a coefficient is not finite or passes 1e30", i);
+    const Reach r = reach_of(k, top), f = reach_of(k, far);
+    if (!(r.inner <= kMostB)) return fail(QHA_ERR_INVALID_ARG, "step %d: a + b s^2 + c s^4 passes 60", i);
+    if (!(r.most <= kMostX)) return fail(QHA_ERR_INVALID_ARG, "step %d: singular values pass 3.8", i);
+    top = r.most + kRounding * top * r.terms;
+    args.most_b[i] = std::min(f.inner + kFar * kRounding * f.terms, kMostB);
+    args.most_x[i + 1] = far = std::min(f.most + kFar * kRounding * far * f.terms, kMostX);
   }
   return QHA_OK;
 }

@@ -151,6 +151,21 @@ def test_steps_that_shrink_x_keep_its_bits(shape):
         assert bool(((out.double() - want).abs() <= bound).all()), own
 
 
+@pytest.mark.parametrize("shape", [(20, 50), (128, 100), (200, 300), (1000, 1100)], ids=lambda s: "x".join(map(str, s)))
+def test_a_steep_fixed_point_stays_in_range(shape):
+    """One value is its matrix's only singular value, 1, where 5 s - 20 s^3 + 16 s^5 has the slope 25: what rounding adds to it in a
+    step, 2e-6 of its terms' 41, grows 25-fold in the next, and half precision's range must hold it."""
+    import torch
+    H.require_gpu()
+    H.note(f"newton-schulz steep fixed point {shape}")
+    xs = []
+    for row, col in ((0, 0), (shape[0] - 1, 3), (7, shape[1] - 1)):
+        xs.append(torch.zeros(shape, device="cuda"))
+        xs[-1][row, col] = -3.7
+    for x, out in zip(xs, _run(xs, [(5, -20, 16)] * 2, eps=0.0)):
+        assert float((out - x.sign()).abs().max()) <= 2e-6 * 41 * 26
+
+
 def test_steps_that_leave_nothing():
     """A step of zeros, and steps behind it, whatever they are."""
     import torch
