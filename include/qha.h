@@ -524,10 +524,11 @@ size_t qha_residual_norm_workspace(int64_t n_rows, int64_t positions, int32_t c)
  * leading dimensions of at least cols; any rows and cols up to 65536 (UNSUPPORTED above).  out may be x (with the same
  * leading dimension and type); otherwise outputs must not overlap inputs or each other.  Accesses are of four elements where cols and the
  * leading dimension are multiples of 4 and the pointer is aligned to four elements.  Matrices without elements are skipped.
- * X, A and B are held in two f16 parts under a power of two, products are three part products and float32 sums.  A value keeps 23 bits
- * or, below 2^-17 of its bound, an absolute 2^-40 of it (the bound: the largest singular value that X can have then, its square for
- * A, the largest a + b s^2 + c s^4 for B, with room for rounding where steps are steep; 5e-32 at least): results have float32's precision with respect to their norm, not each row or column
- * that is far below it.  The norm is summed in float64.  A matrix with a value that is not finite gives NaN throughout; a zero matrix gives zeros.
+ * X, A and B are held in two f16 parts under a power of two, products are three part products and float32 sums.  A value keeps 23
+ * bits or, below 2^-17 of its bound, an absolute 2^-40 of it.  The bound is the largest singular value that X can have then, its square
+ * for A, the largest a + b s^2 + c s^4 for B, with room for rounding where steps are steep, and 5e-32 at least.  So results have
+ * float32's precision with respect to their norm, but not each row or column that is far below it.  The norm is summed in float64.
+ * A matrix with a value that is not finite gives NaN throughout; a zero matrix gives zeros.
  * Results are deterministic.  Those of a matrix do not depend on the other matrices' values, and on their sizes only in the
  * last bits (the list as a whole decides how the sums of those that do not stay on chip are cut).
  * workspace: device, 16-byte aligned, qha_newton_schulz_workspace bytes (0 where every matrix stays on chip: those of up to
